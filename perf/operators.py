@@ -236,7 +236,8 @@ def _ckpt8_split(X, fmt):
     if fmt == "int8":
         q = torch.round(x * torch.exp2((6 - e).double())[..., None]).clamp(-127, 127).to(torch.int8)
     else:
-        q = (x * torch.exp2(-e.double())[..., None]).to(torch.float32).to(torch.float8_e4m3fn)
+        most = torch.where(e == 120, 240.0, 448.0).double()[..., None]  # 256 * 2^120 is not a finite bf16
+        q = (x * torch.exp2(-e.double())[..., None]).clamp(-most, most).to(torch.float32).to(torch.float8_e4m3fn)
     e = torch.where(bad, torch.full_like(e, 128), e) + 127
     return q.view(M, K), e.to(torch.uint8)
 
@@ -408,7 +409,8 @@ def _exact_checkpoint(X, fmt):
     e = (lead - 8 + (big > 448 * torch.exp2(lead - 8))).clamp_min(-127.0)
     v = x / torch.exp2(e)
     step = torch.exp2(torch.floor(torch.log2(v.abs().clamp_min(2.0 ** -6))) - 3)
-    return torch.round(v / step) * step * torch.exp2(e)
+    most = torch.where(e == 120, 240.0, 448.0).double()
+    return torch.clamp(torch.round(v / step) * step, -most, most) * torch.exp2(e)
 
 
 def _exact_restored(q, e):
