@@ -402,13 +402,13 @@ def _exact_checkpoint(X, fmt):
     x = X.double()
     M, K = x.shape
     big = x.reshape(M, -1, 32).abs().max(dim=2).values.repeat_interleave(32, dim=1)
-    lead = torch.floor(torch.log2(big.clamp_min(2.0 ** -133)))
+    lead = torch.frexp(big.clamp_min(2.0 ** -133)).exponent.double() - 1
     if fmt == "int8":
         step = torch.exp2(lead.clamp_min(-127.0) - 6)
         return torch.clamp(torch.round(x / step), -127, 127) * step
     e = (lead - 8 + (big > 448 * torch.exp2(lead - 8))).clamp_min(-127.0)
     v = x / torch.exp2(e)
-    step = torch.exp2(torch.floor(torch.log2(v.abs().clamp_min(2.0 ** -6))) - 3)
+    step = torch.exp2(torch.frexp(v.abs().clamp_min(2.0 ** -6)).exponent.double() - 4)
     most = torch.where(e == 120, 240.0, 448.0).double()
     return torch.clamp(torch.round(v / step) * step, -most, most) * torch.exp2(e)
 
