@@ -15,8 +15,13 @@ synthetic inputs used by the tests and the benchmark.
 from .lynx import (  # noqa: F401
     LYNX_ACT_GELU_TANH,
     LYNX_ACT_NONE,
+    LYNX_CKPT8_E4M3,
+    LYNX_CKPT8_INT8,
     LynxError,
     lynx_check_error,
+    lynx_ckpt8_exponent_bytes,
+    lynx_ckpt8_restore,
+    lynx_ckpt8_store,
     lynx_debug_set_stall,
     lynx_linear,
     lynx_linear_act,
@@ -27,6 +32,11 @@ from .lynx import (  # noqa: F401
     lynx_linear_host,
     lynx_linear_host_act,
     lynx_linear_host_workspace_bytes,
+    lynx_linear_w4,
+    lynx_linear_w4_max_rows,
+    lynx_linear_w4_workspace_bytes,
+    lynx_lora_backward,
+    lynx_lora_backward_workspace_bytes,
     lynx_lora_rank,
     lynx_lora_rank_supported,
     lynx_meta_bytes,
@@ -36,11 +46,16 @@ from .lynx import (  # noqa: F401
     lynx_profile_set_split_event,
     lynx_sparse_gemm,
     lynx_sparsify,
+    lynx_sparsify_backward,
+    lynx_sparsify_backward_workspace_bytes,
     lynx_sparsify_noalloc,
     lynx_sparsify_noalloc_max_rows,
     lynx_sparsify_workspace_bytes,
     lynx_status_string,
     lynx_vals_bytes,
+    lynx_w4_bytes,
+    lynx_w4_dequantize,
+    lynx_w4_quantize,
     lynx_version,
     lynx_workspace_bytes,
     library,

@@ -1,0 +1,130 @@
+// ckpt8_kernel.cu -- an activation to 8 bits and back (lynx_ckpt8_store,
+// lynx_ckpt8_restore).
+//
+// Per 32 values one exponent: store finds the block's largest magnitude on the
+// bf16 bit patterns (which order like the magnitudes), scales by a power of two
+// (exact) and rounds once; restore multiplies back (exact).  Both are bound by
+// memory: 3.03 bytes move per value in each direction.
+#include "lynx_ckpt8.cuh"
+
+namespace lynx {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// Two lanes share a block of 32: each takes 16 values (two 16-byte loads, one
+// 16-byte store).
+template <int FMT>
+__global__ void __launch_bounds__(kThreads) ckpt8_store_kernel(const uint4* __restrict__ x, uint4* __restrict__ q,
+                                                               uint8_t* __restrict__ e, int64_t n16) {
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
+  // n16 is even (K % 64 == 0), so both lanes of a block are in or out together
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n16; i += stride) {
+    uint32_t w[8];
+    *reinterpret_cast<uint4*>(w) = __ldcs(x + 2 * i);
+    *reinterpret_cast<uint4*>(w + 4) = __ldcs(x + 2 * i + 1);
+    uint32_t top2 = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top2 = __vmaxu2(top2, w[j] & 0x7FFF7FFFu);
+    uint32_t top = max(top2 & 0xFFFFu, top2 >> 16);
+    const uint32_t pair = 3u << (threadIdx.x & 30u);
+    top = max(top, __shfl_xor_sync(pair, top, 1));
+    const bool bad = top >= 0x7F80u;
+    const int lead = static_cast<int>(top >> 7) - 127;  // floor(log2 max|x|), -127 below the normal range
+    int ex;
+    if constexpr (FMT == kCkpt8Int8) {
+      ex = lead;
+    } else {
+      ex = max(lead - ((top & 0x7Fu) > 96u ? 7 : 8), -127);  // 448 = 1.75 * 2^8
+    }
+    const int n = (FMT == kCkpt8Int8 ? 6 : 0) - ex;  // x * 2^n is what is rounded
+    const int n1 = min(n, 126);
+    const float f1 = bad ? 0.f : exp2_int(n1), f2 = exp2_int(n - n1);
+    uint32_t out[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float v[4] = {bf16_lo(w[2 * j]), bf16_hi(w[2 * j]), bf16_lo(w[2 * j + 1]), bf16_hi(w[2 * j + 1])};
+      if constexpr (FMT == kCkpt8Int8) {
+        uint32_t o = 0;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int r = max(-127, min(127, __float2int_rn(v[t] * f1 * f2)));
+          o |= (static_cast<uint32_t>(r) & 0xFFu) << (8 * t);
+        }
+        out[j] = bad ? 0u : o;
+      } else {
+        const float most = ex == 120 ? 240.f : 448.f;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) v[t] = fminf(fmaxf(v[t] * f1 * f2, -most), most);
+        uint32_t o;
+        asm("{\n\t.reg .b16 a, b;\n\t"
+            "cvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\t"
+            "mov.b32 %0, {a, b};\n\t}"
+            : "=r"(o)
+            : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]));
+        out[j] = bad ? 0u : o;
+      }
+    }
+    q[i] = make_uint4(out[0], out[1], out[2], out[3]);
+    if ((i & 1) == 0) e[i >> 1] = static_cast<uint8_t>(bad ? 255 : ex + 127);
+  }
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(kThreads) ckpt8_restore_kernel(const uint4* __restrict__ q,
+                                                                 const uint8_t* __restrict__ e,
+                                                                 uint4* __restrict__ x, int64_t n16) {
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n16; i += stride) {
+    uint32_t w[4];
+    *reinterpret_cast<uint4*>(w) = __ldcs(q + i);
+    const float f = ckpt8_factor<FMT>(e[i >> 1]);
+    uint32_t out[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float v[4];
+      ckpt8_decode4<FMT>(w[j], v);
+      out[2 * j] = pack_bf16(v[0] * f, v[1] * f);
+      out[2 * j + 1] = pack_bf16(v[2] * f, v[3] * f);
+    }
+    x[2 * i] = make_uint4(out[0], out[1], out[2], out[3]);
+    x[2 * i + 1] = make_uint4(out[4], out[5], out[6], out[7]);
+  }
+}
+
+// 16 values a thread; at most 8 blocks' worth of threads per SM loop over the rest
+int grid_of(int64_t n16, int sms) {
+  const int64_t blocks = (n16 + kThreads - 1) / kThreads;
+  const int64_t most = static_cast<int64_t>(sms) * 8 * 16;
+  return static_cast<int>(blocks < most ? blocks : most);
+}
+
+}  // namespace
+
+cudaError_t launch_ckpt8_store(const void* x, void* q, void* e, int64_t n, int format, int sms, cudaStream_t s) {
+  const int64_t n16 = n / 16;
+  auto* xp = static_cast<const uint4*>(x);
+  auto* qp = static_cast<uint4*>(q);
+  auto* ep = static_cast<uint8_t*>(e);
+  if (format == kCkpt8Int8)
+    ckpt8_store_kernel<kCkpt8Int8><<<grid_of(n16, sms), kThreads, 0, s>>>(xp, qp, ep, n16);
+  else
+    ckpt8_store_kernel<kCkpt8E4M3><<<grid_of(n16, sms), kThreads, 0, s>>>(xp, qp, ep, n16);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_ckpt8_restore(const void* q, const void* e, void* x, int64_t n, int format, int sms,
+                                 cudaStream_t s) {
+  const int64_t n16 = n / 16;
+  auto* qp = static_cast<const uint4*>(q);
+  auto* ep = static_cast<const uint8_t*>(e);
+  auto* xp = static_cast<uint4*>(x);
+  if (format == kCkpt8Int8)
+    ckpt8_restore_kernel<kCkpt8Int8><<<grid_of(n16, sms), kThreads, 0, s>>>(qp, ep, xp, n16);
+  else
+    ckpt8_restore_kernel<kCkpt8E4M3><<<grid_of(n16, sms), kThreads, 0, s>>>(qp, ep, xp, n16);
+  return cudaGetLastError();
+}
+
+}  // namespace lynx

@@ -1,0 +1,63 @@
+// lynx_ckpt8.cuh -- the 8-bit activation checkpoint's arithmetic, shared by the
+// kernels that write one and those that read one.
+//
+// 32 consecutive values of a row share a power of two 2^n, so value = q * 2^n
+// with q an int8 (7 significant bits) or an e4m3 number (4): exact in bf16, and
+// a tensor-core product with it rounds nothing.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "lynx_internal.h"
+
+namespace lynx {
+
+// 2^n as fp32, -149 <= n <= 127 (subnormal below -126)
+__device__ __forceinline__ float exp2_int(int n) {
+  return __uint_as_float(n >= -126 ? static_cast<uint32_t>(n + 127) << 23 : 1u << (n + 149));
+}
+
+// The multiplier a block's exponent byte stands for; NaN for 255, so that every
+// value of a block that held an infinity or a NaN comes back as NaN.
+template <int FMT>
+__device__ __forceinline__ float ckpt8_factor(uint32_t e) {
+  if (e == 255u) return __uint_as_float(0x7FC00000u);
+  return exp2_int(static_cast<int>(e) - (FMT == kCkpt8Int8 ? 133 : 127));
+}
+
+// 4 stored bytes -> 4 values (before the block's factor)
+template <int FMT>
+__device__ __forceinline__ void ckpt8_decode4(uint32_t w, float (&v)[4]) {
+  if constexpr (FMT == kCkpt8Int8) {
+    // the byte plus 128 in the low mantissa bits of 2^23, then minus 2^23 + 128
+    const uint32_t u = w ^ 0x80808080u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7540 | i)) - 8388736.0f;
+  } else {
+    uint32_t lo, hi;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+    const float2 a = __half22float2(*reinterpret_cast<__half2*>(&lo));
+    const float2 b = __half22float2(*reinterpret_cast<__half2*>(&hi));
+    v[0] = a.x;
+    v[1] = a.y;
+    v[2] = b.x;
+    v[3] = b.y;
+  }
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+}  // namespace lynx

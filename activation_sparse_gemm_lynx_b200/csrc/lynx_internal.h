@@ -143,6 +143,66 @@ cudaError_t once_per_device(std::once_flag (&flags)[64], cudaError_t (&results)[
   return results[dev];
 }
 
+// ---- 8-bit checkpoints, 4-bit weights, backward pass ------------------------
+
+// LYNX_CKPT8_* of the public header
+enum Ckpt8Format : int { kCkpt8Int8 = 0, kCkpt8E4M3 = 1 };
+
+cudaError_t launch_ckpt8_store(const void* x, void* q, void* e, int64_t n, int format, int sms, cudaStream_t s);
+cudaError_t launch_ckpt8_restore(const void* q, const void* e, void* x, int64_t n, int format, int sms,
+                                 cudaStream_t s);
+
+cudaError_t launch_w4_quantize(const void* w, int64_t N, int64_t K, int group, void* wq, void* scales, void* zeros,
+                               cudaStream_t s);
+cudaError_t launch_w4_dequantize(const void* wq, const void* scales, const void* zeros, int64_t N, int64_t K,
+                                 int group, void* w, cudaStream_t s);
+
+constexpr int kLinearW4MaxRows = 32;
+
+struct LinearW4Launch {
+  const void* x;       // [M,K] bf16
+  const void* wq;      // [N,K/2] nibbles
+  const void* scales;  // [K/group,N] bf16
+  const void* zeros;   // [K/group,N] bytes, or null
+  const void* bias;    // [N] bf16, or null
+  const void* a;       // [r,K] bf16, or null
+  const void* b;       // [N,r] bf16 (with a)
+  float* t;            // [M,r] fp32 scratch (with a)
+  void* y;             // [M,N] bf16
+  int64_t N, K;
+  int M, r, group, act;
+};
+cudaError_t launch_linear_w4(const LinearW4Launch& p, int sms, cudaStream_t s);
+
+struct LoraBackwardLaunch {
+  const void* dy;  // [M,N] bf16
+  const void* q;   // [M,K] bytes
+  const void* e;   // [M,K/32] bytes
+  const void* a;   // [r,K] bf16
+  const void* b;   // [N,r] bf16
+  void* da;        // [r,K] bf16
+  void* db;        // [N,r] bf16
+  void* dt;        // [M,r] bf16, or null
+  uint8_t* ws;
+  int64_t M, N, K;
+  int r, format;
+};
+size_t lora_backward_workspace(int64_t M, int64_t N, int64_t K, int64_t r);
+cudaError_t launch_lora_backward(const LoraBackwardLaunch& p, int sms, cudaStream_t s);
+
+struct SparsifyBackwardLaunch {
+  const void* g;   // [M,K] bf16
+  const void* q;   // [M,K] bytes
+  const void* e;   // [M,K/32] bytes
+  const void* dt;  // [M,r] bf16, or null
+  const void* a;   // [r,K] bf16 (with dt)
+  void* dx;        // [M,K] bf16
+  float2* coef;    // [M] scratch: s and D / Lk per row
+  int64_t M, K;
+  int r, format;
+};
+cudaError_t launch_sparsify_backward(const SparsifyBackwardLaunch& p, cudaStream_t s);
+
 // ---- helpers ----------------------------------------------------------------
 
 // 128-row blocks of metadata are allocated in pairs (a CTA pair covers 256 rows)

@@ -1,0 +1,276 @@
+// w4_kernel.cu -- the frozen weight in 4 bits (lynx_w4_quantize,
+// lynx_w4_dequantize) and the layer for a few tokens on it (lynx_linear_w4).
+#include <cuda_bf16.h>
+
+#include "lynx_act.cuh"
+#include "lynx_ckpt8.cuh"
+#include "lynx_internal.h"
+
+namespace lynx {
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// to 4 bits and back: tiles of 32 rows x 256 k, 8 warps, 4 rows a warp, 8 k (one
+// packed word) a lane.  Bound by memory (2.5 bytes a weight each way).  The side
+// arrays are [K/group, N], so a tile's scales go through shared memory to leave
+// (or come) as rows of 32 instead of single values N apart.
+
+constexpr int kTileN = 32;
+constexpr int kTileK = 256;
+constexpr int kThreads = 256;
+
+// Nibble place of k in its word of 8: 0, 2, 4, 6, 1, 3, 5, 7 from the low end, so
+// k sits at 4 * (k / 2 + 4 * (k % 2)) bits.
+__device__ __forceinline__ constexpr int nibble_shift(int k) { return 4 * (k / 2 + 4 * (k % 2)); }
+
+template <int GROUP, bool ZEROS>
+__global__ void __launch_bounds__(kThreads) w4_quantize_kernel(const __nv_bfloat16* __restrict__ w, int64_t N,
+                                                               int64_t K, uint32_t* __restrict__ wq,
+                                                               __nv_bfloat16* __restrict__ scales,
+                                                               uint8_t* __restrict__ zeros) {
+  constexpr int kLanes = GROUP / 8;            // lanes that share a group
+  constexpr int kGroups = kTileK / GROUP;      // groups of a tile row
+  __shared__ __nv_bfloat16 s_sm[kGroups][kTileN];
+  __shared__ uint8_t z_sm[kGroups][kTileN];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const unsigned k_tiles = static_cast<unsigned>((K + kTileK - 1) / kTileK);
+  const int64_t kt = blockIdx.x % k_tiles;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x / k_tiles) * kTileN;
+  const int64_t k0 = kt * kTileK + 8 * lane;
+  const bool k_in = k0 < K;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = 4 * warp + i;
+    const int64_t n = n0 + row;
+    const bool in = k_in && n < N;
+    uint32_t v[4] = {0, 0, 0, 0};
+    if (in) *reinterpret_cast<uint4*>(v) = __ldcs(reinterpret_cast<const uint4*>(w + n * K + k0));
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      x[2 * j] = bf16_lo(v[j]);
+      x[2 * j + 1] = bf16_hi(v[j]);
+    }
+    float hi = x[0], lo = x[0];
+#pragma unroll
+    for (int j = 1; j < 8; ++j) {
+      hi = fmaxf(hi, x[j]);
+      lo = fminf(lo, x[j]);
+    }
+#pragma unroll
+    for (int d = 1; d < kLanes; d *= 2) {
+      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, d));
+      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, d));
+    }
+    // the quotient in 64 bits, one per group: hi - lo of two bf16 is not always an fp32
+    float top;
+    if constexpr (ZEROS) {
+      hi = fmaxf(hi, 0.f);
+      lo = fminf(lo, 0.f);
+      top = __double2float_rn((static_cast<double>(hi) - static_cast<double>(lo)) / 15.0);
+    } else {
+      top = fmaxf(hi, -lo) / 7.f;
+    }
+    const __nv_bfloat16 sb = __float2bfloat16_rn(top);
+    const float s = __bfloat162float(sb);
+    int z = ZEROS ? 0 : 8;
+    uint32_t word = 0;
+    if (s == 0.f) {
+      word = static_cast<uint32_t>(z) * 0x11111111u;
+    } else {
+      if constexpr (ZEROS) z = max(0, min(15, __float2int_rn(-lo / s)));
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int q = max(0, min(15, __float2int_rn(x[k] / s) + z));
+        word |= static_cast<uint32_t>(q) << nibble_shift(k);
+      }
+    }
+    if (in) wq[(n * K + k0) >> 3] = word;
+    if (lane % kLanes == 0) {
+      s_sm[lane / kLanes][row] = sb;
+      if constexpr (ZEROS) z_sm[lane / kLanes][row] = static_cast<uint8_t>(z);
+    }
+  }
+  __syncthreads();
+  const int64_t kg0 = kt * kGroups;
+  for (int i = threadIdx.x; i < kGroups * kTileN; i += kThreads) {
+    const int g = i / kTileN, row = i % kTileN;
+    if (n0 + row < N && (kg0 + g) * GROUP < K) {
+      scales[(kg0 + g) * N + n0 + row] = s_sm[g][row];
+      if constexpr (ZEROS) zeros[(kg0 + g) * N + n0 + row] = z_sm[g][row];
+    }
+  }
+}
+
+template <int GROUP, bool ZEROS>
+__global__ void __launch_bounds__(kThreads) w4_dequantize_kernel(const uint32_t* __restrict__ wq,
+                                                                 const __nv_bfloat16* __restrict__ scales,
+                                                                 const uint8_t* __restrict__ zeros, int64_t N,
+                                                                 int64_t K, __nv_bfloat16* __restrict__ w) {
+  constexpr int kLanes = GROUP / 8;
+  constexpr int kGroups = kTileK / GROUP;
+  __shared__ float s_sm[kGroups][kTileN];
+  __shared__ float z_sm[kGroups][kTileN];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const unsigned k_tiles = static_cast<unsigned>((K + kTileK - 1) / kTileK);
+  const int64_t kt = blockIdx.x % k_tiles;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x / k_tiles) * kTileN;
+  const int64_t k0 = kt * kTileK + 8 * lane;
+  const bool k_in = k0 < K;
+  uint32_t word[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t n = n0 + 4 * warp + i;
+    word[i] = k_in && n < N ? __ldcs(wq + ((n * K + k0) >> 3)) : 0u;
+  }
+  const int64_t kg0 = kt * kGroups;
+  for (int i = threadIdx.x; i < kGroups * kTileN; i += kThreads) {
+    const int g = i / kTileN, row = i % kTileN;
+    const bool in = n0 + row < N && (kg0 + g) * GROUP < K;
+    const int64_t at = (kg0 + g) * N + n0 + row;
+    s_sm[g][row] = in ? __bfloat162float(scales[at]) : 0.f;
+    z_sm[g][row] = ZEROS ? (in ? static_cast<float>(zeros[at] & 15) : 0.f) : 8.f;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = 4 * warp + i;
+    const int64_t n = n0 + row;
+    if (!k_in || n >= N) continue;
+    const float s = s_sm[lane / kLanes][row], z = z_sm[lane / kLanes][row];
+    uint32_t out[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float a = static_cast<float>((word[i] >> nibble_shift(2 * j)) & 15u) - z;
+      const float b = static_cast<float>((word[i] >> nibble_shift(2 * j + 1)) & 15u) - z;
+      out[j] = pack_bf16(a * s, b * s);
+    }
+    *reinterpret_cast<uint4*>(w + n * K + k0) = make_uint4(out[0], out[1], out[2], out[3]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// the layer for a few tokens
+
+// T = X A^T: one warp per (adapter row, token)
+__global__ void __launch_bounds__(kThreads) w4_lora_down_kernel(const __nv_bfloat16* __restrict__ x,
+                                                                const __nv_bfloat16* __restrict__ a, int64_t K, int r,
+                                                                int M, float* __restrict__ t) {
+  const int lane = threadIdx.x & 31;
+  const int id = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  if (id >= r * M) return;
+  const int m = id / r, j = id % r;
+  const uint32_t* xr = reinterpret_cast<const uint32_t*>(x + m * K);
+  const uint32_t* ar = reinterpret_cast<const uint32_t*>(a + j * K);
+  float acc = 0.f;
+  for (int64_t k = lane; k < K / 2; k += 32) {
+    acc = fmaf(bf16_lo(xr[k]), bf16_lo(ar[k]), acc);
+    acc = fmaf(bf16_hi(xr[k]), bf16_hi(ar[k]), acc);
+  }
+  for (int d = 16; d > 0; d >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, d);
+  if (lane == 0) t[id] = acc;
+}
+
+// One warp per output column, 8 tokens at a time.
+__global__ void __launch_bounds__(kThreads) linear_w4_kernel(LinearW4Launch p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t n = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+  if (n >= p.N) return;
+  const auto* x = static_cast<const __nv_bfloat16*>(p.x);
+  const auto* wq = static_cast<const uint32_t*>(p.wq);
+  const auto* scales = static_cast<const __nv_bfloat16*>(p.scales);
+  const auto* zeros = static_cast<const uint8_t*>(p.zeros);
+  const auto* b = static_cast<const __nv_bfloat16*>(p.b);
+  const auto* bias = static_cast<const __nv_bfloat16*>(p.bias);
+  auto* y = static_cast<__nv_bfloat16*>(p.y);
+  for (int m0 = 0; m0 < p.M; m0 += 8) {
+    float acc[8] = {};
+    for (int64_t k = 8 * lane; k < p.K; k += 256) {
+      const int64_t side = (k / p.group) * p.N + n;
+      const float s = __bfloat162float(scales[side]);
+      const float z = zeros != nullptr ? static_cast<float>(zeros[side] & 15) : 8.f;
+      const uint32_t word = wq[(n * p.K + k) >> 3];
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = (static_cast<float>((word >> nibble_shift(j)) & 15u) - z) * s;
+      for (int i = 0; i < 8 && m0 + i < p.M; ++i) {
+        const uint4 xv = *reinterpret_cast<const uint4*>(x + (m0 + i) * p.K + k);
+        const uint32_t xs[4] = {xv.x, xv.y, xv.z, xv.w};
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum += v[2 * j] * bf16_lo(xs[j]) + v[2 * j + 1] * bf16_hi(xs[j]);
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          if (c == i) acc[c] += sum;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float v = acc[i];
+      for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+      if (m0 + i >= p.M) continue;
+      if (p.a != nullptr) {
+        float u = 0.f;
+        for (int j = lane; j < p.r; j += 32)
+          u = fmaf(p.t[(m0 + i) * p.r + j], __bfloat162float(b[n * p.r + j]), u);
+        for (int d = 16; d > 0; d >>= 1) u += __shfl_xor_sync(0xffffffffu, u, d);
+        v += u;
+      }
+      if (bias != nullptr) v += __bfloat162float(bias[n]);
+      if (p.act == kActGeluTanh) v = gelu_tanh(v);
+      if (lane == 0) y[(m0 + i) * p.N + n] = __float2bfloat16_rn(v);
+    }
+  }
+}
+
+unsigned weight_tiles(int64_t N, int64_t K) {
+  return static_cast<unsigned>(((K + kTileK - 1) / kTileK) * ((N + kTileN - 1) / kTileN));
+}
+
+}  // namespace
+
+cudaError_t launch_w4_quantize(const void* w, int64_t N, int64_t K, int group, void* wq, void* scales, void* zeros,
+                               cudaStream_t s) {
+  const unsigned grid = weight_tiles(N, K);
+  auto run = [&](auto kernel) {
+    kernel<<<grid, kThreads, 0, s>>>(static_cast<const __nv_bfloat16*>(w), N, K, static_cast<uint32_t*>(wq),
+                                     static_cast<__nv_bfloat16*>(scales), static_cast<uint8_t*>(zeros));
+    return cudaGetLastError();
+  };
+  if (zeros != nullptr)
+    return group == 32 ? run(w4_quantize_kernel<32, true>)
+                       : group == 64 ? run(w4_quantize_kernel<64, true>) : run(w4_quantize_kernel<128, true>);
+  return group == 32 ? run(w4_quantize_kernel<32, false>)
+                     : group == 64 ? run(w4_quantize_kernel<64, false>) : run(w4_quantize_kernel<128, false>);
+}
+
+cudaError_t launch_w4_dequantize(const void* wq, const void* scales, const void* zeros, int64_t N, int64_t K,
+                                 int group, void* w, cudaStream_t s) {
+  const unsigned grid = weight_tiles(N, K);
+  auto run = [&](auto kernel) {
+    kernel<<<grid, kThreads, 0, s>>>(static_cast<const uint32_t*>(wq), static_cast<const __nv_bfloat16*>(scales),
+                                     static_cast<const uint8_t*>(zeros), N, K, static_cast<__nv_bfloat16*>(w));
+    return cudaGetLastError();
+  };
+  if (zeros != nullptr)
+    return group == 32 ? run(w4_dequantize_kernel<32, true>)
+                       : group == 64 ? run(w4_dequantize_kernel<64, true>) : run(w4_dequantize_kernel<128, true>);
+  return group == 32 ? run(w4_dequantize_kernel<32, false>)
+                     : group == 64 ? run(w4_dequantize_kernel<64, false>) : run(w4_dequantize_kernel<128, false>);
+}
+
+cudaError_t launch_linear_w4(const LinearW4Launch& p, int sms, cudaStream_t s) {
+  (void)sms;
+  constexpr int kWarps = kThreads / 32;
+  if (p.a != nullptr) {
+    w4_lora_down_kernel<<<(p.r * p.M + kWarps - 1) / kWarps, kThreads, 0, s>>>(
+        static_cast<const __nv_bfloat16*>(p.x), static_cast<const __nv_bfloat16*>(p.a), p.K, p.r, p.M, p.t);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  linear_w4_kernel<<<static_cast<unsigned>((p.N + kWarps - 1) / kWarps), kThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace lynx

@@ -27,6 +27,9 @@ LYNX_ERR_DEVICE_TIMEOUT = 6
 LYNX_ACT_NONE = 0
 LYNX_ACT_GELU_TANH = 1
 
+LYNX_CKPT8_INT8 = 0
+LYNX_CKPT8_E4M3 = 1
+
 
 class LynxError(RuntimeError):
     def __init__(self, status, what=""):
@@ -69,6 +72,19 @@ def library():
             "lynx_linear_host": ([p, p, p, p, p, i64, i64, i64, i64, i32, p, p, sz, p], i32),
             "lynx_linear_host_act": ([p, p, p, p, p, i64, i64, i64, i64, i32, i32, p, p, sz, p], i32),
             "lynx_sparse_gemm": ([p, p, p, p, p, p, i64, i64, i64, i64, p, p], i32),
+            "lynx_w4_bytes": ([i64, i64], sz),
+            "lynx_w4_quantize": ([p, i64, i64, i32, p, p, p, p], i32),
+            "lynx_w4_dequantize": ([p, p, p, i64, i64, i32, p, p], i32),
+            "lynx_linear_w4_max_rows": ([], i64),
+            "lynx_linear_w4_workspace_bytes": ([i64, i64, i64, i64], sz),
+            "lynx_linear_w4": ([p, p, p, p, p, p, p, i64, i64, i64, i64, i32, i32, p, p, sz, p], i32),
+            "lynx_ckpt8_exponent_bytes": ([i64, i64], sz),
+            "lynx_ckpt8_store": ([p, i64, i64, i32, p, p, p], i32),
+            "lynx_ckpt8_restore": ([p, p, i64, i64, i32, p, p], i32),
+            "lynx_lora_backward_workspace_bytes": ([i64, i64, i64, i64], sz),
+            "lynx_lora_backward": ([p, p, p, p, p, i64, i64, i64, i64, i32, p, p, p, p, sz, p], i32),
+            "lynx_sparsify_backward_workspace_bytes": ([i64, i64], sz),
+            "lynx_sparsify_backward": ([p, p, p, p, p, i64, i64, i64, i32, p, p, sz, p], i32),
             "lynx_check_error": ([p, p], i32),
             "lynx_meta_hw_to_canonical": ([p, p, i64, i64], i32),
             "lynx_meta_canonical_to_hw": ([p, p, i64, i64], i32),
@@ -410,6 +426,278 @@ def lynx_sparse_gemm(vals, meta, W, bias=None, T=None, B=None, Y=None, stream=No
                                     _ptr(B), M, N, K, r, _ptr(Y), _stream(stream))
     _check(st, "lynx_sparse_gemm")
     return Y
+
+
+# ---- the weight in 4 bits, the 8-bit checkpoint, the backward pass ----------
+
+
+def _on_one_device(**tensors):
+    """Every tensor given on the current CUDA device (the device of the stream)."""
+    import torch
+
+    here = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and t.device.index != here:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{here}")
+
+
+def _empty(shape, dtype, stream):
+    """A buffer of the current device from the memory pool of the stream it is used on."""
+    import torch
+
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device="cuda")
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device="cuda")
+
+
+def _need_workspace(workspace, need, stream):
+    """(pointer, bytes) of a caller's workspace, or of one made here."""
+    import torch
+
+    if workspace is None:
+        if need == 0:
+            return None, 0, None
+        workspace = _empty((need,), torch.uint8, stream)
+    else:
+        _need(workspace, "workspace", torch.uint8)
+        _on_one_device(workspace=workspace)
+    return _ptr(workspace), workspace.numel(), workspace
+
+
+def _w4_args(Wq, scales, zeros):
+    import torch
+
+    _need(Wq, "Wq", torch.uint8)
+    _need(scales, "scales", torch.bfloat16)
+    if Wq.dim() != 2 or scales.dim() != 2:
+        raise ValueError("Wq must be [N,K/2] and scales [K/group,N]")
+    N, K = Wq.shape[0], 2 * Wq.shape[1]
+    groups = scales.shape[0]
+    if scales.shape[1] != N or groups == 0 or K % groups:
+        raise ValueError("scales must be [K/group,N]")
+    if zeros is not None:
+        _need(zeros, "zeros", torch.uint8, (groups, N))
+    return N, K, K // groups
+
+
+def lynx_w4_bytes(N, K):
+    return library().lynx_w4_bytes(N, K)
+
+
+def lynx_w4_quantize(W, group=128, zero_points=False, Wq=None, scales=None, zeros=None, stream=None):
+    """W [N,K] bf16 to 4 bits: returns (Wq [N,K/2] u8, scales [K/group,N] bf16,
+    zeros [K/group,N] u8, or None without zero points).  `zeros` given implies
+    zero points."""
+    import torch
+
+    _need(W, "W", torch.bfloat16)
+    if W.dim() != 2:
+        raise ValueError("W must be [N,K]")
+    N, K = W.shape
+    if group not in (32, 64, 128) or K % group:
+        raise LynxError(LYNX_ERR_UNSUPPORTED_SHAPE, f"lynx_w4_quantize (group {group}, K {K})")
+    _on_one_device(W=W, Wq=Wq, scales=scales, zeros=zeros)
+    if Wq is None:
+        Wq = _empty((N, K // 2), torch.uint8, stream)
+    if scales is None:
+        scales = _empty((K // group, N), torch.bfloat16, stream)
+    if zeros is None and zero_points:
+        zeros = _empty((K // group, N), torch.uint8, stream)
+    _need(Wq, "Wq", torch.uint8, (N, K // 2))
+    _need(scales, "scales", torch.bfloat16, (K // group, N))
+    if zeros is not None:
+        _need(zeros, "zeros", torch.uint8, (K // group, N))
+    st = library().lynx_w4_quantize(_ptr(W), N, K, int(group), _ptr(Wq), _ptr(scales), _ptr(zeros),
+                                    _stream(stream))
+    _check(st, "lynx_w4_quantize")
+    return Wq, scales, zeros
+
+
+def lynx_w4_dequantize(Wq, scales, zeros=None, W=None, stream=None):
+    """W [N,K] bf16 from its 4-bit form (the group is K / scales.shape[0])."""
+    import torch
+
+    N, K, group = _w4_args(Wq, scales, zeros)
+    _on_one_device(Wq=Wq, scales=scales, zeros=zeros, W=W)
+    if W is None:
+        W = _empty((N, K), torch.bfloat16, stream)
+    _need(W, "W", torch.bfloat16, (N, K))
+    st = library().lynx_w4_dequantize(_ptr(Wq), _ptr(scales), _ptr(zeros), N, K, group, _ptr(W),
+                                      _stream(stream))
+    _check(st, "lynx_w4_dequantize")
+    return W
+
+
+def lynx_linear_w4_max_rows():
+    return library().lynx_linear_w4_max_rows()
+
+
+def lynx_linear_w4_workspace_bytes(M, N, K, r=0):
+    return library().lynx_linear_w4_workspace_bytes(M, N, K, r)
+
+
+def lynx_linear_w4(X, Wq, scales, zeros=None, bias=None, A=None, B=None, act=LYNX_ACT_NONE, Y=None,
+                   workspace=None, stream=None):
+    """Y = act(X W^T + bias + (X A^T) B^T) for up to 32 tokens, W in 4 bits
+    (lynx_w4_quantize's outputs).  Returns Y."""
+    import torch
+
+    N, K, group = _w4_args(Wq, scales, zeros)
+    _need(X, "X", torch.bfloat16)
+    if X.dim() != 2 or X.shape[1] != K:
+        raise ValueError("X must be [M,K] with K = 2 * Wq.shape[1]")
+    M = X.shape[0]
+    if bias is not None:
+        _need(bias, "bias", torch.bfloat16, (N,))
+    if (A is None) != (B is None):
+        raise ValueError("A and B must both be given or both be None")
+    r = 0
+    if A is not None:
+        r = A.shape[0]
+        _need(A, "A", torch.bfloat16, (r, K))
+        _need(B, "B", torch.bfloat16, (N, r))
+    _on_one_device(X=X, Wq=Wq, scales=scales, zeros=zeros, bias=bias, A=A, B=B, Y=Y)
+    if Y is None:
+        Y = _empty((M, N), torch.bfloat16, stream)
+    _need(Y, "Y", torch.bfloat16, (M, N))
+    lib = library()
+    need = lib.lynx_linear_w4_workspace_bytes(M, N, K, r) if r else 0
+    ws, ws_bytes, _keep = _need_workspace(workspace, need, stream)
+    st = lib.lynx_linear_w4(_ptr(X), _ptr(Wq), _ptr(scales), _ptr(zeros), _ptr(bias), _ptr(A), _ptr(B), M, N,
+                            K, r, group, int(act), _ptr(Y), ws, ws_bytes, _stream(stream))
+    _check(st, "lynx_linear_w4")
+    return Y
+
+
+def _ckpt8_dtype(format):
+    import torch
+
+    if format == LYNX_CKPT8_INT8:
+        return torch.int8
+    if format == LYNX_CKPT8_E4M3:
+        return torch.float8_e4m3fn
+    raise LynxError(LYNX_ERR_INVALID_ARG, f"checkpoint format {format}")
+
+
+def _ckpt8_args(q, e):
+    """(M, K, format) of a checkpoint; the dtype of q says which format it is."""
+    import torch
+
+    _need(q, "q")
+    if q.dim() != 2 or q.dtype not in (torch.int8, torch.float8_e4m3fn):
+        raise TypeError("q must be an int8 or float8_e4m3fn matrix")
+    M, K = q.shape
+    _need(e, "e", torch.uint8, (M, K // 32))
+    return M, K, LYNX_CKPT8_INT8 if q.dtype == torch.int8 else LYNX_CKPT8_E4M3
+
+
+def lynx_ckpt8_exponent_bytes(M, K):
+    return library().lynx_ckpt8_exponent_bytes(M, K)
+
+
+def lynx_ckpt8_store(X, format=LYNX_CKPT8_INT8, q=None, e=None, stream=None):
+    """The 8-bit checkpoint of X [M,K] bf16: returns (q [M,K] int8 or
+    float8_e4m3fn, e [M,K/32] u8)."""
+    import torch
+
+    _need(X, "X", torch.bfloat16)
+    if X.dim() != 2:
+        raise ValueError("X must be [M,K]")
+    M, K = X.shape
+    dtype = _ckpt8_dtype(format)
+    _on_one_device(X=X, q=q, e=e)
+    if q is None:
+        q = _empty((M, K), dtype, stream)
+    if e is None:
+        e = _empty((M, K // 32), torch.uint8, stream)
+    _need(q, "q", dtype, (M, K))
+    _need(e, "e", torch.uint8, (M, K // 32))
+    st = library().lynx_ckpt8_store(_ptr(X), M, K, int(format), _ptr(q), _ptr(e), _stream(stream))
+    _check(st, "lynx_ckpt8_store")
+    return q, e
+
+
+def lynx_ckpt8_restore(q, e, X=None, stream=None):
+    """The values [M,K] bf16 a checkpoint stands for."""
+    import torch
+
+    M, K, fmt = _ckpt8_args(q, e)
+    _on_one_device(q=q, e=e, X=X)
+    if X is None:
+        X = _empty((M, K), torch.bfloat16, stream)
+    _need(X, "X", torch.bfloat16, (M, K))
+    st = library().lynx_ckpt8_restore(_ptr(q), _ptr(e), M, K, fmt, _ptr(X), _stream(stream))
+    _check(st, "lynx_ckpt8_restore")
+    return X
+
+
+def lynx_lora_backward_workspace_bytes(M, N, K, r=64):
+    return library().lynx_lora_backward_workspace_bytes(M, N, K, r)
+
+
+def lynx_lora_backward(dY, q, e, A, B, dA=None, dB=None, dT=None, workspace=None, stream=None):
+    """The adapter's gradients from the checkpoint (q, e) of X: returns
+    (dA [r,K], dB [N,r], dT [M,r]), bf16, with dT = dY B the gradient of
+    T = X A^T (lynx_sparsify_backward takes it)."""
+    import torch
+
+    M, K, fmt = _ckpt8_args(q, e)
+    _need(dY, "dY", torch.bfloat16)
+    _need(A, "A", torch.bfloat16)
+    _need(B, "B", torch.bfloat16)
+    if dY.dim() != 2 or dY.shape[0] != M:
+        raise ValueError("dY must be [M,N] with the checkpoint's M")
+    N = dY.shape[1]
+    r = A.shape[0]
+    _need(A, "A", torch.bfloat16, (r, K))
+    _need(B, "B", torch.bfloat16, (N, r))
+    _on_one_device(dY=dY, q=q, e=e, A=A, B=B, dA=dA, dB=dB, dT=dT)
+    if dA is None:
+        dA = _empty((r, K), torch.bfloat16, stream)
+    if dB is None:
+        dB = _empty((N, r), torch.bfloat16, stream)
+    if dT is None:
+        dT = _empty((M, r), torch.bfloat16, stream)
+    _need(dA, "dA", torch.bfloat16, (r, K))
+    _need(dB, "dB", torch.bfloat16, (N, r))
+    _need(dT, "dT", torch.bfloat16, (M, r))
+    lib = library()
+    ws, ws_bytes, _keep = _need_workspace(workspace, lib.lynx_lora_backward_workspace_bytes(M, N, K, r), stream)
+    st = lib.lynx_lora_backward(_ptr(dY), _ptr(q), _ptr(e), _ptr(A), _ptr(B), M, N, K, r, fmt, _ptr(dA),
+                                _ptr(dB), _ptr(dT), ws, ws_bytes, _stream(stream))
+    _check(st, "lynx_lora_backward")
+    return dA, dB, dT
+
+
+def lynx_sparsify_backward_workspace_bytes(M, K):
+    return library().lynx_sparsify_backward_workspace_bytes(M, K)
+
+
+def lynx_sparsify_backward(G, q, e, dT=None, A=None, dX=None, workspace=None, stream=None):
+    """dX [M,K] from G, the gradient of S(X), at the checkpoint (q, e) of X, plus
+    the LoRA branch's dT A (see include/lynx.h).  Returns dX."""
+    import torch
+
+    M, K, fmt = _ckpt8_args(q, e)
+    _need(G, "G", torch.bfloat16, (M, K))
+    if (dT is None) != (A is None):
+        raise ValueError("dT and A must both be given or both be None")
+    r = 0
+    if A is not None:
+        r = A.shape[0]
+        _need(A, "A", torch.bfloat16, (r, K))
+        _need(dT, "dT", torch.bfloat16, (M, r))
+    _on_one_device(G=G, q=q, e=e, dT=dT, A=A, dX=dX)
+    if dX is None:
+        dX = _empty((M, K), torch.bfloat16, stream)
+    _need(dX, "dX", torch.bfloat16, (M, K))
+    lib = library()
+    ws, ws_bytes, _keep = _need_workspace(workspace, lib.lynx_sparsify_backward_workspace_bytes(M, K), stream)
+    st = lib.lynx_sparsify_backward(_ptr(G), _ptr(q), _ptr(e), _ptr(dT), _ptr(A), M, K, r, fmt, _ptr(dX), ws,
+                                    ws_bytes, _stream(stream))
+    _check(st, "lynx_sparsify_backward")
+    return dX
 
 
 def lynx_check_error(stream=None):

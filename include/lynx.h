@@ -299,6 +299,140 @@ LYNX_API int lynx_sparse_gemm(const void* vals, const void* meta, const void* T,
                      const void* bias, const void* B, int64_t M, int64_t N, int64_t K, int64_t r,
                      void* Y, void* stream);
 
+/* ---- the frozen weight in 4 bits, and the layer for a few tokens -------- */
+
+/* With few tokens the layer's time is the time to read W.  The entry points
+ * below keep the frozen weight in 4 bits with one scale per `group` consecutive
+ * K-values of a row:
+ *
+ *     w[n,k] = s[k / group, n] * (q[n,k] - z[k / group, n]),   0 <= q, z <= 15
+ *
+ *   Wq      [N, K/2] bytes: row n holds its q in 32-bit little-endian words of 8
+ *           consecutive k; from the low to the high nibble a word holds
+ *           k = 0, 2, 4, 6, 1, 3, 5, 7 (so that one shift and one mask give two
+ *           neighbouring k in the two halves of a register)
+ *   scales  [K/group, N] bf16
+ *   zeros   [K/group, N] bytes, each 0..15 (the low 4 bits are read), or NULL:
+ *           z = 8 everywhere
+ *   group   32, 64 or 128, with K % group == 0 (else LYNX_ERR_UNSUPPORTED_SHAPE)
+ * N and K follow the layer's rules (N % 8 == 0, K % 64 == 0).  Buffers that
+ * one call reads and writes must not overlap.  None of it is on the RT-Lynx
+ * pages, which keep W in bf16. */
+
+/* Bytes of Wq: N * K / 2. */
+LYNX_API size_t lynx_w4_bytes(int64_t N, int64_t K);
+
+/* W [N,K] bf16 -> Wq, scales, zeros (or NULL).  Per row and group:
+ *   zeros == NULL:  s = bf16(max|w| / 7), q = clamp(rint(w / s), -8, 7) + 8;
+ *   else, with hi = max(w, 0), lo = min(w, 0) over the group:
+ *                   s = bf16((hi - lo) / 15), z = clamp(rint(-lo / s), 0, 15),
+ *                   q = clamp(rint(w / s) + z, 0, 15).
+ * A group whose s is 0 stands for zeros (q = z).  rint ties to even. */
+LYNX_API int lynx_w4_quantize(const void* W, int64_t N, int64_t K, int group, void* Wq, void* scales,
+                              void* zeros, void* stream);
+
+/* Wq, scales, zeros (or NULL) -> W [N,K] bf16, each value rounded once.  The
+ * way to the other entry points (lynx_linear and so on) for many tokens. */
+LYNX_API int lynx_w4_dequantize(const void* Wq, const void* scales, const void* zeros, int64_t N,
+                                int64_t K, int group, void* W, void* stream);
+
+/* Most rows of X lynx_linear_w4 takes. */
+#define LYNX_LINEAR_W4_MAX_ROWS 32
+
+/* LYNX_LINEAR_W4_MAX_ROWS, for callers without the header. */
+LYNX_API int64_t lynx_linear_w4_max_rows(void);
+
+/* Bytes of the workspace lynx_linear_w4 needs (T = X A^T in fp32); 0 for r = 0. */
+LYNX_API size_t lynx_linear_w4_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t r);
+
+/* Y = act(X W^T + bias + (X A^T) B^T) with W in 4 bits, for 1 <= M <=
+ * LYNX_LINEAR_W4_MAX_ROWS tokens (more: LYNX_ERR_UNSUPPORTED_SHAPE; dequantise
+ * the weight and call lynx_linear).  The dense layer: S(X) = X.
+ *   X [M,K], bias [N] or NULL, A [r,K] and B [N,r] (both or neither), Y [M,N]
+ *   out, act as for lynx_linear_act.  Every sum and T are kept in fp32; Y is
+ *   rounded once.  The result does not depend on the other rows of X.
+ *   workspace: device scratch of workspace_bytes >=
+ *   lynx_linear_w4_workspace_bytes(M,N,K,r); may be NULL without A and B. */
+LYNX_API int lynx_linear_w4(const void* X, const void* Wq, const void* scales, const void* zeros,
+                            const void* bias, const void* A, const void* B, int64_t M, int64_t N,
+                            int64_t K, int64_t r, int group, int act, void* Y, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* ---- activation checkpoints in 8 bits ---------------------------------- */
+
+/* X kept for the backward pass in 8 bits: per row, every 32 consecutive values
+ * share a power of two, so the values a checkpoint stands for are exact bf16
+ * and a product with them needs no further rounding.
+ *   q  [M,K] bytes: int8 (LYNX_CKPT8_INT8) or e4m3 (LYNX_CKPT8_E4M3)
+ *   e  [M,K/32] bytes: the biased exponent of the block
+ *   value = q * 2^(e - 133) for int8 (|q| <= 127), q * 2^(e - 127) for e4m3
+ * int8: e = 127 + max(floor(log2 max|x|), -127), q = clamp(rint(x / 2^(e-133)),
+ * -127, 127): an absolute error of at most 2^-7 of the block's largest
+ * magnitude.  e4m3: e - 127 is the smallest exponent >= -127 with max|x| <= 448
+ * * 2^(e-127), q rounded to e4m3: a relative error of at most 2^-4 down to 2^-13
+ * of the block's largest magnitude (a block that reaches 2^127 saturates at
+ * 240 * 2^120, since 2^128 is no bf16).  All ties to even.  A block with an
+ * infinity or a NaN is stored as e = 255, q = 0 and stands for NaN throughout.
+ * Shapes: M >= 1, K % 64 == 0.  Not on the RT-Lynx pages, which train the LoRA
+ * branch but do not say what is kept for it. */
+#define LYNX_CKPT8_INT8 0
+#define LYNX_CKPT8_E4M3 1
+
+/* Bytes of e: M * K / 32 (q has M * K). */
+LYNX_API size_t lynx_ckpt8_exponent_bytes(int64_t M, int64_t K);
+
+LYNX_API int lynx_ckpt8_store(const void* X, int64_t M, int64_t K, int format, void* q, void* e,
+                              void* stream);
+
+/* The values (bf16) the checkpoint stands for. */
+LYNX_API int lynx_ckpt8_restore(const void* q, const void* e, int64_t M, int64_t K, int format, void* X,
+                                void* stream);
+
+/* ---- the layer's backward pass from a checkpoint ------------------------ */
+
+/* With x the checkpoint's values and dY [M,N] bf16 the gradient of Y (before
+ * the activation, if one was applied), W frozen:
+ *   the adapter's gradients      lynx_lora_backward
+ *   G = dY W                     lynx_linear_dense(dY, W^T laid out once as [K,N])
+ *   the gradient of X            lynx_sparsify_backward (sparse path);
+ *                                dense path: lynx_linear_dense(dY, W^T [K,N],
+ *                                NULL, B^T [r,N], A^T [K,r])
+ * (lynx_linear_dense sums over N there, so N % 64 == 0.) */
+
+/* Bytes of the workspace lynx_lora_backward needs. */
+LYNX_API size_t lynx_lora_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t r);
+
+/* dT = dY B [M,r], dB = dY^T T [N,r], dA = dT^T x [r,K], with T = x A^T computed
+ * from the checkpoint.  All outputs bf16, overwritten; dT may be NULL (not
+ * wanted).  Sums in fp32 in an order that only the shape fixes (equal calls give
+ * equal bits); T and dT are rounded to bf16 before they enter the second
+ * products, as T is in lynx_linear.
+ *   dY [M,N], q and e as stored (format says how), A [r,K], B [N,r].
+ *   workspace: device scratch of workspace_bytes >=
+ *   lynx_lora_backward_workspace_bytes(M,N,K,r). */
+LYNX_API int lynx_lora_backward(const void* dY, const void* q, const void* e, const void* A,
+                                const void* B, int64_t M, int64_t N, int64_t K, int64_t r, int format,
+                                void* dA, void* dB, void* dT, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/* Bytes of the workspace lynx_sparsify_backward needs. */
+LYNX_API size_t lynx_sparsify_backward_workspace_bytes(int64_t M, int64_t K);
+
+/* dX [M,K] bf16 from G = dL/dS(X) [M,K] bf16 at the checkpoint's values x: with
+ * m the 2:4 selection of x (ties to the lower position), L = sum|x|,
+ * Lk = sum m|x|, s = L / Lk and D = sum m G x of the row,
+ *
+ *   dX = s m G + sign(x) (D / Lk) (1 - s m) + dT A      (sign(0) = 0)
+ *
+ * the exact derivative of S(X) = s m x where the selection does not change (the
+ * bf16 rounding of S(X) passed through).  A row with Lk = 0 has s = 1 and no
+ * second term.  dT [M,r] and A [r,K] (both or neither): the LoRA branch's share.
+ *   workspace: device scratch of workspace_bytes >=
+ *   lynx_sparsify_backward_workspace_bytes(M,K). */
+LYNX_API int lynx_sparsify_backward(const void* G, const void* q, const void* e, const void* dT,
+                                    const void* A, int64_t M, int64_t K, int64_t r, int format, void* dX,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---- errors and metadata conversion ----------------------------------- */
 
 /* Synchronises `stream`, then reports (and clears) the status word of that
