@@ -1,96 +1,575 @@
 // lora_backward_kernel.cu -- the adapter's gradients from an 8-bit checkpoint
-// (lynx_lora_backward):  T = x A^T, dT = dY B, dB = dY^T T, dA = dT^T x.
+// (lynx_lora_backward):
+//
+//   T = x A^T,   dT = dY B,   dB = dY^T T,   dA = dT^T x.
+//
+// Every product has one large matrix S (x from its 8-bit form, or dY) and an
+// adapter-sized one, and r is small: the time is the reading of S.  So one kernel
+// streams S once, in 128 x 128 tiles, and takes from each tile in shared memory
+//
+//   the row product  U[rows, r] += S P      (P [cols, r])
+//   the col product  V[cols, r] += S^T Q    (Q [rows, r])
+//
+// T is a row product of x with P = A^T, dT and dB are the row and the column
+// product of one pass over dY (P = B, Q = T), dA^T a column product of x with
+// Q = dT.  The same tile serves as a K-major and as an MN-major operand of
+// tcgen05.mma; the accumulators (one U, one V per 128 columns) stay in TMEM.
+//
+// A CTA has a range of 128-row blocks and a range of 128-column blocks.  P of its
+// columns stays in shared memory, U leaves after each row block and V at the end,
+// as fp32 partial sums per range, which reduce_kernel adds in the order of the
+// ranges and rounds: no atomics, the order is the shape's.
 #include "lynx_ckpt8.cuh"
+#include "lynx_internal.h"
+#include "lynx_ptx.cuh"
 
 namespace lynx {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kTile = 32;
+constexpr int kSrcBf16 = 2;  // beside kCkpt8Int8 and kCkpt8E4M3
 
-// Readers of an operand by (i, p): i an output index, p along the sum.
-struct Bf16At {
-  const __nv_bfloat16* base;
-  int64_t si, sp;
-  __device__ float operator()(int64_t i, int64_t p) const { return __bfloat162float(base[i * si + p * sp]); }
+constexpr uint32_t kBox = 16384;        // 128 rows x 64 bf16, 128B swizzle
+constexpr uint32_t kTileBytes = 2 * kBox;  // an S tile: two boxes of 64 columns
+constexpr int kMaxStages = 6;
+constexpr int kConvWarps = 8;
+constexpr uint32_t kSmemMost = 227 * 1024 - 1024;  // leaves the static part 1 KB
+constexpr int kPlanSms = 148;           // B200; the plan (and the workspace) go by the shape alone
+
+struct PassPlan {
+  int nb;        // column blocks of a CTA
+  int rpr;       // row blocks of a CTA
+  int n_cr, n_rr;  // ranges
+  int stages, q_bufs, u_bufs;
+  uint32_t tmem_cols;
+  uint32_t smem;
 };
 
-template <int FMT>
-struct CkptAt {
-  const uint8_t* q;
-  const uint8_t* e;
-  int64_t K;
-  bool k_is_sum;  // (i, p) = (m, k), else (k, m)
-  __device__ float operator()(int64_t i, int64_t p) const {
-    const int64_t m = k_is_sum ? i : p, k = k_is_sum ? p : i;
-    float v[4];
-    ckpt8_decode4<FMT>(q[m * K + k], v);
-    return v[0] * ckpt8_factor<FMT>(e[(m * K + k) / 32]);
-  }
+struct PassLaunch {
+  CUtensorMap tm_s;  // dY [R,C] bf16, box 64 x 128 (bf16 source)
+  CUtensorMap tm_p;  // B [C,r], box 64 x 128; or A [r,C], box 64 x r (8-bit source)
+  CUtensorMap tm_q;  // Q [R,r], box 64 x 128
+  const uint8_t* q8;
+  const uint8_t* e8;
+  float* u_part;  // [n_cr][R][r]
+  float* v_part;  // [n_rr][C][r]
+  int64_t R, C;
+  int r;
+  PassPlan plan;
+  int stall_test;
+  uint32_t* status;
 };
 
-// out[i * si + j * sj] = bf16(sum_p left(i, p) right(j, p)), 32 x 32 a block
-template <typename L, typename R>
-__global__ void __launch_bounds__(kThreads) product_kernel(L left, R right, int64_t I, int64_t J, int64_t P,
-                                                           __nv_bfloat16* out, int64_t si, int64_t sj) {
-  __shared__ float ls[kTile][kTile + 1], rs[kTile][kTile + 1];
-  const int tx = threadIdx.x % kTile, ty = threadIdx.x / kTile;
-  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kTile, j0 = static_cast<int64_t>(blockIdx.y) * kTile;
-  float acc[4] = {};
-  for (int64_t p0 = 0; p0 < P; p0 += kTile) {
-    for (int y = ty; y < kTile; y += 8) {
-      ls[y][tx] = i0 + y < I && p0 + tx < P ? left(i0 + y, p0 + tx) : 0.f;
-      rs[y][tx] = j0 + y < J && p0 + tx < P ? right(j0 + y, p0 + tx) : 0.f;
+struct PassBars {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t p_full, q_full[2], q_empty[2], u_full[2], u_empty[2], done;
+  uint32_t tmem_base;
+  volatile uint32_t abort_flag;
+};
+
+__device__ __forceinline__ bool pass_wait(PassBars& b, uint64_t* bar, uint32_t parity, uint32_t* status,
+                                          uint32_t code) {
+  if (b.abort_flag) return false;
+  if (mbar_wait(bar, parity)) return true;
+  record_error(status, code);
+  b.abort_flag = 1u;
+  return false;
+}
+
+template <int SRC>
+constexpr int pass_threads() {
+  // TMA producer, MMA issuer, 4 epilogue warps, and the warps that widen 8-bit tiles
+  return 32 * (6 + (SRC == kSrcBf16 ? 0 : kConvWarps));
+}
+
+template <int SRC, bool ROW, bool COL>
+__global__ void __launch_bounds__(pass_threads<SRC>(), 1) adapter_pass_kernel(const __grid_constant__ PassLaunch p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ PassBars bars;
+  uint8_t* const sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                 ~static_cast<uintptr_t>(1023));
+  const uint32_t warp = warp_id_sync();
+  const uint32_t lane = lane_id();
+  const int r = p.r;
+  const uint32_t r_boxes = static_cast<uint32_t>((r + 63) / 64);   // 64-column boxes of an [*, r] operand
+  const uint32_t r_cols = static_cast<uint32_t>((r + 31) / 32) * 32;  // TMEM columns of an accumulator
+  const int nb = p.plan.nb, stages = p.plan.stages;
+  const int cr = static_cast<int>(blockIdx.x % p.plan.n_cr), rr = static_cast<int>(blockIdx.x / p.plan.n_cr);
+  const int cb0 = cr * nb;
+  const int ncb = min(nb, static_cast<int>((p.C + 127) / 128) - cb0);
+  const int rb0 = rr * p.plan.rpr;
+  const int nrb = min(p.plan.rpr, static_cast<int>((p.R + 127) / 128) - rb0);
+
+  // shared memory: P | Q buffers | S stages
+  constexpr bool kPKmajor = SRC != kSrcBf16;
+  const uint32_t p_block = kPKmajor ? 256u * static_cast<uint32_t>(r) : r_boxes * kBox;
+  const uint32_t q_bytes = r_boxes * kBox;
+  uint8_t* const sm_p = sm;
+  uint8_t* const sm_q = sm_p + (ROW ? static_cast<uint32_t>(nb) * p_block : 0u);
+  uint8_t* const sm_s = sm_q + (COL ? static_cast<uint32_t>(p.plan.q_bufs) * q_bytes : 0u);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(&bars.full[s], SRC == kSrcBf16 ? 1 : kConvWarps);
+      mbar_init(&bars.empty[s], 1);
     }
-    __syncthreads();
-    for (int p = 0; p < kTile; ++p)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) acc[c] = fmaf(ls[ty + 8 * c][p], rs[tx][p], acc[c]);
-    __syncthreads();
+    mbar_init(&bars.p_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.q_full[i], 1);
+      mbar_init(&bars.q_empty[i], 1);
+      mbar_init(&bars.u_full[i], 1);
+      mbar_init(&bars.u_empty[i], 4);
+    }
+    mbar_init(&bars.done, 1);
+    bars.abort_flag = 0u;
+    fence_mbar_init();
   }
+  if (warp == 1) {
+    tmem_alloc(&bars.tmem_base, p.plan.tmem_cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_wait();
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0 && !p.stall_test) {
+      bool ok = true;
+      if (ROW) {
+        tma_prefetch_desc(&p.tm_p);
+        mbar_arrive_expect_tx(&bars.p_full, static_cast<uint32_t>(ncb) * p_block);
+        for (int cb = 0; cb < ncb; ++cb) {
+          uint8_t* dst = sm_p + static_cast<uint32_t>(cb) * p_block;
+          const int32_t c0 = (cb0 + cb) * 128;
+          if constexpr (kPKmajor) {
+            for (int j = 0; j < 2; ++j)
+              tma_load_2d(dst + static_cast<uint32_t>(j) * (p_block / 2), &p.tm_p, &bars.p_full, c0 + 64 * j, 0);
+          } else {
+            for (uint32_t b = 0; b < r_boxes; ++b)
+              tma_load_2d(dst + b * kBox, &p.tm_p, &bars.p_full, static_cast<int32_t>(64 * b), c0);
+          }
+        }
+      }
+      uint32_t g = 0;
+      int q_issued = 0;
+      for (int rb = 0; ok && rb < nrb; ++rb) {
+        const int32_t row0 = (rb0 + rb) * 128;
+        if (COL) {
+          const int qb = rb % p.plan.q_bufs;
+          ok = pass_wait(bars, &bars.q_empty[qb], ((rb / p.plan.q_bufs) & 1) ^ 1, p.status, kDevTimeoutEmpty);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&bars.q_full[qb], q_bytes);
+          for (uint32_t b = 0; b < r_boxes; ++b)
+            tma_load_2d(sm_q + static_cast<uint32_t>(qb) * q_bytes + b * kBox, &p.tm_q, &bars.q_full[qb],
+                        static_cast<int32_t>(64 * b), row0);
+          q_issued = rb + 1;
+        }
+        if constexpr (SRC == kSrcBf16) {
+          for (int cb = 0; cb < ncb; ++cb, ++g) {
+            const uint32_t slot = g % stages;
+            ok = pass_wait(bars, &bars.empty[slot], ((g / stages) & 1u) ^ 1u, p.status, kDevTimeoutEmpty);
+            if (!ok) break;
+            uint8_t* dst = sm_s + slot * kTileBytes;
+            mbar_arrive_expect_tx(&bars.full[slot], kTileBytes);
+            tma_load_2d(dst, &p.tm_s, &bars.full[slot], (cb0 + cb) * 128, row0);
+            tma_load_2d(dst + kBox, &p.tm_s, &bars.full[slot], (cb0 + cb) * 128 + 64, row0);
+          }
+        }
+      }
+      // the last fill of every buffer must have landed before the block exits
+      bool drained = true;
+      if (ROW) drained = mbar_wait(&bars.p_full, 0, kWaitLimitNs / 4);
+      for (int x = q_issued - 1; x >= 0 && x >= q_issued - p.plan.q_bufs; --x)
+        drained &= mbar_wait(&bars.q_full[x % p.plan.q_bufs], (x / p.plan.q_bufs) & 1, kWaitLimitNs / 4);
+      for (uint32_t b = g; b > 0 && b + stages > g; --b)
+        drained &= mbar_wait(&bars.full[(b - 1) % stages], ((b - 1) / stages) & 1u, kWaitLimitNs / 4);
+      if (!drained) record_error(p.status, kDevTimeoutDrain);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      const uint32_t idesc_row = make_idesc_bf16(128, r, false) | (kPKmajor ? 0u : kIdescBMnMajor);
+      const uint32_t idesc_col = make_idesc_bf16(128, r, false) | kIdescAMnMajor | kIdescBMnMajor;
+      const uint32_t t_u = bars.tmem_base;
+      const uint32_t t_v = t_u + (ROW ? static_cast<uint32_t>(p.plan.u_bufs) * r_cols : 0u);
+      bool ok = !ROW || pass_wait(bars, &bars.p_full, 0, p.status, kDevTimeoutFull);
+      uint32_t g = 0;
+      for (int rb = 0; ok && rb < nrb; ++rb) {
+        const int qb = COL ? rb % p.plan.q_bufs : 0, ub = ROW ? rb % p.plan.u_bufs : 0;
+        if (COL) ok = pass_wait(bars, &bars.q_full[qb], (rb / p.plan.q_bufs) & 1, p.status, kDevTimeoutFull);
+        if (ok && ROW)
+          ok = pass_wait(bars, &bars.u_empty[ub], ((rb / p.plan.u_bufs) & 1) ^ 1, p.status, kDevTimeoutAccum);
+        if (!ok) break;
+        const uint32_t sq = smem_u32(sm_q) + static_cast<uint32_t>(qb) * q_bytes;
+        for (int cb = 0; cb < ncb; ++cb, ++g) {
+          const uint32_t slot = g % stages;
+          ok = pass_wait(bars, &bars.full[slot], (g / stages) & 1u, p.status, kDevTimeoutFull);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t ss = smem_u32(sm_s) + slot * kTileBytes;
+          if constexpr (ROW) {
+            const uint32_t sp = smem_u32(sm_p) + static_cast<uint32_t>(cb) * p_block;
 #pragma unroll
-  for (int c = 0; c < 4; ++c)
-    if (i0 + ty + 8 * c < I && j0 + tx < J) out[(i0 + ty + 8 * c) * si + (j0 + tx) * sj] = __float2bfloat16_rn(acc[c]);
+            for (int k = 0; k < 8; ++k) {  // 16 columns of S a step
+              const uint64_t da = make_sdesc(ss + (k / 4) * kBox + (k % 4) * 32, 16, 1024, kSw128);
+              const uint64_t db = kPKmajor
+                                      ? make_sdesc(sp + (k / 4) * (p_block / 2) + (k % 4) * 32, 16, 1024, kSw128)
+                                      : make_sdesc(sp + k * 2048, kBox, 1024, kSw128);
+              mma_bf16(t_u + static_cast<uint32_t>(ub) * r_cols, da, db, idesc_row, (cb | k) != 0);
+            }
+          }
+          if constexpr (COL) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {  // 16 rows of S a step
+              const uint64_t da = make_sdesc(ss + k * 2048, kBox, 1024, kSw128);
+              const uint64_t db = make_sdesc(sq + k * 2048, kBox, 1024, kSw128);
+              mma_bf16(t_v + static_cast<uint32_t>(cb) * r_cols, da, db, idesc_col, (rb | k) != 0);
+            }
+          }
+          tc_commit(&bars.empty[slot]);
+        }
+        if (!ok) break;
+        if (COL) tc_commit(&bars.q_empty[qb]);
+        if (ROW) tc_commit(&bars.u_full[ub]);
+      }
+      tc_commit(&bars.done);
+      if (!mbar_wait(&bars.done, 0)) record_error(p.status, kDevTimeoutDrain);
+    }
+    __syncwarp();
+  } else if (warp < 6) {
+    // ------------------------------------------------------------ epilogue: partial sums out
+    const uint32_t quarter = warp & 3u;  // the TMEM lanes this warp may read
+    const uint32_t t_lane = (32u * quarter) << 16;
+    const int64_t row_in = 32 * quarter + lane;
+    bool ok = true;
+    auto store = [&](uint32_t taddr, float* dst, bool in) {
+      for (int c = 0; c < r; c += 16) {
+        uint32_t v[16];
+        tmem_ld_32x32b_x16(taddr + t_lane + static_cast<uint32_t>(c), v);
+        tmem_ld_wait();
+        if (in) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4*>(dst + c + 4 * i) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        }
+      }
+    };
+    if constexpr (ROW) {
+      for (int rb = 0; rb < nrb; ++rb) {
+        const int ub = rb % p.plan.u_bufs;
+        ok = pass_wait(bars, &bars.u_full[ub], (rb / p.plan.u_bufs) & 1, p.status, kDevTimeoutAccum);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const int64_t row = static_cast<int64_t>(rb0 + rb) * 128 + row_in;
+        store(bars.tmem_base + static_cast<uint32_t>(ub) * r_cols, p.u_part + (cr * p.R + row) * r, row < p.R);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.u_empty[ub]);
+      }
+    }
+    if constexpr (COL) {
+      ok = ok && pass_wait(bars, &bars.done, 0, p.status, kDevTimeoutAccum);
+      ok = __all_sync(0xffffffffu, ok && !bars.abort_flag);
+      if (ok) {
+        tc_fence_after();
+        const uint32_t t_v = bars.tmem_base + (ROW ? static_cast<uint32_t>(p.plan.u_bufs) * r_cols : 0u);
+        for (int cb = 0; cb < ncb; ++cb) {
+          const int64_t col = static_cast<int64_t>(cb0 + cb) * 128 + row_in;
+          store(t_v + static_cast<uint32_t>(cb) * r_cols, p.v_part + (rr * p.C + col) * r, col < p.C);
+        }
+        tc_fence_before();
+      }
+    }
+  } else if constexpr (SRC != kSrcBf16) {
+    // ------------------------------------------------------------ 8 bits -> bf16 tiles
+    // 16 bytes (half a block) a step: 8 lanes cover a row of the tile, a thread
+    // takes rows t / 8 + 32 i.  The next tile's bytes are loaded before this
+    // one's stage is waited for.
+    const uint32_t t = threadIdx.x - 192u;
+    const uint32_t chunk = t & 7u;
+    const uint32_t row_t = t >> 3;
+    const int tiles = p.stall_test ? 0 : nrb * ncb;
+    uint4 raw[4];
+    uint32_t ex[4];
+    auto load = [&](int tile) {
+      const int64_t col = static_cast<int64_t>(cb0 + tile % ncb) * 128 + 16 * chunk;
+      const int64_t row0 = static_cast<int64_t>(rb0 + tile / ncb) * 128 + row_t;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t row = row0 + 32 * i;
+        const bool in = row < p.R && col < p.C;
+        raw[i] = in ? __ldcs(reinterpret_cast<const uint4*>(p.q8 + row * p.C + col)) : make_uint4(0, 0, 0, 0);
+        ex[i] = in ? p.e8[(row * p.C + col) / 32] : 0u;
+      }
+    };
+    if (tiles > 0) load(0);
+    for (int tile = 0; tile < tiles; ++tile) {
+      uint32_t out[4][8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float f = ckpt8_factor<SRC>(ex[i]);
+        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float v[4];
+          ckpt8_decode4<SRC>(w[j], v);
+          out[i][2 * j] = pack_bf16(v[0] * f, v[1] * f);
+          out[i][2 * j + 1] = pack_bf16(v[2] * f, v[3] * f);
+        }
+      }
+      if (tile + 1 < tiles) load(tile + 1);
+      const uint32_t slot = static_cast<uint32_t>(tile) % stages;
+      bool ok = pass_wait(bars, &bars.empty[slot], ((tile / stages) & 1) ^ 1, p.status, kDevTimeoutEmpty);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      uint8_t* box = sm_s + slot * kTileBytes + (chunk >> 2) * kBox;
+      const uint32_t u = (chunk & 3u) * 2u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t row = row_t + 32u * i;
+        uint8_t* line = box + row * 128u;
+        const uint32_t x = row & 7u;
+        *reinterpret_cast<uint4*>(line + ((u ^ x) << 4)) = make_uint4(out[i][0], out[i][1], out[i][2], out[i][3]);
+        *reinterpret_cast<uint4*>(line + (((u + 1u) ^ x) << 4)) = make_uint4(out[i][4], out[i][5], out[i][6], out[i][7]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.full[slot]);
+    }
+  }
+
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(bars.tmem_base, p.plan.tmem_cols);
+  }
 }
 
-template <typename L, typename R>
-void product(L left, R right, int64_t I, int64_t J, int64_t P, void* out, int64_t si, int64_t sj, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>((I + kTile - 1) / kTile), static_cast<unsigned>((J + kTile - 1) / kTile));
-  product_kernel<<<grid, kThreads, 0, s>>>(left, right, I, J, P, static_cast<__nv_bfloat16*>(out), si, sj);
+// ---------------------------------------------------------------------------
+// the ranges' partial sums, added in order and rounded
+
+struct ReduceJob {
+  const float* part;   // [n][rows][r]
+  __nv_bfloat16* out;  // [rows][r], or [r][rows] (transposed)
+  int64_t rows;
+  int n, r;
+};
+
+constexpr int kRedThreads = 256;
+
+__device__ __forceinline__ float4 sum_parts(const float* part, int n, int64_t stride) {
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int i = 0; i < n; ++i) {
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(part + i * stride));
+    s.x += v.x;
+    s.y += v.y;
+    s.z += v.z;
+    s.w += v.w;
+  }
+  return s;
+}
+
+// 4 values a thread; the first blocks take job a, the rest job b
+__global__ void __launch_bounds__(kRedThreads) reduce_kernel(ReduceJob a, ReduceJob b, unsigned a_blocks) {
+  pdl_wait();
+  const bool first = blockIdx.x < a_blocks;
+  const ReduceJob& j = first ? a : b;
+  const int64_t i = (static_cast<int64_t>(blockIdx.x - (first ? 0u : a_blocks)) * kRedThreads + threadIdx.x) * 4;
+  const int64_t total = j.rows * j.r;
+  if (i >= total) return;
+  const float4 s = sum_parts(j.part + i, j.n, total);
+  *reinterpret_cast<uint2*>(j.out + i) = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
+}
+
+// [rows][r] -> [r][rows]: 64 rows x 16 columns a block
+__global__ void __launch_bounds__(kRedThreads) reduce_transposed_kernel(ReduceJob j) {
+  pdl_wait();
+  __shared__ float tile[16][64 + 4];
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * 64;
+  const int c0 = static_cast<int>(blockIdx.y) * 16;
+  const int row = threadIdx.x / 4, c = (threadIdx.x % 4) * 4;
+  if (row0 + row < j.rows) {
+    const float4 s = sum_parts(j.part + (row0 + row) * j.r + c0 + c, j.n, j.rows * j.r);
+    tile[c][row] = s.x;
+    tile[c + 1][row] = s.y;
+    tile[c + 2][row] = s.z;
+    tile[c + 3][row] = s.w;
+  }
+  __syncthreads();
+  const int oc = threadIdx.x / 16, orow = (threadIdx.x % 16) * 4;
+  if (row0 + orow < j.rows) {  // rows is a multiple of 64
+    const float4 v = *reinterpret_cast<const float4*>(&tile[oc][orow]);
+    *reinterpret_cast<uint2*>(j.out + (c0 + oc) * j.rows + row0 + orow) =
+        make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+
+// The ranges of one pass.  A CTA's columns are bounded by shared memory (their P
+// stays there) and TMEM (their V); of the column counts that fit, the one with
+// the least of (tiles of the busiest CTA + partial sums written and read back)
+// is taken, both as bytes over the rate they move at.
+PassPlan plan_pass(int64_t R, int64_t C, int r, bool row, bool col, bool eight) {
+  const int64_t rb = (R + 127) / 128, cb = (C + 127) / 128;
+  const uint32_t rp = static_cast<uint32_t>((r + 63) / 64) * 64, rc = static_cast<uint32_t>((r + 31) / 32) * 32;
+  // 1 KB of the dynamic part goes into its alignment
+  const uint32_t p_block = row ? 256u * (eight ? static_cast<uint32_t>(r) : rp) : 0u;
+  const uint32_t q_one = col ? 256u * rp : 0u;
+  const int min_stages = eight ? 2 : 3;
+  PassPlan best = {};
+  double best_cost = 0;
+  for (int nb = 1; nb <= 16 && nb <= cb; ++nb) {
+    const uint32_t v_cols = col ? nb * rc : 0u;
+    int u_bufs = row ? 2 : 0;
+    if (v_cols + u_bufs * rc > 512) u_bufs = row ? 1 : 0;
+    if (v_cols + u_bufs * rc > 512) break;
+    int q_bufs = col ? 2 : 0;
+    if (nb * p_block + q_bufs * q_one + min_stages * kTileBytes + 1024 > kSmemMost) q_bufs = col ? 1 : 0;
+    if (nb * p_block + q_bufs * q_one + min_stages * kTileBytes + 1024 > kSmemMost) break;
+    PassPlan c = {};
+    c.nb = nb;
+    c.n_cr = static_cast<int>((cb + nb - 1) / nb);
+    int64_t n_rr = kPlanSms / c.n_cr;
+    n_rr = n_rr < 1 ? 1 : (n_rr > rb ? rb : n_rr);
+    c.rpr = static_cast<int>((rb + n_rr - 1) / n_rr);
+    c.n_rr = static_cast<int>((rb + c.rpr - 1) / c.rpr);
+    c.q_bufs = q_bufs;
+    c.u_bufs = u_bufs;
+    uint32_t cols = 32;
+    while (cols < v_cols + u_bufs * rc) cols *= 2;
+    c.tmem_cols = cols;
+    const uint32_t fixed = nb * p_block + q_bufs * q_one;
+    const int stages = static_cast<int>((kSmemMost - 1024 - fixed) / kTileBytes);
+    const int most = eight ? 3 : kMaxStages;
+    c.stages = stages > most ? most : stages;
+    c.smem = fixed + c.stages * kTileBytes + 1024;
+    const double waves = static_cast<double>((static_cast<int64_t>(c.n_cr) * c.n_rr + kPlanSms - 1) / kPlanSms);
+    const double cost = waves * c.rpr * nb * (eight ? 16384.0 : 32768.0) * kPlanSms / 6.0e12 +
+                        2.0 * 4 * r * (row ? static_cast<double>(c.n_cr) * R : 0.0) / 6.0e12 +
+                        2.0 * 4 * r * (col ? static_cast<double>(c.n_rr) * C : 0.0) / 6.0e12;
+    if (best.nb == 0 || cost < best_cost) {
+      best = c;
+      best_cost = cost;
+    }
+  }
+  return best;
+}
+
+size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+struct LoraPlan {
+  PassPlan down, dy, up;  // T; dT and dB; dA
+  size_t t, dt, u, v, total;
+};
+
+LoraPlan plan_lora(int64_t M, int64_t N, int64_t K, int r) {
+  LoraPlan l;
+  l.down = plan_pass(M, K, r, true, false, true);
+  l.dy = plan_pass(M, N, r, true, true, false);
+  l.up = plan_pass(M, K, r, false, true, true);
+  const size_t mr = static_cast<size_t>(M) * r, nr = static_cast<size_t>(N) * r, kr = static_cast<size_t>(K) * r;
+  const size_t u = mr * 4 * static_cast<size_t>(l.down.n_cr > l.dy.n_cr ? l.down.n_cr : l.dy.n_cr);
+  const size_t v_dy = nr * 4 * l.dy.n_rr, v_up = kr * 4 * l.up.n_rr;
+  l.t = 0;
+  l.dt = align256(l.t + mr * 2);
+  l.u = align256(l.dt + mr * 2);
+  l.v = align256(l.u + u);
+  l.total = align256(l.v + (v_dy > v_up ? v_dy : v_up));
+  return l;
+}
+
+template <int SRC, bool ROW, bool COL>
+cudaError_t launch_pass(const PassLaunch& p, cudaStream_t s) {
+  static std::once_flag once[64];
+  static cudaError_t configured[64];
+  const cudaError_t e = once_per_device(once, configured, []() {
+    return cudaFuncSetAttribute(adapter_pass_kernel<SRC, ROW, COL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(kSmemMost));
+  });
+  if (e != cudaSuccess) return e;
+  return launch_after_previous(adapter_pass_kernel<SRC, ROW, COL>,
+                               dim3(static_cast<unsigned>(p.plan.n_cr) * static_cast<unsigned>(p.plan.n_rr)),
+                               dim3(pass_threads<SRC>()), p.plan.smem, s, p);
+}
+
+unsigned reduce_blocks(const ReduceJob& j) {
+  return static_cast<unsigned>((j.rows * j.r / 4 + kRedThreads - 1) / kRedThreads);
+}
+
+cudaError_t launch_reduce(const ReduceJob& a, const ReduceJob& b, cudaStream_t s) {
+  const unsigned na = reduce_blocks(a);
+  return launch_after_previous(reduce_kernel, dim3(na + (b.rows > 0 ? reduce_blocks(b) : 0u)), dim3(kRedThreads), 0, s,
+                               a, b, na);
 }
 
 template <int FMT>
-void run(const LoraBackwardLaunch& p, cudaStream_t s) {
-  const auto* q = static_cast<const uint8_t*>(p.q);
-  const auto* e = static_cast<const uint8_t*>(p.e);
-  const auto* dy = static_cast<const __nv_bfloat16*>(p.dy);
-  const auto* a = static_cast<const __nv_bfloat16*>(p.a);
-  const auto* b = static_cast<const __nv_bfloat16*>(p.b);
-  auto* t = reinterpret_cast<__nv_bfloat16*>(p.ws);
-  auto* dt = p.dt != nullptr ? static_cast<__nv_bfloat16*>(p.dt) : t + p.M * p.r;
-  const int64_t r = p.r;
-  product(CkptAt<FMT>{q, e, p.K, true}, Bf16At{a, p.K, 1}, p.M, r, p.K, t, r, 1, s);
-  product(Bf16At{dy, p.N, 1}, Bf16At{b, 1, r}, p.M, r, p.N, dt, r, 1, s);
-  product(Bf16At{dy, 1, p.N}, Bf16At{t, 1, r}, p.N, r, p.M, p.db, r, 1, s);
-  product(CkptAt<FMT>{q, e, p.K, false}, Bf16At{dt, 1, r}, p.K, r, p.M, p.da, 1, p.K, s);
+cudaError_t run(const LoraBackwardLaunch& l, cudaStream_t s) {
+  const LoraPlan plan = plan_lora(l.M, l.N, l.K, l.r);
+  const uint64_t M = l.M, N = l.N, K = l.K, r = l.r;
+  auto* t = reinterpret_cast<__nv_bfloat16*>(l.ws + plan.t);
+  auto* dt = l.dt != nullptr ? static_cast<__nv_bfloat16*>(l.dt) : reinterpret_cast<__nv_bfloat16*>(l.ws + plan.dt);
+  const ReduceJob none = {};
+  PassLaunch p = {};
+  p.q8 = static_cast<const uint8_t*>(l.q);
+  p.e8 = static_cast<const uint8_t*>(l.e);
+  p.u_part = reinterpret_cast<float*>(l.ws + plan.u);
+  p.v_part = reinterpret_cast<float*>(l.ws + plan.v);
+  p.R = l.M;
+  p.r = l.r;
+  p.stall_test = l.stall_test;
+  p.status = l.status;
+  constexpr auto kSw = CU_TENSOR_MAP_SWIZZLE_128B;
+
+  // T = x A^T
+  PassLaunch down = p;
+  down.C = l.K;
+  down.plan = plan.down;
+  if (!encode_bf16_2d(&down.tm_p, l.a, K, r, K * 2, 64, static_cast<uint32_t>(r), kSw)) return cudaErrorInvalidValue;
+  cudaError_t e = launch_pass<FMT, true, false>(down, s);
+  if (e != cudaSuccess) return e;
+  e = launch_reduce(ReduceJob{p.u_part, t, l.M, plan.down.n_cr, l.r}, none, s);
+  if (e != cudaSuccess) return e;
+
+  // dT = dY B and dB = dY^T T
+  PassLaunch dy = p;
+  dy.C = l.N;
+  dy.plan = plan.dy;
+  if (!encode_bf16_2d(&dy.tm_s, l.dy, N, M, N * 2, 64, 128, kSw) ||
+      !encode_bf16_2d(&dy.tm_p, l.b, r, N, r * 2, 64, 128, kSw) ||
+      !encode_bf16_2d(&dy.tm_q, t, r, M, r * 2, 64, 128, kSw))
+    return cudaErrorInvalidValue;
+  e = launch_pass<kSrcBf16, true, true>(dy, s);
+  if (e != cudaSuccess) return e;
+  e = launch_reduce(ReduceJob{p.u_part, dt, l.M, plan.dy.n_cr, l.r},
+                    ReduceJob{p.v_part, static_cast<__nv_bfloat16*>(l.db), l.N, plan.dy.n_rr, l.r}, s);
+  if (e != cudaSuccess) return e;
+
+  // dA^T = x^T dT
+  PassLaunch up = p;
+  up.C = l.K;
+  up.plan = plan.up;
+  if (!encode_bf16_2d(&up.tm_q, dt, r, M, r * 2, 64, 128, kSw)) return cudaErrorInvalidValue;
+  e = launch_pass<FMT, false, true>(up, s);
+  if (e != cudaSuccess) return e;
+  return launch_after_previous(reduce_transposed_kernel,
+                               dim3(static_cast<unsigned>(l.K / 64), static_cast<unsigned>(l.r / 16)),
+                               dim3(kRedThreads), 0, s,
+                               ReduceJob{p.v_part, static_cast<__nv_bfloat16*>(l.da), l.K, plan.up.n_rr, l.r});
 }
 
 }  // namespace
 
 size_t lora_backward_workspace(int64_t M, int64_t N, int64_t K, int64_t r) {
-  (void)N;
-  (void)K;
-  return static_cast<size_t>(M) * static_cast<size_t>(r) * 4;
+  return plan_lora(M, N, K, static_cast<int>(r)).total;
 }
 
-cudaError_t launch_lora_backward(const LoraBackwardLaunch& p, int sms, cudaStream_t s) {
-  (void)sms;
-  if (p.format == kCkpt8Int8)
-    run<kCkpt8Int8>(p, s);
-  else
-    run<kCkpt8E4M3>(p, s);
-  return cudaGetLastError();
+cudaError_t launch_lora_backward(const LoraBackwardLaunch& p, cudaStream_t s) {
+  return p.format == kCkpt8Int8 ? run<kCkpt8Int8>(p, s) : run<kCkpt8E4M3>(p, s);
 }
 
 }  // namespace lynx

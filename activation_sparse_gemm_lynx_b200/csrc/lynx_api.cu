@@ -410,6 +410,13 @@ int device_sm_count() {
   return d ? d->sms : 0;
 }
 
+uint32_t* stream_status_word(cudaStream_t stream) {
+  DeviceState* d = device_state();
+  return d ? stream_status(d, stream) : nullptr;
+}
+
+int stall_test_enabled() { return g_stall.load(); }
+
 }  // namespace lynx
 
 using namespace lynx;

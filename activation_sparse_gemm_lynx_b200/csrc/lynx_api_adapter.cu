@@ -147,8 +147,8 @@ int lynx_lora_backward(const void* dY, const void* q, const void* e, const void*
   if (any_misaligned(dY, q, e, A, B, dA, dB, dT, workspace)) return LYNX_ERR_MISALIGNED;
   if (workspace == nullptr) return LYNX_ERR_INVALID_ARG;
   if (workspace_bytes < lynx_lora_backward_workspace_bytes(M, N, K, r)) return LYNX_ERR_WORKSPACE_TOO_SMALL;
-  const int sms = device_sm_count();
-  if (sms == 0) return LYNX_ERR_CUDA;
+  uint32_t* status = stream_status_word(static_cast<cudaStream_t>(stream));
+  if (status == nullptr) return LYNX_ERR_CUDA;
   LoraBackwardLaunch p;
   std::memset(&p, 0, sizeof(p));
   p.dy = dY;
@@ -165,7 +165,9 @@ int lynx_lora_backward(const void* dY, const void* q, const void* e, const void*
   p.K = K;
   p.r = static_cast<int>(r);
   p.format = format;
-  return status_of(launch_lora_backward(p, sms, static_cast<cudaStream_t>(stream)));
+  p.stall_test = stall_test_enabled();
+  p.status = status;
+  return status_of(launch_lora_backward(p, static_cast<cudaStream_t>(stream)));
 }
 
 size_t lynx_sparsify_backward_workspace_bytes(int64_t M, int64_t K) {

@@ -186,9 +186,11 @@ struct LoraBackwardLaunch {
   uint8_t* ws;
   int64_t M, N, K;
   int r, format;
+  int stall_test;
+  uint32_t* status;  // the stream's status word
 };
 size_t lora_backward_workspace(int64_t M, int64_t N, int64_t K, int64_t r);
-cudaError_t launch_lora_backward(const LoraBackwardLaunch& p, int sms, cudaStream_t s);
+cudaError_t launch_lora_backward(const LoraBackwardLaunch& p, cudaStream_t s);
 
 struct SparsifyBackwardLaunch {
   const void* g;   // [M,K] bf16
@@ -221,5 +223,10 @@ bool encode_bf16_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t
                     CUtensorMapSwizzle swizzle);
 
 int device_sm_count();
+
+// Status word of `stream` on the current device (null if the device state could
+// not be set up), and the test-only stall switch.
+uint32_t* stream_status_word(cudaStream_t stream);
+int stall_test_enabled();
 
 }  // namespace lynx

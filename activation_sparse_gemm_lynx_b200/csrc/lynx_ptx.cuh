@@ -372,7 +372,11 @@ __device__ __forceinline__ void tmem_ld_wait() {
 // ---------------------------------------------------------------------------
 // UMMA descriptors
 
-// Shared-memory matrix descriptor, K-major operand.
+// Shared-memory matrix descriptor.  K-major operand: stride byte offset = the
+// distance of 8-row groups.  MN-major operand with 128B swizzle (rows of 64
+// bf16 along M or N, one row per K index): stride byte offset = the distance of
+// 8-row groups along K, leading byte offset = the distance of 64-element columns
+// along M or N.
 //   bits  0-13 start address >> 4      bits 16-29 leading byte offset >> 4
 //   bits 32-45 stride byte offset >> 4 bits 46-47 version (1 on sm_100)
 //   bits 61-63 layout: 0 none, 2 128B swizzle, 4 64B swizzle, 6 32B swizzle
@@ -388,6 +392,10 @@ __device__ __forceinline__ uint64_t make_sdesc(uint32_t saddr, uint32_t lbo_byte
   d |= static_cast<uint64_t>(layout & 7u) << 61;
   return d;
 }
+
+// Bits of the instruction descriptor that mark an operand as MN-major.
+constexpr uint32_t kIdescAMnMajor = 1u << 15;
+constexpr uint32_t kIdescBMnMajor = 1u << 16;
 
 // Instruction descriptor, kind::f16 with bf16 A/B, fp32 D, both K-major.
 //   bits 0-1 sparsity selector, bit 2 sparse, bits 4-5 D fmt (1 = f32),
