@@ -18,7 +18,9 @@
 // A CTA has a range of 128-row blocks and a range of 128-column blocks.  P of its
 // columns stays in shared memory, U leaves after each row block and V at the end,
 // as fp32 partial sums per range, which reduce_kernel adds in the order of the
-// ranges and rounds: no atomics, the order is the shape's.
+// ranges and rounds: no atomics, the order is the shape's.  Partial sums lie as
+// [block][column of r][128]: a TMEM lane is a row, so a warp stores 128 bytes at a
+// time (with rows of r floats the 4608 x 12288 pass spent 14 of 41 us storing).
 #include "lynx_ckpt8.cuh"
 #include "lynx_internal.h"
 #include "lynx_ptx.cuh"
@@ -32,7 +34,9 @@ constexpr int kSrcBf16 = 2;  // beside kCkpt8Int8 and kCkpt8E4M3
 constexpr uint32_t kBox = 16384;        // 128 rows x 64 bf16, 128B swizzle
 constexpr uint32_t kTileBytes = 2 * kBox;  // an S tile: two boxes of 64 columns
 constexpr int kMaxStages = 6;
-constexpr int kConvWarps = 8;
+constexpr int kConvWarps = 16;
+constexpr int kAhead = 3;                // 8-bit tiles in flight
+constexpr uint32_t kRawBytes = 16384;    // one of them
 constexpr uint32_t kSmemMost = 227 * 1024 - 1024;  // leaves the static part 1 KB
 constexpr int kPlanSms = 148;           // B200; the plan (and the workspace) go by the shape alone
 
@@ -51,8 +55,8 @@ struct PassLaunch {
   CUtensorMap tm_q;  // Q [R,r], box 64 x 128
   const uint8_t* q8;
   const uint8_t* e8;
-  float* u_part;  // [n_cr][R][r]
-  float* v_part;  // [n_rr][C][r]
+  float* u_part;  // [n_cr][row blocks][r][128]
+  float* v_part;  // [n_rr][column blocks][r][128]
   int64_t R, C;
   int r;
   PassPlan plan;
@@ -100,7 +104,7 @@ __global__ void __launch_bounds__(pass_threads<SRC>(), 1) adapter_pass_kernel(co
   const int rb0 = rr * p.plan.rpr;
   const int nrb = min(p.plan.rpr, static_cast<int>((p.R + 127) / 128) - rb0);
 
-  // shared memory: P | Q buffers | S stages
+  // shared memory: P | Q buffers | S stages | 8-bit tiles
   constexpr bool kPKmajor = SRC != kSrcBf16;
   const uint32_t p_block = kPKmajor ? 256u * static_cast<uint32_t>(r) : r_boxes * kBox;
   const uint32_t q_bytes = r_boxes * kBox;
@@ -189,71 +193,79 @@ __global__ void __launch_bounds__(pass_threads<SRC>(), 1) adapter_pass_kernel(co
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      const uint32_t idesc_row = make_idesc_bf16(128, r, false) | (kPKmajor ? 0u : kIdescBMnMajor);
-      const uint32_t idesc_col = make_idesc_bf16(128, r, false) | kIdescAMnMajor | kIdescBMnMajor;
-      const uint32_t t_u = bars.tmem_base;
-      const uint32_t t_v = t_u + (ROW ? static_cast<uint32_t>(p.plan.u_bufs) * r_cols : 0u);
-      bool ok = !ROW || pass_wait(bars, &bars.p_full, 0, p.status, kDevTimeoutFull);
-      uint32_t g = 0;
-      for (int rb = 0; ok && rb < nrb; ++rb) {
-        const int qb = COL ? rb % p.plan.q_bufs : 0, ub = ROW ? rb % p.plan.u_bufs : 0;
-        if (COL) ok = pass_wait(bars, &bars.q_full[qb], (rb / p.plan.q_bufs) & 1, p.status, kDevTimeoutFull);
-        if (ok && ROW)
-          ok = pass_wait(bars, &bars.u_empty[ub], ((rb / p.plan.u_bufs) & 1) ^ 1, p.status, kDevTimeoutAccum);
+    // The whole warp walks the loop and one elected lane issues, so that the
+    // descriptors stay in warp-uniform registers (issued by a lone lane, a tile's
+    // 16 MMAs took 1400 cycles, more than the tile's bytes).
+    const uint32_t idesc_row = make_idesc_bf16(128, r, false) | (kPKmajor ? 0u : kIdescBMnMajor);
+    const uint32_t idesc_col = make_idesc_bf16(128, r, false) | kIdescAMnMajor | kIdescBMnMajor;
+    const uint32_t t_u = bars.tmem_base;
+    const uint32_t t_v = t_u + (ROW ? static_cast<uint32_t>(p.plan.u_bufs) * r_cols : 0u);
+    auto arrived = [&](uint64_t* bar, uint32_t parity, uint32_t code) {
+      return __all_sync(0xffffffffu, pass_wait(bars, bar, parity, p.status, code)) != 0;
+    };
+    bool ok = !ROW || arrived(&bars.p_full, 0, kDevTimeoutFull);
+    uint32_t slot = 0, phase = 0;
+    for (int rb = 0; ok && rb < nrb; ++rb) {
+      const int qb = COL ? rb % p.plan.q_bufs : 0, ub = ROW ? rb % p.plan.u_bufs : 0;
+      if (COL) ok = arrived(&bars.q_full[qb], (rb / p.plan.q_bufs) & 1, kDevTimeoutFull);
+      if (ok && ROW) ok = arrived(&bars.u_empty[ub], ((rb / p.plan.u_bufs) & 1) ^ 1, kDevTimeoutAccum);
+      if (!ok) break;
+      const uint32_t sq = smem_u32(sm_q) + static_cast<uint32_t>(qb) * q_bytes;
+      const uint32_t d_u = t_u + static_cast<uint32_t>(ub) * r_cols;
+      for (int cb = 0; cb < ncb; ++cb) {
+        ok = arrived(&bars.full[slot], phase, kDevTimeoutFull);
         if (!ok) break;
-        const uint32_t sq = smem_u32(sm_q) + static_cast<uint32_t>(qb) * q_bytes;
-        for (int cb = 0; cb < ncb; ++cb, ++g) {
-          const uint32_t slot = g % stages;
-          ok = pass_wait(bars, &bars.full[slot], (g / stages) & 1u, p.status, kDevTimeoutFull);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t ss = smem_u32(sm_s) + slot * kTileBytes;
-          if constexpr (ROW) {
-            const uint32_t sp = smem_u32(sm_p) + static_cast<uint32_t>(cb) * p_block;
+        tc_fence_after();
+        const uint32_t ss = smem_u32(sm_s) + slot * kTileBytes;
+        if constexpr (ROW) {  // 16 columns of S a step
+          const uint32_t sp = smem_u32(sm_p) + static_cast<uint32_t>(cb) * p_block;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {  // 16 columns of S a step
-              const uint64_t da = make_sdesc(ss + (k / 4) * kBox + (k % 4) * 32, 16, 1024, kSw128);
-              const uint64_t db = kPKmajor
-                                      ? make_sdesc(sp + (k / 4) * (p_block / 2) + (k % 4) * 32, 16, 1024, kSw128)
-                                      : make_sdesc(sp + k * 2048, kBox, 1024, kSw128);
-              mma_bf16(t_u + static_cast<uint32_t>(ub) * r_cols, da, db, idesc_row, (cb | k) != 0);
-            }
+          for (int k = 0; k < 8; ++k) {
+            const uint64_t da = make_sdesc(ss + (k / 4) * kBox + (k % 4) * 32, 16, 1024, kSw128);
+            const uint64_t db = kPKmajor ? make_sdesc(sp + (k / 4) * (p_block / 2) + (k % 4) * 32, 16, 1024, kSw128)
+                                         : make_sdesc(sp + k * 2048, kBox, 1024, kSw128);
+            if (elect_one()) mma_bf16(d_u, da, db, idesc_row, (cb | k) != 0);
+            __syncwarp();
           }
-          if constexpr (COL) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {  // 16 rows of S a step
-              const uint64_t da = make_sdesc(ss + k * 2048, kBox, 1024, kSw128);
-              const uint64_t db = make_sdesc(sq + k * 2048, kBox, 1024, kSw128);
-              mma_bf16(t_v + static_cast<uint32_t>(cb) * r_cols, da, db, idesc_col, (rb | k) != 0);
-            }
-          }
-          tc_commit(&bars.empty[slot]);
         }
-        if (!ok) break;
+        if constexpr (COL) {  // 16 rows of S a step
+          const uint32_t d_v = t_v + static_cast<uint32_t>(cb) * r_cols;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint64_t da = make_sdesc(ss + k * 2048, kBox, 1024, kSw128);
+            const uint64_t db = make_sdesc(sq + k * 2048, kBox, 1024, kSw128);
+            if (elect_one()) mma_bf16(d_v, da, db, idesc_col, (rb | k) != 0);
+            __syncwarp();
+          }
+        }
+        if (elect_one()) tc_commit(&bars.empty[slot]);
+        __syncwarp();
+        if (++slot == static_cast<uint32_t>(stages)) slot = 0, phase ^= 1u;
+      }
+      if (!ok) break;
+      if (elect_one()) {
         if (COL) tc_commit(&bars.q_empty[qb]);
         if (ROW) tc_commit(&bars.u_full[ub]);
       }
-      tc_commit(&bars.done);
-      if (!mbar_wait(&bars.done, 0)) record_error(p.status, kDevTimeoutDrain);
+      __syncwarp();
     }
+    if (elect_one()) tc_commit(&bars.done);
+    __syncwarp();
+    if (!mbar_wait(&bars.done, 0) && lane == 0) record_error(p.status, kDevTimeoutDrain);
     __syncwarp();
   } else if (warp < 6) {
     // ------------------------------------------------------------ epilogue: partial sums out
     const uint32_t quarter = warp & 3u;  // the TMEM lanes this warp may read
     const uint32_t t_lane = (32u * quarter) << 16;
-    const int64_t row_in = 32 * quarter + lane;
     bool ok = true;
-    auto store = [&](uint32_t taddr, float* dst, bool in) {
+    auto store = [&](uint32_t taddr, float* part, int64_t block) {
+      float* dst = part + block * r * 128 + 32 * quarter + lane;
       for (int c = 0; c < r; c += 16) {
         uint32_t v[16];
         tmem_ld_32x32b_x16(taddr + t_lane + static_cast<uint32_t>(c), v);
         tmem_ld_wait();
-        if (in) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<uint4*>(dst + c + 4 * i) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-        }
+        for (int i = 0; i < 16; ++i) dst[(c + i) * 128] = __uint_as_float(v[i]);
       }
     };
     if constexpr (ROW) {
@@ -263,8 +275,7 @@ __global__ void __launch_bounds__(pass_threads<SRC>(), 1) adapter_pass_kernel(co
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        const int64_t row = static_cast<int64_t>(rb0 + rb) * 128 + row_in;
-        store(bars.tmem_base + static_cast<uint32_t>(ub) * r_cols, p.u_part + (cr * p.R + row) * r, row < p.R);
+        store(bars.tmem_base + static_cast<uint32_t>(ub) * r_cols, p.u_part, cr * ((p.R + 127) / 128) + rb0 + rb);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.u_empty[ub]);
@@ -276,68 +287,119 @@ __global__ void __launch_bounds__(pass_threads<SRC>(), 1) adapter_pass_kernel(co
       if (ok) {
         tc_fence_after();
         const uint32_t t_v = bars.tmem_base + (ROW ? static_cast<uint32_t>(p.plan.u_bufs) * r_cols : 0u);
-        for (int cb = 0; cb < ncb; ++cb) {
-          const int64_t col = static_cast<int64_t>(cb0 + cb) * 128 + row_in;
-          store(t_v + static_cast<uint32_t>(cb) * r_cols, p.v_part + (rr * p.C + col) * r, col < p.C);
-        }
+        for (int cb = 0; cb < ncb; ++cb)
+          store(t_v + static_cast<uint32_t>(cb) * r_cols, p.v_part, rr * ((p.C + 127) / 128) + cb0 + cb);
         tc_fence_before();
       }
     }
   } else if constexpr (SRC != kSrcBf16) {
     // ------------------------------------------------------------ 8 bits -> bf16 tiles
     // 16 bytes (half a block) a step: 8 lanes cover a row of the tile, a thread
-    // takes rows t / 8 + 32 i.  The next tile's bytes are loaded before this
-    // one's stage is waited for.
+    // takes rows t / 8 + kRowStep i.  The bytes arrive by cp.async in slots that
+    // only this thread reads, kAhead tiles before they are needed; the exponents
+    // (one byte per 32) come through registers, two tiles ahead.
+    constexpr int kSteps = 4 * 8 / kConvWarps;
+    constexpr int kRowStep = 4 * kConvWarps;
     const uint32_t t = threadIdx.x - 192u;
     const uint32_t chunk = t & 7u;
     const uint32_t row_t = t >> 3;
     const int tiles = p.stall_test ? 0 : nrb * ncb;
-    uint4 raw[4];
-    uint32_t ex[4];
-    auto load = [&](int tile) {
-      const int64_t col = static_cast<int64_t>(cb0 + tile % ncb) * 128 + 16 * chunk;
-      const int64_t row0 = static_cast<int64_t>(rb0 + tile / ncb) * 128 + row_t;
+    const int64_t row0 = static_cast<int64_t>(rb0) * 128 + row_t;
+    const int rows0 = static_cast<int>(p.R - row0);                                      // rows left at the first tile
+    const int cols0 = static_cast<int>(p.C - static_cast<int64_t>(cb0) * 128) - 16 * static_cast<int>(chunk);
+    const int64_t e_pitch = p.C / 32;
+    // This thread's place in the tile that is asked for next, bytes and exponents:
+    // tiles are taken along the columns, then down
+    const uint8_t* q_at = p.q8 + row0 * p.C + static_cast<int64_t>(cb0) * 128 + 16 * chunk;
+    const uint8_t* e_at = p.e8 + row0 * e_pitch + static_cast<int64_t>(cb0) * 4 + chunk / 2;
+    const int64_t q_down = 128 * p.C - 128 * (ncb - 1), e_down = 128 * e_pitch - 4 * (ncb - 1);
+    int q_cb = 0, q_rows = rows0, q_left = tiles, e_cb = 0, e_rows = rows0, e_left = tiles;
+    const uint32_t raw = smem_u32(sm_s) + static_cast<uint32_t>(stages) * kTileBytes + 16u * t;
+    uint32_t fetch_at = 0, take_at = 0;  // byte offsets of the slots
+    auto fetch = [&]() {
+      if (q_left > 0) {
+        const bool col_in = 128 * q_cb < cols0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t row = row0 + 32 * i;
-        const bool in = row < p.R && col < p.C;
-        raw[i] = in ? __ldcs(reinterpret_cast<const uint4*>(p.q8 + row * p.C + col)) : make_uint4(0, 0, 0, 0);
-        ex[i] = in ? p.e8[(row * p.C + col) / 32] : 0u;
+        for (int i = 0; i < kSteps; ++i) {
+          const bool in = col_in && kRowStep * i < q_rows;
+          cp_async_16(raw + fetch_at + (kRawBytes / kSteps) * i, in ? q_at + i * kRowStep * p.C : p.q8, in ? 16u : 0u);
+        }
+        --q_left;
+        if (++q_cb < ncb) {
+          q_at += 128;
+        } else {
+          q_cb = 0;
+          q_at += q_down;
+          q_rows -= 128;
+        }
+        fetch_at = fetch_at == kAhead * kRawBytes ? 0u : fetch_at + kRawBytes;
       }
+      cp_async_commit();
     };
-    if (tiles > 0) load(0);
-    for (int tile = 0; tile < tiles; ++tile) {
-      uint32_t out[4][8];
+    auto exponents = [&](uint32_t (&ex)[kSteps]) {
+      if (e_left > 0) {
+        const bool col_in = 128 * e_cb < cols0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float f = ckpt8_factor<SRC>(ex[i]);
-        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float v[4];
-          ckpt8_decode4<SRC>(w[j], v);
-          out[i][2 * j] = pack_bf16(v[0] * f, v[1] * f);
-          out[i][2 * j + 1] = pack_bf16(v[2] * f, v[3] * f);
+        for (int i = 0; i < kSteps; ++i)
+          ex[i] = col_in && kRowStep * i < e_rows ? __ldg(e_at + i * kRowStep * e_pitch) : 0u;
+        --e_left;
+        if (++e_cb < ncb) {
+          e_at += 4;
+        } else {
+          e_cb = 0;
+          e_at += e_down;
+          e_rows -= 128;
         }
       }
-      if (tile + 1 < tiles) load(tile + 1);
-      const uint32_t slot = static_cast<uint32_t>(tile) % stages;
-      bool ok = pass_wait(bars, &bars.empty[slot], ((tile / stages) & 1) ^ 1, p.status, kDevTimeoutEmpty);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      uint8_t* box = sm_s + slot * kTileBytes + (chunk >> 2) * kBox;
-      const uint32_t u = (chunk & 3u) * 2u;
+    };
+    const uint32_t x = row_t & 7u, u = (chunk & 3u) * 2u;  // kRowStep is a multiple of 8
+    const uint32_t line = smem_u32(sm_s) + (chunk >> 2) * kBox + row_t * 128u;
+    const uint32_t line0 = line + ((u ^ x) << 4), line1 = line + (((u + 1u) ^ x) << 4);
+    uint32_t slot = 0, phase = 1;
+    bool ok = true;
+    auto widen = [&](const uint32_t (&ex)[kSteps]) {
+      cp_async_wait<kAhead - 1>();  // this tile's bytes are here
+      uint2 out[kSteps][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t row = row_t + 32u * i;
-        uint8_t* line = box + row * 128u;
-        const uint32_t x = row & 7u;
-        *reinterpret_cast<uint4*>(line + ((u ^ x) << 4)) = make_uint4(out[i][0], out[i][1], out[i][2], out[i][3]);
-        *reinterpret_cast<uint4*>(line + (((u + 1u) ^ x) << 4)) = make_uint4(out[i][4], out[i][5], out[i][6], out[i][7]);
+      for (int i = 0; i < kSteps; ++i) {
+        const uint32_t f = ckpt8_factor_bits<SRC>(ex[i]);
+        const uint4 w = ld_shared_v4(raw + take_at + (kRawBytes / kSteps) * i);
+        out[i][0] = ckpt8_widen4<SRC>(w.x, f);
+        out[i][1] = ckpt8_widen4<SRC>(w.y, f);
+        out[i][2] = ckpt8_widen4<SRC>(w.z, f);
+        out[i][3] = ckpt8_widen4<SRC>(w.w, f);
+      }
+      take_at = take_at == kAhead * kRawBytes ? 0u : take_at + kRawBytes;
+      fetch();
+      ok = __all_sync(0xffffffffu, pass_wait(bars, &bars.empty[slot], phase, p.status, kDevTimeoutEmpty));
+      if (!ok) return;
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        const uint32_t at = slot * kTileBytes + static_cast<uint32_t>(i) * kRowStep * 128u;
+        st_shared_v4(line0 + at, make_uint4(out[i][0].x, out[i][0].y, out[i][1].x, out[i][1].y));
+        st_shared_v4(line1 + at, make_uint4(out[i][2].x, out[i][2].y, out[i][3].x, out[i][3].y));
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.full[slot]);
+      if (++slot == static_cast<uint32_t>(stages)) slot = 0, phase ^= 1u;
+    };
+    for (int i = 0; i < kAhead; ++i) fetch();
+    uint32_t ex0[kSteps] = {}, ex1[kSteps] = {}, now[kSteps];
+    exponents(ex0);
+    exponents(ex1);
+    for (int tile = 0; ok && tile < tiles; tile += 2) {
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) now[i] = ex0[i];
+      exponents(ex0);
+      widen(now);
+      if (!ok || tile + 1 >= tiles) break;
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) now[i] = ex1[i];
+      exponents(ex1);
+      widen(now);
     }
+    cp_async_wait<0>();
   }
 
   __syncthreads();
@@ -351,7 +413,7 @@ __global__ void __launch_bounds__(pass_threads<SRC>(), 1) adapter_pass_kernel(co
 // the ranges' partial sums, added in order and rounded
 
 struct ReduceJob {
-  const float* part;   // [n][rows][r]
+  const float* part;   // [n][blocks][r][128]
   __nv_bfloat16* out;  // [rows][r], or [r][rows] (transposed)
   int64_t rows;
   int n, r;
@@ -359,51 +421,47 @@ struct ReduceJob {
 
 constexpr int kRedThreads = 256;
 
-__device__ __forceinline__ float4 sum_parts(const float* part, int n, int64_t stride) {
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int i = 0; i < n; ++i) {
-    const float4 v = __ldcg(reinterpret_cast<const float4*>(part + i * stride));
-    s.x += v.x;
-    s.y += v.y;
-    s.z += v.z;
-    s.w += v.w;
-  }
-  return s;
-}
-
-// 4 values a thread; the first blocks take job a, the rest job b
+// A block of threads takes one 128-row block x 16 columns; a warp a column at a
+// time, 4 rows a lane.  The first a_blocks take job a, the rest job b.
+template <bool TRANSPOSED>
 __global__ void __launch_bounds__(kRedThreads) reduce_kernel(ReduceJob a, ReduceJob b, unsigned a_blocks) {
+  __shared__ float tile[16][128 + 4];
   pdl_wait();
   const bool first = blockIdx.x < a_blocks;
   const ReduceJob& j = first ? a : b;
-  const int64_t i = (static_cast<int64_t>(blockIdx.x - (first ? 0u : a_blocks)) * kRedThreads + threadIdx.x) * 4;
-  const int64_t total = j.rows * j.r;
-  if (i >= total) return;
-  const float4 s = sum_parts(j.part + i, j.n, total);
-  *reinterpret_cast<uint2*>(j.out + i) = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
-}
-
-// [rows][r] -> [r][rows]: 64 rows x 16 columns a block
-__global__ void __launch_bounds__(kRedThreads) reduce_transposed_kernel(ReduceJob j) {
-  pdl_wait();
-  __shared__ float tile[16][64 + 4];
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * 64;
-  const int c0 = static_cast<int>(blockIdx.y) * 16;
-  const int row = threadIdx.x / 4, c = (threadIdx.x % 4) * 4;
-  if (row0 + row < j.rows) {
-    const float4 s = sum_parts(j.part + (row0 + row) * j.r + c0 + c, j.n, j.rows * j.r);
-    tile[c][row] = s.x;
-    tile[c + 1][row] = s.y;
-    tile[c + 2][row] = s.z;
-    tile[c + 3][row] = s.w;
+  const unsigned id = blockIdx.x - (first ? 0u : a_blocks);
+  const unsigned groups = static_cast<unsigned>(j.r) / 16;
+  const int64_t block = id / groups;
+  const int c0 = static_cast<int>(id % groups) * 16;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t stride = (j.rows + 127) / 128 * j.r * 128;
+  const float* src = j.part + (block * j.r + c0 + warp) * 128 + 4 * lane;
+  float4 s0 = make_float4(0.f, 0.f, 0.f, 0.f), s1 = s0;
+#pragma unroll 4
+  for (int i = 0; i < j.n; ++i) {
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(src + i * stride));
+    const float4 w = __ldcg(reinterpret_cast<const float4*>(src + i * stride + 8 * 128));
+    s0.x += v.x, s0.y += v.y, s0.z += v.z, s0.w += v.w;
+    s1.x += w.x, s1.y += w.y, s1.z += w.z, s1.w += w.w;
   }
-  __syncthreads();
-  const int oc = threadIdx.x / 16, orow = (threadIdx.x % 16) * 4;
-  if (row0 + orow < j.rows) {  // rows is a multiple of 64
-    const float4 v = *reinterpret_cast<const float4*>(&tile[oc][orow]);
-    *reinterpret_cast<uint2*>(j.out + (c0 + oc) * j.rows + row0 + orow) =
-        make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+  if constexpr (TRANSPOSED) {
+    const int64_t row = block * 128 + 4 * lane;  // rows is a multiple of 64
+    if (row < j.rows) {
+      __nv_bfloat16* dst = j.out + (c0 + warp) * j.rows + row;
+      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(s0.x, s0.y), pack_bf16(s0.z, s0.w));
+      *reinterpret_cast<uint2*>(dst + 8 * j.rows) = make_uint2(pack_bf16(s1.x, s1.y), pack_bf16(s1.z, s1.w));
+    }
+  } else {
+    *reinterpret_cast<float4*>(&tile[warp][4 * lane]) = s0;
+    *reinterpret_cast<float4*>(&tile[warp + 8][4 * lane]) = s1;
+    __syncthreads();
+    const int row = threadIdx.x >> 1, c = (threadIdx.x & 1) * 8;
+    if (block * 128 + row < j.rows) {
+      uint32_t o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = pack_bf16(tile[c + 2 * i][row], tile[c + 2 * i + 1][row]);
+      *reinterpret_cast<uint4*>(j.out + (block * 128 + row) * j.r + c0 + c) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
   }
 }
 
@@ -418,6 +476,7 @@ PassPlan plan_pass(int64_t R, int64_t C, int r, bool row, bool col, bool eight) 
   const int64_t rb = (R + 127) / 128, cb = (C + 127) / 128;
   const uint32_t rp = static_cast<uint32_t>((r + 63) / 64) * 64, rc = static_cast<uint32_t>((r + 31) / 32) * 32;
   // 1 KB of the dynamic part goes into its alignment
+  const uint32_t raw = eight ? (kAhead + 1) * kRawBytes : 0u;
   const uint32_t p_block = row ? 256u * (eight ? static_cast<uint32_t>(r) : rp) : 0u;
   const uint32_t q_one = col ? 256u * rp : 0u;
   const int min_stages = eight ? 2 : 3;
@@ -429,8 +488,8 @@ PassPlan plan_pass(int64_t R, int64_t C, int r, bool row, bool col, bool eight) 
     if (v_cols + u_bufs * rc > 512) u_bufs = row ? 1 : 0;
     if (v_cols + u_bufs * rc > 512) break;
     int q_bufs = col ? 2 : 0;
-    if (nb * p_block + q_bufs * q_one + min_stages * kTileBytes + 1024 > kSmemMost) q_bufs = col ? 1 : 0;
-    if (nb * p_block + q_bufs * q_one + min_stages * kTileBytes + 1024 > kSmemMost) break;
+    if (nb * p_block + q_bufs * q_one + min_stages * kTileBytes + raw + 1024 > kSmemMost) q_bufs = col ? 1 : 0;
+    if (nb * p_block + q_bufs * q_one + min_stages * kTileBytes + raw + 1024 > kSmemMost) break;
     PassPlan c = {};
     c.nb = nb;
     c.n_cr = static_cast<int>((cb + nb - 1) / nb);
@@ -443,7 +502,7 @@ PassPlan plan_pass(int64_t R, int64_t C, int r, bool row, bool col, bool eight) 
     uint32_t cols = 32;
     while (cols < v_cols + u_bufs * rc) cols *= 2;
     c.tmem_cols = cols;
-    const uint32_t fixed = nb * p_block + q_bufs * q_one;
+    const uint32_t fixed = nb * p_block + q_bufs * q_one + raw;
     const int stages = static_cast<int>((kSmemMost - 1024 - fixed) / kTileBytes);
     const int most = eight ? 3 : kMaxStages;
     c.stages = stages > most ? most : stages;
@@ -472,9 +531,10 @@ LoraPlan plan_lora(int64_t M, int64_t N, int64_t K, int r) {
   l.down = plan_pass(M, K, r, true, false, true);
   l.dy = plan_pass(M, N, r, true, true, false);
   l.up = plan_pass(M, K, r, false, true, true);
-  const size_t mr = static_cast<size_t>(M) * r, nr = static_cast<size_t>(N) * r, kr = static_cast<size_t>(K) * r;
-  const size_t u = mr * 4 * static_cast<size_t>(l.down.n_cr > l.dy.n_cr ? l.down.n_cr : l.dy.n_cr);
-  const size_t v_dy = nr * 4 * l.dy.n_rr, v_up = kr * 4 * l.up.n_rr;
+  const size_t mr = static_cast<size_t>(M) * r;
+  auto part = [r](int64_t rows, int n) { return static_cast<size_t>((rows + 127) / 128) * 512 * r * n; };
+  const size_t u = part(M, l.down.n_cr > l.dy.n_cr ? l.down.n_cr : l.dy.n_cr);
+  const size_t v_dy = part(N, l.dy.n_rr), v_up = part(K, l.up.n_rr);
   l.t = 0;
   l.dt = align256(l.t + mr * 2);
   l.u = align256(l.dt + mr * 2);
@@ -498,13 +558,14 @@ cudaError_t launch_pass(const PassLaunch& p, cudaStream_t s) {
 }
 
 unsigned reduce_blocks(const ReduceJob& j) {
-  return static_cast<unsigned>((j.rows * j.r / 4 + kRedThreads - 1) / kRedThreads);
+  return static_cast<unsigned>((j.rows + 127) / 128) * static_cast<unsigned>(j.r / 16);
 }
 
+template <bool TRANSPOSED>
 cudaError_t launch_reduce(const ReduceJob& a, const ReduceJob& b, cudaStream_t s) {
   const unsigned na = reduce_blocks(a);
-  return launch_after_previous(reduce_kernel, dim3(na + (b.rows > 0 ? reduce_blocks(b) : 0u)), dim3(kRedThreads), 0, s,
-                               a, b, na);
+  return launch_after_previous(reduce_kernel<TRANSPOSED>, dim3(na + (b.rows > 0 ? reduce_blocks(b) : 0u)),
+                               dim3(kRedThreads), 0, s, a, b, na);
 }
 
 template <int FMT>
@@ -532,7 +593,7 @@ cudaError_t run(const LoraBackwardLaunch& l, cudaStream_t s) {
   if (!encode_bf16_2d(&down.tm_p, l.a, K, r, K * 2, 64, static_cast<uint32_t>(r), kSw)) return cudaErrorInvalidValue;
   cudaError_t e = launch_pass<FMT, true, false>(down, s);
   if (e != cudaSuccess) return e;
-  e = launch_reduce(ReduceJob{p.u_part, t, l.M, plan.down.n_cr, l.r}, none, s);
+  e = launch_reduce<false>(ReduceJob{p.u_part, t, l.M, plan.down.n_cr, l.r}, none, s);
   if (e != cudaSuccess) return e;
 
   // dT = dY B and dB = dY^T T
@@ -545,7 +606,7 @@ cudaError_t run(const LoraBackwardLaunch& l, cudaStream_t s) {
     return cudaErrorInvalidValue;
   e = launch_pass<kSrcBf16, true, true>(dy, s);
   if (e != cudaSuccess) return e;
-  e = launch_reduce(ReduceJob{p.u_part, dt, l.M, plan.dy.n_cr, l.r},
+  e = launch_reduce<false>(ReduceJob{p.u_part, dt, l.M, plan.dy.n_cr, l.r},
                     ReduceJob{p.v_part, static_cast<__nv_bfloat16*>(l.db), l.N, plan.dy.n_rr, l.r}, s);
   if (e != cudaSuccess) return e;
 
@@ -556,10 +617,7 @@ cudaError_t run(const LoraBackwardLaunch& l, cudaStream_t s) {
   if (!encode_bf16_2d(&up.tm_q, dt, r, M, r * 2, 64, 128, kSw)) return cudaErrorInvalidValue;
   e = launch_pass<FMT, false, true>(up, s);
   if (e != cudaSuccess) return e;
-  return launch_after_previous(reduce_transposed_kernel,
-                               dim3(static_cast<unsigned>(l.K / 64), static_cast<unsigned>(l.r / 16)),
-                               dim3(kRedThreads), 0, s,
-                               ReduceJob{p.v_part, static_cast<__nv_bfloat16*>(l.da), l.K, plan.up.n_rr, l.r});
+  return launch_reduce<true>(ReduceJob{p.v_part, static_cast<__nv_bfloat16*>(l.da), l.K, plan.up.n_rr, l.r}, none, s);
 }
 
 }  // namespace

@@ -52,6 +52,46 @@ __device__ __forceinline__ void ckpt8_decode4(uint32_t w, float (&v)[4]) {
   }
 }
 
+// The same multiplier for ckpt8_widen4: int8 takes it as a bf16 pair.
+template <int FMT>
+__device__ __forceinline__ uint32_t ckpt8_factor_bits(uint32_t e) {
+  if constexpr (FMT == kCkpt8Int8) {
+    // 2^(e - 133): exponent field e - 6, or a subnormal
+    uint32_t f = e >= 7u ? (e - 6u) << 7 : 1u << e;
+    if (e == 255u) f = 0x7FC0u;
+    return f | (f << 16);
+  } else {
+    return __float_as_uint(ckpt8_factor<FMT>(e));
+  }
+}
+
+// 4 stored bytes -> 4 bf16 values times the block's factor (two packed pairs), exact.
+// int8 in packed bf16 arithmetic, 5 instructions a pair: with the low 7 bits in
+// the mantissa of 128 it reads 128 + low, and the sign bit turns the 128 that is
+// taken off into 256.
+template <int FMT>
+__device__ __forceinline__ uint2 ckpt8_widen4(uint32_t w, uint32_t factor) {
+  if constexpr (FMT == kCkpt8Int8) {
+    uint32_t out[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t b = __byte_perm(w, 0u, i == 0 ? 0x4140 : 0x4342);
+      const uint32_t v = (b & 0x007F007Fu) | 0x43004300u, off = (b & 0x00800080u) | 0xC300C300u;
+      __nv_bfloat162 x = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&v),
+                                 *reinterpret_cast<const __nv_bfloat162*>(&off));
+      x = __hmul2(x, *reinterpret_cast<const __nv_bfloat162*>(&factor));
+      out[i] = *reinterpret_cast<uint32_t*>(&x);
+    }
+    return make_uint2(out[0], out[1]);
+  } else {
+    const float f = __uint_as_float(factor);
+    float v[4];
+    ckpt8_decode4<FMT>(w, v);
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0] * f, v[1] * f), b = __floats2bfloat162_rn(v[2] * f, v[3] * f);
+    return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  }
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&h);
