@@ -173,6 +173,9 @@ struct LinearW4Launch {
   int M, r, group, act;
 };
 cudaError_t launch_linear_w4(const LinearW4Launch& p, int sms, cudaStream_t s);
+cudaError_t launch_linear_w4_g32(const LinearW4Launch& p, int sms, cudaStream_t s);
+cudaError_t launch_linear_w4_g64(const LinearW4Launch& p, int sms, cudaStream_t s);
+cudaError_t launch_linear_w4_g128(const LinearW4Launch& p, int sms, cudaStream_t s);
 
 struct LoraBackwardLaunch {
   const void* dy;  // [M,N] bf16

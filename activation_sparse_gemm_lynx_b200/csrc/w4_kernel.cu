@@ -1,8 +1,7 @@
-// w4_kernel.cu -- the frozen weight in 4 bits (lynx_w4_quantize,
-// lynx_w4_dequantize) and the layer for a few tokens on it (lynx_linear_w4).
+// w4_kernel.cu -- the frozen weight to 4 bits and back (lynx_w4_quantize,
+// lynx_w4_dequantize).
 #include <cuda_bf16.h>
 
-#include "lynx_act.cuh"
 #include "lynx_ckpt8.cuh"
 #include "lynx_internal.h"
 
@@ -150,80 +149,6 @@ __global__ void __launch_bounds__(kThreads) w4_dequantize_kernel(const uint32_t*
   }
 }
 
-// ---------------------------------------------------------------------------
-// the layer for a few tokens
-
-// T = X A^T: one warp per (adapter row, token)
-__global__ void __launch_bounds__(kThreads) w4_lora_down_kernel(const __nv_bfloat16* __restrict__ x,
-                                                                const __nv_bfloat16* __restrict__ a, int64_t K, int r,
-                                                                int M, float* __restrict__ t) {
-  const int lane = threadIdx.x & 31;
-  const int id = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  if (id >= r * M) return;
-  const int m = id / r, j = id % r;
-  const uint32_t* xr = reinterpret_cast<const uint32_t*>(x + m * K);
-  const uint32_t* ar = reinterpret_cast<const uint32_t*>(a + j * K);
-  float acc = 0.f;
-  for (int64_t k = lane; k < K / 2; k += 32) {
-    acc = fmaf(bf16_lo(xr[k]), bf16_lo(ar[k]), acc);
-    acc = fmaf(bf16_hi(xr[k]), bf16_hi(ar[k]), acc);
-  }
-  for (int d = 16; d > 0; d >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, d);
-  if (lane == 0) t[id] = acc;
-}
-
-// One warp per output column, 8 tokens at a time.
-__global__ void __launch_bounds__(kThreads) linear_w4_kernel(LinearW4Launch p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t n = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-  if (n >= p.N) return;
-  const auto* x = static_cast<const __nv_bfloat16*>(p.x);
-  const auto* wq = static_cast<const uint32_t*>(p.wq);
-  const auto* scales = static_cast<const __nv_bfloat16*>(p.scales);
-  const auto* zeros = static_cast<const uint8_t*>(p.zeros);
-  const auto* b = static_cast<const __nv_bfloat16*>(p.b);
-  const auto* bias = static_cast<const __nv_bfloat16*>(p.bias);
-  auto* y = static_cast<__nv_bfloat16*>(p.y);
-  for (int m0 = 0; m0 < p.M; m0 += 8) {
-    float acc[8] = {};
-    for (int64_t k = 8 * lane; k < p.K; k += 256) {
-      const int64_t side = (k / p.group) * p.N + n;
-      const float s = __bfloat162float(scales[side]);
-      const float z = zeros != nullptr ? static_cast<float>(zeros[side] & 15) : 8.f;
-      const uint32_t word = wq[(n * p.K + k) >> 3];
-      float v[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = (static_cast<float>((word >> nibble_shift(j)) & 15u) - z) * s;
-      for (int i = 0; i < 8 && m0 + i < p.M; ++i) {
-        const uint4 xv = *reinterpret_cast<const uint4*>(x + (m0 + i) * p.K + k);
-        const uint32_t xs[4] = {xv.x, xv.y, xv.z, xv.w};
-        float sum = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sum += v[2 * j] * bf16_lo(xs[j]) + v[2 * j + 1] * bf16_hi(xs[j]);
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          if (c == i) acc[c] += sum;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float v = acc[i];
-      for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-      if (m0 + i >= p.M) continue;
-      if (p.a != nullptr) {
-        float u = 0.f;
-        for (int j = lane; j < p.r; j += 32)
-          u = fmaf(p.t[(m0 + i) * p.r + j], __bfloat162float(b[n * p.r + j]), u);
-        for (int d = 16; d > 0; d >>= 1) u += __shfl_xor_sync(0xffffffffu, u, d);
-        v += u;
-      }
-      if (bias != nullptr) v += __bfloat162float(bias[n]);
-      if (p.act == kActGeluTanh) v = gelu_tanh(v);
-      if (lane == 0) y[(m0 + i) * p.N + n] = __float2bfloat16_rn(v);
-    }
-  }
-}
-
 unsigned weight_tiles(int64_t N, int64_t K) {
   return static_cast<unsigned>(((K + kTileK - 1) / kTileK) * ((N + kTileN - 1) / kTileN));
 }
@@ -261,16 +186,8 @@ cudaError_t launch_w4_dequantize(const void* wq, const void* scales, const void*
 }
 
 cudaError_t launch_linear_w4(const LinearW4Launch& p, int sms, cudaStream_t s) {
-  (void)sms;
-  constexpr int kWarps = kThreads / 32;
-  if (p.a != nullptr) {
-    w4_lora_down_kernel<<<(p.r * p.M + kWarps - 1) / kWarps, kThreads, 0, s>>>(
-        static_cast<const __nv_bfloat16*>(p.x), static_cast<const __nv_bfloat16*>(p.a), p.K, p.r, p.M, p.t);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-  }
-  linear_w4_kernel<<<static_cast<unsigned>((p.N + kWarps - 1) / kWarps), kThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  return p.group == 32 ? launch_linear_w4_g32(p, sms, s)
+                       : p.group == 64 ? launch_linear_w4_g64(p, sms, s) : launch_linear_w4_g128(p, sms, s);
 }
 
 }  // namespace lynx

@@ -9,6 +9,7 @@ The functions carry the C names; tensors are torch tensors on the current CUDA
 device, bf16 unless stated, row-major and contiguous.
 """
 import ctypes
+import functools
 import os
 import re
 
@@ -429,56 +430,76 @@ def lynx_sparse_gemm(vals, meta, W, bias=None, T=None, B=None, Y=None, stream=No
 
 
 # ---- the weight in 4 bits, the 8-bit checkpoint, the backward pass ----------
+#
+# These calls can be shorter on the device than a tensor check is on the host, so
+# the checks are one expression a tensor; only a tensor that fails is looked at
+# more closely, for the message.
 
 
-def _on_one_device(**tensors):
-    """Every tensor given on the current CUDA device (the device of the stream)."""
+def _place(t, name, stream):
+    """(index of the current device, raw handle of the stream a call runs on);
+    `t` is the call's first tensor."""
     import torch
 
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
     here = torch.cuda.current_device()
-    for name, t in tensors.items():
-        if t is not None and t.device.index != here:
-            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{here}")
-
-
-def _empty(shape, dtype, stream):
-    """A buffer of the current device from the memory pool of the stream it is used on."""
-    import torch
-
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device="cuda")
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device="cuda")
+        return here, torch._C._cuda_getCurrentRawStream(here)
+    if stream.device.index != here:
+        raise ValueError(f"stream is on {stream.device}, the current device is cuda:{here}")
+    return here, stream.cuda_stream
 
 
-def _need_workspace(workspace, need, stream):
-    """(pointer, bytes) of a caller's workspace, or of one made here."""
+def _take(t, name, here, dtype, shape):
+    """The address of a contiguous tensor of this type and shape on the current device."""
+    if t.get_device() == here and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    _need(t, name, dtype, shape)
+    raise ValueError(f"{name} is on {t.device}, the current device is cuda:{here}")
+
+
+def _matrix(t, name):
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix")
+    return t.shape
+
+
+def _out(t, name, here, like, dtype, shape, stream):
+    """(tensor, address): the caller's, or one (on the device of `like`) from the
+    memory pool of the stream it is written on."""
+    if t is not None:
+        return t, _take(t, name, here, dtype, shape)
+    if stream is None:
+        t = like.new_empty(shape, dtype=dtype)
+    else:
+        import torch
+
+        with torch.cuda.stream(stream):
+            t = like.new_empty(shape, dtype=dtype)
+    return t, t.data_ptr()
+
+
+def _scratch(workspace, here, like, need, stream):
+    """(tensor, address, bytes) of the caller's workspace, or of one made here."""
     import torch
 
     if workspace is None:
         if need == 0:
-            return None, 0, None
-        workspace = _empty((need,), torch.uint8, stream)
-    else:
-        _need(workspace, "workspace", torch.uint8)
-        _on_one_device(workspace=workspace)
-    return _ptr(workspace), workspace.numel(), workspace
+            return None, None, 0
+        return *_out(None, "workspace", here, like, torch.uint8, (need,), stream), need
+    n = workspace.numel()
+    return workspace, _take(workspace, "workspace", here, torch.uint8, (n,)), n
 
 
-def _w4_args(Wq, scales, zeros):
-    import torch
-
-    _need(Wq, "Wq", torch.uint8)
-    _need(scales, "scales", torch.bfloat16)
-    if Wq.dim() != 2 or scales.dim() != 2:
-        raise ValueError("Wq must be [N,K/2] and scales [K/group,N]")
-    N, K = Wq.shape[0], 2 * Wq.shape[1]
-    groups = scales.shape[0]
-    if scales.shape[1] != N or groups == 0 or K % groups:
+def _w4_shape(Wq, scales):
+    N, K2 = _matrix(Wq, "Wq")
+    groups, n = _matrix(scales, "scales")
+    if n != N or groups == 0 or 2 * K2 % groups:
         raise ValueError("scales must be [K/group,N]")
-    if zeros is not None:
-        _need(zeros, "zeros", torch.uint8, (groups, N))
-    return N, K, K // groups
+    return N, 2 * K2, groups
 
 
 def lynx_w4_bytes(N, K):
@@ -491,26 +512,17 @@ def lynx_w4_quantize(W, group=128, zero_points=False, Wq=None, scales=None, zero
     zero points."""
     import torch
 
-    _need(W, "W", torch.bfloat16)
-    if W.dim() != 2:
-        raise ValueError("W must be [N,K]")
-    N, K = W.shape
+    N, K = _matrix(W, "W")
     if group not in (32, 64, 128) or K % group:
         raise LynxError(LYNX_ERR_UNSUPPORTED_SHAPE, f"lynx_w4_quantize (group {group}, K {K})")
-    _on_one_device(W=W, Wq=Wq, scales=scales, zeros=zeros)
-    if Wq is None:
-        Wq = _empty((N, K // 2), torch.uint8, stream)
-    if scales is None:
-        scales = _empty((K // group, N), torch.bfloat16, stream)
-    if zeros is None and zero_points:
-        zeros = _empty((K // group, N), torch.uint8, stream)
-    _need(Wq, "Wq", torch.uint8, (N, K // 2))
-    _need(scales, "scales", torch.bfloat16, (K // group, N))
-    if zeros is not None:
-        _need(zeros, "zeros", torch.uint8, (K // group, N))
-    st = library().lynx_w4_quantize(_ptr(W), N, K, int(group), _ptr(Wq), _ptr(scales), _ptr(zeros),
-                                    _stream(stream))
-    _check(st, "lynx_w4_quantize")
+    here, s = _place(W, "W", stream)
+    w = _take(W, "W", here, torch.bfloat16, (N, K))
+    Wq, q = _out(Wq, "Wq", here, W, torch.uint8, (N, K // 2), stream)
+    scales, sc = _out(scales, "scales", here, W, torch.bfloat16, (K // group, N), stream)
+    z = None
+    if zeros is not None or zero_points:
+        zeros, z = _out(zeros, "zeros", here, W, torch.uint8, (K // group, N), stream)
+    _check(library().lynx_w4_quantize(w, N, K, group, q, sc, z, s), "lynx_w4_quantize")
     return Wq, scales, zeros
 
 
@@ -518,14 +530,13 @@ def lynx_w4_dequantize(Wq, scales, zeros=None, W=None, stream=None):
     """W [N,K] bf16 from its 4-bit form (the group is K / scales.shape[0])."""
     import torch
 
-    N, K, group = _w4_args(Wq, scales, zeros)
-    _on_one_device(Wq=Wq, scales=scales, zeros=zeros, W=W)
-    if W is None:
-        W = _empty((N, K), torch.bfloat16, stream)
-    _need(W, "W", torch.bfloat16, (N, K))
-    st = library().lynx_w4_dequantize(_ptr(Wq), _ptr(scales), _ptr(zeros), N, K, group, _ptr(W),
-                                      _stream(stream))
-    _check(st, "lynx_w4_dequantize")
+    N, K, groups = _w4_shape(Wq, scales)
+    here, s = _place(Wq, "Wq", stream)
+    q = _take(Wq, "Wq", here, torch.uint8, (N, K // 2))
+    sc = _take(scales, "scales", here, torch.bfloat16, (groups, N))
+    z = None if zeros is None else _take(zeros, "zeros", here, torch.uint8, (groups, N))
+    W, w = _out(W, "W", here, Wq, torch.bfloat16, (N, K), stream)
+    _check(library().lynx_w4_dequantize(q, sc, z, N, K, K // groups, w, s), "lynx_w4_dequantize")
     return W
 
 
@@ -533,6 +544,7 @@ def lynx_linear_w4_max_rows():
     return library().lynx_linear_w4_max_rows()
 
 
+@functools.lru_cache(maxsize=1024)
 def lynx_linear_w4_workspace_bytes(M, N, K, r=0):
     return library().lynx_linear_w4_workspace_bytes(M, N, K, r)
 
@@ -543,53 +555,42 @@ def lynx_linear_w4(X, Wq, scales, zeros=None, bias=None, A=None, B=None, act=LYN
     (lynx_w4_quantize's outputs).  Returns Y."""
     import torch
 
-    N, K, group = _w4_args(Wq, scales, zeros)
-    _need(X, "X", torch.bfloat16)
-    if X.dim() != 2 or X.shape[1] != K:
+    bf16 = torch.bfloat16
+    N, K, groups = _w4_shape(Wq, scales)
+    M, k = _matrix(X, "X")
+    if k != K:
         raise ValueError("X must be [M,K] with K = 2 * Wq.shape[1]")
-    M = X.shape[0]
-    if bias is not None:
-        _need(bias, "bias", torch.bfloat16, (N,))
-    if (A is None) != (B is None):
-        raise ValueError("A and B must both be given or both be None")
-    r = 0
-    if A is not None:
+    here, s = _place(X, "X", stream)
+    x = _take(X, "X", here, bf16, (M, K))
+    q = _take(Wq, "Wq", here, torch.uint8, (N, K // 2))
+    sc = _take(scales, "scales", here, bf16, (groups, N))
+    z = None if zeros is None else _take(zeros, "zeros", here, torch.uint8, (groups, N))
+    bi = None if bias is None else _take(bias, "bias", here, bf16, (N,))
+    a = b = _ws = ws = None
+    r = ws_bytes = 0
+    if A is not None or B is not None:
+        if A is None or B is None:
+            raise ValueError("A and B must both be given or both be None")
         r = A.shape[0]
-        _need(A, "A", torch.bfloat16, (r, K))
-        _need(B, "B", torch.bfloat16, (N, r))
-    _on_one_device(X=X, Wq=Wq, scales=scales, zeros=zeros, bias=bias, A=A, B=B, Y=Y)
-    if Y is None:
-        Y = _empty((M, N), torch.bfloat16, stream)
-    _need(Y, "Y", torch.bfloat16, (M, N))
-    lib = library()
-    need = lib.lynx_linear_w4_workspace_bytes(M, N, K, r) if r else 0
-    ws, ws_bytes, _keep = _need_workspace(workspace, need, stream)
-    st = lib.lynx_linear_w4(_ptr(X), _ptr(Wq), _ptr(scales), _ptr(zeros), _ptr(bias), _ptr(A), _ptr(B), M, N,
-                            K, r, group, int(act), _ptr(Y), ws, ws_bytes, _stream(stream))
-    _check(st, "lynx_linear_w4")
+        a = _take(A, "A", here, bf16, (r, K))
+        b = _take(B, "B", here, bf16, (N, r))
+        _ws, ws, ws_bytes = _scratch(workspace, here, X, lynx_linear_w4_workspace_bytes(M, N, K, r), stream)
+    Y, y = _out(Y, "Y", here, X, bf16, (M, N), stream)
+    _check(library().lynx_linear_w4(x, q, sc, z, bi, a, b, M, N, K, r, K // groups, act, y, ws, ws_bytes, s),
+           "lynx_linear_w4")
     return Y
 
 
-def _ckpt8_dtype(format):
-    import torch
-
-    if format == LYNX_CKPT8_INT8:
-        return torch.int8
-    if format == LYNX_CKPT8_E4M3:
-        return torch.float8_e4m3fn
-    raise LynxError(LYNX_ERR_INVALID_ARG, f"checkpoint format {format}")
-
-
-def _ckpt8_args(q, e):
+def _ckpt8_shape(q, e):
     """(M, K, format) of a checkpoint; the dtype of q says which format it is."""
     import torch
 
-    _need(q, "q")
-    if q.dim() != 2 or q.dtype not in (torch.int8, torch.float8_e4m3fn):
-        raise TypeError("q must be an int8 or float8_e4m3fn matrix")
-    M, K = q.shape
-    _need(e, "e", torch.uint8, (M, K // 32))
-    return M, K, LYNX_CKPT8_INT8 if q.dtype == torch.int8 else LYNX_CKPT8_E4M3
+    M, K = _matrix(q, "q")
+    if q.dtype is torch.int8:
+        return M, K, LYNX_CKPT8_INT8
+    if q.dtype is torch.float8_e4m3fn:
+        return M, K, LYNX_CKPT8_E4M3
+    raise TypeError(f"q must be int8 or float8_e4m3fn, got {q.dtype}")
 
 
 def lynx_ckpt8_exponent_bytes(M, K):
@@ -601,20 +602,14 @@ def lynx_ckpt8_store(X, format=LYNX_CKPT8_INT8, q=None, e=None, stream=None):
     float8_e4m3fn, e [M,K/32] u8)."""
     import torch
 
-    _need(X, "X", torch.bfloat16)
-    if X.dim() != 2:
-        raise ValueError("X must be [M,K]")
-    M, K = X.shape
-    dtype = _ckpt8_dtype(format)
-    _on_one_device(X=X, q=q, e=e)
-    if q is None:
-        q = _empty((M, K), dtype, stream)
-    if e is None:
-        e = _empty((M, K // 32), torch.uint8, stream)
-    _need(q, "q", dtype, (M, K))
-    _need(e, "e", torch.uint8, (M, K // 32))
-    st = library().lynx_ckpt8_store(_ptr(X), M, K, int(format), _ptr(q), _ptr(e), _stream(stream))
-    _check(st, "lynx_ckpt8_store")
+    M, K = _matrix(X, "X")
+    if format not in (LYNX_CKPT8_INT8, LYNX_CKPT8_E4M3):
+        raise LynxError(LYNX_ERR_INVALID_ARG, f"lynx_ckpt8_store (format {format})")
+    here, s = _place(X, "X", stream)
+    x = _take(X, "X", here, torch.bfloat16, (M, K))
+    q, qp = _out(q, "q", here, X, torch.int8 if format == LYNX_CKPT8_INT8 else torch.float8_e4m3fn, (M, K), stream)
+    e, ep = _out(e, "e", here, X, torch.uint8, (M, K // 32), stream)
+    _check(library().lynx_ckpt8_store(x, M, K, format, qp, ep, s), "lynx_ckpt8_store")
     return q, e
 
 
@@ -622,16 +617,16 @@ def lynx_ckpt8_restore(q, e, X=None, stream=None):
     """The values [M,K] bf16 a checkpoint stands for."""
     import torch
 
-    M, K, fmt = _ckpt8_args(q, e)
-    _on_one_device(q=q, e=e, X=X)
-    if X is None:
-        X = _empty((M, K), torch.bfloat16, stream)
-    _need(X, "X", torch.bfloat16, (M, K))
-    st = library().lynx_ckpt8_restore(_ptr(q), _ptr(e), M, K, fmt, _ptr(X), _stream(stream))
-    _check(st, "lynx_ckpt8_restore")
+    M, K, fmt = _ckpt8_shape(q, e)
+    here, s = _place(q, "q", stream)
+    qp = _take(q, "q", here, q.dtype, (M, K))
+    ep = _take(e, "e", here, torch.uint8, (M, K // 32))
+    X, x = _out(X, "X", here, q, torch.bfloat16, (M, K), stream)
+    _check(library().lynx_ckpt8_restore(qp, ep, M, K, fmt, x, s), "lynx_ckpt8_restore")
     return X
 
 
+@functools.lru_cache(maxsize=1024)
 def lynx_lora_backward_workspace_bytes(M, N, K, r=64):
     return library().lynx_lora_backward_workspace_bytes(M, N, K, r)
 
@@ -642,34 +637,28 @@ def lynx_lora_backward(dY, q, e, A, B, dA=None, dB=None, dT=None, workspace=None
     T = X A^T (lynx_sparsify_backward takes it)."""
     import torch
 
-    M, K, fmt = _ckpt8_args(q, e)
-    _need(dY, "dY", torch.bfloat16)
-    _need(A, "A", torch.bfloat16)
-    _need(B, "B", torch.bfloat16)
-    if dY.dim() != 2 or dY.shape[0] != M:
+    bf16 = torch.bfloat16
+    M, K, fmt = _ckpt8_shape(q, e)
+    m, N = _matrix(dY, "dY")
+    if m != M:
         raise ValueError("dY must be [M,N] with the checkpoint's M")
-    N = dY.shape[1]
-    r = A.shape[0]
-    _need(A, "A", torch.bfloat16, (r, K))
-    _need(B, "B", torch.bfloat16, (N, r))
-    _on_one_device(dY=dY, q=q, e=e, A=A, B=B, dA=dA, dB=dB, dT=dT)
-    if dA is None:
-        dA = _empty((r, K), torch.bfloat16, stream)
-    if dB is None:
-        dB = _empty((N, r), torch.bfloat16, stream)
-    if dT is None:
-        dT = _empty((M, r), torch.bfloat16, stream)
-    _need(dA, "dA", torch.bfloat16, (r, K))
-    _need(dB, "dB", torch.bfloat16, (N, r))
-    _need(dT, "dT", torch.bfloat16, (M, r))
-    lib = library()
-    ws, ws_bytes, _keep = _need_workspace(workspace, lib.lynx_lora_backward_workspace_bytes(M, N, K, r), stream)
-    st = lib.lynx_lora_backward(_ptr(dY), _ptr(q), _ptr(e), _ptr(A), _ptr(B), M, N, K, r, fmt, _ptr(dA),
-                                _ptr(dB), _ptr(dT), ws, ws_bytes, _stream(stream))
-    _check(st, "lynx_lora_backward")
+    r = _matrix(A, "A")[0]
+    here, s = _place(dY, "dY", stream)
+    dy = _take(dY, "dY", here, bf16, (M, N))
+    qp = _take(q, "q", here, q.dtype, (M, K))
+    ep = _take(e, "e", here, torch.uint8, (M, K // 32))
+    a = _take(A, "A", here, bf16, (r, K))
+    b = _take(B, "B", here, bf16, (N, r))
+    dA, da = _out(dA, "dA", here, dY, bf16, (r, K), stream)
+    dB, db = _out(dB, "dB", here, dY, bf16, (N, r), stream)
+    dT, dt = _out(dT, "dT", here, dY, bf16, (M, r), stream)
+    _ws, ws, ws_bytes = _scratch(workspace, here, dY, lynx_lora_backward_workspace_bytes(M, N, K, r), stream)
+    _check(library().lynx_lora_backward(dy, qp, ep, a, b, M, N, K, r, fmt, da, db, dt, ws, ws_bytes, s),
+           "lynx_lora_backward")
     return dA, dB, dT
 
 
+@functools.lru_cache(maxsize=1024)
 def lynx_sparsify_backward_workspace_bytes(M, K):
     return library().lynx_sparsify_backward_workspace_bytes(M, K)
 
@@ -679,24 +668,24 @@ def lynx_sparsify_backward(G, q, e, dT=None, A=None, dX=None, workspace=None, st
     the LoRA branch's dT A (see include/lynx.h).  Returns dX."""
     import torch
 
-    M, K, fmt = _ckpt8_args(q, e)
-    _need(G, "G", torch.bfloat16, (M, K))
-    if (dT is None) != (A is None):
-        raise ValueError("dT and A must both be given or both be None")
+    bf16 = torch.bfloat16
+    M, K, fmt = _ckpt8_shape(q, e)
+    here, s = _place(G, "G", stream)
+    g = _take(G, "G", here, bf16, (M, K))
+    qp = _take(q, "q", here, q.dtype, (M, K))
+    ep = _take(e, "e", here, torch.uint8, (M, K // 32))
+    dt = a = None
     r = 0
-    if A is not None:
-        r = A.shape[0]
-        _need(A, "A", torch.bfloat16, (r, K))
-        _need(dT, "dT", torch.bfloat16, (M, r))
-    _on_one_device(G=G, q=q, e=e, dT=dT, A=A, dX=dX)
-    if dX is None:
-        dX = _empty((M, K), torch.bfloat16, stream)
-    _need(dX, "dX", torch.bfloat16, (M, K))
-    lib = library()
-    ws, ws_bytes, _keep = _need_workspace(workspace, lib.lynx_sparsify_backward_workspace_bytes(M, K), stream)
-    st = lib.lynx_sparsify_backward(_ptr(G), _ptr(q), _ptr(e), _ptr(dT), _ptr(A), M, K, r, fmt, _ptr(dX), ws,
-                                    ws_bytes, _stream(stream))
-    _check(st, "lynx_sparsify_backward")
+    if dT is not None or A is not None:
+        if dT is None or A is None:
+            raise ValueError("dT and A must both be given or both be None")
+        r = _matrix(A, "A")[0]
+        a = _take(A, "A", here, bf16, (r, K))
+        dt = _take(dT, "dT", here, bf16, (M, r))
+    dX, dx = _out(dX, "dX", here, G, bf16, (M, K), stream)
+    _ws, ws, ws_bytes = _scratch(workspace, here, G, lynx_sparsify_backward_workspace_bytes(M, K), stream)
+    _check(library().lynx_sparsify_backward(g, qp, ep, dt, a, M, K, r, fmt, dx, ws, ws_bytes, s),
+           "lynx_sparsify_backward")
     return dX
 
 

@@ -123,7 +123,7 @@ def test_bindings_refuse_cpu_tensors():
     x = torch.zeros(4, 64, dtype=torch.bfloat16)
     q, e = torch.zeros(4, 64, dtype=torch.int8), torch.zeros(4, 2, dtype=torch.uint8)
     with pytest.raises(ValueError):
-        lynx.lynx_w4_quantize(x)
+        lynx.lynx_w4_quantize(x, 64)
     with pytest.raises(ValueError):
         lynx.lynx_ckpt8_store(x)
     with pytest.raises(ValueError):
