@@ -202,9 +202,10 @@ struct SparsifyBackwardLaunch {
   const void* dt;  // [M,r] bf16, or null
   const void* a;   // [r,K] bf16 (with dt)
   void* dx;        // [M,K] bf16
-  float2* coef;    // [M] scratch: s and D / Lk per row
   int64_t M, K;
   int r, format;
+  int stall_test;
+  uint32_t* status;  // the stream's status word
 };
 cudaError_t launch_sparsify_backward(const SparsifyBackwardLaunch& p, cudaStream_t s);
 
@@ -216,9 +217,10 @@ inline int64_t meta_row_blocks(int64_t M) { return (M + 255) / 256 * 2; }
 // 32-row slices of the pair GEMM's combining step (one state word each)
 inline int64_t fin_slices(int64_t M) { return (M + 31) / 32; }
 
-// 2-D uint8 tensor map (no swizzle)
+// 2-D uint8 tensor map
 bool encode_u8_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
-                  uint64_t row_pitch_bytes, uint32_t box_inner, uint32_t box_outer);
+                  uint64_t row_pitch_bytes, uint32_t box_inner, uint32_t box_outer,
+                  CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_NONE);
 
 // 2-D bf16 tensor map: inner (contiguous) extent, outer extent, row pitch in bytes
 bool encode_bf16_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,

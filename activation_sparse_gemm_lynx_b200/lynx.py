@@ -84,8 +84,7 @@ def library():
             "lynx_ckpt8_restore": ([p, p, i64, i64, i32, p, p], i32),
             "lynx_lora_backward_workspace_bytes": ([i64, i64, i64, i64], sz),
             "lynx_lora_backward": ([p, p, p, p, p, i64, i64, i64, i64, i32, p, p, p, p, sz, p], i32),
-            "lynx_sparsify_backward_workspace_bytes": ([i64, i64], sz),
-            "lynx_sparsify_backward": ([p, p, p, p, p, i64, i64, i64, i32, p, p, sz, p], i32),
+            "lynx_sparsify_backward": ([p, p, p, p, p, i64, i64, i64, i32, p, p], i32),
             "lynx_check_error": ([p, p], i32),
             "lynx_meta_hw_to_canonical": ([p, p, i64, i64], i32),
             "lynx_meta_canonical_to_hw": ([p, p, i64, i64], i32),
@@ -607,7 +606,8 @@ def lynx_ckpt8_store(X, format=LYNX_CKPT8_INT8, q=None, e=None, stream=None):
         raise LynxError(LYNX_ERR_INVALID_ARG, f"lynx_ckpt8_store (format {format})")
     here, s = _place(X, "X", stream)
     x = _take(X, "X", here, torch.bfloat16, (M, K))
-    q, qp = _out(q, "q", here, X, torch.int8 if format == LYNX_CKPT8_INT8 else torch.float8_e4m3fn, (M, K), stream)
+    dtype = torch.int8 if format == LYNX_CKPT8_INT8 else torch.float8_e4m3fn
+    q, qp = _out(q, "q", here, X, dtype, (M, K), stream)
     e, ep = _out(e, "e", here, X, torch.uint8, (M, K // 32), stream)
     _check(library().lynx_ckpt8_store(x, M, K, format, qp, ep, s), "lynx_ckpt8_store")
     return q, e
@@ -658,12 +658,7 @@ def lynx_lora_backward(dY, q, e, A, B, dA=None, dB=None, dT=None, workspace=None
     return dA, dB, dT
 
 
-@functools.lru_cache(maxsize=1024)
-def lynx_sparsify_backward_workspace_bytes(M, K):
-    return library().lynx_sparsify_backward_workspace_bytes(M, K)
-
-
-def lynx_sparsify_backward(G, q, e, dT=None, A=None, dX=None, workspace=None, stream=None):
+def lynx_sparsify_backward(G, q, e, dT=None, A=None, dX=None, stream=None):
     """dX [M,K] from G, the gradient of S(X), at the checkpoint (q, e) of X, plus
     the LoRA branch's dT A (see include/lynx.h).  Returns dX."""
     import torch
@@ -683,9 +678,7 @@ def lynx_sparsify_backward(G, q, e, dT=None, A=None, dX=None, workspace=None, st
         a = _take(A, "A", here, bf16, (r, K))
         dt = _take(dT, "dT", here, bf16, (M, r))
     dX, dx = _out(dX, "dX", here, G, bf16, (M, K), stream)
-    _ws, ws, ws_bytes = _scratch(workspace, here, G, lynx_sparsify_backward_workspace_bytes(M, K), stream)
-    _check(library().lynx_sparsify_backward(g, qp, ep, dt, a, M, K, r, fmt, dx, ws, ws_bytes, s),
-           "lynx_sparsify_backward")
+    _check(library().lynx_sparsify_backward(g, qp, ep, dt, a, M, K, r, fmt, dx, s), "lynx_sparsify_backward")
     return dX
 
 

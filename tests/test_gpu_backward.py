@@ -86,14 +86,11 @@ def test_sparsify_backward(M, K, r, fmt):
     q, e, x = checkpoint(X, fmt)
     G = normal(2, M, K)
     dT, A = (normal(3, M, r), normal(4, r, K, std=0.2)) if r else (None, None)
-    need = lynx.lynx_sparsify_backward_workspace_bytes(M, K)
-    raws = [guarded((M, K), torch.bfloat16), guarded((max(need, 1),), torch.uint8)]
-    (_, dX), (_, ws) = raws
-    lynx.lynx_sparsify_backward(G, q, e, dT, A, dX, ws)
+    raw, dX = guarded((M, K), torch.bfloat16)
+    lynx.lynx_sparsify_backward(G, q, e, dT, A, dX)
     within(dX, *ao.sparsify_backward(G, x, dT, A))
-    assert all(intact(r_, t) for r_, t in raws)
-    ws.fill_(0xFF)
-    assert torch.equal(dX, lynx.lynx_sparsify_backward(G, q, e, dT, A, workspace=ws))
+    assert intact(raw, dX)
+    assert torch.equal(dX, lynx.lynx_sparsify_backward(G, q, e, dT, A))
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
