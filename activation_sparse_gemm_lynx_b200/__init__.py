@@ -47,6 +47,7 @@ from .lynx import (  # noqa: F401
     lynx_sparse_gemm,
     lynx_sparsify,
     lynx_sparsify_backward,
+    lynx_sparsify_backward_workspace_bytes,
     lynx_sparsify_noalloc,
     lynx_sparsify_noalloc_max_rows,
     lynx_sparsify_workspace_bytes,

@@ -170,14 +170,23 @@ int lynx_lora_backward(const void* dY, const void* q, const void* e, const void*
   return status_of(launch_lora_backward(p, static_cast<cudaStream_t>(stream)));
 }
 
+size_t lynx_sparsify_backward_workspace_bytes(int64_t M, int64_t K) {
+  if (!rows_ok(M) || !k_ok(K)) return 0;
+  return align256(static_cast<size_t>(M) * sizeof(float2));
+}
+
 int lynx_sparsify_backward(const void* G, const void* q, const void* e, const void* dT, const void* A, int64_t M,
-                           int64_t K, int64_t r, int format, void* dX, void* stream) {
+                           int64_t K, int64_t r, int format, void* dX, void* workspace, size_t workspace_bytes,
+                           void* stream) {
   if (any_null(G, q, e, dX) || !format_ok(format)) return LYNX_ERR_INVALID_ARG;
   if (const int st = check_branch(dT, A, r)) return st;
   if (!rows_ok(M) || !k_ok(K)) return LYNX_ERR_UNSUPPORTED_SHAPE;
-  if (any_misaligned(G, q, e, dT, A, dX)) return LYNX_ERR_MISALIGNED;
+  if (any_misaligned(G, q, e, dT, A, dX, workspace)) return LYNX_ERR_MISALIGNED;
+  if (workspace == nullptr) return LYNX_ERR_INVALID_ARG;
+  if (workspace_bytes < lynx_sparsify_backward_workspace_bytes(M, K)) return LYNX_ERR_WORKSPACE_TOO_SMALL;
+  const int sms = device_sm_count();
   uint32_t* status = stream_status_word(static_cast<cudaStream_t>(stream));
-  if (status == nullptr) return LYNX_ERR_CUDA;
+  if (sms == 0 || status == nullptr) return LYNX_ERR_CUDA;
   SparsifyBackwardLaunch p;
   std::memset(&p, 0, sizeof(p));
   p.g = G;
@@ -186,13 +195,14 @@ int lynx_sparsify_backward(const void* G, const void* q, const void* e, const vo
   p.dt = dT;
   p.a = A;
   p.dx = dX;
+  p.coef = static_cast<float2*>(workspace);
   p.M = M;
   p.K = K;
   p.r = dT != nullptr ? static_cast<int>(r) : 0;
   p.format = format;
   p.stall_test = stall_test_enabled();
   p.status = status;
-  return status_of(launch_sparsify_backward(p, static_cast<cudaStream_t>(stream)));
+  return status_of(launch_sparsify_backward(p, sms, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

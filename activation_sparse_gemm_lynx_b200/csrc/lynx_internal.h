@@ -202,12 +202,13 @@ struct SparsifyBackwardLaunch {
   const void* dt;  // [M,r] bf16, or null
   const void* a;   // [r,K] bf16 (with dt)
   void* dx;        // [M,K] bf16
+  float2* coef;    // [M] scratch: s and D / Lk per row
   int64_t M, K;
   int r, format;
   int stall_test;
   uint32_t* status;  // the stream's status word
 };
-cudaError_t launch_sparsify_backward(const SparsifyBackwardLaunch& p, cudaStream_t s);
+cudaError_t launch_sparsify_backward(const SparsifyBackwardLaunch& p, int sms, cudaStream_t s);
 
 // ---- helpers ----------------------------------------------------------------
 

@@ -84,7 +84,8 @@ def library():
             "lynx_ckpt8_restore": ([p, p, i64, i64, i32, p, p], i32),
             "lynx_lora_backward_workspace_bytes": ([i64, i64, i64, i64], sz),
             "lynx_lora_backward": ([p, p, p, p, p, i64, i64, i64, i64, i32, p, p, p, p, sz, p], i32),
-            "lynx_sparsify_backward": ([p, p, p, p, p, i64, i64, i64, i32, p, p], i32),
+            "lynx_sparsify_backward_workspace_bytes": ([i64, i64], sz),
+            "lynx_sparsify_backward": ([p, p, p, p, p, i64, i64, i64, i32, p, p, sz, p], i32),
             "lynx_check_error": ([p, p], i32),
             "lynx_meta_hw_to_canonical": ([p, p, i64, i64], i32),
             "lynx_meta_canonical_to_hw": ([p, p, i64, i64], i32),
@@ -658,7 +659,12 @@ def lynx_lora_backward(dY, q, e, A, B, dA=None, dB=None, dT=None, workspace=None
     return dA, dB, dT
 
 
-def lynx_sparsify_backward(G, q, e, dT=None, A=None, dX=None, stream=None):
+@functools.lru_cache(maxsize=1024)
+def lynx_sparsify_backward_workspace_bytes(M, K):
+    return library().lynx_sparsify_backward_workspace_bytes(M, K)
+
+
+def lynx_sparsify_backward(G, q, e, dT=None, A=None, dX=None, workspace=None, stream=None):
     """dX [M,K] from G, the gradient of S(X), at the checkpoint (q, e) of X, plus
     the LoRA branch's dT A (see include/lynx.h).  Returns dX."""
     import torch
@@ -678,7 +684,9 @@ def lynx_sparsify_backward(G, q, e, dT=None, A=None, dX=None, stream=None):
         a = _take(A, "A", here, bf16, (r, K))
         dt = _take(dT, "dT", here, bf16, (M, r))
     dX, dx = _out(dX, "dX", here, G, bf16, (M, K), stream)
-    _check(library().lynx_sparsify_backward(g, qp, ep, dt, a, M, K, r, fmt, dx, s), "lynx_sparsify_backward")
+    _ws, ws, ws_bytes = _scratch(workspace, here, G, lynx_sparsify_backward_workspace_bytes(M, K), stream)
+    _check(library().lynx_sparsify_backward(g, qp, ep, dt, a, M, K, r, fmt, dx, ws, ws_bytes, s),
+           "lynx_sparsify_backward")
     return dX
 
 

@@ -415,6 +415,9 @@ LYNX_API int lynx_lora_backward(const void* dY, const void* q, const void* e, co
                                 void* dA, void* dB, void* dT, void* workspace, size_t workspace_bytes,
                                 void* stream);
 
+/* Bytes of the workspace lynx_sparsify_backward needs (two floats a row). */
+LYNX_API size_t lynx_sparsify_backward_workspace_bytes(int64_t M, int64_t K);
+
 /* dX [M,K] bf16 from G = dL/dS(X) [M,K] bf16 at the checkpoint's values x: with
  * m the 2:4 selection of x (ties to the lower position), L = sum|x|,
  * Lk = sum m|x|, s = L / Lk and D = sum m G x of the row,
@@ -424,11 +427,11 @@ LYNX_API int lynx_lora_backward(const void* dY, const void* q, const void* e, co
  * the exact derivative of S(X) = s m x where the selection does not change (the
  * bf16 rounding of S(X) passed through).  A row with Lk = 0 has s = 1 and no
  * second term.  dT [M,r] and A [r,K] (both or neither): the LoRA branch's share.
- * The first call on a device asks how many clusters of blocks it holds; make it
- * before any stream capture. */
+ *   workspace: device scratch of workspace_bytes >=
+ *   lynx_sparsify_backward_workspace_bytes(M,K). */
 LYNX_API int lynx_sparsify_backward(const void* G, const void* q, const void* e, const void* dT,
                                     const void* A, int64_t M, int64_t K, int64_t r, int format, void* dX,
-                                    void* stream);
+                                    void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---- errors and metadata conversion ----------------------------------- */
 

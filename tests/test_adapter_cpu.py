@@ -49,8 +49,9 @@ ENTRY = {
                             "stream"],
                            dict(dY=P, q=P, e=P, A=P, B=P, M=4, N=64, K=256, r=16, format=0, dA=P, dB=P, dT=None, ws=P,
                                 bytes=BIG, stream=None)),
-    "lynx_sparsify_backward": (["G", "q", "e", "dT", "A", "M", "K", "r", "format", "dX", "stream"],
-                               dict(G=P, q=P, e=P, dT=None, A=None, M=4, K=256, r=0, format=0, dX=P, stream=None)),
+    "lynx_sparsify_backward": (["G", "q", "e", "dT", "A", "M", "K", "r", "format", "dX", "ws", "bytes", "stream"],
+                               dict(G=P, q=P, e=P, dT=None, A=None, M=4, K=256, r=0, format=0, dX=P, ws=P, bytes=BIG,
+                                    stream=None)),
 }
 
 INVALID, SHAPE, ALIGN, SMALL = (lynx.LYNX_ERR_INVALID_ARG, lynx.LYNX_ERR_UNSUPPORTED_SHAPE, lynx.LYNX_ERR_MISALIGNED,
@@ -91,6 +92,7 @@ BAD = [
     ("lynx_sparsify_backward", dict(r=7), SHAPE), ("lynx_sparsify_backward", dict(K=65), SHAPE),
     ("lynx_sparsify_backward", dict(M=0), SHAPE), ("lynx_sparsify_backward", dict(dX=P + 2), ALIGN),
     ("lynx_sparsify_backward", dict(dX=None), INVALID), ("lynx_sparsify_backward", dict(format=2), INVALID),
+    ("lynx_sparsify_backward", dict(ws=None), INVALID), ("lynx_sparsify_backward", dict(bytes=0), SMALL),
 ]
 
 
@@ -115,6 +117,8 @@ def test_sizes(lib):
     assert lynx.lynx_ckpt8_exponent_bytes(7, 320) == 70
     assert lynx.lynx_lora_backward_workspace_bytes(0, 64, 256, 16) == 0
     assert lynx.lynx_lora_backward_workspace_bytes(300, 1000, 576, 16) > 0
+    assert lynx.lynx_sparsify_backward_workspace_bytes(5, 60) == 0
+    assert lynx.lynx_sparsify_backward_workspace_bytes(5, 64) >= 5 * 8
 
 
 def test_bindings_refuse_cpu_tensors():

@@ -86,11 +86,13 @@ def test_sparsify_backward(M, K, r, fmt):
     q, e, x = checkpoint(X, fmt)
     G = normal(2, M, K)
     dT, A = (normal(3, M, r), normal(4, r, K, std=0.2)) if r else (None, None)
-    raw, dX = guarded((M, K), torch.bfloat16)
-    lynx.lynx_sparsify_backward(G, q, e, dT, A, dX)
+    raws = [guarded((M, K), torch.bfloat16), guarded((lynx.lynx_sparsify_backward_workspace_bytes(M, K),), torch.uint8)]
+    (_, dX), (_, ws) = raws
+    lynx.lynx_sparsify_backward(G, q, e, dT, A, dX, ws)
     within(dX, *ao.sparsify_backward(G, x, dT, A))
-    assert intact(raw, dX)
-    assert torch.equal(dX, lynx.lynx_sparsify_backward(G, q, e, dT, A))
+    assert all(intact(r_, t) for r_, t in raws)
+    ws.fill_(0xFF)
+    assert torch.equal(dX, lynx.lynx_sparsify_backward(G, q, e, dT, A, workspace=ws))
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
