@@ -60,7 +60,7 @@ __device__ __forceinline__ float masked(float v, uint32_t mask) { return __uint_
 
 constexpr int kRowThreads = 256;
 constexpr int kRowWarps = kRowThreads / 32;
-constexpr int kAhead = 2;  // steps in flight
+constexpr int kAhead = 2;  // steps in flight (3, with a quarter fewer blocks an SM, took 49 us for 38)
 
 // 16 values: sums of |x|, of the kept |x| and of the kept g x, before the factor
 template <int FMT>
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) row_sums_kernel(SparsifyBackwa
 // outputs
 //   warp 0   TMA: G, the stored bytes and A's rows of a tile
 //   warp 1   the MMAs
-//   warp 2   TMA stores of dX
+//   warps 2, 3  TMA stores of dX
 //   warps 4-19  two groups of 8 that take the tiles in turn; a thread has one row
 //               (a TMEM lane) and 32 columns.  Selection and sign need no
 //               exponents, which the row coefficients have seen.
@@ -185,6 +185,7 @@ struct BackLaunch {
   int ranges;         // blocks of a row block
   int per;            // tiles of a block
   int stages;
+  int turns;          // output buffers of a group, 1 or 2
   uint32_t stage_bytes;
   int stall_test;
   uint32_t* status;
@@ -192,7 +193,7 @@ struct BackLaunch {
 
 struct BackBars {
   uint64_t full[kMaxStages], empty[kMaxStages];
-  uint64_t dt_full, d_full[2], d_empty[2], done[2], out_empty[2];
+  uint64_t dt_full, d_full[2], d_empty[2], done[4], out_empty[4];
   uint32_t tmem_base;
   volatile uint32_t abort_flag;
 };
@@ -228,8 +229,8 @@ __global__ void __launch_bounds__(kThreads, 1) sparsify_backward_kernel(const __
   const int tile0 = static_cast<int>(at % static_cast<unsigned>(p.ranges)) * p.per;
   const int tiles = max(0, min(p.per, static_cast<int>(p.K / kCols) - tile0));
   const uint32_t t_boxes = LORA ? static_cast<uint32_t>((p.r + 63) / 64) : 0u;
-  uint8_t* const out_sm = sm + t_boxes * kTBox;  // two tiles of dX
-  uint8_t* const ring = out_sm + 2 * kGBytes;
+  uint8_t* const out_sm = sm + t_boxes * kTBox;  // tiles of dX, `turns` for each group
+  uint8_t* const ring = out_sm + 2 * p.turns * kGBytes;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
@@ -240,6 +241,8 @@ __global__ void __launch_bounds__(kThreads, 1) sparsify_backward_kernel(const __
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.d_full[i], 1);
       mbar_init(&bars.d_empty[i], kGroupWarps);
+    }
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&bars.done[i], kGroupWarps);
       mbar_init(&bars.out_empty[i], 1);
     }
@@ -314,43 +317,54 @@ __global__ void __launch_bounds__(kThreads, 1) sparsify_backward_kernel(const __
         if (++slot == stages) slot = 0, phase ^= 1u;
       }
     }
-  } else if (warp == 2) {
+  } else if (warp < kRoleWarps) {
     // ------------------------------------------------------------ stores of dX
+    // One warp a group, so that neither group waits for the other's tile.
     if (lane == 0) {
-      for (int i = 0; i < tiles; ++i) {
-        const int buf = i & 1;
-        if (!back_wait(bars, &bars.done[buf], (i >> 1) & 1, p.status, kDevTimeoutAccum)) break;
+      const int group = static_cast<int>(warp) - 2;
+      int turn = 0;
+      uint32_t parity = 0;
+      for (int i = group; i < tiles; i += 2) {
+        const int buf = group + 2 * turn;
+        if (!back_wait(bars, &bars.done[buf], parity, p.status, kDevTimeoutAccum)) break;
         tma_store_2d(&p.tm_dx, out_sm + buf * kGBytes, (tile0 + i) * kCols, row0);
         bulk_commit();
-        bulk_wait_read_le1();  // the store before this one has left its buffer
-        if (i > 0) mbar_arrive(&bars.out_empty[buf ^ 1]);
+        if (p.turns == 2) {
+          bulk_wait_read_le1();  // the group's store before this one has left its buffer
+          if (i > group) mbar_arrive(&bars.out_empty[buf ^ 2]);
+        } else {
+          bulk_wait_read_all();
+          mbar_arrive(&bars.out_empty[buf]);
+        }
+        if (++turn == p.turns) turn = 0, parity ^= 1u;
       }
       bulk_wait_all();
     }
     __syncwarp();
-  } else if (warp >= kRoleWarps) {
+  } else {
     // ------------------------------------------------------------ outputs
     const uint32_t quarter = warp & 3u, half = ((warp - kRoleWarps) >> 2) & 1u;
-    const int buf = static_cast<int>((warp - kRoleWarps) >> 3);  // this group's tiles, TMEM and output buffers
+    const int buf = static_cast<int>((warp - kRoleWarps) >> 3);  // this group: its tiles and TMEM buffer
     const uint32_t row = 32u * quarter + lane;
     // 16 columns: one 16-byte unit of the stored values, two of G (swizzled by the row)
     auto q_unit = [&](uint32_t h) { return kGBytes + row * 64 + (((2 * half + h) ^ ((row >> 1) & 3u)) << 4); };
     auto g_unit = [&](uint32_t h, uint32_t u) { return row * 128 + (((4 * half + 2 * h + u) ^ (row & 7u)) << 4); };
     const uint32_t t_at = bars.tmem_base + buf * kCols + 32 * half + ((32u * quarter) << 16);
-    uint8_t* const dst = out_sm + buf * kGBytes;
     pdl_wait();
     const float2 c = row0 + static_cast<int64_t>(row) < p.M ? __ldcg(p.coef + row0 + row) : make_float2(0.f, 0.f);
     // dX = kept: s g + sign(x) c (1 - s); dropped: sign(x) c, c = D / Lk
     const float s = c.x;
     const uint32_t dropped = __float_as_uint(c.y), kept = __float_as_uint(c.y * (1.f - s));
     int slot = buf % stages;
-    uint32_t phase = static_cast<uint32_t>(buf / stages) & 1u, parity = 0;
+    uint32_t phase = static_cast<uint32_t>(buf / stages) & 1u, parity = 0, out_parity = 1;
+    int turn = 0;  // of the group's output buffers
     for (int i = buf; i < tiles; i += 2) {
       bool ok = back_wait(bars, &bars.full[slot], phase, p.status, kDevTimeoutFull) &&
-                back_wait(bars, &bars.out_empty[buf], parity ^ 1u, p.status, kDevTimeoutEmpty);
+                back_wait(bars, &bars.out_empty[buf + 2 * turn], out_parity, p.status, kDevTimeoutEmpty);
       if (LORA) ok = ok && back_wait(bars, &bars.d_full[buf], parity, p.status, kDevTimeoutAccum);
       if (!__all_sync(0xffffffffu, ok)) break;
       const uint8_t* st = ring + static_cast<uint32_t>(slot) * p.stage_bytes;
+      uint8_t* const dst = out_sm + (buf + 2 * turn) * kGBytes;
       if constexpr (LORA) tc_fence_after();
 #pragma unroll
       for (uint32_t h = 0; h < 2; ++h) {
@@ -392,8 +406,9 @@ __global__ void __launch_bounds__(kThreads, 1) sparsify_backward_kernel(const __
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.done[buf]);
+      if (lane == 0) mbar_arrive(&bars.done[buf + 2 * turn]);
       parity ^= 1u;
+      if (++turn == p.turns) turn = 0, out_parity ^= 1u;
       slot += 2;
       if (slot >= stages) slot -= stages, phase ^= 1u;
     }
@@ -442,9 +457,12 @@ cudaError_t launch_sparsify_backward(const SparsifyBackwardLaunch& p, int sms, c
   b.stall_test = p.stall_test;
   b.status = p.status;
   const bool lora = p.dt != nullptr;
-  const uint32_t fixed = 1024 + 2 * kGBytes + (lora ? static_cast<uint32_t>((p.r + 63) / 64) * kTBox : 0u);
+  const uint32_t t_bytes = lora ? static_cast<uint32_t>((p.r + 63) / 64) * kTBox : 0u;
   b.stage_bytes = kGBytes + kQBytes + 128u * static_cast<uint32_t>(p.r);
-  const uint32_t fit = (kSmemMost - fixed) / b.stage_bytes;
+  // two output buffers a group where three stages are left for the loads (r <= 128)
+  auto stages = [&](uint32_t turns) { return (kSmemMost - 1024 - t_bytes - 2 * turns * kGBytes) / b.stage_bytes; };
+  b.turns = stages(2) >= 3 ? 2 : 1;
+  const uint32_t fit = stages(static_cast<uint32_t>(b.turns));
   b.stages = static_cast<int>(fit < kMaxStages ? fit : kMaxStages);
   // blocks of a row block: the number with the fewest tiles one after another
   // (waves of one block an SM times tiles of a block), the smallest such
@@ -459,7 +477,7 @@ cudaError_t launch_sparsify_backward(const SparsifyBackwardLaunch& p, int sms, c
   }
   b.per = static_cast<int>((tiles + b.ranges - 1) / b.ranges);
   b.ranges = static_cast<int>((tiles + b.per - 1) / b.per);
-  const uint32_t smem = fixed + b.stages * b.stage_bytes;
+  const uint32_t smem = 1024 + t_bytes + 2 * b.turns * kGBytes + b.stages * b.stage_bytes;
   const uint64_t M = p.M, K = p.K, r = p.r;
   constexpr auto kSw = CU_TENSOR_MAP_SWIZZLE_128B;
   if (!encode_bf16_2d(&b.tm_g, p.g, K, M, K * 2, kCols, 128, kSw) ||

@@ -23,6 +23,17 @@ constexpr int kThreads = 256;
 // k sits at 4 * (k / 2 + 4 * (k % 2)) bits.
 __device__ __forceinline__ constexpr int nibble_shift(int k) { return 4 * (k / 2 + 4 * (k % 2)); }
 
+// Saturated to 0..15, two at a time, in the word's order
+__device__ __forceinline__ uint32_t pack_nibbles(const int (&q)[8]) {
+  uint32_t w;
+  asm("{\n\t.reg .b32 a;\n\t"
+      "cvt.pack.sat.u4.s32.b32 a, %8, %6, 0;\n\tcvt.pack.sat.u4.s32.b32 a, %4, %2, a;\n\t"
+      "cvt.pack.sat.u4.s32.b32 a, %7, %5, a;\n\tcvt.pack.sat.u4.s32.b32 %0, %3, %1, a;\n\t}"
+      : "=r"(w)
+      : "r"(q[0]), "r"(q[1]), "r"(q[2]), "r"(q[3]), "r"(q[4]), "r"(q[5]), "r"(q[6]), "r"(q[7]));
+  return w;
+}
+
 template <int GROUP, bool ZEROS>
 __global__ void __launch_bounds__(kThreads) w4_quantize_kernel(const __nv_bfloat16* __restrict__ w, int64_t N,
                                                                int64_t K, uint32_t* __restrict__ wq,
@@ -38,58 +49,91 @@ __global__ void __launch_bounds__(kThreads) w4_quantize_kernel(const __nv_bfloat
   const int64_t n0 = static_cast<int64_t>(blockIdx.x / k_tiles) * kTileN;
   const int64_t k0 = kt * kTileK + 8 * lane;
   const bool k_in = k0 < K;
+  uint4 rows[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int row = 4 * warp + i;
-    const int64_t n = n0 + row;
-    const bool in = k_in && n < N;
-    uint32_t v[4] = {0, 0, 0, 0};
-    if (in) *reinterpret_cast<uint4*>(v) = __ldcs(reinterpret_cast<const uint4*>(w + n * K + k0));
-    float x[8];
+    const int64_t n = n0 + 4 * warp + i;
+    rows[i] = k_in && n < N ? __ldcs(reinterpret_cast<const uint4*>(w + n * K + k0)) : make_uint4(0, 0, 0, 0);
+  }
+  // Largest and smallest of a lane's 8 values, row by row; without zero points the
+  // largest magnitude alone.
+  float hi[4], lo[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t v[4] = {rows[i].x, rows[i].y, rows[i].z, rows[i].w};
+    hi[i] = lo[i] = 0.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      x[2 * j] = bf16_lo(v[j]);
-      x[2 * j + 1] = bf16_hi(v[j]);
-    }
-    float hi = x[0], lo = x[0];
-#pragma unroll
-    for (int j = 1; j < 8; ++j) {
-      hi = fmaxf(hi, x[j]);
-      lo = fminf(lo, x[j]);
-    }
-#pragma unroll
-    for (int d = 1; d < kLanes; d *= 2) {
-      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, d));
-      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, d));
-    }
-    // the quotient in 64 bits, one per group: hi - lo of two bf16 is not always an fp32
-    float top;
-    if constexpr (ZEROS) {
-      hi = fmaxf(hi, 0.f);
-      lo = fminf(lo, 0.f);
-      top = __double2float_rn((static_cast<double>(hi) - static_cast<double>(lo)) / 15.0);
-    } else {
-      top = fmaxf(hi, -lo) / 7.f;
-    }
-    const __nv_bfloat16 sb = __float2bfloat16_rn(top);
-    const float s = __bfloat162float(sb);
-    int z = ZEROS ? 0 : 8;
-    uint32_t word = 0;
-    if (s == 0.f) {
-      word = static_cast<uint32_t>(z) * 0x11111111u;
-    } else {
-      if constexpr (ZEROS) z = max(0, min(15, __float2int_rn(-lo / s)));
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int q = max(0, min(15, __float2int_rn(x[k] / s) + z));
-        word |= static_cast<uint32_t>(q) << nibble_shift(k);
+      const float x = bf16_lo(v[j]), y = bf16_hi(v[j]);
+      if constexpr (ZEROS) {
+        hi[i] = fmaxf(hi[i], fmaxf(x, y));
+        lo[i] = fminf(lo[i], fminf(x, y));
+      } else {
+        hi[i] = fmaxf(hi[i], fmaxf(fabsf(x), fabsf(y)));
       }
     }
-    if (in) wq[(n * K + k0) >> 3] = word;
-    if (lane % kLanes == 0) {
-      s_sm[lane / kLanes][row] = sb;
-      if constexpr (ZEROS) z_sm[lane / kLanes][row] = static_cast<uint8_t>(z);
+  }
+  // Over the lanes of a group, each of 4 neighbours keeping one of the 4 rows, so
+  // that a lane divides once: row lane % 4.
+  const bool odd = lane & 1, upper = lane & 2;
+  auto exchange = [&](const float (&v)[4], auto pick) {
+    const float a = pick(odd ? v[1] : v[0], __shfl_xor_sync(0xffffffffu, odd ? v[0] : v[1], 1));
+    const float c = pick(odd ? v[3] : v[2], __shfl_xor_sync(0xffffffffu, odd ? v[2] : v[3], 1));
+    float r = pick(upper ? c : a, __shfl_xor_sync(0xffffffffu, upper ? a : c, 2));
+#pragma unroll
+    for (int d = 4; d < kLanes; d *= 2) r = pick(r, __shfl_xor_sync(0xffffffffu, r, d));
+    return r;
+  };
+  const float top = exchange(hi, [](float a, float c) { return fmaxf(a, c); });
+  float ratio;
+  if constexpr (ZEROS) {
+    const float low = exchange(lo, [](float a, float c) { return fminf(a, c); });
+    const float range = top - low;
+    lo[0] = low;
+    // two bf16 more than 16 binades apart: their difference is no fp32
+    if (range - top == -low && top - range == low)
+      ratio = range / 15.f;
+    else
+      ratio = __double2float_rn((static_cast<double>(top) - static_cast<double>(low)) / 15.0);
+  } else {
+    ratio = top / 7.f;
+  }
+  const __nv_bfloat16 sb = __float2bfloat16_rn(ratio);
+  const float my_s = __bfloat162float(sb);
+  int my_z = 8;
+  if constexpr (ZEROS) my_z = my_s == 0.f ? 0 : max(0, min(15, __float2int_rn(-lo[0] / my_s)));
+  const float my_inv = my_s >= 0x1p-100f ? 1.f / my_s : 0.f;  // 1 / s may not be finite below
+  if (lane % kLanes < 4) {
+    s_sm[lane / kLanes][4 * warp + (lane & 3)] = sb;
+    if constexpr (ZEROS) z_sm[lane / kLanes][4 * warp + (lane & 3)] = static_cast<uint8_t>(my_z);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t n = n0 + 4 * warp + i;
+    const uint32_t v[4] = {rows[i].x, rows[i].y, rows[i].z, rows[i].w};
+    const int from = (lane & ~3) | i;
+    const float s = __shfl_sync(0xffffffffu, my_s, from), inv = __shfl_sync(0xffffffffu, my_inv, from);
+    const int z = ZEROS ? __shfl_sync(0xffffffffu, my_z, from) : 8;
+    int q[8];
+    if (inv != 0.f) {
+      // The quotient with one Newton correction (Markstein's division): exact
+      // wherever x / s is an fp32, so at every tie of rint; any other quotient of
+      // two bf16 below 16 is over 2^-12 away from one.  Adding 1.5 * 2^23 rounds.
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float x = k % 2 ? bf16_hi(v[k / 2]) : bf16_lo(v[k / 2]);
+        const float first = x * inv;
+        const float quotient = fmaf(fmaf(-first, s, x), inv, first);
+        q[k] = __float_as_int(quotient + 12582912.f) + (z - 0x4B400000);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float x = k % 2 ? bf16_hi(v[k / 2]) : bf16_lo(v[k / 2]);
+        q[k] = s == 0.f ? z : __float2int_rn(x / s) + z;
+      }
     }
+    if (k_in && n < N) wq[(n * K + k0) >> 3] = pack_nibbles(q);
   }
   __syncthreads();
   const int64_t kg0 = kt * kGroups;
