@@ -2,6 +2,10 @@
 
     python -m activation_sparse_gemm_lynx_b200.build [--force] [--verbose]
 
+The host compiler also builds ``_build/_lynx_torch.so`` from
+``csrc/torch_binding.cpp``: the tensor marshalling of the calls that are short
+on the device, linked to that library and to torch's own.
+
 One nvcc invocation compiles every ``csrc/*.cu`` file with
 ``-gencode arch=compute_100a,code=sm_100a -lineinfo`` and links a shared
 library with the CUDA runtime linked statically (the driver API is reached
@@ -19,6 +23,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "liblynx.so")
+BINDING = os.path.join(OUT_DIR, "_lynx_torch.so")
+BINDING_SOURCE = os.path.join(CSRC, "torch_binding.cpp")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -52,10 +58,45 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
+def binding_up_to_date() -> bool:
+    if not os.path.exists(BINDING):
+        return False
+    t = os.path.getmtime(BINDING)
+    return all(os.path.getmtime(f) <= t for f in (BINDING_SOURCE, os.path.join(INCLUDE, "lynx.h")))
+
+
+def build_binding() -> str:
+    """Compile the tensor marshalling against torch; return its path."""
+    import sysconfig
+
+    import torch
+
+    home = os.path.dirname(torch.__file__)
+    tmp = BINDING + ".tmp%d" % os.getpid()
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI), "-I", INCLUDE,
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include")]
+    cmd += ["-isystem", os.path.join(home, "include"),
+            "-isystem", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+            "-o", tmp, BINDING_SOURCE, "-L", OUT_DIR, "-llynx", "-Wl,-rpath,$ORIGIN",
+            "-L", os.path.join(home, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile the library if any source is newer than it; return its path."""
-    if not force and up_to_date():
-        return LIB
+    """Compile what any source is newer than; return the library's path."""
+    if force or not up_to_date():
+        build_library(verbose)
+    if force or not binding_up_to_date():
+        build_binding()
+    return LIB
+
+
+def build_library(verbose: bool = False) -> str:
+    """Compile the CUDA library; return its path."""
     os.makedirs(OUT_DIR, exist_ok=True)
     tmp = LIB + ".tmp%d" % os.getpid()
     cmd = [_nvcc(), *NVCC_FLAGS, "-I", INCLUDE, "-I", CSRC, "-o", tmp, *_sources()]

@@ -9,7 +9,6 @@ The functions carry the C names; tensors are torch tensors on the current CUDA
 device, bf16 unless stated, row-major and contiguous.
 """
 import ctypes
-import functools
 import os
 import re
 
@@ -431,75 +430,36 @@ def lynx_sparse_gemm(vals, meta, W, bias=None, T=None, B=None, Y=None, stream=No
 
 # ---- the weight in 4 bits, the 8-bit checkpoint, the backward pass ----------
 #
-# These calls can be shorter on the device than a tensor check is on the host, so
-# the checks are one expression a tensor; only a tensor that fails is looked at
-# more closely, for the message.
+# These calls can be shorter on the device than a tensor check in Python, so their
+# marshalling is compiled (_build/_lynx_torch.so): it checks the tensors, which
+# must be contiguous and on the current device, makes the outputs and workspaces
+# that are not given, from the memory pool of the stream, and calls the C ABI.
+
+_compiled = None
 
 
-def _place(t, name, stream):
-    """(index of the current device, raw handle of the stream a call runs on);
-    `t` is the call's first tensor."""
-    import torch
+def _binding():
+    global _compiled
+    if _compiled is None:
+        library()
+        if not os.path.exists(_build.BINDING):
+            raise ImportError(
+                f"Lynx tensor binding not built ({_build.BINDING} missing); run "
+                "`python -m activation_sparse_gemm_lynx_b200.build`")
+        import importlib.util
 
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    here = torch.cuda.current_device()
-    if stream is None:
-        return here, torch._C._cuda_getCurrentRawStream(here)
-    if stream.device.index != here:
-        raise ValueError(f"stream is on {stream.device}, the current device is cuda:{here}")
-    return here, stream.cuda_stream
+        import torch  # noqa: F401  (the binding links to its libraries)
 
-
-def _take(t, name, here, dtype, shape):
-    """The address of a contiguous tensor of this type and shape on the current device."""
-    if t.get_device() == here and t.dtype is dtype and t.shape == shape and t.is_contiguous():
-        return t.data_ptr()
-    _need(t, name, dtype, shape)
-    raise ValueError(f"{name} is on {t.device}, the current device is cuda:{here}")
+        spec = importlib.util.spec_from_file_location("_lynx_torch", _build.BINDING)
+        _compiled = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(_compiled)
+    return _compiled
 
 
-def _matrix(t, name):
-    if t is None:
-        raise ValueError(f"{name} is required")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be a matrix")
-    return t.shape
-
-
-def _out(t, name, here, like, dtype, shape, stream):
-    """(tensor, address): the caller's, or one (on the device of `like`) from the
-    memory pool of the stream it is written on."""
-    if t is not None:
-        return t, _take(t, name, here, dtype, shape)
-    if stream is None:
-        t = like.new_empty(shape, dtype=dtype)
-    else:
-        import torch
-
-        with torch.cuda.stream(stream):
-            t = like.new_empty(shape, dtype=dtype)
-    return t, t.data_ptr()
-
-
-def _scratch(workspace, here, like, need, stream):
-    """(tensor, address, bytes) of the caller's workspace, or of one made here."""
-    import torch
-
-    if workspace is None:
-        if need == 0:
-            return None, None, 0
-        return *_out(None, "workspace", here, like, torch.uint8, (need,), stream), need
-    n = workspace.numel()
-    return workspace, _take(workspace, "workspace", here, torch.uint8, (n,)), n
-
-
-def _w4_shape(Wq, scales):
-    N, K2 = _matrix(Wq, "Wq")
-    groups, n = _matrix(scales, "scales")
-    if n != N or groups == 0 or 2 * K2 % groups:
-        raise ValueError("scales must be [K/group,N]")
-    return N, 2 * K2, groups
+def _result(r, what):
+    if type(r) is int:
+        raise LynxError(r, what)
+    return r
 
 
 def lynx_w4_bytes(N, K):
@@ -510,41 +470,18 @@ def lynx_w4_quantize(W, group=128, zero_points=False, Wq=None, scales=None, zero
     """W [N,K] bf16 to 4 bits: returns (Wq [N,K/2] u8, scales [K/group,N] bf16,
     zeros [K/group,N] u8, or None without zero points).  `zeros` given implies
     zero points."""
-    import torch
-
-    N, K = _matrix(W, "W")
-    if group not in (32, 64, 128) or K % group:
-        raise LynxError(LYNX_ERR_UNSUPPORTED_SHAPE, f"lynx_w4_quantize (group {group}, K {K})")
-    here, s = _place(W, "W", stream)
-    w = _take(W, "W", here, torch.bfloat16, (N, K))
-    Wq, q = _out(Wq, "Wq", here, W, torch.uint8, (N, K // 2), stream)
-    scales, sc = _out(scales, "scales", here, W, torch.bfloat16, (K // group, N), stream)
-    z = None
-    if zeros is not None or zero_points:
-        zeros, z = _out(zeros, "zeros", here, W, torch.uint8, (K // group, N), stream)
-    _check(library().lynx_w4_quantize(w, N, K, group, q, sc, z, s), "lynx_w4_quantize")
-    return Wq, scales, zeros
+    return _result(_binding().w4_quantize(W, group, zero_points, Wq, scales, zeros, stream), "lynx_w4_quantize")
 
 
 def lynx_w4_dequantize(Wq, scales, zeros=None, W=None, stream=None):
     """W [N,K] bf16 from its 4-bit form (the group is K / scales.shape[0])."""
-    import torch
-
-    N, K, groups = _w4_shape(Wq, scales)
-    here, s = _place(Wq, "Wq", stream)
-    q = _take(Wq, "Wq", here, torch.uint8, (N, K // 2))
-    sc = _take(scales, "scales", here, torch.bfloat16, (groups, N))
-    z = None if zeros is None else _take(zeros, "zeros", here, torch.uint8, (groups, N))
-    W, w = _out(W, "W", here, Wq, torch.bfloat16, (N, K), stream)
-    _check(library().lynx_w4_dequantize(q, sc, z, N, K, K // groups, w, s), "lynx_w4_dequantize")
-    return W
+    return _result(_binding().w4_dequantize(Wq, scales, zeros, W, stream), "lynx_w4_dequantize")
 
 
 def lynx_linear_w4_max_rows():
     return library().lynx_linear_w4_max_rows()
 
 
-@functools.lru_cache(maxsize=1024)
 def lynx_linear_w4_workspace_bytes(M, N, K, r=0):
     return library().lynx_linear_w4_workspace_bytes(M, N, K, r)
 
@@ -553,44 +490,8 @@ def lynx_linear_w4(X, Wq, scales, zeros=None, bias=None, A=None, B=None, act=LYN
                    workspace=None, stream=None):
     """Y = act(X W^T + bias + (X A^T) B^T) for up to 32 tokens, W in 4 bits
     (lynx_w4_quantize's outputs).  Returns Y."""
-    import torch
-
-    bf16 = torch.bfloat16
-    N, K, groups = _w4_shape(Wq, scales)
-    M, k = _matrix(X, "X")
-    if k != K:
-        raise ValueError("X must be [M,K] with K = 2 * Wq.shape[1]")
-    here, s = _place(X, "X", stream)
-    x = _take(X, "X", here, bf16, (M, K))
-    q = _take(Wq, "Wq", here, torch.uint8, (N, K // 2))
-    sc = _take(scales, "scales", here, bf16, (groups, N))
-    z = None if zeros is None else _take(zeros, "zeros", here, torch.uint8, (groups, N))
-    bi = None if bias is None else _take(bias, "bias", here, bf16, (N,))
-    a = b = _ws = ws = None
-    r = ws_bytes = 0
-    if A is not None or B is not None:
-        if A is None or B is None:
-            raise ValueError("A and B must both be given or both be None")
-        r = A.shape[0]
-        a = _take(A, "A", here, bf16, (r, K))
-        b = _take(B, "B", here, bf16, (N, r))
-        _ws, ws, ws_bytes = _scratch(workspace, here, X, lynx_linear_w4_workspace_bytes(M, N, K, r), stream)
-    Y, y = _out(Y, "Y", here, X, bf16, (M, N), stream)
-    _check(library().lynx_linear_w4(x, q, sc, z, bi, a, b, M, N, K, r, K // groups, act, y, ws, ws_bytes, s),
-           "lynx_linear_w4")
-    return Y
-
-
-def _ckpt8_shape(q, e):
-    """(M, K, format) of a checkpoint; the dtype of q says which format it is."""
-    import torch
-
-    M, K = _matrix(q, "q")
-    if q.dtype is torch.int8:
-        return M, K, LYNX_CKPT8_INT8
-    if q.dtype is torch.float8_e4m3fn:
-        return M, K, LYNX_CKPT8_E4M3
-    raise TypeError(f"q must be int8 or float8_e4m3fn, got {q.dtype}")
+    return _result(_binding().linear_w4(X, Wq, scales, zeros, bias, A, B, act, Y, workspace, stream),
+                   "lynx_linear_w4")
 
 
 def lynx_ckpt8_exponent_bytes(M, K):
@@ -600,34 +501,15 @@ def lynx_ckpt8_exponent_bytes(M, K):
 def lynx_ckpt8_store(X, format=LYNX_CKPT8_INT8, q=None, e=None, stream=None):
     """The 8-bit checkpoint of X [M,K] bf16: returns (q [M,K] int8 or
     float8_e4m3fn, e [M,K/32] u8)."""
-    import torch
-
-    M, K = _matrix(X, "X")
-    if format not in (LYNX_CKPT8_INT8, LYNX_CKPT8_E4M3):
-        raise LynxError(LYNX_ERR_INVALID_ARG, f"lynx_ckpt8_store (format {format})")
-    here, s = _place(X, "X", stream)
-    x = _take(X, "X", here, torch.bfloat16, (M, K))
-    dtype = torch.int8 if format == LYNX_CKPT8_INT8 else torch.float8_e4m3fn
-    q, qp = _out(q, "q", here, X, dtype, (M, K), stream)
-    e, ep = _out(e, "e", here, X, torch.uint8, (M, K // 32), stream)
-    _check(library().lynx_ckpt8_store(x, M, K, format, qp, ep, s), "lynx_ckpt8_store")
-    return q, e
+    return _result(_binding().ckpt8_store(X, format, q, e, stream), "lynx_ckpt8_store")
 
 
 def lynx_ckpt8_restore(q, e, X=None, stream=None):
-    """The values [M,K] bf16 a checkpoint stands for."""
-    import torch
-
-    M, K, fmt = _ckpt8_shape(q, e)
-    here, s = _place(q, "q", stream)
-    qp = _take(q, "q", here, q.dtype, (M, K))
-    ep = _take(e, "e", here, torch.uint8, (M, K // 32))
-    X, x = _out(X, "X", here, q, torch.bfloat16, (M, K), stream)
-    _check(library().lynx_ckpt8_restore(qp, ep, M, K, fmt, x, s), "lynx_ckpt8_restore")
-    return X
+    """The values [M,K] bf16 a checkpoint stands for (the dtype of q says which
+    format it is)."""
+    return _result(_binding().ckpt8_restore(q, e, X, stream), "lynx_ckpt8_restore")
 
 
-@functools.lru_cache(maxsize=1024)
 def lynx_lora_backward_workspace_bytes(M, N, K, r=64):
     return library().lynx_lora_backward_workspace_bytes(M, N, K, r)
 
@@ -636,30 +518,9 @@ def lynx_lora_backward(dY, q, e, A, B, dA=None, dB=None, dT=None, workspace=None
     """The adapter's gradients from the checkpoint (q, e) of X: returns
     (dA [r,K], dB [N,r], dT [M,r]), bf16, with dT = dY B the gradient of
     T = X A^T (lynx_sparsify_backward takes it)."""
-    import torch
-
-    bf16 = torch.bfloat16
-    M, K, fmt = _ckpt8_shape(q, e)
-    m, N = _matrix(dY, "dY")
-    if m != M:
-        raise ValueError("dY must be [M,N] with the checkpoint's M")
-    r = _matrix(A, "A")[0]
-    here, s = _place(dY, "dY", stream)
-    dy = _take(dY, "dY", here, bf16, (M, N))
-    qp = _take(q, "q", here, q.dtype, (M, K))
-    ep = _take(e, "e", here, torch.uint8, (M, K // 32))
-    a = _take(A, "A", here, bf16, (r, K))
-    b = _take(B, "B", here, bf16, (N, r))
-    dA, da = _out(dA, "dA", here, dY, bf16, (r, K), stream)
-    dB, db = _out(dB, "dB", here, dY, bf16, (N, r), stream)
-    dT, dt = _out(dT, "dT", here, dY, bf16, (M, r), stream)
-    _ws, ws, ws_bytes = _scratch(workspace, here, dY, lynx_lora_backward_workspace_bytes(M, N, K, r), stream)
-    _check(library().lynx_lora_backward(dy, qp, ep, a, b, M, N, K, r, fmt, da, db, dt, ws, ws_bytes, s),
-           "lynx_lora_backward")
-    return dA, dB, dT
+    return _result(_binding().lora_backward(dY, q, e, A, B, dA, dB, dT, workspace, stream), "lynx_lora_backward")
 
 
-@functools.lru_cache(maxsize=1024)
 def lynx_sparsify_backward_workspace_bytes(M, K):
     return library().lynx_sparsify_backward_workspace_bytes(M, K)
 
@@ -667,27 +528,7 @@ def lynx_sparsify_backward_workspace_bytes(M, K):
 def lynx_sparsify_backward(G, q, e, dT=None, A=None, dX=None, workspace=None, stream=None):
     """dX [M,K] from G, the gradient of S(X), at the checkpoint (q, e) of X, plus
     the LoRA branch's dT A (see include/lynx.h).  Returns dX."""
-    import torch
-
-    bf16 = torch.bfloat16
-    M, K, fmt = _ckpt8_shape(q, e)
-    here, s = _place(G, "G", stream)
-    g = _take(G, "G", here, bf16, (M, K))
-    qp = _take(q, "q", here, q.dtype, (M, K))
-    ep = _take(e, "e", here, torch.uint8, (M, K // 32))
-    dt = a = None
-    r = 0
-    if dT is not None or A is not None:
-        if dT is None or A is None:
-            raise ValueError("dT and A must both be given or both be None")
-        r = _matrix(A, "A")[0]
-        a = _take(A, "A", here, bf16, (r, K))
-        dt = _take(dT, "dT", here, bf16, (M, r))
-    dX, dx = _out(dX, "dX", here, G, bf16, (M, K), stream)
-    _ws, ws, ws_bytes = _scratch(workspace, here, G, lynx_sparsify_backward_workspace_bytes(M, K), stream)
-    _check(library().lynx_sparsify_backward(g, qp, ep, dt, a, M, K, r, fmt, dx, ws, ws_bytes, s),
-           "lynx_sparsify_backward")
-    return dX
+    return _result(_binding().sparsify_backward(G, q, e, dT, A, dX, workspace, stream), "lynx_sparsify_backward")
 
 
 def lynx_check_error(stream=None):
