@@ -10,17 +10,22 @@
 //   the row product  U[rows, r] += S P      (P [cols, r])
 //   the col product  V[cols, r] += S^T Q    (Q [rows, r])
 //
-// T is a row product of x with P = A^T, dT and dB are the row and the column
-// product of one pass over dY (P = B, Q = T), dA^T a column product of x with
-// Q = dT.  The same tile serves as a K-major and as an MN-major operand of
-// tcgen05.mma; the accumulators (one U, one V per 128 columns) stay in TMEM.
+// in three modes: T is the row product of x with P = A^T (kDown), dT and dB are
+// both products of one pass over dY with P = B and Q = T (kBoth), dA^T the col
+// product of x with Q = dT (kUp).  The same tile serves as a K-major and as an
+// MN-major operand of tcgen05.mma.
 //
-// A CTA has a range of 128-row blocks and a range of 128-column blocks.  P of its
-// columns stays in shared memory, U leaves after each row block and V at the end,
-// as fp32 partial sums per range, which reduce_kernel adds in the order of the
-// ranges and rounds: no atomics, the order is the shape's.  Partial sums lie as
-// [block][column of r][128]: a TMEM lane is a row, so a warp stores 128 bytes at a
-// time (with rows of r floats the 4608 x 12288 pass spent 14 of 41 us storing).
+// A block has some inner blocks of 128 (rows for kDown, else columns), whose
+// accumulators stay in TMEM, and walks a range of outer ones, whose operand (P of
+// the columns, or Q of the rows) streams beside the tiles.  The outer ranges of the
+// same inner blocks are a cluster's blocks: they add their accumulators through
+// distributed shared memory, in the order of the ranks, and write the rounded
+// result.  Only where one cluster is too few for the length (few inner blocks),
+// groups of clusters leave fp32 sums that reduce_kernel adds.  kBoth's U leaves
+// after each row block, as fp32 sums per column range for reduce_kernel.  No
+// atomics: the order is the shape's.  fp32 sums lie as [block][column of r][128]: a
+// TMEM lane is a row, so a warp stores 128 bytes at a time (with rows of r floats
+// the 4608 x 12288 pass spent 14 of 41 us storing).
 #include "lynx_ckpt8.cuh"
 #include "lynx_internal.h"
 #include "lynx_ptx.cuh"
@@ -31,32 +36,36 @@ namespace {
 
 constexpr int kSrcBf16 = 2;  // beside kCkpt8Int8 and kCkpt8E4M3
 
+enum PassMode : int { kDown, kBoth, kUp };
+
 constexpr uint32_t kBox = 16384;        // 128 rows x 64 bf16, 128B swizzle
 constexpr uint32_t kTileBytes = 2 * kBox;  // an S tile: two boxes of 64 columns
 constexpr int kMaxStages = 6;
 constexpr int kConvWarps = 16;
 constexpr int kAhead = 3;                // 8-bit tiles in flight
 constexpr uint32_t kRawBytes = 16384;    // one of them
+constexpr int kMaxRanks = 6;
 constexpr uint32_t kSmemMost = 227 * 1024 - 1024;  // leaves the static part 1 KB
-constexpr int kPlanSms = 148;           // B200; the plan (and the workspace) go by the shape alone
 
 struct PassPlan {
-  int nb;        // column blocks of a CTA
-  int rpr;       // row blocks of a CTA
-  int n_cr, n_rr;  // ranges
-  int stages, q_bufs, u_bufs;
+  int inner;             // inner blocks of a block
+  int outer;             // outer blocks of a block
+  int n_inner;           // ranges of inner blocks
+  int ranks, groups;     // outer ranges: blocks of a cluster, clusters
+  int stages, op_bufs, u_bufs;
   uint32_t tmem_cols;
   uint32_t smem;
 };
 
 struct PassLaunch {
-  CUtensorMap tm_s;  // dY [R,C] bf16, box 64 x 128 (bf16 source)
-  CUtensorMap tm_p;  // B [C,r], box 64 x 128; or A [r,C], box 64 x r (8-bit source)
-  CUtensorMap tm_q;  // Q [R,r], box 64 x 128
+  CUtensorMap tm_s;   // kBoth: dY [R,C], box 64 x 128
+  CUtensorMap tm_p;   // kBoth: B [C,r], box 64 x 128
+  CUtensorMap tm_op;  // the streamed operand: A [r,C], box 64 x r (kDown); Q [R,r], box 64 x 128
   const uint8_t* q8;
   const uint8_t* e8;
-  float* u_part;  // [n_cr][row blocks][r][128]
-  float* v_part;  // [n_rr][column blocks][r][128]
+  float* u_part;       // kBoth: [n_inner][row blocks][r][128]
+  float* part;         // groups > 1: [groups][inner blocks][r][128]
+  __nv_bfloat16* out;  // groups == 1: [inner rows][r], kUp: [r][inner rows]
   int64_t R, C;
   int r;
   PassPlan plan;
@@ -66,7 +75,7 @@ struct PassLaunch {
 
 struct PassBars {
   uint64_t full[kMaxStages], empty[kMaxStages];
-  uint64_t p_full, q_full[2], q_empty[2], u_full[2], u_empty[2], done;
+  uint64_t p_full, op_full[2], op_empty[2], u_full[2], u_empty[2], done;
   uint32_t tmem_base;
   volatile uint32_t abort_flag;
 };
@@ -80,37 +89,38 @@ __device__ __forceinline__ bool pass_wait(PassBars& b, uint64_t* bar, uint32_t p
   return false;
 }
 
+// TMA producer, MMA issuer, 4 epilogue warps, and the warps that widen 8-bit tiles
 template <int SRC>
-constexpr int pass_threads() {
-  // TMA producer, MMA issuer, 4 epilogue warps, and the warps that widen 8-bit tiles
-  return 32 * (6 + (SRC == kSrcBf16 ? 0 : kConvWarps));
-}
+constexpr int kPassThreads = 32 * (6 + (SRC == kSrcBf16 ? 0 : kConvWarps));
 
-template <int SRC, bool ROW, bool COL>
-__global__ void __launch_bounds__(pass_threads<SRC>(), 1) adapter_pass_kernel(const __grid_constant__ PassLaunch p) {
+template <int SRC, int MODE>
+__global__ void __launch_bounds__(kPassThreads<SRC>, 1) adapter_pass_kernel(const __grid_constant__ PassLaunch p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ PassBars bars;
-  uint8_t* const sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                                 ~static_cast<uintptr_t>(1023));
+  uint8_t* const sm = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);
   const uint32_t warp = warp_id_sync();
   const uint32_t lane = lane_id();
   const int r = p.r;
   const uint32_t r_boxes = static_cast<uint32_t>((r + 63) / 64);   // 64-column boxes of an [*, r] operand
   const uint32_t r_cols = static_cast<uint32_t>((r + 31) / 32) * 32;  // TMEM columns of an accumulator
-  const int nb = p.plan.nb, stages = p.plan.stages;
-  const int cr = static_cast<int>(blockIdx.x % p.plan.n_cr), rr = static_cast<int>(blockIdx.x / p.plan.n_cr);
-  const int cb0 = cr * nb;
-  const int ncb = min(nb, static_cast<int>((p.C + 127) / 128) - cb0);
-  const int rb0 = rr * p.plan.rpr;
-  const int nrb = min(p.plan.rpr, static_cast<int>((p.R + 127) / 128) - rb0);
+  const int stages = p.plan.stages;
+  const int row_blocks = static_cast<int>((p.R + 127) / 128), col_blocks = static_cast<int>((p.C + 127) / 128);
+  const int inner_blocks = MODE == kDown ? row_blocks : col_blocks, outer_blocks = MODE == kDown ? col_blocks : row_blocks;
+  const uint32_t rank = cluster_ctarank();
+  const int ranks = p.plan.ranks;
+  const int cluster = static_cast<int>(blockIdx.x) / ranks;
+  const int group = cluster % p.plan.groups, range = cluster / p.plan.groups;
+  const int i0 = range * p.plan.inner;
+  const int ni = min(p.plan.inner, inner_blocks - i0);
+  const int o0 = (group * ranks + static_cast<int>(rank)) * p.plan.outer;
+  const int no = max(0, min(p.plan.outer, outer_blocks - o0));
 
-  // shared memory: P | Q buffers | S stages | 8-bit tiles
-  constexpr bool kPKmajor = SRC != kSrcBf16;
-  const uint32_t p_block = kPKmajor ? 256u * static_cast<uint32_t>(r) : r_boxes * kBox;
-  const uint32_t q_bytes = r_boxes * kBox;
+  // shared memory: P (kBoth) | streamed operand | S stages | 8-bit tiles
+  const uint32_t p_block = r_boxes * kBox;
+  const uint32_t op_bytes = MODE == kDown ? 256u * static_cast<uint32_t>(r) : r_boxes * kBox;
   uint8_t* const sm_p = sm;
-  uint8_t* const sm_q = sm_p + (ROW ? static_cast<uint32_t>(nb) * p_block : 0u);
-  uint8_t* const sm_s = sm_q + (COL ? static_cast<uint32_t>(p.plan.q_bufs) * q_bytes : 0u);
+  uint8_t* const sm_op = sm_p + (MODE == kBoth ? static_cast<uint32_t>(p.plan.inner) * p_block : 0u);
+  uint8_t* const sm_s = sm_op + static_cast<uint32_t>(p.plan.op_bufs) * op_bytes;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
@@ -119,8 +129,8 @@ __global__ void __launch_bounds__(pass_threads<SRC>(), 1) adapter_pass_kernel(co
     }
     mbar_init(&bars.p_full, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars.q_full[i], 1);
-      mbar_init(&bars.q_empty[i], 1);
+      mbar_init(&bars.op_full[i], 1);
+      mbar_init(&bars.op_empty[i], 1);
       mbar_init(&bars.u_full[i], 1);
       mbar_init(&bars.u_empty[i], 4);
     }
@@ -137,56 +147,56 @@ __global__ void __launch_bounds__(pass_threads<SRC>(), 1) adapter_pass_kernel(co
   tc_fence_after();
   pdl_wait();
 
+  // one block a cluster and several groups: its sums are one of the partial sums
+  const bool alone = ranks == 1 && p.plan.groups > 1;
+  const uint32_t t_acc = bars.tmem_base;  // the inner blocks' accumulators, then U
+  const uint32_t t_u = t_acc + static_cast<uint32_t>(p.plan.inner) * r_cols;
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0 && !p.stall_test) {
       bool ok = true;
-      if (ROW) {
-        tma_prefetch_desc(&p.tm_p);
-        mbar_arrive_expect_tx(&bars.p_full, static_cast<uint32_t>(ncb) * p_block);
-        for (int cb = 0; cb < ncb; ++cb) {
-          uint8_t* dst = sm_p + static_cast<uint32_t>(cb) * p_block;
-          const int32_t c0 = (cb0 + cb) * 128;
-          if constexpr (kPKmajor) {
-            for (int j = 0; j < 2; ++j)
-              tma_load_2d(dst + static_cast<uint32_t>(j) * (p_block / 2), &p.tm_p, &bars.p_full, c0 + 64 * j, 0);
-          } else {
-            for (uint32_t b = 0; b < r_boxes; ++b)
-              tma_load_2d(dst + b * kBox, &p.tm_p, &bars.p_full, static_cast<int32_t>(64 * b), c0);
-          }
-        }
-      }
-      uint32_t g = 0;
-      int q_issued = 0;
-      for (int rb = 0; ok && rb < nrb; ++rb) {
-        const int32_t row0 = (rb0 + rb) * 128;
-        if (COL) {
-          const int qb = rb % p.plan.q_bufs;
-          ok = pass_wait(bars, &bars.q_empty[qb], ((rb / p.plan.q_bufs) & 1) ^ 1, p.status, kDevTimeoutEmpty);
-          if (!ok) break;
-          mbar_arrive_expect_tx(&bars.q_full[qb], q_bytes);
+      if constexpr (MODE == kBoth) {
+        mbar_arrive_expect_tx(&bars.p_full, static_cast<uint32_t>(ni) * p_block);
+        for (int i = 0; i < ni; ++i)
           for (uint32_t b = 0; b < r_boxes; ++b)
-            tma_load_2d(sm_q + static_cast<uint32_t>(qb) * q_bytes + b * kBox, &p.tm_q, &bars.q_full[qb],
-                        static_cast<int32_t>(64 * b), row0);
-          q_issued = rb + 1;
+            tma_load_2d(sm_p + static_cast<uint32_t>(i) * p_block + b * kBox, &p.tm_p, &bars.p_full,
+                        static_cast<int32_t>(64 * b), (i0 + i) * 128);
+      }
+      const uint64_t once = l2_evict_first();  // dY is read once: leave L2 to the sums
+      uint32_t g = 0;
+      int issued = 0;
+      for (int o = 0; ok && o < no; ++o) {
+        const int buf = o % p.plan.op_bufs;
+        ok = pass_wait(bars, &bars.op_empty[buf], ((o / p.plan.op_bufs) & 1) ^ 1, p.status, kDevTimeoutEmpty);
+        if (!ok) break;
+        const int32_t at = (o0 + o) * 128;
+        uint8_t* dst = sm_op + static_cast<uint32_t>(buf) * op_bytes;
+        mbar_arrive_expect_tx(&bars.op_full[buf], op_bytes);
+        if constexpr (MODE == kDown) {
+          for (int j = 0; j < 2; ++j)
+            tma_load_2d(dst + static_cast<uint32_t>(j) * (op_bytes / 2), &p.tm_op, &bars.op_full[buf], at + 64 * j, 0);
+        } else {
+          for (uint32_t b = 0; b < r_boxes; ++b)
+            tma_load_2d(dst + b * kBox, &p.tm_op, &bars.op_full[buf], static_cast<int32_t>(64 * b), at);
         }
+        issued = o + 1;
         if constexpr (SRC == kSrcBf16) {
-          for (int cb = 0; cb < ncb; ++cb, ++g) {
+          for (int i = 0; i < ni; ++i, ++g) {
             const uint32_t slot = g % stages;
             ok = pass_wait(bars, &bars.empty[slot], ((g / stages) & 1u) ^ 1u, p.status, kDevTimeoutEmpty);
             if (!ok) break;
-            uint8_t* dst = sm_s + slot * kTileBytes;
+            uint8_t* tile = sm_s + slot * kTileBytes;
             mbar_arrive_expect_tx(&bars.full[slot], kTileBytes);
-            tma_load_2d(dst, &p.tm_s, &bars.full[slot], (cb0 + cb) * 128, row0);
-            tma_load_2d(dst + kBox, &p.tm_s, &bars.full[slot], (cb0 + cb) * 128 + 64, row0);
+            tma_load_2d_once(tile, &p.tm_s, &bars.full[slot], (i0 + i) * 128, at, once);
+            tma_load_2d_once(tile + kBox, &p.tm_s, &bars.full[slot], (i0 + i) * 128 + 64, at, once);
           }
         }
       }
       // the last fill of every buffer must have landed before the block exits
       bool drained = true;
-      if (ROW) drained = mbar_wait(&bars.p_full, 0, kWaitLimitNs / 4);
-      for (int x = q_issued - 1; x >= 0 && x >= q_issued - p.plan.q_bufs; --x)
-        drained &= mbar_wait(&bars.q_full[x % p.plan.q_bufs], (x / p.plan.q_bufs) & 1, kWaitLimitNs / 4);
+      if (MODE == kBoth) drained = mbar_wait(&bars.p_full, 0, kWaitLimitNs / 4);
+      for (int x = issued - 1; x >= 0 && x >= issued - p.plan.op_bufs; --x)
+        drained &= mbar_wait(&bars.op_full[x % p.plan.op_bufs], (x / p.plan.op_bufs) & 1, kWaitLimitNs / 4);
       for (uint32_t b = g; b > 0 && b + stages > g; --b)
         drained &= mbar_wait(&bars.full[(b - 1) % stages], ((b - 1) / stages) & 1u, kWaitLimitNs / 4);
       if (!drained) record_error(p.status, kDevTimeoutDrain);
@@ -196,45 +206,45 @@ __global__ void __launch_bounds__(pass_threads<SRC>(), 1) adapter_pass_kernel(co
     // The whole warp walks the loop and one elected lane issues, so that the
     // descriptors stay in warp-uniform registers (issued by a lone lane, a tile's
     // 16 MMAs took 1400 cycles, more than the tile's bytes).
-    const uint32_t idesc_row = make_idesc_bf16(128, r, false) | (kPKmajor ? 0u : kIdescBMnMajor);
+    constexpr bool kRow = MODE != kUp, kCol = MODE != kDown;
+    const uint32_t idesc_row = make_idesc_bf16(128, r, false) | (MODE == kDown ? 0u : kIdescBMnMajor);
     const uint32_t idesc_col = make_idesc_bf16(128, r, false) | kIdescAMnMajor | kIdescBMnMajor;
-    const uint32_t t_u = bars.tmem_base;
-    const uint32_t t_v = t_u + (ROW ? static_cast<uint32_t>(p.plan.u_bufs) * r_cols : 0u);
     auto arrived = [&](uint64_t* bar, uint32_t parity, uint32_t code) {
       return __all_sync(0xffffffffu, pass_wait(bars, bar, parity, p.status, code)) != 0;
     };
-    bool ok = !ROW || arrived(&bars.p_full, 0, kDevTimeoutFull);
+    bool ok = MODE != kBoth || arrived(&bars.p_full, 0, kDevTimeoutFull);
     uint32_t slot = 0, phase = 0;
-    for (int rb = 0; ok && rb < nrb; ++rb) {
-      const int qb = COL ? rb % p.plan.q_bufs : 0, ub = ROW ? rb % p.plan.u_bufs : 0;
-      if (COL) ok = arrived(&bars.q_full[qb], (rb / p.plan.q_bufs) & 1, kDevTimeoutFull);
-      if (ok && ROW) ok = arrived(&bars.u_empty[ub], ((rb / p.plan.u_bufs) & 1) ^ 1, kDevTimeoutAccum);
+    for (int o = 0; ok && o < no; ++o) {
+      const int buf = o % p.plan.op_bufs, ub = MODE == kBoth ? o % p.plan.u_bufs : 0;
+      ok = arrived(&bars.op_full[buf], (o / p.plan.op_bufs) & 1, kDevTimeoutFull);
+      if (ok && MODE == kBoth) ok = arrived(&bars.u_empty[ub], ((o / p.plan.u_bufs) & 1) ^ 1, kDevTimeoutAccum);
       if (!ok) break;
-      const uint32_t sq = smem_u32(sm_q) + static_cast<uint32_t>(qb) * q_bytes;
-      const uint32_t d_u = t_u + static_cast<uint32_t>(ub) * r_cols;
-      for (int cb = 0; cb < ncb; ++cb) {
+      const uint32_t sop = smem_u32(sm_op) + static_cast<uint32_t>(buf) * op_bytes;
+      for (int i = 0; i < ni; ++i) {
         ok = arrived(&bars.full[slot], phase, kDevTimeoutFull);
         if (!ok) break;
         tc_fence_after();
         const uint32_t ss = smem_u32(sm_s) + slot * kTileBytes;
-        if constexpr (ROW) {  // 16 columns of S a step
-          const uint32_t sp = smem_u32(sm_p) + static_cast<uint32_t>(cb) * p_block;
+        const uint32_t d_inner = t_acc + static_cast<uint32_t>(i) * r_cols;
+        if constexpr (kRow) {  // 16 columns of S a step
+          const uint32_t d_row = MODE == kDown ? d_inner : t_u + static_cast<uint32_t>(ub) * r_cols;
+          const uint32_t sp = smem_u32(sm_p) + static_cast<uint32_t>(i) * p_block;
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const uint64_t da = make_sdesc(ss + (k / 4) * kBox + (k % 4) * 32, 16, 1024, kSw128);
-            const uint64_t db = kPKmajor ? make_sdesc(sp + (k / 4) * (p_block / 2) + (k % 4) * 32, 16, 1024, kSw128)
-                                         : make_sdesc(sp + k * 2048, kBox, 1024, kSw128);
-            if (elect_one()) mma_bf16(d_u, da, db, idesc_row, (cb | k) != 0);
+            const uint64_t db = MODE == kDown
+                                    ? make_sdesc(sop + (k / 4) * (op_bytes / 2) + (k % 4) * 32, 16, 1024, kSw128)
+                                    : make_sdesc(sp + k * 2048, kBox, 1024, kSw128);
+            if (elect_one()) mma_bf16(d_row, da, db, idesc_row, ((MODE == kDown ? o : i) | k) != 0);
             __syncwarp();
           }
         }
-        if constexpr (COL) {  // 16 rows of S a step
-          const uint32_t d_v = t_v + static_cast<uint32_t>(cb) * r_cols;
+        if constexpr (kCol) {  // 16 rows of S a step
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const uint64_t da = make_sdesc(ss + k * 2048, kBox, 1024, kSw128);
-            const uint64_t db = make_sdesc(sq + k * 2048, kBox, 1024, kSw128);
-            if (elect_one()) mma_bf16(d_v, da, db, idesc_col, (rb | k) != 0);
+            const uint64_t db = make_sdesc(sop + k * 2048, kBox, 1024, kSw128);
+            if (elect_one()) mma_bf16(d_inner, da, db, idesc_col, (o | k) != 0);
             __syncwarp();
           }
         }
@@ -244,8 +254,8 @@ __global__ void __launch_bounds__(pass_threads<SRC>(), 1) adapter_pass_kernel(co
       }
       if (!ok) break;
       if (elect_one()) {
-        if (COL) tc_commit(&bars.q_empty[qb]);
-        if (ROW) tc_commit(&bars.u_full[ub]);
+        tc_commit(&bars.op_empty[buf]);
+        if (MODE == kBoth) tc_commit(&bars.u_full[ub]);
       }
       __syncwarp();
     }
@@ -254,107 +264,117 @@ __global__ void __launch_bounds__(pass_threads<SRC>(), 1) adapter_pass_kernel(co
     if (!mbar_wait(&bars.done, 0) && lane == 0) record_error(p.status, kDevTimeoutDrain);
     __syncwarp();
   } else if (warp < 6) {
-    // ------------------------------------------------------------ epilogue: partial sums out
+    // ------------------------------------------------------------ accumulators out
     const uint32_t quarter = warp & 3u;  // the TMEM lanes this warp may read
     const uint32_t t_lane = (32u * quarter) << 16;
     bool ok = true;
-    auto store = [&](uint32_t taddr, float* part, int64_t block) {
-      float* dst = part + block * r * 128 + 32 * quarter + lane;
+    // 16 columns at a time to dst[column][128]
+    auto store = [&](uint32_t taddr, float* dst) {
       for (int c = 0; c < r; c += 16) {
         uint32_t v[16];
         tmem_ld_32x32b_x16(taddr + t_lane + static_cast<uint32_t>(c), v);
         tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) dst[(c + i) * 128] = __uint_as_float(v[i]);
+        for (int i = 0; i < 16; ++i) dst[(c + i) * 128 + 32 * quarter + lane] = __uint_as_float(v[i]);
       }
     };
-    if constexpr (ROW) {
-      for (int rb = 0; rb < nrb; ++rb) {
-        const int ub = rb % p.plan.u_bufs;
-        ok = pass_wait(bars, &bars.u_full[ub], (rb / p.plan.u_bufs) & 1, p.status, kDevTimeoutAccum);
+    if constexpr (MODE == kBoth) {
+      for (int o = 0; o < no; ++o) {
+        const int ub = o % p.plan.u_bufs;
+        ok = pass_wait(bars, &bars.u_full[ub], (o / p.plan.u_bufs) & 1, p.status, kDevTimeoutAccum);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        store(bars.tmem_base + static_cast<uint32_t>(ub) * r_cols, p.u_part, cr * ((p.R + 127) / 128) + rb0 + rb);
+        store(t_u + static_cast<uint32_t>(ub) * r_cols,
+              p.u_part + (static_cast<int64_t>(range) * row_blocks + o0 + o) * r * 128);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.u_empty[ub]);
       }
     }
-    if constexpr (COL) {
-      ok = ok && pass_wait(bars, &bars.done, 0, p.status, kDevTimeoutAccum);
-      ok = __all_sync(0xffffffffu, ok && !bars.abort_flag);
-      if (ok) {
-        tc_fence_after();
-        const uint32_t t_v = bars.tmem_base + (ROW ? static_cast<uint32_t>(p.plan.u_bufs) * r_cols : 0u);
-        for (int cb = 0; cb < ncb; ++cb)
-          store(t_v + static_cast<uint32_t>(cb) * r_cols, p.v_part, rr * ((p.C + 127) / 128) + cb0 + cb);
-        tc_fence_before();
+    // every MMA is done: the block's sums go out, or take the place of the operands
+    ok = ok && pass_wait(bars, &bars.done, 0, p.status, kDevTimeoutAccum);
+    ok = __all_sync(0xffffffffu, ok && !bars.abort_flag);
+    if (ok) {
+      tc_fence_after();
+      float* dst = alone ? p.part + (static_cast<int64_t>(group) * inner_blocks + i0) * r * 128
+                         : reinterpret_cast<float*>(sm);
+      if (no > 0) {
+        for (int i = 0; i < ni; ++i) store(t_acc + static_cast<uint32_t>(i) * r_cols, dst + i * r * 128);
+      } else {  // no outer block for this rank
+        for (int i = static_cast<int>(threadIdx.x) - 64; i < ni * r * 128; i += 128) dst[i] = 0.f;
       }
+      tc_fence_before();
     }
   } else if constexpr (SRC != kSrcBf16) {
     // ------------------------------------------------------------ 8 bits -> bf16 tiles
     // 16 bytes (half a block) a step: 8 lanes cover a row of the tile, a thread
-    // takes rows t / 8 + kRowStep i.  The bytes arrive by cp.async in slots that
+    // takes every kRowStep-th row.  4 lanes have one row's half and the next 4 the
+    // row below's, whose swizzled units are the other banks.  The bytes arrive by cp.async in slots that
     // only this thread reads, kAhead tiles before they are needed; the exponents
     // (one byte per 32) come through registers, two tiles ahead.
     constexpr int kSteps = 4 * 8 / kConvWarps;
     constexpr int kRowStep = 4 * kConvWarps;
     const uint32_t t = threadIdx.x - 192u;
-    const uint32_t chunk = t & 7u;
-    const uint32_t row_t = t >> 3;
-    const int tiles = p.stall_test ? 0 : nrb * ncb;
-    const int64_t row0 = static_cast<int64_t>(rb0) * 128 + row_t;
-    const int rows0 = static_cast<int>(p.R - row0);                                      // rows left at the first tile
-    const int cols0 = static_cast<int>(p.C - static_cast<int64_t>(cb0) * 128) - 16 * static_cast<int>(chunk);
+    const uint32_t chunk = (t & 3u) | ((t >> 1) & 4u);
+    const uint32_t row_t = ((t >> 2) & 1u) | ((t >> 4) << 1);
+    const int tiles = p.stall_test ? 0 : no * ni;
+    // The walk over the tiles, inner blocks first: offsets of the next inner block
+    // and, from the last one, of the next outer block's first
+    const int64_t row0 = static_cast<int64_t>(MODE == kDown ? i0 : o0) * 128 + row_t;
+    const int64_t col0 = static_cast<int64_t>(MODE == kDown ? o0 : i0) * 128;
     const int64_t e_pitch = p.C / 32;
-    // This thread's place in the tile that is asked for next, bytes and exponents:
-    // tiles are taken along the columns, then down
-    const uint8_t* q_at = p.q8 + row0 * p.C + static_cast<int64_t>(cb0) * 128 + 16 * chunk;
-    const uint8_t* e_at = p.e8 + row0 * e_pitch + static_cast<int64_t>(cb0) * 4 + chunk / 2;
-    const int64_t q_down = 128 * p.C - 128 * (ncb - 1), e_down = 128 * e_pitch - 4 * (ncb - 1);
-    int q_cb = 0, q_rows = rows0, q_left = tiles, e_cb = 0, e_rows = rows0, e_left = tiles;
+    const int64_t q_row = 128 * p.C, e_row = 128 * e_pitch;
+    const int64_t q_inner = MODE == kDown ? q_row : 128, e_inner = MODE == kDown ? e_row : 4;
+    const int64_t q_outer = (MODE == kDown ? 128 : q_row) - q_inner * (ni - 1);
+    const int64_t e_outer = (MODE == kDown ? 4 : e_row) - e_inner * (ni - 1);
+    struct Walk {
+      int rows, cols;  // rows from this thread's first one on, columns from its first one on
+      int i, left;     // inner block, tiles left
+    };
+    Walk wq = {static_cast<int>(p.R - row0), static_cast<int>(p.C - col0) - 16 * static_cast<int>(chunk), 0, tiles};
+    Walk we = wq;
+    auto advance = [&](Walk& w) {
+      --w.left;
+      const bool next_outer = ++w.i == ni;
+      if (next_outer) w.i = 0;
+      if constexpr (MODE == kDown) {
+        w.rows += next_outer ? 128 * (ni - 1) : -128;
+        if (next_outer) w.cols -= 128;
+      } else {
+        w.cols += next_outer ? 128 * (ni - 1) : -128;
+        if (next_outer) w.rows -= 128;
+      }
+      return next_outer;
+    };
+    const uint8_t* q_at = p.q8 + row0 * p.C + col0 + 16 * chunk;
+    const uint8_t* e_at = p.e8 + row0 * e_pitch + col0 / 32 + chunk / 2;
     const uint32_t raw = smem_u32(sm_s) + static_cast<uint32_t>(stages) * kTileBytes + 16u * t;
     uint32_t fetch_at = 0, take_at = 0;  // byte offsets of the slots
     auto fetch = [&]() {
-      if (q_left > 0) {
-        const bool col_in = 128 * q_cb < cols0;
+      if (wq.left > 0) {
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
-          const bool in = col_in && kRowStep * i < q_rows;
+          const bool in = wq.cols > 0 && kRowStep * i < wq.rows;
           cp_async_16(raw + fetch_at + (kRawBytes / kSteps) * i, in ? q_at + i * kRowStep * p.C : p.q8, in ? 16u : 0u);
         }
-        --q_left;
-        if (++q_cb < ncb) {
-          q_at += 128;
-        } else {
-          q_cb = 0;
-          q_at += q_down;
-          q_rows -= 128;
-        }
+        q_at += advance(wq) ? q_outer : q_inner;
         fetch_at = fetch_at == kAhead * kRawBytes ? 0u : fetch_at + kRawBytes;
       }
       cp_async_commit();
     };
     auto exponents = [&](uint32_t (&ex)[kSteps]) {
-      if (e_left > 0) {
-        const bool col_in = 128 * e_cb < cols0;
+      if (we.left > 0) {
 #pragma unroll
         for (int i = 0; i < kSteps; ++i)
-          ex[i] = col_in && kRowStep * i < e_rows ? __ldg(e_at + i * kRowStep * e_pitch) : 0u;
-        --e_left;
-        if (++e_cb < ncb) {
-          e_at += 4;
-        } else {
-          e_cb = 0;
-          e_at += e_down;
-          e_rows -= 128;
-        }
+          ex[i] = we.cols > 0 && kRowStep * i < we.rows ? __ldg(e_at + i * kRowStep * e_pitch) : 0u;
+        e_at += advance(we) ? e_outer : e_inner;
       }
     };
     const uint32_t x = row_t & 7u, u = (chunk & 3u) * 2u;  // kRowStep is a multiple of 8
     const uint32_t line = smem_u32(sm_s) + (chunk >> 2) * kBox + row_t * 128u;
     const uint32_t line0 = line + ((u ^ x) << 4), line1 = line + (((u + 1u) ^ x) << 4);
+    const Ckpt8Widen<SRC> to_bf16;
     uint32_t slot = 0, phase = 1;
     bool ok = true;
     auto widen = [&](const uint32_t (&ex)[kSteps]) {
@@ -364,10 +384,10 @@ __global__ void __launch_bounds__(pass_threads<SRC>(), 1) adapter_pass_kernel(co
       for (int i = 0; i < kSteps; ++i) {
         const uint32_t f = ckpt8_factor_bits<SRC>(ex[i]);
         const uint4 w = ld_shared_v4(raw + take_at + (kRawBytes / kSteps) * i);
-        out[i][0] = ckpt8_widen4<SRC>(w.x, f);
-        out[i][1] = ckpt8_widen4<SRC>(w.y, f);
-        out[i][2] = ckpt8_widen4<SRC>(w.z, f);
-        out[i][3] = ckpt8_widen4<SRC>(w.w, f);
+        out[i][0] = to_bf16(w.x, f);
+        out[i][1] = to_bf16(w.y, f);
+        out[i][2] = to_bf16(w.z, f);
+        out[i][3] = to_bf16(w.w, f);
       }
       take_at = take_at == kAhead * kRawBytes ? 0u : take_at + kRawBytes;
       fetch();
@@ -402,11 +422,68 @@ __global__ void __launch_bounds__(pass_threads<SRC>(), 1) adapter_pass_kernel(co
     cp_async_wait<0>();
   }
 
-  __syncthreads();
+  // ------------------------------------------------------------ the cluster's sums
+  __syncwarp();
+  tc_fence_before();
+  if (ranks == 1)
+    __syncthreads();
+  else
+    cluster_sync_all();
+  if (!alone && !bars.abort_flag) {
+    const uint32_t red = smem_u32(sm);
+    const int64_t inner_rows = MODE == kDown ? p.R : p.C;
+    // 4 rows of one column a lane; the columns of the inner blocks dealt out to the
+    // ranks' warps
+    auto column_sum = [&](int column) {
+      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int q = 0; q < kMaxRanks; ++q) {
+        if (q < ranks) {
+          const float4 v = ld_cluster_f32x4(mapa_shared(red + (column * 128 + 4 * lane) * 4, q));
+          s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+        }
+      }
+      return s;
+    };
+    const int ways = ranks * (kPassThreads<SRC> / 32), way = static_cast<int>(rank) * (kPassThreads<SRC> / 32) + warp;
+    if (p.plan.groups > 1) {
+      for (int c = way; c < ni * r; c += ways)
+        *reinterpret_cast<float4*>(p.part + ((static_cast<int64_t>(group) * inner_blocks + i0) * r + c) * 128 + 4 * lane) =
+            column_sum(c);
+    } else if (MODE == kUp) {
+      for (int c = way; c < ni * r; c += ways) {
+        const float4 s = column_sum(c);
+        const int64_t row = static_cast<int64_t>(i0 + c / r) * 128 + 4 * lane;  // inner_rows is a multiple of 64
+        if (row < inner_rows)
+          *reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(c % r) * inner_rows + row) =
+              make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
+      }
+    } else {
+      // 8 columns at a time, so that 4 rows leave as 16 bytes each
+      for (int c = 8 * way; c < ni * r; c += 8 * ways) {
+        float4 s[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] = column_sum(c + j);
+        const int64_t row = static_cast<int64_t>(i0 + c / r) * 128 + 4 * lane;
+        __nv_bfloat16* dst = p.out + row * r + c % r;
+        auto put = [&](int k, float a0, float a1, float a2, float a3, float a4, float a5, float a6, float a7) {
+          if (row + k < inner_rows)
+            *reinterpret_cast<uint4*>(dst + k * r) =
+                make_uint4(pack_bf16(a0, a1), pack_bf16(a2, a3), pack_bf16(a4, a5), pack_bf16(a6, a7));
+        };
+        put(0, s[0].x, s[1].x, s[2].x, s[3].x, s[4].x, s[5].x, s[6].x, s[7].x);
+        put(1, s[0].y, s[1].y, s[2].y, s[3].y, s[4].y, s[5].y, s[6].y, s[7].y);
+        put(2, s[0].z, s[1].z, s[2].z, s[3].z, s[4].z, s[5].z, s[6].z, s[7].z);
+        put(3, s[0].w, s[1].w, s[2].w, s[3].w, s[4].w, s[5].w, s[6].w, s[7].w);
+      }
+    }
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(bars.tmem_base, p.plan.tmem_cols);
   }
+  __syncwarp();
+  if (ranks > 1) cluster_sync_all();  // no block leaves while another reads its sums
 }
 
 // ---------------------------------------------------------------------------
@@ -437,7 +514,7 @@ __global__ void __launch_bounds__(kRedThreads) reduce_kernel(ReduceJob a, Reduce
   const int64_t stride = (j.rows + 127) / 128 * j.r * 128;
   const float* src = j.part + (block * j.r + c0 + warp) * 128 + 4 * lane;
   float4 s0 = make_float4(0.f, 0.f, 0.f, 0.f), s1 = s0;
-#pragma unroll 4
+#pragma unroll 8
   for (int i = 0; i < j.n; ++i) {
     const float4 v = __ldcg(reinterpret_cast<const float4*>(src + i * stride));
     const float4 w = __ldcg(reinterpret_cast<const float4*>(src + i * stride + 8 * 128));
@@ -468,52 +545,75 @@ __global__ void __launch_bounds__(kRedThreads) reduce_kernel(ReduceJob a, Reduce
 // ---------------------------------------------------------------------------
 // host side
 
-// The ranges of one pass.  A CTA's columns are bounded by shared memory (their P
-// stays there) and TMEM (their V); of the column counts that fit, the one with
-// the least of (tiles of the busiest CTA + partial sums written and read back)
-// is taken, both as bytes over the rate they move at.
-PassPlan plan_pass(int64_t R, int64_t C, int r, bool row, bool col, bool eight) {
+// The ranges of one pass: of the inner block counts that shared memory and TMEM
+// hold and of the cluster sizes, the one with the least estimated time.  What it
+// adds up, each measured on the passes themselves: a tile takes 0.7 us to widen, or
+// the time of its bytes at 6.2 TB/s over the blocks at work (0.4 us at least) and
+// 0.2 us, more where U or the streamed operand has one buffer; a cluster's sums cost
+// 3 us and 40 GB/s a block; sums that go through memory are written and read at
+// 8 TB/s, and a reduce_kernel of its own costs 5 us with its launch.
+PassPlan plan_pass(int64_t R, int64_t C, int r, int mode) {
+  const bool eight = mode != kBoth;
   const int64_t rb = (R + 127) / 128, cb = (C + 127) / 128;
-  const uint32_t rp = static_cast<uint32_t>((r + 63) / 64) * 64, rc = static_cast<uint32_t>((r + 31) / 32) * 32;
+  const int64_t inner_blocks = mode == kDown ? rb : cb, outer_blocks = mode == kDown ? cb : rb;
+  const uint32_t boxes = static_cast<uint32_t>((r + 63) / 64), rc = static_cast<uint32_t>((r + 31) / 32) * 32;
   // 1 KB of the dynamic part goes into its alignment
   const uint32_t raw = eight ? (kAhead + 1) * kRawBytes : 0u;
-  const uint32_t p_block = row ? 256u * (eight ? static_cast<uint32_t>(r) : rp) : 0u;
-  const uint32_t q_one = col ? 256u * rp : 0u;
-  const int min_stages = eight ? 2 : 3;
+  const uint32_t p_block = mode == kBoth ? boxes * kBox : 0u;
+  const uint32_t op_one = mode == kDown ? 256u * static_cast<uint32_t>(r) : boxes * kBox;
+  const uint32_t min_stages = eight ? 2 : 3, most_stages = eight ? 3 : kMaxStages;
+  // clusters of 1 to 6 such blocks that a B200 holds at once, less one for the sizes
+  // that depend on which SMs a chip has
+  constexpr int kRoom[kMaxRanks + 1] = {0, 148, 74, 44, 32, 25, 21};
   PassPlan best = {};
   double best_cost = 0;
-  for (int nb = 1; nb <= 16 && nb <= cb; ++nb) {
-    const uint32_t v_cols = col ? nb * rc : 0u;
-    int u_bufs = row ? 2 : 0;
-    if (v_cols + u_bufs * rc > 512) u_bufs = row ? 1 : 0;
-    if (v_cols + u_bufs * rc > 512) break;
-    int q_bufs = col ? 2 : 0;
-    if (nb * p_block + q_bufs * q_one + min_stages * kTileBytes + raw + 1024 > kSmemMost) q_bufs = col ? 1 : 0;
-    if (nb * p_block + q_bufs * q_one + min_stages * kTileBytes + raw + 1024 > kSmemMost) break;
+  for (int inner = 1; inner <= 8 && inner <= inner_blocks; ++inner) {
     PassPlan c = {};
-    c.nb = nb;
-    c.n_cr = static_cast<int>((cb + nb - 1) / nb);
-    int64_t n_rr = kPlanSms / c.n_cr;
-    n_rr = n_rr < 1 ? 1 : (n_rr > rb ? rb : n_rr);
-    c.rpr = static_cast<int>((rb + n_rr - 1) / n_rr);
-    c.n_rr = static_cast<int>((rb + c.rpr - 1) / c.rpr);
-    c.q_bufs = q_bufs;
-    c.u_bufs = u_bufs;
-    uint32_t cols = 32;
-    while (cols < v_cols + u_bufs * rc) cols *= 2;
-    c.tmem_cols = cols;
-    const uint32_t fixed = nb * p_block + q_bufs * q_one + raw;
-    const int stages = static_cast<int>((kSmemMost - 1024 - fixed) / kTileBytes);
-    const int most = eight ? 3 : kMaxStages;
-    c.stages = stages > most ? most : stages;
-    c.smem = fixed + c.stages * kTileBytes + 1024;
-    const double waves = static_cast<double>((static_cast<int64_t>(c.n_cr) * c.n_rr + kPlanSms - 1) / kPlanSms);
-    const double cost = waves * c.rpr * nb * (eight ? 16384.0 : 32768.0) * kPlanSms / 6.0e12 +
-                        2.0 * 4 * r * (row ? static_cast<double>(c.n_cr) * R : 0.0) / 6.0e12 +
-                        2.0 * 4 * r * (col ? static_cast<double>(c.n_rr) * C : 0.0) / 6.0e12;
-    if (best.nb == 0 || cost < best_cost) {
-      best = c;
-      best_cost = cost;
+    c.inner = inner;
+    c.u_bufs = mode == kBoth ? 2 : 0;
+    if (inner * rc + c.u_bufs * rc > 512 && c.u_bufs == 2) c.u_bufs = 1;
+    if (inner * rc + c.u_bufs * rc > 512) break;
+    const uint32_t red = static_cast<uint32_t>(inner * r) * 512u;
+    c.op_bufs = 2;
+    auto fixed = [&]() { return inner * p_block + c.op_bufs * op_one + raw + 1024u; };
+    if (fixed() + min_stages * kTileBytes > kSmemMost) c.op_bufs = 1;
+    if (fixed() + min_stages * kTileBytes > kSmemMost || red + 1024u > kSmemMost) break;
+    const uint32_t fit = (kSmemMost - fixed()) / kTileBytes;
+    c.stages = static_cast<int>(fit < most_stages ? fit : most_stages);
+    c.smem = fixed() + c.stages * kTileBytes;
+    if (c.smem < red + 1024u) c.smem = red + 1024u;
+    c.tmem_cols = 32;
+    while (c.tmem_cols < inner * rc + c.u_bufs * rc) c.tmem_cols *= 2;
+    const int64_t n_inner = (inner_blocks + inner - 1) / inner;
+    c.n_inner = static_cast<int>(n_inner);
+    const double u_cost = mode == kBoth ? 8.0 * r * 128 * static_cast<double>(n_inner * rb) / 8.0e12 : 0.0;
+    // kBoth's sums are too many for a cluster's exchange to pay (17 us at 4608 x 12288)
+    const int most_ranks = mode == kBoth ? 1 : kMaxRanks;
+    for (int ranks = 1; ranks <= most_ranks && ranks <= outer_blocks; ++ranks) {
+      const int64_t fill = kRoom[ranks] / n_inner;  // groups that still fit at once
+      for (int pass = 0; pass < (fill > 1 ? 2 : 1); ++pass) {
+        int64_t groups = pass == 0 ? 1 : fill;
+        const int64_t outer = (outer_blocks + ranks * groups - 1) / (ranks * groups);
+        groups = (outer_blocks + ranks * outer - 1) / (ranks * outer);
+        if (pass == 1 && groups == 1) continue;
+        const int64_t clusters = n_inner * groups;
+        const double waves = static_cast<double>((clusters + kRoom[ranks] - 1) / kRoom[ranks]);
+        const double at_work = static_cast<double>(clusters < kRoom[ranks] ? clusters * ranks : kRoom[ranks] * ranks);
+        const double bytes = (eight ? 16384.0 : 32768.0) * at_work / 6.2e12, least = eight ? 0.7e-6 : 0.4e-6;
+        double tile = (bytes > least ? bytes : least) + (eight ? 0.0 : 0.2e-6);
+        if (mode == kBoth && (c.u_bufs == 1 || c.op_bufs == 1)) tile *= 1.3;
+        double cost = waves * (outer * inner * tile + 1e-6) + u_cost;
+        if (ranks > 1) cost += 3e-6 + inner * r * 512 / 40e9;
+        if (groups > 1)
+          cost += (mode == kBoth ? 0.0 : 5e-6) + 8.0 * r * 128 * static_cast<double>(groups * inner_blocks) / 8.0e12;
+        if (best.inner == 0 || cost < best_cost) {
+          best_cost = cost;
+          best = c;
+          best.ranks = ranks;
+          best.groups = static_cast<int>(groups);
+          best.outer = static_cast<int>(outer);
+        }
+      }
     }
   }
   return best;
@@ -523,38 +623,53 @@ size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 struct LoraPlan {
   PassPlan down, dy, up;  // T; dT and dB; dA
-  size_t t, dt, u, v, total;
+  size_t t, dt, u, part, total;
 };
 
 LoraPlan plan_lora(int64_t M, int64_t N, int64_t K, int r) {
   LoraPlan l;
-  l.down = plan_pass(M, K, r, true, false, true);
-  l.dy = plan_pass(M, N, r, true, true, false);
-  l.up = plan_pass(M, K, r, false, true, true);
+  l.down = plan_pass(M, K, r, kDown);
+  l.dy = plan_pass(M, N, r, kBoth);
+  l.up = plan_pass(M, K, r, kUp);
   const size_t mr = static_cast<size_t>(M) * r;
-  auto part = [r](int64_t rows, int n) { return static_cast<size_t>((rows + 127) / 128) * 512 * r * n; };
-  const size_t u = part(M, l.down.n_cr > l.dy.n_cr ? l.down.n_cr : l.dy.n_cr);
-  const size_t v_dy = part(N, l.dy.n_rr), v_up = part(K, l.up.n_rr);
+  auto sums = [r](int64_t rows, int n) { return static_cast<size_t>((rows + 127) / 128) * 512 * r * n; };
+  size_t part = 0;
+  auto more = [&part](size_t n) { part = n > part ? n : part; };
+  if (l.down.groups > 1) more(sums(M, l.down.groups));
+  if (l.dy.groups > 1) more(sums(N, l.dy.groups));
+  if (l.up.groups > 1) more(sums(K, l.up.groups));
   l.t = 0;
   l.dt = align256(l.t + mr * 2);
   l.u = align256(l.dt + mr * 2);
-  l.v = align256(l.u + u);
-  l.total = align256(l.v + (v_dy > v_up ? v_dy : v_up));
+  l.part = align256(l.u + sums(M, l.dy.n_inner));
+  l.total = align256(l.part + part);
   return l;
 }
 
-template <int SRC, bool ROW, bool COL>
+template <int SRC, int MODE>
 cudaError_t launch_pass(const PassLaunch& p, cudaStream_t s) {
   static std::once_flag once[64];
   static cudaError_t configured[64];
   const cudaError_t e = once_per_device(once, configured, []() {
-    return cudaFuncSetAttribute(adapter_pass_kernel<SRC, ROW, COL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(adapter_pass_kernel<SRC, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 static_cast<int>(kSmemMost));
   });
   if (e != cudaSuccess) return e;
-  return launch_after_previous(adapter_pass_kernel<SRC, ROW, COL>,
-                               dim3(static_cast<unsigned>(p.plan.n_cr) * static_cast<unsigned>(p.plan.n_rr)),
-                               dim3(pass_threads<SRC>()), p.plan.smem, s, p);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.plan.n_inner) * static_cast<unsigned>(p.plan.groups * p.plan.ranks));
+  cfg.blockDim = dim3(kPassThreads<SRC>);
+  cfg.dynamicSmemBytes = p.plan.smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(p.plan.ranks);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, adapter_pass_kernel<SRC, MODE>, p);
 }
 
 unsigned reduce_blocks(const ReduceJob& j) {
@@ -574,12 +689,13 @@ cudaError_t run(const LoraBackwardLaunch& l, cudaStream_t s) {
   const uint64_t M = l.M, N = l.N, K = l.K, r = l.r;
   auto* t = reinterpret_cast<__nv_bfloat16*>(l.ws + plan.t);
   auto* dt = l.dt != nullptr ? static_cast<__nv_bfloat16*>(l.dt) : reinterpret_cast<__nv_bfloat16*>(l.ws + plan.dt);
+  auto* part = reinterpret_cast<float*>(l.ws + plan.part);
   const ReduceJob none = {};
   PassLaunch p = {};
   p.q8 = static_cast<const uint8_t*>(l.q);
   p.e8 = static_cast<const uint8_t*>(l.e);
   p.u_part = reinterpret_cast<float*>(l.ws + plan.u);
-  p.v_part = reinterpret_cast<float*>(l.ws + plan.v);
+  p.part = part;
   p.R = l.M;
   p.r = l.r;
   p.stall_test = l.stall_test;
@@ -587,37 +703,38 @@ cudaError_t run(const LoraBackwardLaunch& l, cudaStream_t s) {
   constexpr auto kSw = CU_TENSOR_MAP_SWIZZLE_128B;
 
   // T = x A^T
-  PassLaunch down = p;
-  down.C = l.K;
-  down.plan = plan.down;
-  if (!encode_bf16_2d(&down.tm_p, l.a, K, r, K * 2, 64, static_cast<uint32_t>(r), kSw)) return cudaErrorInvalidValue;
-  cudaError_t e = launch_pass<FMT, true, false>(down, s);
-  if (e != cudaSuccess) return e;
-  e = launch_reduce<false>(ReduceJob{p.u_part, t, l.M, plan.down.n_cr, l.r}, none, s);
+  p.C = l.K;
+  p.plan = plan.down;
+  p.out = t;
+  if (!encode_bf16_2d(&p.tm_op, l.a, K, r, K * 2, 64, static_cast<uint32_t>(r), kSw)) return cudaErrorInvalidValue;
+  cudaError_t e = launch_pass<FMT, kDown>(p, s);
+  if (e == cudaSuccess && plan.down.groups > 1)
+    e = launch_reduce<false>(ReduceJob{part, t, l.M, plan.down.groups, l.r}, none, s);
   if (e != cudaSuccess) return e;
 
   // dT = dY B and dB = dY^T T
-  PassLaunch dy = p;
-  dy.C = l.N;
-  dy.plan = plan.dy;
-  if (!encode_bf16_2d(&dy.tm_s, l.dy, N, M, N * 2, 64, 128, kSw) ||
-      !encode_bf16_2d(&dy.tm_p, l.b, r, N, r * 2, 64, 128, kSw) ||
-      !encode_bf16_2d(&dy.tm_q, t, r, M, r * 2, 64, 128, kSw))
+  p.C = l.N;
+  p.plan = plan.dy;
+  p.out = static_cast<__nv_bfloat16*>(l.db);
+  if (!encode_bf16_2d(&p.tm_s, l.dy, N, M, N * 2, 64, 128, kSw) ||
+      !encode_bf16_2d(&p.tm_p, l.b, r, N, r * 2, 64, 128, kSw) ||
+      !encode_bf16_2d(&p.tm_op, t, r, M, r * 2, 64, 128, kSw))
     return cudaErrorInvalidValue;
-  e = launch_pass<kSrcBf16, true, true>(dy, s);
+  e = launch_pass<kSrcBf16, kBoth>(p, s);
   if (e != cudaSuccess) return e;
-  e = launch_reduce<false>(ReduceJob{p.u_part, dt, l.M, plan.dy.n_cr, l.r},
-                    ReduceJob{p.v_part, static_cast<__nv_bfloat16*>(l.db), l.N, plan.dy.n_rr, l.r}, s);
+  e = launch_reduce<false>(ReduceJob{p.u_part, dt, l.M, plan.dy.n_inner, l.r},
+                           plan.dy.groups > 1 ? ReduceJob{part, p.out, l.N, plan.dy.groups, l.r} : none, s);
   if (e != cudaSuccess) return e;
 
   // dA^T = x^T dT
-  PassLaunch up = p;
-  up.C = l.K;
-  up.plan = plan.up;
-  if (!encode_bf16_2d(&up.tm_q, dt, r, M, r * 2, 64, 128, kSw)) return cudaErrorInvalidValue;
-  e = launch_pass<FMT, false, true>(up, s);
-  if (e != cudaSuccess) return e;
-  return launch_reduce<true>(ReduceJob{p.v_part, static_cast<__nv_bfloat16*>(l.da), l.K, plan.up.n_rr, l.r}, none, s);
+  p.C = l.K;
+  p.plan = plan.up;
+  p.out = static_cast<__nv_bfloat16*>(l.da);
+  if (!encode_bf16_2d(&p.tm_op, dt, r, M, r * 2, 64, 128, kSw)) return cudaErrorInvalidValue;
+  e = launch_pass<FMT, kUp>(p, s);
+  if (e == cudaSuccess && plan.up.groups > 1)
+    e = launch_reduce<true>(ReduceJob{part, p.out, l.K, plan.up.groups, l.r}, none, s);
+  return e;
 }
 
 }  // namespace

@@ -52,7 +52,7 @@ __device__ __forceinline__ void ckpt8_decode4(uint32_t w, float (&v)[4]) {
   }
 }
 
-// The same multiplier for ckpt8_widen4: int8 takes it as a bf16 pair.
+// The same multiplier for Ckpt8Widen: int8 takes it as a bf16 pair.
 template <int FMT>
 __device__ __forceinline__ uint32_t ckpt8_factor_bits(uint32_t e) {
   if constexpr (FMT == kCkpt8Int8) {
@@ -65,32 +65,53 @@ __device__ __forceinline__ uint32_t ckpt8_factor_bits(uint32_t e) {
   }
 }
 
+// A constant that stays in a register: and_or() is then one instruction.  With both
+// constants as immediates the compiler makes it two, and the integer pipe (half the
+// rate of the others) is what bounds the kernels that unpack.
+__device__ __forceinline__ uint32_t in_register(uint32_t v) {
+  uint32_t r;
+  asm volatile("mov.b32 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+
 // 4 stored bytes -> 4 bf16 values times the block's factor (two packed pairs), exact.
 // int8 in packed bf16 arithmetic, 5 instructions a pair: with the low 7 bits in
 // the mantissa of 128 it reads 128 + low, and the sign bit turns the 128 that is
 // taken off into 256.
 template <int FMT>
-__device__ __forceinline__ uint2 ckpt8_widen4(uint32_t w, uint32_t factor) {
-  if constexpr (FMT == kCkpt8Int8) {
-    uint32_t out[2];
+struct Ckpt8Widen {
+  uint32_t low, base, sign, minus;
+  __device__ __forceinline__ Ckpt8Widen()
+      : low(in_register(0x007F007Fu)), base(in_register(0x43004300u)), sign(in_register(0x00800080u)),
+        minus(in_register(0xC300C300u)) {}
+  __device__ __forceinline__ uint2 operator()(uint32_t w, uint32_t factor) const {
+    if constexpr (FMT == kCkpt8Int8) {
+      uint32_t out[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t b = __byte_perm(w, 0u, i == 0 ? 0x4140 : 0x4342);
-      const uint32_t v = (b & 0x007F007Fu) | 0x43004300u, off = (b & 0x00800080u) | 0xC300C300u;
-      __nv_bfloat162 x = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&v),
-                                 *reinterpret_cast<const __nv_bfloat162*>(&off));
-      x = __hmul2(x, *reinterpret_cast<const __nv_bfloat162*>(&factor));
-      out[i] = *reinterpret_cast<uint32_t*>(&x);
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t b = __byte_perm(w, 0u, i == 0 ? 0x4140 : 0x4342);
+        const uint32_t v = and_or(b, low, base), off = and_or(b, sign, minus);
+        __nv_bfloat162 x = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&v),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&off));
+        x = __hmul2(x, *reinterpret_cast<const __nv_bfloat162*>(&factor));
+        out[i] = *reinterpret_cast<uint32_t*>(&x);
+      }
+      return make_uint2(out[0], out[1]);
+    } else {
+      const float f = __uint_as_float(factor);
+      float v[4];
+      ckpt8_decode4<FMT>(w, v);
+      const __nv_bfloat162 a = __floats2bfloat162_rn(v[0] * f, v[1] * f), b = __floats2bfloat162_rn(v[2] * f, v[3] * f);
+      return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
     }
-    return make_uint2(out[0], out[1]);
-  } else {
-    const float f = __uint_as_float(factor);
-    float v[4];
-    ckpt8_decode4<FMT>(w, v);
-    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0] * f, v[1] * f), b = __floats2bfloat162_rn(v[2] * f, v[3] * f);
-    return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
   }
-}
+};
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
