@@ -6,6 +6,7 @@
 // (exact) and rounds once; restore multiplies back (exact).  Both are bound by
 // memory: 3.03 bytes move per value in each direction.
 #include "lynx_ckpt8.cuh"
+#include "lynx_ptx.cuh"
 
 namespace lynx {
 
@@ -18,6 +19,7 @@ constexpr int kThreads = 256;
 template <int FMT>
 __global__ void __launch_bounds__(kThreads) ckpt8_store_kernel(const uint4* __restrict__ x, uint4* __restrict__ q,
                                                                uint8_t* __restrict__ e, int64_t n16) {
+  pdl_wait();
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
   // n16 is even (K % 64 == 0), so both lanes of a block are in or out together
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n16; i += stride) {
@@ -75,6 +77,7 @@ template <int FMT>
 __global__ void __launch_bounds__(kThreads) ckpt8_restore_kernel(const uint4* __restrict__ q,
                                                                  const uint8_t* __restrict__ e,
                                                                  uint4* __restrict__ x, int64_t n16) {
+  pdl_wait();
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n16; i += stride) {
     uint32_t w[4];
@@ -94,10 +97,10 @@ __global__ void __launch_bounds__(kThreads) ckpt8_restore_kernel(const uint4* __
 }
 
 // 16 values a thread; at most 8 blocks' worth of threads per SM loop over the rest
-int grid_of(int64_t n16, int sms) {
+unsigned grid_of(int64_t n16, int sms) {
   const int64_t blocks = (n16 + kThreads - 1) / kThreads;
   const int64_t most = static_cast<int64_t>(sms) * 8 * 16;
-  return static_cast<int>(blocks < most ? blocks : most);
+  return static_cast<unsigned>(blocks < most ? blocks : most);
 }
 
 }  // namespace
@@ -107,11 +110,8 @@ cudaError_t launch_ckpt8_store(const void* x, void* q, void* e, int64_t n, int f
   auto* xp = static_cast<const uint4*>(x);
   auto* qp = static_cast<uint4*>(q);
   auto* ep = static_cast<uint8_t*>(e);
-  if (format == kCkpt8Int8)
-    ckpt8_store_kernel<kCkpt8Int8><<<grid_of(n16, sms), kThreads, 0, s>>>(xp, qp, ep, n16);
-  else
-    ckpt8_store_kernel<kCkpt8E4M3><<<grid_of(n16, sms), kThreads, 0, s>>>(xp, qp, ep, n16);
-  return cudaGetLastError();
+  return launch_after_previous(format == kCkpt8Int8 ? ckpt8_store_kernel<kCkpt8Int8> : ckpt8_store_kernel<kCkpt8E4M3>,
+                               dim3(grid_of(n16, sms)), dim3(kThreads), 0, s, xp, qp, ep, n16);
 }
 
 cudaError_t launch_ckpt8_restore(const void* q, const void* e, void* x, int64_t n, int format, int sms,
@@ -120,11 +120,9 @@ cudaError_t launch_ckpt8_restore(const void* q, const void* e, void* x, int64_t 
   auto* qp = static_cast<const uint4*>(q);
   auto* ep = static_cast<const uint8_t*>(e);
   auto* xp = static_cast<uint4*>(x);
-  if (format == kCkpt8Int8)
-    ckpt8_restore_kernel<kCkpt8Int8><<<grid_of(n16, sms), kThreads, 0, s>>>(qp, ep, xp, n16);
-  else
-    ckpt8_restore_kernel<kCkpt8E4M3><<<grid_of(n16, sms), kThreads, 0, s>>>(qp, ep, xp, n16);
-  return cudaGetLastError();
+  return launch_after_previous(
+      format == kCkpt8Int8 ? ckpt8_restore_kernel<kCkpt8Int8> : ckpt8_restore_kernel<kCkpt8E4M3>,
+      dim3(grid_of(n16, sms)), dim3(kThreads), 0, s, qp, ep, xp, n16);
 }
 
 }  // namespace lynx

@@ -8,7 +8,8 @@
 //
 // The time is the reading of the nibbles.  A block has up to 6 tiles of 16
 // weight rows, all of K.  It takes K in turns of 128 on 8 cp.async rings; two
-// warps share a ring, fill it together and have half of the tiles each.  No
+// warps share a ring, fill it together and have half of the tiles each (with one
+// or two tiles a warp has a ring of its own).  No
 // barrier between rings until the end, where their sums meet in shared memory (a
 // fixed order, no workspace).  (TMA, with its rows of 64 bytes, was issued at
 // about 200 cycles a box and fed the rings at half of this rate.)
@@ -33,7 +34,6 @@ namespace {
 constexpr int kChunk = 128;        // k a stage
 constexpr int kThreads = 256;      // of the adapter's kernel
 constexpr int kWarps = kThreads / 32;
-constexpr int kRings = 8;
 constexpr uint32_t kMaxSlots = 4;
 constexpr uint32_t kFewSmem = 224 * 1024;
 constexpr int kMaxCluster = 8;
@@ -45,9 +45,14 @@ constexpr int kMaxCluster = 8;
 template <int NT>
 constexpr int kFewTiles = NT == 4 ? 4 : 6;
 
-// Compute warps: two a ring, but for a single tile
-template <int T>
-constexpr int kFewWarps = T == 1 ? kRings : 2 * kRings;
+// Warps of a ring: two, or one where there are few tiles to share; and rings: 8, or
+// 16 of one warp where the tokens' bytes leave room for them
+template <int T, int NT>
+constexpr int kHalves = T == 1 || (T == 2 && NT <= 2) ? 1 : 2;
+template <int T, int NT>
+constexpr int kRings = T <= 2 && NT <= 2 ? 16 : 8;
+template <int T, int NT>
+constexpr int kFewThreads = 32 * kHalves<T, NT> * kRings<T, NT>;
 
 __device__ __forceinline__ void mma_m16n8k16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                              uint32_t b0, uint32_t b1) {
@@ -69,7 +74,8 @@ template <int NT>
 __global__ void __launch_bounds__(kThreads) w4_lora_down_kernel(LinearW4Launch p) {
   __shared__ float part[kWarps][NT * 8][16];
   __shared__ float sum[NT * 8][16];
-  pdl_launch_dependents();
+  pdl_wait();
+  pdl_launch_dependents();  // the sums may start beside this, once all earlier work is done
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const uint32_t rank = cluster_ctarank(), ranks = cluster_nctarank();
   const int j0 = static_cast<int>(blockIdx.x / ranks) * 16;
@@ -78,17 +84,29 @@ __global__ void __launch_bounds__(kThreads) w4_lora_down_kernel(LinearW4Launch p
   const auto* x = static_cast<const __nv_bfloat16*>(p.x);
   const auto* a = static_cast<const __nv_bfloat16*>(p.a) + j0 * p.K;
   float c[NT][4] = {};
-#pragma unroll(NT == 1 ? 6 : 3)
-  for (int64_t i = static_cast<int64_t>(rank) * kWarps + warp; i < steps; i += ways) {
-    const int64_t k = 32 * i + 8 * t;
-    const uint4 a0 = __ldg(reinterpret_cast<const uint4*>(a + g * p.K + k));
-    const uint4 a1 = __ldg(reinterpret_cast<const uint4*>(a + (g + 8) * p.K + k));
+  constexpr int kBatch = NT == 4 ? 2 : 4;  // steps whose loads are in flight together
+  for (int64_t first = static_cast<int64_t>(rank) * kWarps + warp; first < steps; first += kBatch * ways) {
+    uint4 a0[kBatch], a1[kBatch], b[kBatch][NT];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int m = 8 * n + g;
-      const uint4 b = m < p.M ? __ldg(reinterpret_cast<const uint4*>(x + m * p.K + k)) : make_uint4(0, 0, 0, 0);
-      mma_m16n8k16(c[n], a0.x, a1.x, a0.y, a1.y, b.x, b.y);
-      mma_m16n8k16(c[n], a0.z, a1.z, a0.w, a1.w, b.z, b.w);
+    for (int u = 0; u < kBatch; ++u) {
+      const int64_t i = first + u * ways;
+      const int64_t k = 32 * i + 8 * t;
+      const uint4 none = make_uint4(0, 0, 0, 0);
+      a0[u] = i < steps ? __ldg(reinterpret_cast<const uint4*>(a + g * p.K + k)) : none;
+      a1[u] = i < steps ? __ldg(reinterpret_cast<const uint4*>(a + (g + 8) * p.K + k)) : none;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int m = 8 * n + g;
+        b[u][n] = i < steps && m < p.M ? __ldg(reinterpret_cast<const uint4*>(x + m * p.K + k)) : none;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        mma_m16n8k16(c[n], a0[u].x, a1[u].x, a0[u].y, a1[u].y, b[u][n].x, b[u][n].y);
+        mma_m16n8k16(c[n], a0[u].z, a1[u].z, a0[u].w, a1[u].w, b[u][n].z, b[u][n].w);
+      }
     }
   }
 #pragma unroll
@@ -129,25 +147,25 @@ struct FewCfg {
   static constexpr uint32_t kZ = kS + kGroups * kRows * 2u;
   static constexpr uint32_t kX = kZ + (ZEROS ? kGroups * kRows : 0u);
   static constexpr uint32_t kPad = NT * 8u * 256u;  // behind the last slot
-  static constexpr uint32_t kRed = kRings * NT * 8u * kRows * 4u;
+  static constexpr uint32_t kRed = kRings<T, NT> * NT * 8u * kRows * 4u;
   static constexpr uint32_t slot(int M) { return (kX + static_cast<uint32_t>(M) * 256u + 127u) & ~127u; }
 };
 
 template <int T, int NT, int GROUP, bool ZEROS>
-__global__ void __launch_bounds__(32 * kFewWarps<T>, 1) linear_w4_kernel(LinearW4Launch p, int slots,
+__global__ void __launch_bounds__(kFewThreads<T, NT>, 1) linear_w4_kernel(LinearW4Launch p, int slots,
                                                                          uint32_t slot_bytes) {
   using C = FewCfg<T, NT, GROUP, ZEROS>;
   constexpr int kGroups = C::kGroups;
   constexpr uint32_t rows = C::kRows;
-  constexpr int kHalves = kFewWarps<T> / kRings;
-  constexpr int TW = T / kHalves;                // tiles of a warp
-  constexpr uint32_t kLanes = 32 * kHalves;      // threads of a ring
+  constexpr int kRing = kRings<T, NT>;
+  constexpr int TW = T / kHalves<T, NT>;             // tiles of a warp
+  constexpr uint32_t kLanes = 32 * kHalves<T, NT>;   // threads of a ring
   extern __shared__ __align__(128) uint8_t sm[];
   const uint32_t warp = warp_id_sync(), lane = lane_id(), g = lane >> 2, t = lane & 3;
-  const uint32_t ring = warp % kRings, half = warp / kRings, id = 32 * half + lane;
+  const uint32_t ring = warp % kRing, half = warp / kRing, id = 32 * half + lane;
   const int64_t n0 = static_cast<int64_t>(blockIdx.x) * rows;
   const int chunks = static_cast<int>((p.K + kChunk - 1) / kChunk);
-  const int count = (chunks - static_cast<int>(ring) + kRings - 1) / kRings;  // of this ring
+  const int count = (chunks - static_cast<int>(ring) + kRing - 1) / kRing;  // of this ring
   uint8_t* const base = sm + ring * static_cast<uint32_t>(slots) * slot_bytes;
 
   // what this thread copies of a chunk: every kLanes-th 16 bytes
@@ -161,18 +179,25 @@ __global__ void __launch_bounds__(32 * kFewWarps<T>, 1) linear_w4_kernel(LinearW
   const uint8_t* w_src = wq + (n0 + w_row) * (p.K / 2) + 16 * w_piece + 64 * static_cast<int64_t>(ring);
   const uint32_t w_dst = w_row * 64 + ((w_piece ^ ((w_row >> 1) & 3)) << 4);
   const int64_t w_step = kWRows * (p.K / 2);
+  const bool whole = n0 + rows <= p.N;
   const int w_left = static_cast<int>(p.N - n0 - w_row < 4096 ? p.N - n0 - w_row : 4096);  // rows from this one on
 
   auto fill = [&](int j, int slot) {
     if (j < count) {
       const uint32_t st = smem_u32(base) + static_cast<uint32_t>(slot) * slot_bytes;
-      const int64_t k0 = (static_cast<int64_t>(ring) + static_cast<int64_t>(j) * kRings) * kChunk;
+      const int64_t k0 = (static_cast<int64_t>(ring) + static_cast<int64_t>(j) * kRing) * kChunk;
       const bool k_in = k0 + 32 * w_piece < p.K;
-      const uint8_t* src = w_src + static_cast<int64_t>(j) * (kRings * 64);
+      const uint8_t* src = w_src + static_cast<int64_t>(j) * (kRing * 64);
+      if (whole && k0 + kChunk <= p.K) {
+        const uint8_t* at = src;
 #pragma unroll
-      for (int i = 0; i < kWSteps; ++i) {
-        const bool in = k_in && kWRows * i < w_left;
-        cp_async_16(st + w_dst + i * kWRows * 64, in ? src + i * w_step : wq, in ? 16u : 0u);
+        for (int i = 0; i < kWSteps; ++i, at += w_step) cp_async_16(st + w_dst + i * kWRows * 64, at, 16u);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kWSteps; ++i) {
+          const bool in = k_in && kWRows * i < w_left;
+          cp_async_16(st + w_dst + i * kWRows * 64, in ? src + i * w_step : wq, in ? 16u : 0u);
+        }
       }
       for (uint32_t i = id; i < static_cast<uint32_t>(p.M) * 16; i += kLanes) {
         const uint32_t m = i >> 4, piece = i & 15;
@@ -191,10 +216,11 @@ __global__ void __launch_bounds__(32 * kFewWarps<T>, 1) linear_w4_kernel(LinearW
     cp_async_commit();
   };
 
+  if (p.b == nullptr) pdl_wait();  // else the kernel before this one is T's, which has waited
   for (int j = 0; j < slots - 1; ++j) fill(j, j);
   if (p.b != nullptr) {  // needed at the end: bring B's rows near
     const uint32_t lines = (2 * p.r + 127) / 128;
-    for (uint32_t i = threadIdx.x; i < rows * lines; i += 32 * kFewWarps<T>) {
+    for (uint32_t i = threadIdx.x; i < rows * lines; i += kFewThreads<T, NT>) {
       const int64_t n = n0 + i / lines;
       if (n < p.N) prefetch_l2(static_cast<const uint8_t*>(p.b) + n * p.r * 2 + (i % lines) * 128);
     }
@@ -214,7 +240,7 @@ __global__ void __launch_bounds__(32 * kFewWarps<T>, 1) linear_w4_kernel(LinearW
     else
       cp_async_wait<0>();
     // all of the ring's threads have this chunk's bytes and are done with the one before
-    if constexpr (kHalves == 2)
+    if constexpr (kHalves<T, NT> == 2)
       named_bar_sync(1 + ring, kLanes);
     else
       __syncwarp();
@@ -276,11 +302,10 @@ __global__ void __launch_bounds__(32 * kFewWarps<T>, 1) linear_w4_kernel(LinearW
   if (p.b != nullptr) {
     // The adapter's T B^T, 16 of r a step, the steps dealt out to the rings.  T
     // stays fp32: it enters as the sum of three bf16 (8 bits each).
-    // T comes from the kernel before this one, which everything above ran beside:
-    // that kernel started only after all earlier work on the stream.
+    // T comes from the kernel before this one, which everything above ran beside.
     pdl_wait();
     const auto* b = static_cast<const uint32_t*>(p.b);
-    for (int i = static_cast<int>(ring); i < p.r / 16; i += kRings) {
+    for (int i = static_cast<int>(ring); i < p.r / 16; i += kRing) {
       float2 tv[NT][2];
 #pragma unroll
       for (int c = 0; c < NT; ++c) {
@@ -331,38 +356,36 @@ __global__ void __launch_bounds__(32 * kFewWarps<T>, 1) linear_w4_kernel(LinearW
   __syncthreads();
   const auto* bias = static_cast<const __nv_bfloat16*>(p.bias);
   auto* y = static_cast<__nv_bfloat16*>(p.y);
-  for (uint32_t i = threadIdx.x; i < static_cast<uint32_t>(p.M) * rows; i += 32 * kFewWarps<T>) {
+  for (uint32_t i = threadIdx.x; i < static_cast<uint32_t>(p.M) * rows; i += kFewThreads<T, NT>) {
     const int64_t n = n0 + i % rows;
     if (n >= p.N) continue;
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < kRings; ++w) v += red[w * NT * 8 * rows + i];
+    for (int w = 0; w < kRing; ++w) v += red[w * NT * 8 * rows + i];
     if (bias != nullptr) v += __bfloat162float(bias[n]);
     if (p.act == kActGeluTanh) v = gelu_tanh(v);
     y[(i / rows) * p.N + n] = __float2bfloat16_rn(v);
   }
 }
 
+// Programmatic launch, in clusters where `cluster` is not 0
 template <typename... P, typename... A>
 cudaError_t launch_with(void (*kernel)(P...), unsigned blocks, int threads, unsigned cluster, size_t smem,
-                        bool dependent, cudaStream_t s, const A&... args) {
+                        cudaStream_t s, const A&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks);
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  if (cluster > 0) {
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = cluster;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-  } else {
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-  }
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = cluster > 0 || dependent ? 1 : 0;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
@@ -370,7 +393,7 @@ template <int T, int NT, int GROUP, bool ZEROS>
 cudaError_t launch_few(const LinearW4Launch& p, cudaStream_t s) {
   using C = FewCfg<T, NT, GROUP, ZEROS>;
   constexpr uint32_t kMostSlot = C::slot(8 * NT);
-  static_assert(kRings * 2 * kMostSlot + C::kPad <= kFewSmem && C::kRed <= kFewSmem, "a ring holds two chunks at least");
+  static_assert(kRings<T, NT> * 2 * kMostSlot + C::kPad <= kFewSmem && C::kRed <= kFewSmem, "a ring holds two chunks at least");
   static std::once_flag once[64];
   static cudaError_t configured[64];
   cudaError_t e = once_per_device(once, configured, []() {
@@ -379,18 +402,18 @@ cudaError_t launch_few(const LinearW4Launch& p, cudaStream_t s) {
   });
   if (e != cudaSuccess) return e;
   const uint32_t slot_bytes = C::slot(p.M);
-  const uint32_t fit = (kFewSmem - C::kPad) / (kRings * slot_bytes);
+  const uint32_t fit = (kFewSmem - C::kPad) / (kRings<T, NT> * slot_bytes);
   const int slots = static_cast<int>(fit < kMaxSlots ? fit : kMaxSlots);
-  const uint32_t ring = kRings * slots * slot_bytes + C::kPad;
+  const uint32_t ring = kRings<T, NT> * slots * slot_bytes + C::kPad;
   const uint32_t smem = ring > C::kRed ? ring : C::kRed;
   if (p.b != nullptr) {
     const int64_t steps = (p.K / 32 + kWarps - 1) / kWarps;
     const unsigned ranks = static_cast<unsigned>(steps < kMaxCluster ? steps : kMaxCluster);
-    e = launch_with(w4_lora_down_kernel<NT>, static_cast<unsigned>(p.r / 16) * ranks, kThreads, ranks, 0, false, s, p);
+    e = launch_with(w4_lora_down_kernel<NT>, static_cast<unsigned>(p.r / 16) * ranks, kThreads, ranks, 0, s, p);
     if (e != cudaSuccess) return e;
   }
   return launch_with(linear_w4_kernel<T, NT, GROUP, ZEROS>, static_cast<unsigned>((p.N + C::kRows - 1) / C::kRows),
-                     32 * kFewWarps<T>, 0, smem, p.b != nullptr, s, p, slots, slot_bytes);
+                     kFewThreads<T, NT>, 0, smem, s, p, slots, slot_bytes);
 }
 
 template <int NT, int GROUP, bool ZEROS>

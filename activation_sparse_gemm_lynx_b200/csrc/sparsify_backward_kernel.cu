@@ -90,7 +90,8 @@ __device__ __forceinline__ void sums16(const uint4& qv, const uint4& ga, const u
 template <int FMT>
 __global__ void __launch_bounds__(kRowThreads, 4) row_sums_kernel(SparsifyBackwardLaunch p, int rows) {
   __shared__ float part[kRowWarps][3];
-  pdl_launch_dependents();
+  pdl_wait();
+  pdl_launch_dependents();  // the outputs' loads may start beside this, once all earlier work is done
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ways = kRowWarps / rows, way = warp % ways;
   const int64_t m = static_cast<int64_t>(blockIdx.x) * rows + warp / ways;
@@ -257,8 +258,8 @@ __global__ void __launch_bounds__(kThreads, 1) sparsify_backward_kernel(const __
   __syncthreads();
   tc_fence_after();
 
-  // Only the row coefficients come from the kernel before this one, which started
-  // after all earlier work on the stream: everything else may be read beside it.
+  // Only the row coefficients come from the kernel before this one, which let this one
+  // start after all earlier work on the stream: everything else may be read beside it.
   if (warp == 0) {
     // ------------------------------------------------------------ loads
     if (lane == 0 && !p.stall_test) {
@@ -440,8 +441,8 @@ cudaError_t run(const SparsifyBackwardLaunch& p, const BackLaunch& b, unsigned b
   // a warp a row, more where the rows alone would leave SMs idle
   int rows = kRowWarps;
   while (rows > 1 && (p.M + rows - 1) / rows < 2 * sms) rows /= 2;
-  row_sums_kernel<FMT><<<static_cast<unsigned>((p.M + rows - 1) / rows), kRowThreads, 0, s>>>(p, rows);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_after_previous(
+      row_sums_kernel<FMT>, dim3(static_cast<unsigned>((p.M + rows - 1) / rows)), dim3(kRowThreads), 0, s, p, rows);
   if (e != cudaSuccess) return e;
   return p.dt != nullptr ? launch<FMT, true>(b, blocks, smem, s) : launch<FMT, false>(b, blocks, smem, s);
 }

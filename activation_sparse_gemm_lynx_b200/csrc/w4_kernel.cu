@@ -4,6 +4,7 @@
 
 #include "lynx_ckpt8.cuh"
 #include "lynx_internal.h"
+#include "lynx_ptx.cuh"
 
 namespace lynx {
 
@@ -43,6 +44,7 @@ __global__ void __launch_bounds__(kThreads) w4_quantize_kernel(const __nv_bfloat
   constexpr int kGroups = kTileK / GROUP;      // groups of a tile row
   __shared__ __nv_bfloat16 s_sm[kGroups][kTileN];
   __shared__ uint8_t z_sm[kGroups][kTileN];
+  pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const unsigned k_tiles = static_cast<unsigned>((K + kTileK - 1) / kTileK);
   const int64_t kt = blockIdx.x % k_tiles;
@@ -155,6 +157,7 @@ __global__ void __launch_bounds__(kThreads) w4_dequantize_kernel(const uint32_t*
   constexpr int kGroups = kTileK / GROUP;
   __shared__ float s_sm[kGroups][kTileN];
   __shared__ float z_sm[kGroups][kTileN];
+  pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const unsigned k_tiles = static_cast<unsigned>((K + kTileK - 1) / kTileK);
   const int64_t kt = blockIdx.x % k_tiles;
@@ -203,9 +206,9 @@ cudaError_t launch_w4_quantize(const void* w, int64_t N, int64_t K, int group, v
                                cudaStream_t s) {
   const unsigned grid = weight_tiles(N, K);
   auto run = [&](auto kernel) {
-    kernel<<<grid, kThreads, 0, s>>>(static_cast<const __nv_bfloat16*>(w), N, K, static_cast<uint32_t*>(wq),
-                                     static_cast<__nv_bfloat16*>(scales), static_cast<uint8_t*>(zeros));
-    return cudaGetLastError();
+    return launch_after_previous(kernel, dim3(grid), dim3(kThreads), 0, s, static_cast<const __nv_bfloat16*>(w), N, K,
+                                 static_cast<uint32_t*>(wq), static_cast<__nv_bfloat16*>(scales),
+                                 static_cast<uint8_t*>(zeros));
   };
   if (zeros != nullptr)
     return group == 32 ? run(w4_quantize_kernel<32, true>)
@@ -218,9 +221,9 @@ cudaError_t launch_w4_dequantize(const void* wq, const void* scales, const void*
                                  int group, void* w, cudaStream_t s) {
   const unsigned grid = weight_tiles(N, K);
   auto run = [&](auto kernel) {
-    kernel<<<grid, kThreads, 0, s>>>(static_cast<const uint32_t*>(wq), static_cast<const __nv_bfloat16*>(scales),
-                                     static_cast<const uint8_t*>(zeros), N, K, static_cast<__nv_bfloat16*>(w));
-    return cudaGetLastError();
+    return launch_after_previous(kernel, dim3(grid), dim3(kThreads), 0, s, static_cast<const uint32_t*>(wq),
+                                 static_cast<const __nv_bfloat16*>(scales), static_cast<const uint8_t*>(zeros), N, K,
+                                 static_cast<__nv_bfloat16*>(w));
   };
   if (zeros != nullptr)
     return group == 32 ? run(w4_dequantize_kernel<32, true>)

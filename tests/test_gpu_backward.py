@@ -211,3 +211,30 @@ def test_bindings_refuse():
         lynx.lynx_sparsify_backward(G.float(), q, e)
     with pytest.raises(ValueError):
         lynx.lynx_sparsify_backward(G, q, e[:4])
+
+
+@pytest.mark.parametrize("op", ["lora", "sparsify"])
+def test_waits_that_run_out_are_reported(op):
+    """With the loads switched off the kernels' bounded waits run out, the call's
+    stream says so, and the next call is right."""
+    M, N, K, r = 200, 264, 320, 32
+    q, e, x = checkpoint(heavy(1, M, K), lynx.LYNX_CKPT8_INT8)
+    dY, A, B, G, dT = normal(2, M, N), normal(3, r, K), normal(4, N, r), normal(5, M, K), normal(6, M, r)
+
+    def call():
+        if op == "lora":
+            return lynx.lynx_lora_backward(dY, q, e, A, B)[2]
+        return lynx.lynx_sparsify_backward(G, q, e, dT, A)
+
+    lynx.lynx_check_error()
+    lynx.lynx_debug_set_stall(True)
+    try:
+        call()
+    finally:
+        lynx.lynx_debug_set_stall(False)
+    st, code = lynx.lynx_check_error()
+    assert st == lynx.LYNX_ERR_DEVICE_TIMEOUT and code != 0
+    got = call()
+    st, _ = lynx.lynx_check_error()
+    assert st == lynx.LYNX_OK
+    within(got, *(ao.lora_backward(dY, x, A, B)["dT"] if op == "lora" else ao.sparsify_backward(G, x, dT, A)))
