@@ -10,12 +10,13 @@
 //   the row product  U[rows, r] += S P      (P [cols, r])
 //   the col product  V[cols, r] += S^T Q    (Q [rows, r])
 //
-// in three modes: T is the row product of x with P = A^T (kDown), dT and dB are
-// both products of one pass over dY with P = B and Q = T (kBoth), dA^T the col
-// product of x with Q = dT (kUp).  The same tile serves as a K-major and as an
-// MN-major operand of tcgen05.mma.
+// in three modes: T is the row product of x with P = A^T (kRow), dT and dB are both
+// products of one pass over dY with P = B and Q = T (kBoth), dA^T the col product of
+// x with Q = dT (kCol).  The same tile serves as a K-major and as an MN-major operand
+// of tcgen05.mma.  At large ranks (256 at 4608 x 12288) kBoth's sums U weigh more
+// than dY, and two passes over dY, kRow and kCol, take its place.
 //
-// A block has some inner blocks of 128 (rows for kDown, else columns), whose
+// A block has some inner blocks of 128 (rows for kRow, else columns), whose
 // accumulators stay in TMEM, and walks a range of outer ones, whose operand (P of
 // the columns, or Q of the rows) streams beside the tiles.  The outer ranges of the
 // same inner blocks are a cluster's blocks: they add their accumulators through
@@ -36,7 +37,7 @@ namespace {
 
 constexpr int kSrcBf16 = 2;  // beside kCkpt8Int8 and kCkpt8E4M3
 
-enum PassMode : int { kDown, kBoth, kUp };
+enum PassMode : int { kRow, kBoth, kCol };
 
 constexpr uint32_t kBox = 16384;        // 128 rows x 64 bf16, 128B swizzle
 constexpr uint32_t kTileBytes = 2 * kBox;  // an S tile: two boxes of 64 columns
@@ -55,17 +56,20 @@ struct PassPlan {
   int stages, op_bufs, u_bufs;
   uint32_t tmem_cols;
   uint32_t smem;
+  double cost;           // the estimated time, s
 };
 
 struct PassLaunch {
-  CUtensorMap tm_s;   // kBoth: dY [R,C], box 64 x 128
+  CUtensorMap tm_s;   // dY [R,C], box 64 x 128 (bf16 source)
   CUtensorMap tm_p;   // kBoth: B [C,r], box 64 x 128
-  CUtensorMap tm_op;  // the streamed operand: A [r,C], box 64 x r (kDown); Q [R,r], box 64 x 128
+  CUtensorMap tm_op;  // the streamed operand: kRow A [r,C], box 64 x r (x), or B [C,r], box 64 x 128 (dY);
+                      // else Q [R,r], box 64 x 128
   const uint8_t* q8;
   const uint8_t* e8;
   float* u_part;       // kBoth: [n_inner][row blocks][r][128]
   float* part;         // groups > 1: [groups][inner blocks][r][128]
-  __nv_bfloat16* out;  // groups == 1: [inner rows][r], kUp: [r][inner rows]
+  __nv_bfloat16* out;  // groups == 1: [inner rows][r], or [r][inner rows] (transposed)
+  int transposed;
   int64_t R, C;
   int r;
   PassPlan plan;
@@ -105,7 +109,7 @@ __global__ void __launch_bounds__(kPassThreads<SRC>, 1) adapter_pass_kernel(cons
   const uint32_t r_cols = static_cast<uint32_t>((r + 31) / 32) * 32;  // TMEM columns of an accumulator
   const int stages = p.plan.stages;
   const int row_blocks = static_cast<int>((p.R + 127) / 128), col_blocks = static_cast<int>((p.C + 127) / 128);
-  const int inner_blocks = MODE == kDown ? row_blocks : col_blocks, outer_blocks = MODE == kDown ? col_blocks : row_blocks;
+  const int inner_blocks = MODE == kRow ? row_blocks : col_blocks, outer_blocks = MODE == kRow ? col_blocks : row_blocks;
   const uint32_t rank = cluster_ctarank();
   const int ranks = p.plan.ranks;
   const int cluster = static_cast<int>(blockIdx.x) / ranks;
@@ -117,7 +121,8 @@ __global__ void __launch_bounds__(kPassThreads<SRC>, 1) adapter_pass_kernel(cons
 
   // shared memory: P (kBoth) | streamed operand | S stages | 8-bit tiles
   const uint32_t p_block = r_boxes * kBox;
-  const uint32_t op_bytes = MODE == kDown ? 256u * static_cast<uint32_t>(r) : r_boxes * kBox;
+  constexpr bool kOpKmajor = MODE == kRow && SRC != kSrcBf16;  // A, whose rows lie along the sum
+  const uint32_t op_bytes = kOpKmajor ? 256u * static_cast<uint32_t>(r) : r_boxes * kBox;
   uint8_t* const sm_p = sm;
   uint8_t* const sm_op = sm_p + (MODE == kBoth ? static_cast<uint32_t>(p.plan.inner) * p_block : 0u);
   uint8_t* const sm_s = sm_op + static_cast<uint32_t>(p.plan.op_bufs) * op_bytes;
@@ -172,7 +177,7 @@ __global__ void __launch_bounds__(kPassThreads<SRC>, 1) adapter_pass_kernel(cons
         const int32_t at = (o0 + o) * 128;
         uint8_t* dst = sm_op + static_cast<uint32_t>(buf) * op_bytes;
         mbar_arrive_expect_tx(&bars.op_full[buf], op_bytes);
-        if constexpr (MODE == kDown) {
+        if constexpr (kOpKmajor) {
           for (int j = 0; j < 2; ++j)
             tma_load_2d(dst + static_cast<uint32_t>(j) * (op_bytes / 2), &p.tm_op, &bars.op_full[buf], at + 64 * j, 0);
         } else {
@@ -187,8 +192,9 @@ __global__ void __launch_bounds__(kPassThreads<SRC>, 1) adapter_pass_kernel(cons
             if (!ok) break;
             uint8_t* tile = sm_s + slot * kTileBytes;
             mbar_arrive_expect_tx(&bars.full[slot], kTileBytes);
-            tma_load_2d_once(tile, &p.tm_s, &bars.full[slot], (i0 + i) * 128, at, once);
-            tma_load_2d_once(tile + kBox, &p.tm_s, &bars.full[slot], (i0 + i) * 128 + 64, at, once);
+            const int32_t in = (i0 + i) * 128, col = MODE == kRow ? at : in, row = MODE == kRow ? in : at;
+            tma_load_2d_once(tile, &p.tm_s, &bars.full[slot], col, row, once);
+            tma_load_2d_once(tile + kBox, &p.tm_s, &bars.full[slot], col + 64, row, once);
           }
         }
       }
@@ -206,8 +212,8 @@ __global__ void __launch_bounds__(kPassThreads<SRC>, 1) adapter_pass_kernel(cons
     // The whole warp walks the loop and one elected lane issues, so that the
     // descriptors stay in warp-uniform registers (issued by a lone lane, a tile's
     // 16 MMAs took 1400 cycles, more than the tile's bytes).
-    constexpr bool kRow = MODE != kUp, kCol = MODE != kDown;
-    const uint32_t idesc_row = make_idesc_bf16(128, r, false) | (MODE == kDown ? 0u : kIdescBMnMajor);
+    constexpr bool kHasRow = MODE != kCol, kHasCol = MODE != kRow;
+    const uint32_t idesc_row = make_idesc_bf16(128, r, false) | (kOpKmajor ? 0u : kIdescBMnMajor);
     const uint32_t idesc_col = make_idesc_bf16(128, r, false) | kIdescAMnMajor | kIdescBMnMajor;
     auto arrived = [&](uint64_t* bar, uint32_t parity, uint32_t code) {
       return __all_sync(0xffffffffu, pass_wait(bars, bar, parity, p.status, code)) != 0;
@@ -226,20 +232,20 @@ __global__ void __launch_bounds__(kPassThreads<SRC>, 1) adapter_pass_kernel(cons
         tc_fence_after();
         const uint32_t ss = smem_u32(sm_s) + slot * kTileBytes;
         const uint32_t d_inner = t_acc + static_cast<uint32_t>(i) * r_cols;
-        if constexpr (kRow) {  // 16 columns of S a step
-          const uint32_t d_row = MODE == kDown ? d_inner : t_u + static_cast<uint32_t>(ub) * r_cols;
+        if constexpr (kHasRow) {  // 16 columns of S a step
+          const uint32_t d_row = MODE == kRow ? d_inner : t_u + static_cast<uint32_t>(ub) * r_cols;
           const uint32_t sp = smem_u32(sm_p) + static_cast<uint32_t>(i) * p_block;
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const uint64_t da = make_sdesc(ss + (k / 4) * kBox + (k % 4) * 32, 16, 1024, kSw128);
-            const uint64_t db = MODE == kDown
+            const uint64_t db = kOpKmajor
                                     ? make_sdesc(sop + (k / 4) * (op_bytes / 2) + (k % 4) * 32, 16, 1024, kSw128)
-                                    : make_sdesc(sp + k * 2048, kBox, 1024, kSw128);
-            if (elect_one()) mma_bf16(d_row, da, db, idesc_row, ((MODE == kDown ? o : i) | k) != 0);
+                                    : make_sdesc((MODE == kRow ? sop : sp) + k * 2048, kBox, 1024, kSw128);
+            if (elect_one()) mma_bf16(d_row, da, db, idesc_row, ((MODE == kRow ? o : i) | k) != 0);
             __syncwarp();
           }
         }
-        if constexpr (kCol) {  // 16 rows of S a step
+        if constexpr (kHasCol) {  // 16 rows of S a step
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const uint64_t da = make_sdesc(ss + k * 2048, kBox, 1024, kSw128);
@@ -321,13 +327,13 @@ __global__ void __launch_bounds__(kPassThreads<SRC>, 1) adapter_pass_kernel(cons
     const int tiles = p.stall_test ? 0 : no * ni;
     // The walk over the tiles, inner blocks first: offsets of the next inner block
     // and, from the last one, of the next outer block's first
-    const int64_t row0 = static_cast<int64_t>(MODE == kDown ? i0 : o0) * 128 + row_t;
-    const int64_t col0 = static_cast<int64_t>(MODE == kDown ? o0 : i0) * 128;
+    const int64_t row0 = static_cast<int64_t>(MODE == kRow ? i0 : o0) * 128 + row_t;
+    const int64_t col0 = static_cast<int64_t>(MODE == kRow ? o0 : i0) * 128;
     const int64_t e_pitch = p.C / 32;
     const int64_t q_row = 128 * p.C, e_row = 128 * e_pitch;
-    const int64_t q_inner = MODE == kDown ? q_row : 128, e_inner = MODE == kDown ? e_row : 4;
-    const int64_t q_outer = (MODE == kDown ? 128 : q_row) - q_inner * (ni - 1);
-    const int64_t e_outer = (MODE == kDown ? 4 : e_row) - e_inner * (ni - 1);
+    const int64_t q_inner = MODE == kRow ? q_row : 128, e_inner = MODE == kRow ? e_row : 4;
+    const int64_t q_outer = (MODE == kRow ? 128 : q_row) - q_inner * (ni - 1);
+    const int64_t e_outer = (MODE == kRow ? 4 : e_row) - e_inner * (ni - 1);
     struct Walk {
       int rows, cols;  // rows from this thread's first one on, columns from its first one on
       int i, left;     // inner block, tiles left
@@ -338,7 +344,7 @@ __global__ void __launch_bounds__(kPassThreads<SRC>, 1) adapter_pass_kernel(cons
       --w.left;
       const bool next_outer = ++w.i == ni;
       if (next_outer) w.i = 0;
-      if constexpr (MODE == kDown) {
+      if constexpr (MODE == kRow) {
         w.rows += next_outer ? 128 * (ni - 1) : -128;
         if (next_outer) w.cols -= 128;
       } else {
@@ -431,7 +437,7 @@ __global__ void __launch_bounds__(kPassThreads<SRC>, 1) adapter_pass_kernel(cons
     cluster_sync_all();
   if (!alone && !bars.abort_flag) {
     const uint32_t red = smem_u32(sm);
-    const int64_t inner_rows = MODE == kDown ? p.R : p.C;
+    const int64_t inner_rows = MODE == kRow ? p.R : p.C;
     // 4 rows of one column a lane; the columns of the inner blocks dealt out to the
     // ranks' warps
     auto column_sum = [&](int column) {
@@ -450,7 +456,7 @@ __global__ void __launch_bounds__(kPassThreads<SRC>, 1) adapter_pass_kernel(cons
       for (int c = way; c < ni * r; c += ways)
         *reinterpret_cast<float4*>(p.part + ((static_cast<int64_t>(group) * inner_blocks + i0) * r + c) * 128 + 4 * lane) =
             column_sum(c);
-    } else if (MODE == kUp) {
+    } else if (p.transposed) {
       for (int c = way; c < ni * r; c += ways) {
         const float4 s = column_sum(c);
         const int64_t row = static_cast<int64_t>(i0 + c / r) * 128 + 4 * lane;  // inner_rows is a multiple of 64
@@ -549,24 +555,23 @@ __global__ void __launch_bounds__(kRedThreads) reduce_kernel(ReduceJob a, Reduce
 // hold and of the cluster sizes, the one with the least estimated time.  What it
 // adds up, each measured on the passes themselves: a tile takes 0.7 us to widen, or
 // the time of its bytes at 6.2 TB/s over the blocks at work (0.4 us at least) and
-// 0.2 us, more where U or the streamed operand has one buffer; a cluster's sums cost
-// 3 us and 40 GB/s a block; sums that go through memory are written and read at
-// 8 TB/s, and a reduce_kernel of its own costs 5 us with its launch.
-PassPlan plan_pass(int64_t R, int64_t C, int r, int mode) {
-  const bool eight = mode != kBoth;
+// 0.2 us, more where U has one buffer; the streamed operand comes at 80 GB/s a block,
+// beside the tiles where it has two buffers; a cluster's sums cost 3 us and 40 GB/s a
+// block (80 GB/s without a cluster); sums that go through memory are written and read
+// at 8 TB/s, and a reduce_kernel of its own costs 5 us with its launch.
+PassPlan plan_pass(int64_t R, int64_t C, int r, int mode, bool eight) {
   const int64_t rb = (R + 127) / 128, cb = (C + 127) / 128;
-  const int64_t inner_blocks = mode == kDown ? rb : cb, outer_blocks = mode == kDown ? cb : rb;
+  const int64_t inner_blocks = mode == kRow ? rb : cb, outer_blocks = mode == kRow ? cb : rb;
   const uint32_t boxes = static_cast<uint32_t>((r + 63) / 64), rc = static_cast<uint32_t>((r + 31) / 32) * 32;
   // 1 KB of the dynamic part goes into its alignment
   const uint32_t raw = eight ? (kAhead + 1) * kRawBytes : 0u;
   const uint32_t p_block = mode == kBoth ? boxes * kBox : 0u;
-  const uint32_t op_one = mode == kDown ? 256u * static_cast<uint32_t>(r) : boxes * kBox;
+  const uint32_t op_one = mode == kRow && eight ? 256u * static_cast<uint32_t>(r) : boxes * kBox;
   const uint32_t min_stages = eight ? 2 : 3, most_stages = eight ? 3 : kMaxStages;
   // clusters of 1 to 6 such blocks that a B200 holds at once, less one for the sizes
   // that depend on which SMs a chip has
   constexpr int kRoom[kMaxRanks + 1] = {0, 148, 74, 44, 32, 25, 21};
   PassPlan best = {};
-  double best_cost = 0;
   for (int inner = 1; inner <= 8 && inner <= inner_blocks; ++inner) {
     PassPlan c = {};
     c.inner = inner;
@@ -602,13 +607,16 @@ PassPlan plan_pass(int64_t R, int64_t C, int r, int mode) {
         const double bytes = (eight ? 16384.0 : 32768.0) * at_work / 6.2e12, least = eight ? 0.7e-6 : 0.4e-6;
         double tile = (bytes > least ? bytes : least) + (eight ? 0.0 : 0.2e-6);
         if (mode == kBoth && (c.u_bufs == 1 || c.op_bufs == 1)) tile *= 1.3;
-        double cost = waves * (outer * inner * tile + 1e-6) + u_cost;
+        const double tiles = inner * tile, op = op_one / 80e9;
+        const double step = c.op_bufs == 1 ? tiles + op + 0.5e-6 : tiles > op ? tiles : op;
+        double cost = waves * (outer * step + 1e-6) + u_cost;
         if (ranks > 1) cost += 3e-6 + inner * r * 512 / 40e9;
+        if (ranks == 1 && groups == 1) cost += inner * r * 512 / 80e9;
         if (groups > 1)
           cost += (mode == kBoth ? 0.0 : 5e-6) + 8.0 * r * 128 * static_cast<double>(groups * inner_blocks) / 8.0e12;
-        if (best.inner == 0 || cost < best_cost) {
-          best_cost = cost;
+        if (best.inner == 0 || cost < best.cost) {
           best = c;
+          best.cost = cost;
           best.ranks = ranks;
           best.groups = static_cast<int>(groups);
           best.outer = static_cast<int>(outer);
@@ -622,26 +630,33 @@ PassPlan plan_pass(int64_t R, int64_t C, int r, int mode) {
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 struct LoraPlan {
-  PassPlan down, dy, up;  // T; dT and dB; dA
+  PassPlan down, dy, dy_col, up;  // T; dT and dB, or dT alone; dB; dA
+  bool both;
   size_t t, dt, u, part, total;
 };
 
 LoraPlan plan_lora(int64_t M, int64_t N, int64_t K, int r) {
   LoraPlan l;
-  l.down = plan_pass(M, K, r, kDown);
-  l.dy = plan_pass(M, N, r, kBoth);
-  l.up = plan_pass(M, K, r, kUp);
+  l.down = plan_pass(M, K, r, kRow, true);
+  l.up = plan_pass(M, K, r, kCol, true);
+  l.dy = plan_pass(M, N, r, kBoth, false);
+  const PassPlan row = plan_pass(M, N, r, kRow, false);
+  l.dy_col = plan_pass(M, N, r, kCol, false);
+  // (measured at 4608 x 12288: rank 128 102 us with kBoth, 109 without; rank 256 323, 142)
+  l.both = l.dy.cost <= row.cost + l.dy_col.cost + 5e-6;
+  if (!l.both) l.dy = row;
   const size_t mr = static_cast<size_t>(M) * r;
   auto sums = [r](int64_t rows, int n) { return static_cast<size_t>((rows + 127) / 128) * 512 * r * n; };
   size_t part = 0;
   auto more = [&part](size_t n) { part = n > part ? n : part; };
   if (l.down.groups > 1) more(sums(M, l.down.groups));
-  if (l.dy.groups > 1) more(sums(N, l.dy.groups));
+  if (l.dy.groups > 1) more(sums(l.both ? N : M, l.dy.groups));
+  if (!l.both && l.dy_col.groups > 1) more(sums(N, l.dy_col.groups));
   if (l.up.groups > 1) more(sums(K, l.up.groups));
   l.t = 0;
   l.dt = align256(l.t + mr * 2);
   l.u = align256(l.dt + mr * 2);
-  l.part = align256(l.u + sums(M, l.dy.n_inner));
+  l.part = align256(l.u + (l.both ? sums(M, l.dy.n_inner) : 0));
   l.total = align256(l.part + part);
   return l;
 }
@@ -702,39 +717,52 @@ cudaError_t run(const LoraBackwardLaunch& l, cudaStream_t s) {
   p.status = l.status;
   constexpr auto kSw = CU_TENSOR_MAP_SWIZZLE_128B;
 
+  // one pass and, where its clusters leave several sums, their reduction
+  auto pass = [&](auto launch, const PassPlan& pass_plan, int64_t C, __nv_bfloat16* out, int64_t rows,
+                  bool transposed) {
+    p.C = C;
+    p.plan = pass_plan;
+    p.out = out;
+    p.transposed = transposed ? 1 : 0;
+    const cudaError_t e = launch(p, s);
+    if (e != cudaSuccess || pass_plan.groups == 1) return e;
+    const ReduceJob job = {part, out, rows, pass_plan.groups, l.r};
+    return transposed ? launch_reduce<true>(job, none, s) : launch_reduce<false>(job, none, s);
+  };
+  auto* db = static_cast<__nv_bfloat16*>(l.db);
+
   // T = x A^T
-  p.C = l.K;
-  p.plan = plan.down;
-  p.out = t;
   if (!encode_bf16_2d(&p.tm_op, l.a, K, r, K * 2, 64, static_cast<uint32_t>(r), kSw)) return cudaErrorInvalidValue;
-  cudaError_t e = launch_pass<FMT, kDown>(p, s);
-  if (e == cudaSuccess && plan.down.groups > 1)
-    e = launch_reduce<false>(ReduceJob{part, t, l.M, plan.down.groups, l.r}, none, s);
+  cudaError_t e = pass(launch_pass<FMT, kRow>, plan.down, l.K, t, l.M, false);
   if (e != cudaSuccess) return e;
 
   // dT = dY B and dB = dY^T T
-  p.C = l.N;
-  p.plan = plan.dy;
-  p.out = static_cast<__nv_bfloat16*>(l.db);
+  CUtensorMap tm_b, tm_t;
   if (!encode_bf16_2d(&p.tm_s, l.dy, N, M, N * 2, 64, 128, kSw) ||
-      !encode_bf16_2d(&p.tm_p, l.b, r, N, r * 2, 64, 128, kSw) ||
-      !encode_bf16_2d(&p.tm_op, t, r, M, r * 2, 64, 128, kSw))
+      !encode_bf16_2d(&tm_b, l.b, r, N, r * 2, 64, 128, kSw) || !encode_bf16_2d(&tm_t, t, r, M, r * 2, 64, 128, kSw))
     return cudaErrorInvalidValue;
-  e = launch_pass<kSrcBf16, kBoth>(p, s);
-  if (e != cudaSuccess) return e;
-  e = launch_reduce<false>(ReduceJob{p.u_part, dt, l.M, plan.dy.n_inner, l.r},
-                           plan.dy.groups > 1 ? ReduceJob{part, p.out, l.N, plan.dy.groups, l.r} : none, s);
+  if (plan.both) {
+    p.tm_p = tm_b;
+    p.tm_op = tm_t;
+    p.C = l.N;
+    p.plan = plan.dy;
+    p.out = db;
+    p.transposed = 0;
+    e = launch_pass<kSrcBf16, kBoth>(p, s);
+    if (e == cudaSuccess)
+      e = launch_reduce<false>(ReduceJob{p.u_part, dt, l.M, plan.dy.n_inner, l.r},
+                               plan.dy.groups > 1 ? ReduceJob{part, db, l.N, plan.dy.groups, l.r} : none, s);
+  } else {
+    p.tm_op = tm_b;
+    e = pass(launch_pass<kSrcBf16, kRow>, plan.dy, l.N, dt, l.M, false);
+    p.tm_op = tm_t;
+    if (e == cudaSuccess) e = pass(launch_pass<kSrcBf16, kCol>, plan.dy_col, l.N, db, l.N, false);
+  }
   if (e != cudaSuccess) return e;
 
   // dA^T = x^T dT
-  p.C = l.K;
-  p.plan = plan.up;
-  p.out = static_cast<__nv_bfloat16*>(l.da);
   if (!encode_bf16_2d(&p.tm_op, dt, r, M, r * 2, 64, 128, kSw)) return cudaErrorInvalidValue;
-  e = launch_pass<FMT, kUp>(p, s);
-  if (e == cudaSuccess && plan.up.groups > 1)
-    e = launch_reduce<true>(ReduceJob{part, p.out, l.K, plan.up.groups, l.r}, none, s);
-  return e;
+  return pass(launch_pass<FMT, kCol>, plan.up, l.K, static_cast<__nv_bfloat16*>(l.da), l.K, true);
 }
 
 }  // namespace

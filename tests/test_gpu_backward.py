@@ -40,7 +40,8 @@ def within(got, ref, tol, what=""):
 @pytest.mark.parametrize("M,N,K,r", [(1, 8, 64, 16), (2, 16, 64, 64), (127, 136, 128, 32), (128, 128, 128, 64),
                                      (129, 264, 192, 48), (300, 1000, 576, 16), (520, 520, 1088, 144),
                                      (1, 4104, 4096, 64), (1000, 640, 256, 256), (257, 3080, 2112, 64),
-                                     (2049, 72, 64, 80), (384, 1024, 1024, 128)])
+                                     (2049, 72, 64, 80), (384, 1024, 1024, 128), (300, 4104, 320, 256),
+                                     (1025, 2056, 128, 192), (70, 12296, 64, 240), (1500, 1032, 2048, 112)])
 def test_lora_backward(M, N, K, r, fmt):
     q, e, x = checkpoint(heavy(M + K, M, K), fmt)
     dY, A, B = normal(2, M, N, std=1e-2), normal(3, r, K, std=0.1), normal(4, N, r, std=0.1)
