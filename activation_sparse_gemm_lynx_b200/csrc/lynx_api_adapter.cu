@@ -2,6 +2,7 @@
 // 8-bit activation checkpoint and the backward pass: argument checks and
 // launches.  As everywhere, a failed check launches nothing.
 #include <cstring>
+#include <initializer_list>
 
 #include "lynx.h"
 #include "lynx_internal.h"
@@ -42,6 +43,32 @@ int check_branch(const void* a, const void* b, int64_t r) {
   return LYNX_OK;
 }
 
+struct Span {
+  const void* p;  // null: not there
+  uint64_t bytes;
+};
+
+bool overlap(const Span& a, const Span& b) {
+  const auto x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x != 0 && y != 0 && x < y + b.bytes && y < x + a.bytes;
+}
+
+// What a call writes must overlap neither what it reads nor its other outputs: its
+// kernels read and write in an order that only the shape fixes.
+bool any_overlap(std::initializer_list<Span> out, std::initializer_list<Span> in) {
+  for (const Span* o = out.begin(); o != out.end(); ++o) {
+    for (const Span& i : in)
+      if (overlap(*o, i)) return true;
+    for (const Span* q = out.begin(); q != o; ++q)
+      if (overlap(*o, *q)) return true;
+  }
+  return false;
+}
+
+uint64_t bytes_of(int64_t rows, int64_t cols, int size) {
+  return static_cast<uint64_t>(rows) * static_cast<uint64_t>(cols) * static_cast<uint64_t>(size);
+}
+
 }  // namespace
 
 extern "C" {
@@ -56,6 +83,9 @@ int lynx_w4_quantize(const void* W, int64_t N, int64_t K, int group, void* Wq, v
   if (any_null(W, Wq, scales)) return LYNX_ERR_INVALID_ARG;
   if (!n_ok(N) || !k_ok(K) || !group_ok(K, group)) return LYNX_ERR_UNSUPPORTED_SHAPE;
   if (any_misaligned(W, Wq, scales, zeros)) return LYNX_ERR_MISALIGNED;
+  if (any_overlap({{Wq, bytes_of(N, K / 2, 1)}, {scales, bytes_of(K / group, N, 2)}, {zeros, bytes_of(K / group, N, 1)}},
+                  {{W, bytes_of(N, K, 2)}}))
+    return LYNX_ERR_INVALID_ARG;
   return status_of(launch_w4_quantize(W, N, K, group, Wq, scales, zeros, static_cast<cudaStream_t>(stream)));
 }
 
@@ -64,6 +94,10 @@ int lynx_w4_dequantize(const void* Wq, const void* scales, const void* zeros, in
   if (any_null(Wq, scales, W)) return LYNX_ERR_INVALID_ARG;
   if (!n_ok(N) || !k_ok(K) || !group_ok(K, group)) return LYNX_ERR_UNSUPPORTED_SHAPE;
   if (any_misaligned(W, Wq, scales, zeros)) return LYNX_ERR_MISALIGNED;
+  if (any_overlap({{W, bytes_of(N, K, 2)}}, {{Wq, bytes_of(N, K / 2, 1)},
+                                             {scales, bytes_of(K / group, N, 2)},
+                                             {zeros, bytes_of(K / group, N, 1)}}))
+    return LYNX_ERR_INVALID_ARG;
   return status_of(launch_w4_dequantize(Wq, scales, zeros, N, K, group, W, static_cast<cudaStream_t>(stream)));
 }
 
@@ -89,6 +123,16 @@ int lynx_linear_w4(const void* X, const void* Wq, const void* scales, const void
     if (workspace == nullptr) return LYNX_ERR_INVALID_ARG;
     if (workspace_bytes < lynx_linear_w4_workspace_bytes(M, N, K, r)) return LYNX_ERR_WORKSPACE_TOO_SMALL;
   }
+  const Span ws = {A != nullptr ? workspace : nullptr, lynx_linear_w4_workspace_bytes(M, N, K, r)};
+  if (any_overlap({{Y, bytes_of(M, N, 2)}, ws},
+                  {{X, bytes_of(M, K, 2)},
+                   {Wq, bytes_of(N, K / 2, 1)},
+                   {scales, bytes_of(K / group, N, 2)},
+                   {zeros, bytes_of(K / group, N, 1)},
+                   {bias, bytes_of(1, N, 2)},
+                   {A, bytes_of(r, K, 2)},
+                   {B, bytes_of(N, r, 2)}}))
+    return LYNX_ERR_INVALID_ARG;
   const int sms = device_sm_count();
   if (sms == 0) return LYNX_ERR_CUDA;
   LinearW4Launch p;
@@ -120,6 +164,8 @@ int lynx_ckpt8_store(const void* X, int64_t M, int64_t K, int format, void* q, v
   if (any_null(X, q, e) || !format_ok(format)) return LYNX_ERR_INVALID_ARG;
   if (!rows_ok(M) || !k_ok(K)) return LYNX_ERR_UNSUPPORTED_SHAPE;
   if (any_misaligned(X, q, e)) return LYNX_ERR_MISALIGNED;
+  if (any_overlap({{q, bytes_of(M, K, 1)}, {e, bytes_of(M, K / 32, 1)}}, {{X, bytes_of(M, K, 2)}}))
+    return LYNX_ERR_INVALID_ARG;
   const int sms = device_sm_count();
   if (sms == 0) return LYNX_ERR_CUDA;
   return status_of(launch_ckpt8_store(X, q, e, M * K, format, sms, static_cast<cudaStream_t>(stream)));
@@ -129,6 +175,8 @@ int lynx_ckpt8_restore(const void* q, const void* e, int64_t M, int64_t K, int f
   if (any_null(X, q, e) || !format_ok(format)) return LYNX_ERR_INVALID_ARG;
   if (!rows_ok(M) || !k_ok(K)) return LYNX_ERR_UNSUPPORTED_SHAPE;
   if (any_misaligned(X, q, e)) return LYNX_ERR_MISALIGNED;
+  if (any_overlap({{X, bytes_of(M, K, 2)}}, {{q, bytes_of(M, K, 1)}, {e, bytes_of(M, K / 32, 1)}}))
+    return LYNX_ERR_INVALID_ARG;
   const int sms = device_sm_count();
   if (sms == 0) return LYNX_ERR_CUDA;
   return status_of(launch_ckpt8_restore(q, e, X, M * K, format, sms, static_cast<cudaStream_t>(stream)));
@@ -146,7 +194,15 @@ int lynx_lora_backward(const void* dY, const void* q, const void* e, const void*
   if (!rows_ok(M) || !n_ok(N) || !k_ok(K) || !rank_ok(r)) return LYNX_ERR_UNSUPPORTED_SHAPE;
   if (any_misaligned(dY, q, e, A, B, dA, dB, dT, workspace)) return LYNX_ERR_MISALIGNED;
   if (workspace == nullptr) return LYNX_ERR_INVALID_ARG;
-  if (workspace_bytes < lynx_lora_backward_workspace_bytes(M, N, K, r)) return LYNX_ERR_WORKSPACE_TOO_SMALL;
+  const size_t need = lynx_lora_backward_workspace_bytes(M, N, K, r);
+  if (workspace_bytes < need) return LYNX_ERR_WORKSPACE_TOO_SMALL;
+  if (any_overlap({{dA, bytes_of(r, K, 2)}, {dB, bytes_of(N, r, 2)}, {dT, bytes_of(M, r, 2)}, {workspace, need}},
+                  {{dY, bytes_of(M, N, 2)},
+                   {q, bytes_of(M, K, 1)},
+                   {e, bytes_of(M, K / 32, 1)},
+                   {A, bytes_of(r, K, 2)},
+                   {B, bytes_of(N, r, 2)}}))
+    return LYNX_ERR_INVALID_ARG;
   uint32_t* status = stream_status_word(static_cast<cudaStream_t>(stream));
   if (status == nullptr) return LYNX_ERR_CUDA;
   LoraBackwardLaunch p;
@@ -183,7 +239,14 @@ int lynx_sparsify_backward(const void* G, const void* q, const void* e, const vo
   if (!rows_ok(M) || !k_ok(K)) return LYNX_ERR_UNSUPPORTED_SHAPE;
   if (any_misaligned(G, q, e, dT, A, dX, workspace)) return LYNX_ERR_MISALIGNED;
   if (workspace == nullptr) return LYNX_ERR_INVALID_ARG;
-  if (workspace_bytes < lynx_sparsify_backward_workspace_bytes(M, K)) return LYNX_ERR_WORKSPACE_TOO_SMALL;
+  const size_t need = lynx_sparsify_backward_workspace_bytes(M, K);
+  if (workspace_bytes < need) return LYNX_ERR_WORKSPACE_TOO_SMALL;
+  if (any_overlap({{dX, bytes_of(M, K, 2)}, {workspace, need}}, {{G, bytes_of(M, K, 2)},
+                                                                 {q, bytes_of(M, K, 1)},
+                                                                 {e, bytes_of(M, K / 32, 1)},
+                                                                 {dT, bytes_of(M, r, 2)},
+                                                                 {A, bytes_of(r, K, 2)}}))
+    return LYNX_ERR_INVALID_ARG;
   const int sms = device_sm_count();
   uint32_t* status = stream_status_word(static_cast<cudaStream_t>(stream));
   if (sms == 0 || status == nullptr) return LYNX_ERR_CUDA;

@@ -315,9 +315,12 @@ LYNX_API int lynx_sparse_gemm(const void* vals, const void* meta, const void* T,
  *   zeros   [K/group, N] bytes, each 0..15 (the low 4 bits are read), or NULL:
  *           z = 8 everywhere
  *   group   32, 64 or 128, with K % group == 0 (else LYNX_ERR_UNSUPPORTED_SHAPE)
- * N and K follow the layer's rules (N % 8 == 0, K % 64 == 0).  Buffers that
- * one call reads and writes must not overlap.  None of it is on the RT-Lynx
- * pages, which keep W in bf16. */
+ * N and K follow the layer's rules (N % 8 == 0, K % 64 == 0).  None of it is on
+ * the RT-Lynx pages, which keep W in bf16.
+ *
+ * This section, the checkpoints and the backward pass: a buffer that a call writes
+ * (the workspace among them) must overlap no other of its buffers, else
+ * LYNX_ERR_INVALID_ARG. */
 
 /* Bytes of Wq: N * K / 2. */
 LYNX_API size_t lynx_w4_bytes(int64_t N, int64_t K);

@@ -54,6 +54,11 @@ ENTRY = {
                                     stream=None)),
 }
 
+for _order, _kw in ENTRY.values():  # buffers of their own
+    for _i, _k in enumerate(_order):
+        if _k in PTRS and _kw[_k] is not None:
+            _kw[_k] = P + (_i << 36)
+
 INVALID, SHAPE, ALIGN, SMALL = (lynx.LYNX_ERR_INVALID_ARG, lynx.LYNX_ERR_UNSUPPORTED_SHAPE, lynx.LYNX_ERR_MISALIGNED,
                                 lynx.LYNX_ERR_WORKSPACE_TOO_SMALL)
 
@@ -136,6 +141,30 @@ def test_bindings_refuse_cpu_tensors():
         lynx.lynx_lora_backward(x, q, e, x, x)
     with pytest.raises(ValueError):
         lynx.lynx_linear_w4(x, torch.zeros(8, 32, dtype=torch.uint8), x[:1, :8])
+
+
+OUTPUTS = {
+    "lynx_w4_quantize": ["Wq", "scales", "zeros"], "lynx_w4_dequantize": ["W"], "lynx_linear_w4": ["Y", "ws"],
+    "lynx_ckpt8_store": ["q", "e"], "lynx_ckpt8_restore": ["X"],
+    "lynx_lora_backward": ["dA", "dB", "dT", "ws"], "lynx_sparsify_backward": ["dX", "ws"],
+}
+
+
+@pytest.mark.parametrize("name", sorted(ENTRY))
+def test_an_output_overlaps_no_other_buffer(lib, name):
+    order, kw = ENTRY[name]
+    kw = {**kw, **({"dT": P + (20 << 36), "A": P + (21 << 36), "r": 16} if name == "lynx_sparsify_backward" else {}),
+          **{k: P + (22 + i << 36) for i, k in enumerate(["zeros", "bias", "dT"]) if k in kw and kw[k] is None}}
+    buffers = [k for k in order if k in PTRS and k != "stream"]
+    for out in OUTPUTS[name]:
+        for other in buffers:
+            if other != out:
+                # from its start, and from its second 16 bytes on
+                assert call(lib, name, order, {**kw, out: kw[other]}) == INVALID, (out, other)
+                assert call(lib, name, order, {**kw, out: kw[other] + 16}) == INVALID, (out, other)
+    # inputs may be the same buffer
+    if name == "lynx_lora_backward" and not torch.cuda.is_available():
+        assert call(lib, name, order, {**kw, "N": 256, "M": 4, "A": kw["B"]}) == lynx.LYNX_ERR_CUDA
 
 
 # ---- the oracle's formulas --------------------------------------------------
