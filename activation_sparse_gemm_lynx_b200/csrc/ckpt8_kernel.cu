@@ -73,26 +73,35 @@ __global__ void __launch_bounds__(kThreads) ckpt8_store_kernel(const uint4* __re
   }
 }
 
+// A warp takes 512 values a turn, a lane 8 of the first 256 and 8 of the rest, so that
+// its loads and stores are whole lines.  `units` is n / 8.
 template <int FMT>
-__global__ void __launch_bounds__(kThreads) ckpt8_restore_kernel(const uint4* __restrict__ q,
+__global__ void __launch_bounds__(kThreads) ckpt8_restore_kernel(const uint2* __restrict__ q,
                                                                  const uint8_t* __restrict__ e,
-                                                                 uint4* __restrict__ x, int64_t n16) {
+                                                                 uint4* __restrict__ x, int64_t units) {
   pdl_wait();
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n16; i += stride) {
-    uint32_t w[4];
-    *reinterpret_cast<uint4*>(w) = __ldcs(q + i);
-    const float f = ckpt8_factor<FMT>(e[i >> 1]);
-    uint32_t out[8];
+  const int lane = threadIdx.x & 31;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads * 2;
+  for (int64_t i0 = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x - lane) * 2 + lane; i0 < units;
+       i0 += stride) {
+    uint2 in[2];
+    uint32_t ex[2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float v[4];
-      ckpt8_decode4<FMT>(w[j], v);
-      out[2 * j] = pack_bf16(v[0] * f, v[1] * f);
-      out[2 * j + 1] = pack_bf16(v[2] * f, v[3] * f);
+    for (int h = 0; h < 2; ++h) {
+      const bool there = i0 + 32 * h < units;
+      in[h] = there ? __ldcs(q + i0 + 32 * h) : make_uint2(0, 0);
+      ex[h] = there ? e[(i0 + 32 * h) >> 2] : 0u;
     }
-    x[2 * i] = make_uint4(out[0], out[1], out[2], out[3]);
-    x[2 * i + 1] = make_uint4(out[4], out[5], out[6], out[7]);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float f = ckpt8_factor<FMT>(ex[h]);
+      float a[4], b[4];
+      ckpt8_decode4<FMT>(in[h].x, a);
+      ckpt8_decode4<FMT>(in[h].y, b);
+      if (i0 + 32 * h < units)
+        x[i0 + 32 * h] = make_uint4(pack_bf16(a[0] * f, a[1] * f), pack_bf16(a[2] * f, a[3] * f),
+                                    pack_bf16(b[0] * f, b[1] * f), pack_bf16(b[2] * f, b[3] * f));
+    }
   }
 }
 
@@ -116,13 +125,12 @@ cudaError_t launch_ckpt8_store(const void* x, void* q, void* e, int64_t n, int f
 
 cudaError_t launch_ckpt8_restore(const void* q, const void* e, void* x, int64_t n, int format, int sms,
                                  cudaStream_t s) {
-  const int64_t n16 = n / 16;
-  auto* qp = static_cast<const uint4*>(q);
+  auto* qp = static_cast<const uint2*>(q);
   auto* ep = static_cast<const uint8_t*>(e);
   auto* xp = static_cast<uint4*>(x);
   return launch_after_previous(
       format == kCkpt8Int8 ? ckpt8_restore_kernel<kCkpt8Int8> : ckpt8_restore_kernel<kCkpt8E4M3>,
-      dim3(grid_of(n16, sms)), dim3(kThreads), 0, s, qp, ep, xp, n16);
+      dim3(grid_of(n / 16, sms)), dim3(kThreads), 0, s, qp, ep, xp, n / 8);
 }
 
 }  // namespace lynx

@@ -12,8 +12,6 @@
 // L2), adds dT A from tcgen05.mma and writes dX.  (One kernel over clusters that
 // kept a row block between the two passes measured 118 us at 4608 x 12288: the
 // rows in flight are more than L2 holds, and the exchange stalls the loads.)
-// Beside the memory the integer pipe (half the rate of the others) is the bound,
-// so what can be is fp32: comparisons as differences, signs as saturated products.
 #include "lynx_ckpt8.cuh"
 #include "lynx_internal.h"
 #include "lynx_ptx.cuh"
@@ -22,38 +20,42 @@ namespace lynx {
 
 namespace {
 
-// Two of three, the inputs inverted where the bit of INV (4: a, 2: b, 1: c) is set
-template <int INV>
+// The bits that at least two of a, b and not c have
 __device__ __forceinline__ uint32_t two_of_three(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t r;
-  if constexpr (INV == 0)
-    asm("lop3.b32 %0, %1, %2, %3, 0xE8;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-  else if constexpr (INV == 1)
-    asm("lop3.b32 %0, %1, %2, %3, 0xD4;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-  else if constexpr (INV == 3)
-    asm("lop3.b32 %0, %1, %2, %3, 0x71;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-  else
-    asm("lop3.b32 %0, %1, %2, %3, 0x17;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  asm("lop3.b32 %0, %1, %2, %3, 0xD4;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
   return r;
 }
 
-// keep[i]: all ones if value i is one of the two largest magnitudes of 4, ties to
-// the lower position: it is kept if it goes before at least two of the others.
-// The comparisons are differences (the sign bit of |a| - |b| is set where b goes
-// before a, and a difference of equals is +0), which run on the fp32 pipe; the
-// sign bits are combined three at a time and spread over the word.
-__device__ __forceinline__ void keep4(const float (&v)[4], uint32_t (&keep)[4]) {
-  auto behind = [&](int i, int j) { return __float_as_uint(fabsf(v[i]) - fabsf(v[j])); };  // i < j
-  const uint32_t b01 = behind(0, 1), b02 = behind(0, 2), b03 = behind(0, 3);
-  const uint32_t b12 = behind(1, 2), b13 = behind(1, 3), b23 = behind(2, 3);
-  auto spread = [](uint32_t w) { return static_cast<uint32_t>(static_cast<int32_t>(w) >> 31); };
-  keep[0] = spread(two_of_three<7>(b01, b02, b03));
-  keep[1] = spread(two_of_three<3>(b01, b12, b13));
-  keep[2] = spread(two_of_three<1>(b02, b12, b23));
-  keep[3] = spread(two_of_three<0>(b03, b13, b23));
+template <uint32_t SEL>
+__device__ __forceinline__ uint32_t prmt(uint32_t a) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(a), "n"(SEL));
+  return r;
 }
 
-__device__ __forceinline__ float masked(float v, uint32_t mask) { return __uint_as_float(__float_as_uint(v) & mask); }
+// Magnitudes of 4 stored values as bytes of 0..127 that order as they do
+template <int FMT>
+__device__ __forceinline__ uint32_t magnitudes(uint32_t q) {
+  if constexpr (FMT == kCkpt8Int8) {
+    const uint32_t sign = prmt<0xBA98>(q);  // the sign bit over each byte
+    return (q ^ sign) + (sign & 0x01010101u);
+  } else {
+    return q & 0x7F7F7F7Fu;
+  }
+}
+
+// Bit 7 of byte i: value i is one of the two largest magnitudes of 4, ties to the lower
+// position: it is kept if it goes before at least two of the others.  Byte i of `next`
+// says a_i goes before a_(i+1), of `over` before a_(i+2), indices modulo 4: a_i + 128 -
+// a_j has bit 7 set where a_i >= a_j, and with 127 where a_i > a_j, which is what a
+// higher position needs.  No byte borrows from its neighbour.  (Six fp32 differences a
+// group of 4 took 61 us for 55 in the outputs' kernel at 4608 x 12288.)
+__device__ __forceinline__ uint32_t keep_bits(uint32_t a) {
+  const uint32_t next = a + 0x7F808080u - prmt<0x0321>(a);
+  const uint32_t over = a + 0x7F7F8080u - prmt<0x1032>(a);
+  return two_of_three(next, over, prmt<0x2103>(next));
+}
 
 // ---------------------------------------------------------------------------
 // row sums
@@ -70,17 +72,17 @@ __device__ __forceinline__ void sums16(const uint4& qv, const uint4& ga, const u
   const uint32_t gw[8] = {ga.x, ga.y, ga.z, ga.w, gb.x, gb.y, gb.z, gb.w};
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
+    const uint32_t keep = keep_bits(magnitudes<FMT>(qw[w]));
     float v[4];
-    uint32_t keep[4];
     ckpt8_decode4<FMT>(qw[w], v);
-    keep4(v, keep);
     const float g[4] = {bf16_lo(gw[2 * w]), bf16_hi(gw[2 * w]), bf16_lo(gw[2 * w + 1]), bf16_hi(gw[2 * w + 1])};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float x = masked(v[j], keep[j]);
       bl += fabsf(v[j]);
-      bk += fabsf(x);
-      bd = fmaf(g[j], x, bd);
+      if (keep & (0x80u << 8 * j)) {
+        bk += fabsf(v[j]);
+        bd = fmaf(g[j], v[j], bd);
+      }
     }
   }
 }
@@ -163,11 +165,13 @@ __global__ void __launch_bounds__(kRowThreads, 4) row_sums_kernel(SparsifyBackwa
 //               (a TMEM lane) and 32 columns.  Selection and sign need no
 //               exponents, which the row coefficients have seen.
 
-constexpr int kRoleWarps = 4;
-constexpr int kOutWarps = 16;
-constexpr int kGroupWarps = kOutWarps / 2;
+constexpr int kGroups = 2;
+constexpr int kGroupWarps = 8;
+constexpr int kRoleWarps = 2 + kGroups;
+constexpr int kOutWarps = kGroups * kGroupWarps;
 constexpr int kThreads = 32 * (kRoleWarps + kOutWarps);
 constexpr int kCols = 64;
+constexpr uint32_t kTmemCols = kGroups <= 2 ? 128 : 256;
 constexpr int kMaxStages = 6;
 constexpr uint32_t kGBytes = 128 * 128;  // 128 rows x 64 bf16, 128B swizzle
 constexpr uint32_t kQBytes = 128 * 64;   // 128 rows x 64 bytes, 64B swizzle
@@ -186,7 +190,6 @@ struct BackLaunch {
   int ranges;         // blocks of a row block
   int per;            // tiles of a block
   int stages;
-  int turns;          // output buffers of a group, 1 or 2
   uint32_t stage_bytes;
   int stall_test;
   uint32_t* status;
@@ -194,7 +197,7 @@ struct BackLaunch {
 
 struct BackBars {
   uint64_t full[kMaxStages], empty[kMaxStages];
-  uint64_t dt_full, d_full[2], d_empty[2], done[4], out_empty[4];
+  uint64_t dt_full, d_full[kGroups], d_empty[kGroups], done[kGroups], out_empty[kGroups];
   uint32_t tmem_base;
   volatile uint32_t abort_flag;
 };
@@ -207,14 +210,6 @@ __device__ __forceinline__ bool back_wait(BackBars& b, uint64_t* bar, uint32_t p
     b.abort_flag = 1u;
   }
   return ok;
-}
-
-// Sign of a stored value before the block's factor (an integer, or an e4m3 whose
-// smallest magnitude is 2^-9): 1, -1 or 0 (NaN: 0, its row is NaN through s)
-template <int FMT>
-__device__ __forceinline__ float stored_sign(float v) {
-  constexpr float k = FMT == kCkpt8Int8 ? 1.f : 512.f;
-  return __saturatef(v * k) - __saturatef(v * -k);
 }
 
 template <int FMT, bool LORA>
@@ -230,8 +225,8 @@ __global__ void __launch_bounds__(kThreads, 1) sparsify_backward_kernel(const __
   const int tile0 = static_cast<int>(at % static_cast<unsigned>(p.ranges)) * p.per;
   const int tiles = max(0, min(p.per, static_cast<int>(p.K / kCols) - tile0));
   const uint32_t t_boxes = LORA ? static_cast<uint32_t>((p.r + 63) / 64) : 0u;
-  uint8_t* const out_sm = sm + t_boxes * kTBox;  // tiles of dX, `turns` for each group
-  uint8_t* const ring = out_sm + 2 * p.turns * kGBytes;
+  uint8_t* const out_sm = sm + t_boxes * kTBox;  // a tile of dX for each group
+  uint8_t* const ring = out_sm + kGroups * kGBytes;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
@@ -239,11 +234,9 @@ __global__ void __launch_bounds__(kThreads, 1) sparsify_backward_kernel(const __
       mbar_init(&bars.empty[s], kGroupWarps);
     }
     mbar_init(&bars.dt_full, 1);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kGroups; ++i) {
       mbar_init(&bars.d_full[i], 1);
       mbar_init(&bars.d_empty[i], kGroupWarps);
-    }
-    for (int i = 0; i < 4; ++i) {
       mbar_init(&bars.done[i], kGroupWarps);
       mbar_init(&bars.out_empty[i], 1);
     }
@@ -251,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1) sparsify_backward_kernel(const __
     fence_mbar_init();
   }
   if (LORA && warp == 1) {
-    tmem_alloc(&bars.tmem_base, 128);
+    tmem_alloc(&bars.tmem_base, kTmemCols);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -300,9 +293,9 @@ __global__ void __launch_bounds__(kThreads, 1) sparsify_backward_kernel(const __
       int slot = 0;
       uint32_t phase = 0;
       for (int i = 0; ok && i < tiles; ++i) {
-        const int buf = i & 1;
+        const int buf = i % kGroups;
         ok = arrived(&bars.full[slot], phase, kDevTimeoutFull) &&
-             arrived(&bars.d_empty[buf], ((i >> 1) & 1) ^ 1, kDevTimeoutAccum);
+             arrived(&bars.d_empty[buf], ((i / kGroups) & 1) ^ 1, kDevTimeoutAccum);
         if (!ok) break;
         tc_fence_after();
         const uint32_t sa = smem_u32(sm);
@@ -323,21 +316,13 @@ __global__ void __launch_bounds__(kThreads, 1) sparsify_backward_kernel(const __
     // One warp a group, so that neither group waits for the other's tile.
     if (lane == 0) {
       const int group = static_cast<int>(warp) - 2;
-      int turn = 0;
       uint32_t parity = 0;
-      for (int i = group; i < tiles; i += 2) {
-        const int buf = group + 2 * turn;
-        if (!back_wait(bars, &bars.done[buf], parity, p.status, kDevTimeoutAccum)) break;
-        tma_store_2d(&p.tm_dx, out_sm + buf * kGBytes, (tile0 + i) * kCols, row0);
+      for (int i = group; i < tiles; i += kGroups, parity ^= 1u) {
+        if (!back_wait(bars, &bars.done[group], parity, p.status, kDevTimeoutAccum)) break;
+        tma_store_2d(&p.tm_dx, out_sm + group * kGBytes, (tile0 + i) * kCols, row0);
         bulk_commit();
-        if (p.turns == 2) {
-          bulk_wait_read_le1();  // the group's store before this one has left its buffer
-          if (i > group) mbar_arrive(&bars.out_empty[buf ^ 2]);
-        } else {
-          bulk_wait_read_all();
-          mbar_arrive(&bars.out_empty[buf]);
-        }
-        if (++turn == p.turns) turn = 0, parity ^= 1u;
+        bulk_wait_read_all();
+        mbar_arrive(&bars.out_empty[group]);
       }
       bulk_wait_all();
     }
@@ -355,17 +340,16 @@ __global__ void __launch_bounds__(kThreads, 1) sparsify_backward_kernel(const __
     const float2 c = row0 + static_cast<int64_t>(row) < p.M ? __ldcg(p.coef + row0 + row) : make_float2(0.f, 0.f);
     // dX = kept: s g + sign(x) c (1 - s); dropped: sign(x) c, c = D / Lk
     const float s = c.x;
-    const uint32_t dropped = __float_as_uint(c.y), kept = __float_as_uint(c.y * (1.f - s));
+    const float dropped = 2.f * c.y, kept = 2.f * (c.y * (1.f - s));
     int slot = buf % stages;
-    uint32_t phase = static_cast<uint32_t>(buf / stages) & 1u, parity = 0, out_parity = 1;
-    int turn = 0;  // of the group's output buffers
-    for (int i = buf; i < tiles; i += 2) {
+    uint32_t phase = static_cast<uint32_t>(buf / stages) & 1u, parity = 0;
+    for (int i = buf; i < tiles; i += kGroups) {
       bool ok = back_wait(bars, &bars.full[slot], phase, p.status, kDevTimeoutFull) &&
-                back_wait(bars, &bars.out_empty[buf + 2 * turn], out_parity, p.status, kDevTimeoutEmpty);
+                back_wait(bars, &bars.out_empty[buf], parity ^ 1u, p.status, kDevTimeoutEmpty);
       if (LORA) ok = ok && back_wait(bars, &bars.d_full[buf], parity, p.status, kDevTimeoutAccum);
       if (!__all_sync(0xffffffffu, ok)) break;
       const uint8_t* st = ring + static_cast<uint32_t>(slot) * p.stage_bytes;
-      uint8_t* const dst = out_sm + (buf + 2 * turn) * kGBytes;
+      uint8_t* const dst = out_sm + buf * kGBytes;
       if constexpr (LORA) tc_fence_after();
 #pragma unroll
       for (uint32_t h = 0; h < 2; ++h) {
@@ -388,16 +372,17 @@ __global__ void __launch_bounds__(kThreads, 1) sparsify_backward_kernel(const __
         uint32_t out[8];
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          float v[4], o[4];
-          uint32_t keep[4];
-          ckpt8_decode4<FMT>(qw[w], v);
-          keep4(v, keep);
+          const uint32_t a = magnitudes<FMT>(qw[w]), bits = keep_bits(a);
+          // the upper half of 0.5 with the sign, or of 0
+          const uint32_t half_sign = ((qw[w] & 0x80808080u) | 0x3F3F3F3Fu) & prmt<0xBA98>(a + 0x7F7F7F7Fu);
           const float g[4] = {bf16_lo(gw[2 * w]), bf16_hi(gw[2 * w]), bf16_lo(gw[2 * w + 1]), bf16_hi(gw[2 * w + 1])};
+          float o[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float step = __uint_as_float((kept & keep[j]) | (dropped & ~keep[j]));
-            o[j] = fmaf(stored_sign<FMT>(v[j]), step, __uint_as_float(branch[4 * w + j]));
-            o[j] = fmaf(s, masked(g[j], keep[j]), o[j]);
+            const float sign = __uint_as_float(__byte_perm(half_sign, 0u, (j << 12) | 0x0444));
+            const bool keep = bits & (0x80u << 8 * j);
+            o[j] = fmaf(sign, keep ? kept : dropped, __uint_as_float(branch[4 * w + j]));
+            if (keep) o[j] = fmaf(s, g[j], o[j]);
           }
           out[2 * w] = pack_bf16(o[0], o[1]);
           out[2 * w + 1] = pack_bf16(o[2], o[3]);
@@ -407,11 +392,9 @@ __global__ void __launch_bounds__(kThreads, 1) sparsify_backward_kernel(const __
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.done[buf + 2 * turn]);
+      if (lane == 0) mbar_arrive(&bars.done[buf]);
       parity ^= 1u;
-      if (++turn == p.turns) turn = 0, out_parity ^= 1u;
-      slot += 2;
-      if (slot >= stages) slot -= stages, phase ^= 1u;
+      for (slot += kGroups; slot >= stages; slot -= stages) phase ^= 1u;
     }
   }
 
@@ -419,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1) sparsify_backward_kernel(const __
   __syncthreads();
   if (LORA && warp == 1) {
     tc_fence_after();
-    tmem_dealloc(bars.tmem_base, 128);
+    tmem_dealloc(bars.tmem_base, kTmemCols);
   }
 }
 
@@ -460,10 +443,7 @@ cudaError_t launch_sparsify_backward(const SparsifyBackwardLaunch& p, int sms, c
   const bool lora = p.dt != nullptr;
   const uint32_t t_bytes = lora ? static_cast<uint32_t>((p.r + 63) / 64) * kTBox : 0u;
   b.stage_bytes = kGBytes + kQBytes + 128u * static_cast<uint32_t>(p.r);
-  // two output buffers a group where three stages are left for the loads (r <= 128)
-  auto stages = [&](uint32_t turns) { return (kSmemMost - 1024 - t_bytes - 2 * turns * kGBytes) / b.stage_bytes; };
-  b.turns = stages(2) >= 3 ? 2 : 1;
-  const uint32_t fit = stages(static_cast<uint32_t>(b.turns));
+  const uint32_t fit = (kSmemMost - 1024 - t_bytes - kGroups * kGBytes) / b.stage_bytes;
   b.stages = static_cast<int>(fit < kMaxStages ? fit : kMaxStages);
   // blocks of a row block: the number with the fewest tiles one after another
   // (waves of one block an SM times tiles of a block), the smallest such
@@ -478,7 +458,7 @@ cudaError_t launch_sparsify_backward(const SparsifyBackwardLaunch& p, int sms, c
   }
   b.per = static_cast<int>((tiles + b.ranges - 1) / b.ranges);
   b.ranges = static_cast<int>((tiles + b.per - 1) / b.per);
-  const uint32_t smem = 1024 + t_bytes + 2 * b.turns * kGBytes + b.stages * b.stage_bytes;
+  const uint32_t smem = 1024 + t_bytes + kGroups * kGBytes + b.stages * b.stage_bytes;
   const uint64_t M = p.M, K = p.K, r = p.r;
   constexpr auto kSw = CU_TENSOR_MAP_SWIZZLE_128B;
   if (!encode_bf16_2d(&b.tm_g, p.g, K, M, K * 2, kCols, 128, kSw) ||

@@ -127,6 +127,22 @@ def test_a_block_that_is_not_finite_marks_its_row():
     assert not bool(dX[1].isfinite().any()) and bool(dX[[0, 2, 3]].isfinite().all())
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_what_the_selection_drops_is_not_read(fmt):
+    """G may hold anything where the selection drops the value, and a kept zero
+    (a row of zeros keeps its first two places) has sign 0."""
+    M, K = 5, 320
+    X = heavy(3, M, K)
+    X[2] = 0
+    q, e, x = checkpoint(X, fmt)
+    G = normal(4, M, K)
+    want = lynx.lynx_sparsify_backward(G, q, e)
+    kept = ao.keep(x) > 0
+    for bad in (float("inf"), float("-inf"), float("nan"), torch.finfo(torch.bfloat16).min):
+        assert torch.equal(lynx.lynx_sparsify_backward(torch.where(kept, G, bad), q, e), want)
+    assert torch.equal(want[2], torch.where(kept[2], G[2], 0))
+
+
 def test_graph_replay_and_streams():
     M, N, K, r = 300, 520, 640, 64
     q, e, x = checkpoint(heavy(1, M, K), lynx.LYNX_CKPT8_E4M3)
