@@ -41,32 +41,38 @@ __global__ void __launch_bounds__(kThreads) ckpt8_store_kernel(const uint4* __re
       ex = max(lead - ((top & 0x7Fu) > 96u ? 7 : 8), -127);  // 448 = 1.75 * 2^8
     }
     const int n = (FMT == kCkpt8Int8 ? 6 : 0) - ex;  // x * 2^n is what is rounded
-    const int n1 = min(n, 126);
-    const float f1 = bad ? 0.f : exp2_int(n1), f2 = exp2_int(n - n1);
+    const float f = bad ? 0.f : exp2_int(min(n, 126));
     uint32_t out[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       float v[4] = {bf16_lo(w[2 * j]), bf16_hi(w[2 * j]), bf16_lo(w[2 * j + 1]), bf16_hi(w[2 * j + 1])};
+      if (n > 126) {  // 2^n is no fp32: the rest of it, exact on values this small
+#pragma unroll
+        for (int t = 0; t < 4; ++t) v[t] *= exp2_int(n - 126);
+      }
+      uint32_t o;
       if constexpr (FMT == kCkpt8Int8) {
-        uint32_t o = 0;
+        // Adding 1.5 * 2^23 rounds; the low byte is the integer
+        uint32_t b[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const int r = max(-127, min(127, __float2int_rn(v[t] * f1 * f2)));
-          o |= (static_cast<uint32_t>(r) & 0xFFu) << (8 * t);
-        }
-        out[j] = bad ? 0u : o;
+        for (int t = 0; t < 4; ++t)
+          b[t] = __float_as_uint(fminf(fmaxf(fmaf(v[t], f, 12582912.f), 12582912.f - 127.f), 12582912.f + 127.f));
+        o = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
       } else {
-        const float most = ex == 120 ? 240.f : 448.f;
+        // The conversion saturates at 448, which a block below 2^127 needs no more than
 #pragma unroll
-        for (int t = 0; t < 4; ++t) v[t] = fminf(fmaxf(v[t] * f1 * f2, -most), most);
-        uint32_t o;
+        for (int t = 0; t < 4; ++t) v[t] *= f;
+        if (ex == 120) {
+#pragma unroll
+          for (int t = 0; t < 4; ++t) v[t] = fminf(fmaxf(v[t], -240.f), 240.f);
+        }
         asm("{\n\t.reg .b16 a, b;\n\t"
             "cvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\t"
             "mov.b32 %0, {a, b};\n\t}"
             : "=r"(o)
             : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]));
-        out[j] = bad ? 0u : o;
       }
+      out[j] = bad ? 0u : o;
     }
     q[i] = make_uint4(out[0], out[1], out[2], out[3]);
     if ((i & 1) == 0) e[i >> 1] = static_cast<uint8_t>(bad ? 255 : ex + 127);
