@@ -4,7 +4,9 @@
 // Per 32 values one exponent: store finds the block's largest magnitude on the
 // bf16 bit patterns (which order like the magnitudes), scales by a power of two
 // (exact) and rounds once; restore multiplies back (exact).  Both are bound by
-// memory: 3.03 bytes move per value in each direction.
+// memory: 3.03 bytes move per value in each direction.  At 4608 x 12288 (172 MB):
+// store 29 us (int8) and 30 us (e4m3), 5.8 TB/s; restore 26 us behind it, 6.7 TB/s,
+// part of it from L2.
 #include "lynx_ckpt8.cuh"
 #include "lynx_ptx.cuh"
 
@@ -15,7 +17,8 @@ namespace {
 constexpr int kThreads = 256;
 
 // Two lanes share a block of 32: each takes 16 values (two 16-byte loads, one
-// 16-byte store).
+// 16-byte store).  (4 lanes with 8 values each, whose loads are whole lines, double the
+// instructions for the exponent: 38 us for 33.)
 template <int FMT>
 __global__ void __launch_bounds__(kThreads) ckpt8_store_kernel(const uint4* __restrict__ x, uint4* __restrict__ q,
                                                                uint8_t* __restrict__ e, int64_t n16) {

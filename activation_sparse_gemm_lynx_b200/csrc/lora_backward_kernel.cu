@@ -27,6 +27,11 @@
 // atomics: the order is the shape's.  fp32 sums lie as [block][column of r][128]: a
 // TMEM lane is a row, so a warp stores 128 bytes at a time (with rows of r floats
 // the 4608 x 12288 pass spent 14 of 41 us storing).
+//
+// At 4608 x 4096 -> 12288, rank 64, int8 (137 MB in all) 66 us in a CUDA graph: T 17 us
+// (19 MB, bound by the warps that widen it and the cluster's sums), the pass over dY
+// 28 us (113 MB in at 4.0 TB/s with its start, 28 MB of sums out), reduce_kernel 7 us
+// (those 28 MB from L2), dA 14 us.
 #include "lynx_ckpt8.cuh"
 #include "lynx_internal.h"
 #include "lynx_ptx.cuh"

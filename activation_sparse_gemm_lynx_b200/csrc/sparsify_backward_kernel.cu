@@ -11,7 +11,14 @@
 // takes 128 x 64 tiles in the opposite order (the rows read last are still in
 // L2), adds dT A from tcgen05.mma and writes dX.  (One kernel over clusters that
 // kept a row block between the two passes measured 118 us at 4608 x 12288: the
-// rows in flight are more than L2 holds, and the exchange stalls the loads.)
+// rows in flight are more than L2 holds, and the exchange stalls the loads.  The two
+// passes over a quarter of the rows at a time, so that L2 holds them between, took
+// 111 us: every launch starts and drains anew.)
+//
+// At 4608 x 12288, rank 64, 85 us: row sums 38 us and outputs 55 us, 8 us of them
+// side by side.  They read G and the bytes twice and write dX, 458 MB, a quarter of
+// the second reading out of L2: 4.9 TB/s from memory, which bounds both (the sums
+// take the same time with fewer instructions, the outputs without their stores).
 #include "lynx_ckpt8.cuh"
 #include "lynx_internal.h"
 #include "lynx_ptx.cuh"

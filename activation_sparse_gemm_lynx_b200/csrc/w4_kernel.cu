@@ -12,9 +12,13 @@ namespace {
 
 // ---------------------------------------------------------------------------
 // to 4 bits and back: tiles of 32 rows x 256 k, 8 warps, 4 rows a warp, 8 k (one
-// packed word) a lane.  Bound by memory (2.5 bytes a weight each way).  The side
-// arrays are [K/group, N], so a tile's scales go through shared memory to leave
-// (or come) as rows of 32 instead of single values N apart.
+// packed word) a lane.  2.5 bytes a weight each way.  The side arrays are
+// [K/group, N], so a tile's scales go through shared memory to leave (or come) as
+// rows of 32 instead of single values N apart.
+//
+// At 12288 x 4096, group 128 with zero points (127 MB a direction): quantise 33 us,
+// 3.9 TB/s, bound by its instructions (about 18 a weight; three quarters of the issue
+// slots are taken); dequantise 17 us behind it, 7.4 TB/s, the words still in L2.
 
 constexpr int kTileN = 32;
 constexpr int kTileK = 256;
@@ -77,7 +81,7 @@ __global__ void __launch_bounds__(kThreads) w4_quantize_kernel(const __nv_bfloat
     }
   }
   // Over the lanes of a group, each of 4 neighbours keeping one of the 4 rows, so
-  // that a lane divides once: row lane % 4.
+  // that a lane divides once for its row, lane % 4, and not for all four.
   const bool odd = lane & 1, upper = lane & 2;
   auto exchange = [&](const float (&v)[4], auto pick) {
     const float a = pick(odd ? v[1] : v[0], __shfl_xor_sync(0xffffffffu, odd ? v[0] : v[1], 1));
