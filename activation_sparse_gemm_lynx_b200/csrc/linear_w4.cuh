@@ -14,10 +14,10 @@
 // fixed order, no workspace).  (TMA, with its rows of 64 bytes, was issued at
 // about 200 cycles a box and fed the rings at half of this rate.)
 //
-// One token, 12288 x 4096, group 128 with zero points, r = 64: 12.5 us (28.5 MB, 2.3
-// TB/s); 32 tokens, 9216 x 4096: 18.7 us.  What bounds it is the unpacking: 13,000
-// instructions a scheduler at about half of the issue slots, where the bytes take 4.4
-// us; then the start and the sums at the end, about 3 us.
+// One token, 12288 x 4096, group 128 with zero points: 10.2 us (26 MB, 2.6 TB/s), with
+// an adapter of r = 64 12.6 us; 32 tokens, 9216 x 4096: 13.7 and 15.9 us.  What bounds
+// it is the unpacking: 13,000 instructions a scheduler at about half of the issue
+// slots, where the bytes take 4.4 us; then the start and the sums at the end, 1.6 us.
 //
 // mma wants k pairs (2t, 2t+1) and (2t+8, 2t+9) of thread t; any assignment of k
 // to those places will do if both operands share it.  Thread t takes k = 8t..8t+7
@@ -37,7 +37,7 @@ namespace lynx {
 namespace {
 
 constexpr int kChunk = 128;        // k a stage
-constexpr int kThreads = 256;      // of the adapter's kernel
+constexpr int kThreads = 512;      // of the adapter's kernel
 constexpr int kWarps = kThreads / 32;
 constexpr uint32_t kMaxSlots = 4;
 constexpr uint32_t kFewSmem = 224 * 1024;
@@ -74,8 +74,8 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
 }
 
 // T[m][j] = sum_k x[m,k] a[j,k]: 16 adapter rows a cluster, K over its blocks and
-// their 8 warps, 8 NT tokens.  4 us (r = 64, K = 4096), all of it latency: the main
-// kernel starts beside it and needs T only at its end.
+// their 16 warps, 8 NT tokens.  4 us for one token (r = 64, K = 4096), 8 us for 32, most of it
+// latency: the main kernel starts beside it and needs T only at its end.
 template <int NT>
 __global__ void __launch_bounds__(kThreads) w4_lora_down_kernel(LinearW4Launch p) {
   __shared__ float part[kWarps][NT * 8][16];
@@ -396,7 +396,7 @@ cudaError_t launch_with(void (*kernel)(P...), unsigned blocks, int threads, unsi
 }
 
 template <int T, int NT, int GROUP, bool ZEROS>
-cudaError_t launch_few(const LinearW4Launch& p, cudaStream_t s) {
+cudaError_t launch_few(const LinearW4Launch& p, int sms, cudaStream_t s) {
   using C = FewCfg<T, NT, GROUP, ZEROS>;
   constexpr uint32_t kMostSlot = C::slot(8 * NT);
   static_assert(kRings<T, NT> * 2 * kMostSlot + C::kPad <= kFewSmem && C::kRed <= kFewSmem, "a ring holds two chunks at least");
@@ -412,14 +412,19 @@ cudaError_t launch_few(const LinearW4Launch& p, cudaStream_t s) {
   const int slots = static_cast<int>(fit < kMaxSlots ? fit : kMaxSlots);
   const uint32_t ring = kRings<T, NT> * slots * slot_bytes + C::kPad;
   const uint32_t smem = ring > C::kRed ? ring : C::kRed;
+  const unsigned blocks = static_cast<unsigned>((p.N + C::kRows - 1) / C::kRows);
   if (p.b != nullptr) {
-    const int64_t steps = (p.K / 32 + kWarps - 1) / kWarps;
-    const unsigned ranks = static_cast<unsigned>(steps < kMaxCluster ? steps : kMaxCluster);
+    const int64_t steps = (p.K / 32 + kWarps - 1) / kWarps, most = steps < kMaxCluster ? steps : kMaxCluster;
+    // Where the main kernel leaves SMs over, T runs on those: a block of the main kernel
+    // does not fit beside one of T's and would start late (a cluster of 8 in every case:
+    // 14.3 us for 12.6 with one token, 12288 x 4096; 19.2 for 15.9 with 32, 9216 x 4096).
+    const int64_t spare = (sms - static_cast<int64_t>(blocks)) / (p.r / 16);
+    const unsigned ranks = static_cast<unsigned>(spare >= 1 && spare < most ? spare : most);
     e = launch_with(w4_lora_down_kernel<NT>, static_cast<unsigned>(p.r / 16) * ranks, kThreads, ranks, 0, s, p);
     if (e != cudaSuccess) return e;
   }
-  return launch_with(linear_w4_kernel<T, NT, GROUP, ZEROS>, static_cast<unsigned>((p.N + C::kRows - 1) / C::kRows),
-                     kFewThreads<T, NT>, 0, smem, s, p, slots, slot_bytes);
+  return launch_with(linear_w4_kernel<T, NT, GROUP, ZEROS>, blocks, kFewThreads<T, NT>, 0, smem, s, p, slots,
+                     slot_bytes);
 }
 
 template <int NT, int GROUP, bool ZEROS>
@@ -429,11 +434,11 @@ cudaError_t launch_few_tiles(const LinearW4Launch& p, int sms, cudaStream_t s) {
   const int64_t tiles = (p.N + 15) / 16, most = static_cast<int64_t>(sms) * kFewTiles<NT>;
   const int64_t blocks = (tiles + most - 1) / most * sms;
   const int64_t each = (tiles + blocks - 1) / blocks;
-  if (each <= 1) return launch_few<1, NT, GROUP, ZEROS>(p, s);
-  if (each == 2) return launch_few<2, NT, GROUP, ZEROS>(p, s);
+  if (each <= 1) return launch_few<1, NT, GROUP, ZEROS>(p, sms, s);
+  if (each == 2) return launch_few<2, NT, GROUP, ZEROS>(p, sms, s);
   if constexpr (kFewTiles<NT> == 6)
-    if (each > 4) return launch_few<6, NT, GROUP, ZEROS>(p, s);
-  return launch_few<4, NT, GROUP, ZEROS>(p, s);
+    if (each > 4) return launch_few<6, NT, GROUP, ZEROS>(p, sms, s);
+  return launch_few<4, NT, GROUP, ZEROS>(p, sms, s);
 }
 
 // 8 tokens are one MMA wide
