@@ -17,8 +17,9 @@
 //
 // At 4608 x 12288, rank 64, 85 us: row sums 38 us and outputs 55 us, 8 us of them
 // side by side.  They read G and the bytes twice and write dX, 458 MB, a quarter of
-// the second reading out of L2: 4.9 TB/s from memory, which bounds both (the sums
-// take the same time with fewer instructions, the outputs without their stores).
+// the second reading out of L2: 4.8 and 4.3 TB/s from memory with the integer pipe
+// half busy.  Neither bounds them alone, and neither fewer instructions (sums),
+// missing stores (outputs) nor more loads in flight (both) change the time much.
 #include "lynx_ckpt8.cuh"
 #include "lynx_internal.h"
 #include "lynx_ptx.cuh"
