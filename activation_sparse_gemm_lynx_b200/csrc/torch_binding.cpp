@@ -101,16 +101,22 @@ class Call {
     return {p, need};
   }
 
-  long integer(int i) const {
+  int integer(int i) const {
     const long v = PyLong_AsLong(args_[i]);
-    if (v == -1 && PyErr_Occurred()) {
-      PyErr_Clear();
-      refuse(PyExc_TypeError, "an integer is required");
-    }
-    return v;
+    const bool failed = v == -1 && PyErr_Occurred();
+    if (failed) PyErr_Clear();
+    if (failed || v != static_cast<int>(v)) refuse(PyExc_TypeError, "an integer is required");
+    return static_cast<int>(v);
   }
 
-  bool truth(int i) const { return PyObject_IsTrue(args_[i]) == 1; }
+  bool truth(int i) const {
+    const int v = PyObject_IsTrue(args_[i]);
+    if (v < 0) {
+      PyErr_Clear();
+      refuse(PyExc_TypeError, "a truth value is required");
+    }
+    return v == 1;
+  }
 
   void* stream() const { return stream_; }
 
@@ -211,7 +217,7 @@ struct Ckpt {
 PyObject* w4_quantize(PyObject* const* args, Py_ssize_t n) {
   const Call c(args, n, 7, "W");
   const auto [N, K] = c.matrix(0, "W");
-  const long group = c.integer(1);
+  const int group = c.integer(1);
   if ((group != 32 && group != 64 && group != 128) || K % group != 0) return PyLong_FromLong(LYNX_ERR_UNSUPPORTED_SHAPE);
   at::Tensor wq, scales, zeros;
   const void* w = c.in(0, "W", at::kBFloat16, {N, K});
@@ -219,7 +225,7 @@ PyObject* w4_quantize(PyObject* const* args, Py_ssize_t n) {
   void* s = c.out(4, "scales", at::kBFloat16, {K / group, N}, scales);
   void* z = nullptr;
   if (c.given(5) || c.truth(2)) z = c.out(5, "zeros", at::kByte, {K / group, N}, zeros);
-  const int st = lynx_w4_quantize(w, N, K, static_cast<int>(group), q, s, z, c.stream());
+  const int st = lynx_w4_quantize(w, N, K, group, q, s, z, c.stream());
   return st != LYNX_OK ? PyLong_FromLong(st) : wrap_all({wq, scales, zeros});
 }
 
@@ -259,7 +265,7 @@ PyObject* linear_w4(PyObject* const* args, Py_ssize_t n) {
     work = c.workspace(9, lynx_linear_w4_workspace_bytes(M, g.N, g.K, r), ws);
   }
   void* y = c.out(8, "Y", at::kBFloat16, {M, g.N}, Y);
-  const int st = lynx_linear_w4(x, q, s, z, bias, a, b, M, g.N, g.K, r, g.group(), static_cast<int>(c.integer(7)), y,
+  const int st = lynx_linear_w4(x, q, s, z, bias, a, b, M, g.N, g.K, r, g.group(), c.integer(7), y,
                                 work.first, work.second, c.stream());
   return st != LYNX_OK ? PyLong_FromLong(st) : wrap(Y);
 }
@@ -268,13 +274,13 @@ PyObject* linear_w4(PyObject* const* args, Py_ssize_t n) {
 PyObject* ckpt8_store(PyObject* const* args, Py_ssize_t n) {
   const Call c(args, n, 5, "X");
   const auto [M, K] = c.matrix(0, "X");
-  const long format = c.integer(1);
+  const int format = c.integer(1);
   if (format != LYNX_CKPT8_INT8 && format != LYNX_CKPT8_E4M3) return PyLong_FromLong(LYNX_ERR_INVALID_ARG);
   at::Tensor q, e;
   const void* x = c.in(0, "X", at::kBFloat16, {M, K});
   void* qp = c.out(2, "q", format == LYNX_CKPT8_INT8 ? at::kChar : at::kFloat8_e4m3fn, {M, K}, q);
   void* ep = c.out(3, "e", at::kByte, {M, K / 32}, e);
-  const int st = lynx_ckpt8_store(x, M, K, static_cast<int>(format), qp, ep, c.stream());
+  const int st = lynx_ckpt8_store(x, M, K, format, qp, ep, c.stream());
   return st != LYNX_OK ? PyLong_FromLong(st) : wrap_all({q, e});
 }
 

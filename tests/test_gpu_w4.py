@@ -188,3 +188,28 @@ def test_bindings_refuse():
         lynx.lynx_w4_quantize(normal(1, 64, 192), 128)
     with pytest.raises(lynx.LynxError):
         lynx.lynx_linear_w4(X, Wq, sc, act=7)
+
+
+def test_arguments_of_other_kinds_are_refused():
+    Wq, sc, ze, _ = w4_case(12, 64, 256, 64, True)
+    X, W = normal(1, 4, 256), normal(2, 64, 256)
+    for act in (1 << 32, 0.0, None, "gelu"):  # the first is 0 in 32 bits
+        with pytest.raises(TypeError):
+            lynx.lynx_linear_w4(X, Wq, sc, act=act)
+    for group in ((1 << 32) + 64, 64.0, None):
+        with pytest.raises(TypeError):
+            lynx.lynx_w4_quantize(W, group)
+    with pytest.raises(TypeError):
+        lynx.lynx_w4_quantize(W, 64, zero_points=torch.zeros(2))
+    with pytest.raises(TypeError):
+        lynx.lynx_linear_w4(X, Wq, sc, stream=0)
+    with pytest.raises(TypeError):
+        lynx.lynx_linear_w4([1.0], Wq, sc)
+    with pytest.raises(ValueError):
+        lynx.lynx_linear_w4(None, Wq, sc)
+    with pytest.raises(lynx.LynxError):
+        lynx.lynx_linear_w4(X, Wq, sc, ze, Y=X[:, :64].contiguous(), workspace=None, A=normal(3, 16, 256),
+                            B=normal(4, 64, 16)[:, :16], act=2)
+    Y = torch.empty(4, 64, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(lynx.LynxError):  # the output in the place of the bias
+        lynx.lynx_linear_w4(X, Wq, sc, ze, Y[0], Y=Y)
