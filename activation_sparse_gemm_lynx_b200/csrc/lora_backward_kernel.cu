@@ -75,6 +75,7 @@ struct PassLaunch {
   float* part;         // groups > 1: [groups][inner blocks][r][128]
   __nv_bfloat16* out;  // groups == 1: [inner rows][r], or [r][inner rows] (transposed)
   int transposed;
+  int early;           // a pass follows: it may launch beside this one's end
   int64_t R, C;
   int r;
   PassPlan plan;
@@ -434,6 +435,9 @@ __global__ void __launch_bounds__(kPassThreads<SRC>, 1) adapter_pass_kernel(cons
   }
 
   // ------------------------------------------------------------ the cluster's sums
+  // Only for a pass, whose blocks take an SM each.  reduce_kernel's small blocks would
+  // crowd onto the first SMs that are free (4608 x 12288: 72 us for 66).
+  if (p.early) pdl_launch_dependents();
   __syncwarp();
   tc_fence_before();
   if (ranks == 1)
@@ -532,6 +536,7 @@ __global__ void __launch_bounds__(kRedThreads) reduce_kernel(ReduceJob a, Reduce
     s0.x += v.x, s0.y += v.y, s0.z += v.z, s0.w += v.w;
     s1.x += w.x, s1.y += w.y, s1.z += w.z, s1.w += w.w;
   }
+  pdl_launch_dependents();
   if constexpr (TRANSPOSED) {
     const int64_t row = block * 128 + 4 * lane;  // rows is a multiple of 64
     if (row < j.rows) {
@@ -729,6 +734,7 @@ cudaError_t run(const LoraBackwardLaunch& l, cudaStream_t s) {
     p.plan = pass_plan;
     p.out = out;
     p.transposed = transposed ? 1 : 0;
+    p.early = pass_plan.groups == 1 && !transposed ? 1 : 0;  // dA's pass is the last
     const cudaError_t e = launch(p, s);
     if (e != cudaSuccess || pass_plan.groups == 1) return e;
     const ReduceJob job = {part, out, rows, pass_plan.groups, l.r};
@@ -753,6 +759,7 @@ cudaError_t run(const LoraBackwardLaunch& l, cudaStream_t s) {
     p.plan = plan.dy;
     p.out = db;
     p.transposed = 0;
+    p.early = 0;
     e = launch_pass<kSrcBf16, kBoth>(p, s);
     if (e == cudaSuccess)
       e = launch_reduce<false>(ReduceJob{p.u_part, dt, l.M, plan.dy.n_inner, l.r},
