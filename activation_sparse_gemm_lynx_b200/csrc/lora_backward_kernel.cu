@@ -24,11 +24,14 @@
 // result.  Only where one cluster is too few for the length (few inner blocks),
 // groups of clusters leave fp32 sums that reduce_kernel adds.  kBoth's U leaves
 // after each row block, as fp32 sums per column range for reduce_kernel.  No
-// atomics: the order is the shape's.  fp32 sums lie as [block][column of r][128]: a
+// atomics: the order is the shape's.  T and dT are rounded to bf16 before they enter
+// their second product, as T is in the forward pass: the gradients then differ from the
+// formula by 0.0023 of their norm, the bf16 of the results alone by 0.0017.  Two bf16
+// for each would double the col products and their operand's bytes.  fp32 sums lie as [block][column of r][128]: a
 // TMEM lane is a row, so a warp stores 128 bytes at a time (with rows of r floats
 // the 4608 x 12288 pass spent 14 of 41 us storing).
 //
-// At 4608 x 4096 -> 12288, rank 64, int8 (137 MB in all) 66 us in a CUDA graph: T 17 us
+// At 4608 x 4096 -> 12288, rank 64, int8 (137 MB in all) 65 us in a CUDA graph: T 17 us
 // (19 MB, bound by the warps that widen it and the cluster's sums), the pass over dY
 // 28 us (113 MB in at 4.0 TB/s with its start, 28 MB of sums out), reduce_kernel 7 us
 // (those 28 MB from L2), dA 14 us.
@@ -436,7 +439,7 @@ __global__ void __launch_bounds__(kPassThreads<SRC>, 1) adapter_pass_kernel(cons
 
   // ------------------------------------------------------------ the cluster's sums
   // Only for a pass, whose blocks take an SM each.  reduce_kernel's small blocks would
-  // crowd onto the first SMs that are free (4608 x 12288: 72 us for 66).
+  // crowd onto the first SMs that are free (4608 x 12288: 72 us for 65).
   if (p.early) pdl_launch_dependents();
   __syncwarp();
   tc_fence_before();
