@@ -13,7 +13,7 @@
 // in three modes: T is the row product of x with P = A^T (kRow), dT and dB are both
 // products of one pass over dY with P = B and Q = T (kBoth), dA^T the col product of
 // x with Q = dT (kCol).  The same tile serves as a K-major and as an MN-major operand
-// of tcgen05.mma.  At large ranks (256 at 4608 x 12288) kBoth's sums U weigh more
+// of tcgen05.mma.  At large ranks (from 128 at 4608 x 12288) kBoth's sums U weigh more
 // than dY, and two passes over dY, kRow and kCol, take its place.
 //
 // A block has some inner blocks of 128 (rows for kRow, else columns), whose
@@ -24,17 +24,19 @@
 // result.  Only where one cluster is too few for the length (few inner blocks),
 // groups of clusters leave fp32 sums that reduce_kernel adds.  kBoth's U leaves
 // after each row block, as fp32 sums per column range for reduce_kernel.  No
-// atomics: the order is the shape's.  T and dT are rounded to bf16 before they enter
-// their second product, as T is in the forward pass: the gradients then differ from the
-// formula by 0.0023 of their norm, the bf16 of the results alone by 0.0017.  Two bf16
-// for each would double the col products and their operand's bytes.  fp32 sums lie as [block][column of r][128]: a
+// atomics: the order is the shape's.  T and dT enter their second product as the sum of
+// two bf16 (Q's two halves, a col product each): 2^-17 off, below what the rounding of
+// the results shows.  One bf16 (2^-8) put the gradients 0.0024 of their norm away from the
+// formula, where that rounding alone takes 0.0017; three (all of fp32) would change
+// nothing in bf16 results.  fp32 sums lie as [block][column of r][128]: a
 // TMEM lane is a row, so a warp stores 128 bytes at a time (with rows of r floats
 // the 4608 x 12288 pass spent 14 of 41 us storing).
 //
-// At 4608 x 4096 -> 12288, rank 64, int8 (137 MB in all) 65 us in a CUDA graph: T 17 us
-// (19 MB, bound by the warps that widen it and the cluster's sums), the pass over dY
-// 28 us (113 MB in at 4.0 TB/s with its start, 28 MB of sums out), reduce_kernel 7 us
-// (those 28 MB from L2), dA 14 us.
+// At 4608 x 4096 -> 12288, rank 64, int8 (137 MB in all) 72 us: T 18 us (19 MB, bound by
+// the warps that widen it and the cluster's sums), the pass over dY 30 us behind it
+// (113 MB in, 28 MB of sums out; 24 MMAs a tile read 144 KB of shared memory, 0.6 us),
+// reduce_kernel 7 us (those 28 MB from L2), dA 17 us.  One bf16 for T and dT takes 65 us;
+// at ranks 128 and 256 101 and 145 us for 126 and 202.
 #include "lynx_ckpt8.cuh"
 #include "lynx_internal.h"
 #include "lynx_ptx.cuh"
@@ -61,7 +63,8 @@ struct PassPlan {
   int outer;             // outer blocks of a block
   int n_inner;           // ranges of inner blocks
   int ranks, groups;     // outer ranges: blocks of a cluster, clusters
-  int stages, op_bufs, u_bufs;
+  int stages, u_bufs;
+  int op_bufs, subs;     // buffers of the streamed operand; pieces of an outer block that it comes in
   uint32_t tmem_cols;
   uint32_t smem;
   double cost;           // the estimated time, s
@@ -71,12 +74,14 @@ struct PassLaunch {
   CUtensorMap tm_s;   // dY [R,C], box 64 x 128 (bf16 source)
   CUtensorMap tm_p;   // kBoth: B [C,r], box 64 x 128
   CUtensorMap tm_op;  // the streamed operand: kRow A [r,C], box 64 x r (x), or B [C,r], box 64 x 128 (dY);
-                      // else Q [R,r], box 64 x 128
+                      // else Q's two halves side by side [R,2r], box 64 x 128 / subs
   const uint8_t* q8;
   const uint8_t* e8;
   float* u_part;       // kBoth: [n_inner][row blocks][r][128]
   float* part;         // groups > 1: [groups][inner blocks][r][128]
-  __nv_bfloat16* out;  // groups == 1: [inner rows][r], or [r][inner rows] (transposed)
+  // groups == 1, either may be null:
+  __nv_bfloat16* out;   // [inner rows][r], or [r][inner rows] (transposed)
+  __nv_bfloat16* pair;  // [inner rows][2 r]: two bf16 whose sum is the value, first the upper ones
   int transposed;
   int early;           // a pass follows: it may launch beside this one's end
   int64_t R, C;
@@ -100,6 +105,30 @@ __device__ __forceinline__ bool pass_wait(PassBars& b, uint64_t* bar, uint32_t p
   record_error(status, code);
   b.abort_flag = 1u;
   return false;
+}
+
+// Two fp32 as the sums of two bf16 each (16 bits, 2^-17 off at most): the upper halves
+// are the values rounded.
+struct Halves {
+  uint32_t hi, lo;
+};
+
+__device__ __forceinline__ Halves split_bf16(float a, float b) {
+  Halves h;
+  h.hi = pack_bf16(a, b);
+  h.lo = pack_bf16(bf16_rest(a, bf16_lo(h.hi)), bf16_rest(b, bf16_hi(h.hi)));
+  return h;
+}
+
+// 8 columns of a row, rounded in `out` and as two halves in `pair`
+__device__ __forceinline__ void store_halves(__nv_bfloat16* out, __nv_bfloat16* pair, int64_t row, int r, int col,
+                                             Halves a, Halves b, Halves c, Halves d) {
+  const uint4 hi = make_uint4(a.hi, b.hi, c.hi, d.hi);
+  if (out != nullptr) *reinterpret_cast<uint4*>(out + row * r + col) = hi;
+  if (pair != nullptr) {
+    *reinterpret_cast<uint4*>(pair + row * 2 * r + col) = hi;
+    *reinterpret_cast<uint4*>(pair + row * 2 * r + r + col) = make_uint4(a.lo, b.lo, c.lo, d.lo);
+  }
 }
 
 // TMA producer, MMA issuer, 4 epilogue warps, and the warps that widen 8-bit tiles
@@ -131,7 +160,11 @@ __global__ void __launch_bounds__(kPassThreads<SRC>, 1) adapter_pass_kernel(cons
   // shared memory: P (kBoth) | streamed operand | S stages | 8-bit tiles
   const uint32_t p_block = r_boxes * kBox;
   constexpr bool kOpKmajor = MODE == kRow && SRC != kSrcBf16;  // A, whose rows lie along the sum
-  const uint32_t op_bytes = kOpKmajor ? 256u * static_cast<uint32_t>(r) : r_boxes * kBox;
+  // Q comes in pieces of 128 / subs rows, the upper halves of all columns and then the low
+  // ones: with both, a whole block does not always leave room for two buffers.
+  const int subs = MODE == kRow ? 1 : p.plan.subs;
+  const uint32_t op_box = kBox / static_cast<uint32_t>(subs), op_half = r_boxes * op_box;
+  const uint32_t op_bytes = kOpKmajor ? 256u * static_cast<uint32_t>(r) : MODE == kRow ? op_half : 2 * op_half;
   uint8_t* const sm_p = sm;
   uint8_t* const sm_op = sm_p + (MODE == kBoth ? static_cast<uint32_t>(p.plan.inner) * p_block : 0u);
   uint8_t* const sm_s = sm_op + static_cast<uint32_t>(p.plan.op_bufs) * op_bytes;
@@ -179,23 +212,30 @@ __global__ void __launch_bounds__(kPassThreads<SRC>, 1) adapter_pass_kernel(cons
       const uint64_t once = l2_evict_first();  // dY is read once: leave L2 to the sums
       uint32_t g = 0;
       int issued = 0;
-      for (int o = 0; ok && o < no; ++o) {
-        const int buf = o % p.plan.op_bufs;
-        ok = pass_wait(bars, &bars.op_empty[buf], ((o / p.plan.op_bufs) & 1) ^ 1, p.status, kDevTimeoutEmpty);
-        if (!ok) break;
-        const int32_t at = (o0 + o) * 128;
+      auto operand = [&](int o, int sb) {  // a piece of outer block o's operand
+        const int n = o * subs + sb, buf = n % p.plan.op_bufs;
+        ok = pass_wait(bars, &bars.op_empty[buf], ((n / p.plan.op_bufs) & 1) ^ 1, p.status, kDevTimeoutEmpty);
+        if (!ok) return;
+        const int32_t at = (o0 + o) * 128 + sb * (128 / subs);
         uint8_t* dst = sm_op + static_cast<uint32_t>(buf) * op_bytes;
         mbar_arrive_expect_tx(&bars.op_full[buf], op_bytes);
         if constexpr (kOpKmajor) {
           for (int j = 0; j < 2; ++j)
             tma_load_2d(dst + static_cast<uint32_t>(j) * (op_bytes / 2), &p.tm_op, &bars.op_full[buf], at + 64 * j, 0);
         } else {
-          for (uint32_t b = 0; b < r_boxes; ++b)
-            tma_load_2d(dst + b * kBox, &p.tm_op, &bars.op_full[buf], static_cast<int32_t>(64 * b), at);
+          for (uint32_t b = 0; b < r_boxes; ++b) {
+            const int32_t col = static_cast<int32_t>(64 * b);
+            tma_load_2d(dst + b * op_box, &p.tm_op, &bars.op_full[buf], col, at);
+            if (MODE != kRow) tma_load_2d(dst + op_half + b * op_box, &p.tm_op, &bars.op_full[buf], r + col, at);
+          }
         }
-        issued = o + 1;
+        issued = n + 1;
+      };
+      for (int o = 0; ok && o < no; ++o) {
+        operand(o, 0);
         if constexpr (SRC == kSrcBf16) {
-          for (int i = 0; i < ni; ++i, ++g) {
+          const int32_t at = (o0 + o) * 128;
+          for (int i = 0; ok && i < ni; ++i) {
             const uint32_t slot = g % stages;
             ok = pass_wait(bars, &bars.empty[slot], ((g / stages) & 1u) ^ 1u, p.status, kDevTimeoutEmpty);
             if (!ok) break;
@@ -204,8 +244,10 @@ __global__ void __launch_bounds__(kPassThreads<SRC>, 1) adapter_pass_kernel(cons
             const int32_t in = (i0 + i) * 128, col = MODE == kRow ? at : in, row = MODE == kRow ? in : at;
             tma_load_2d_once(tile, &p.tm_s, &bars.full[slot], col, row, once);
             tma_load_2d_once(tile + kBox, &p.tm_s, &bars.full[slot], col + 64, row, once);
+            ++g;
           }
         }
+        for (int sb = 1; ok && sb < subs; ++sb) operand(o, sb);
       }
       // the last fill of every buffer must have landed before the block exits
       bool drained = true;
@@ -228,51 +270,70 @@ __global__ void __launch_bounds__(kPassThreads<SRC>, 1) adapter_pass_kernel(cons
       return __all_sync(0xffffffffu, pass_wait(bars, bar, parity, p.status, code)) != 0;
     };
     bool ok = MODE != kBoth || arrived(&bars.p_full, 0, kDevTimeoutFull);
-    uint32_t slot = 0, phase = 0;
+    uint32_t slot = 0, phase = 0;  // of an outer block's first tile
     for (int o = 0; ok && o < no; ++o) {
-      const int buf = o % p.plan.op_bufs, ub = MODE == kBoth ? o % p.plan.u_bufs : 0;
-      ok = arrived(&bars.op_full[buf], (o / p.plan.op_bufs) & 1, kDevTimeoutFull);
-      if (ok && MODE == kBoth) ok = arrived(&bars.u_empty[ub], ((o / p.plan.u_bufs) & 1) ^ 1, kDevTimeoutAccum);
-      if (!ok) break;
-      const uint32_t sop = smem_u32(sm_op) + static_cast<uint32_t>(buf) * op_bytes;
-      for (int i = 0; i < ni; ++i) {
-        ok = arrived(&bars.full[slot], phase, kDevTimeoutFull);
+      const int ub = MODE == kBoth ? o % p.plan.u_bufs : 0;
+      // The pieces of the operand one after another, each over all the tiles, which stay
+      // until the last one has been multiplied.
+      for (int sb = 0; ok && sb < subs; ++sb) {
+        const int n = o * subs + sb, buf = n % p.plan.op_bufs;
+        ok = arrived(&bars.op_full[buf], (n / p.plan.op_bufs) & 1, kDevTimeoutFull);
+        if (ok && MODE == kBoth && sb == 0)
+          ok = arrived(&bars.u_empty[ub], ((o / p.plan.u_bufs) & 1) ^ 1, kDevTimeoutAccum);
         if (!ok) break;
-        tc_fence_after();
-        const uint32_t ss = smem_u32(sm_s) + slot * kTileBytes;
-        const uint32_t d_inner = t_acc + static_cast<uint32_t>(i) * r_cols;
-        if constexpr (kHasRow) {  // 16 columns of S a step
-          const uint32_t d_row = MODE == kRow ? d_inner : t_u + static_cast<uint32_t>(ub) * r_cols;
-          const uint32_t sp = smem_u32(sm_p) + static_cast<uint32_t>(i) * p_block;
+        const uint32_t sop = smem_u32(sm_op) + static_cast<uint32_t>(buf) * op_bytes;
+        uint32_t at = slot, at_phase = phase;
+        for (int i = 0; i < ni; ++i) {
+          if (sb == 0) {
+            ok = arrived(&bars.full[at], at_phase, kDevTimeoutFull);
+            if (!ok) break;
+            tc_fence_after();
+          }
+          const uint32_t ss = smem_u32(sm_s) + at * kTileBytes;
+          const uint32_t d_inner = t_acc + static_cast<uint32_t>(i) * r_cols;
+          if constexpr (kHasRow) {  // 16 columns of S a step
+            const uint32_t d_row = MODE == kRow ? d_inner : t_u + static_cast<uint32_t>(ub) * r_cols;
+            const uint32_t sp = smem_u32(sm_p) + static_cast<uint32_t>(i) * p_block;
+            if (sb == 0) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint64_t da = make_sdesc(ss + (k / 4) * kBox + (k % 4) * 32, 16, 1024, kSw128);
-            const uint64_t db = kOpKmajor
-                                    ? make_sdesc(sop + (k / 4) * (op_bytes / 2) + (k % 4) * 32, 16, 1024, kSw128)
-                                    : make_sdesc((MODE == kRow ? sop : sp) + k * 2048, kBox, 1024, kSw128);
-            if (elect_one()) mma_bf16(d_row, da, db, idesc_row, ((MODE == kRow ? o : i) | k) != 0);
+              for (int k = 0; k < 8; ++k) {
+                const uint64_t da = make_sdesc(ss + (k / 4) * kBox + (k % 4) * 32, 16, 1024, kSw128);
+                const uint64_t db = kOpKmajor
+                                        ? make_sdesc(sop + (k / 4) * (op_bytes / 2) + (k % 4) * 32, 16, 1024, kSw128)
+                                        : make_sdesc((MODE == kRow ? sop : sp) + k * 2048, kBox, 1024, kSw128);
+                if (elect_one()) mma_bf16(d_row, da, db, idesc_row, ((MODE == kRow ? o : i) | k) != 0);
+                __syncwarp();
+              }
+            }
+          }
+          if constexpr (kHasCol) {  // 16 rows of S a step, with the upper and the low halves
+            const int steps = 8 / subs;
+#pragma unroll 2
+            for (int k = 0; k < steps; ++k) {
+              const uint64_t da = make_sdesc(ss + (sb * steps + k) * 2048, kBox, 1024, kSw128);
+              const uint64_t db = make_sdesc(sop + k * 2048, op_box, 1024, kSw128);
+              const uint64_t db_low = make_sdesc(sop + op_half + k * 2048, op_box, 1024, kSw128);
+              if (elect_one()) {
+                mma_bf16(d_inner, da, db, idesc_col, (o | sb | k) != 0);
+                mma_bf16(d_inner, da, db_low, idesc_col, true);
+              }
+              __syncwarp();
+            }
+          }
+          if (sb == subs - 1) {
+            if (elect_one()) tc_commit(&bars.empty[at]);
             __syncwarp();
           }
+          if (++at == static_cast<uint32_t>(stages)) at = 0, at_phase ^= 1u;
         }
-        if constexpr (kHasCol) {  // 16 rows of S a step
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint64_t da = make_sdesc(ss + k * 2048, kBox, 1024, kSw128);
-            const uint64_t db = make_sdesc(sop + k * 2048, kBox, 1024, kSw128);
-            if (elect_one()) mma_bf16(d_inner, da, db, idesc_col, (o | k) != 0);
-            __syncwarp();
-          }
+        if (!ok) break;
+        if (elect_one()) {
+          tc_commit(&bars.op_empty[buf]);
+          if (MODE == kBoth && sb == 0) tc_commit(&bars.u_full[ub]);
         }
-        if (elect_one()) tc_commit(&bars.empty[slot]);
         __syncwarp();
-        if (++slot == static_cast<uint32_t>(stages)) slot = 0, phase ^= 1u;
+        if (sb == subs - 1) slot = at, phase = at_phase;
       }
-      if (!ok) break;
-      if (elect_one()) {
-        tc_commit(&bars.op_empty[buf]);
-        if (MODE == kBoth) tc_commit(&bars.u_full[ub]);
-      }
-      __syncwarp();
     }
     if (elect_one()) tc_commit(&bars.done);
     __syncwarp();
@@ -483,11 +544,10 @@ __global__ void __launch_bounds__(kPassThreads<SRC>, 1) adapter_pass_kernel(cons
 #pragma unroll
         for (int j = 0; j < 8; ++j) s[j] = column_sum(c + j);
         const int64_t row = static_cast<int64_t>(i0 + c / r) * 128 + 4 * lane;
-        __nv_bfloat16* dst = p.out + row * r + c % r;
         auto put = [&](int k, float a0, float a1, float a2, float a3, float a4, float a5, float a6, float a7) {
           if (row + k < inner_rows)
-            *reinterpret_cast<uint4*>(dst + k * r) =
-                make_uint4(pack_bf16(a0, a1), pack_bf16(a2, a3), pack_bf16(a4, a5), pack_bf16(a6, a7));
+            store_halves(p.out, p.pair, row + k, r, c % r, split_bf16(a0, a1), split_bf16(a2, a3), split_bf16(a4, a5),
+                         split_bf16(a6, a7));
         };
         put(0, s[0].x, s[1].x, s[2].x, s[3].x, s[4].x, s[5].x, s[6].x, s[7].x);
         put(1, s[0].y, s[1].y, s[2].y, s[3].y, s[4].y, s[5].y, s[6].y, s[7].y);
@@ -508,8 +568,9 @@ __global__ void __launch_bounds__(kPassThreads<SRC>, 1) adapter_pass_kernel(cons
 // the ranges' partial sums, added in order and rounded
 
 struct ReduceJob {
-  const float* part;   // [n][blocks][r][128]
-  __nv_bfloat16* out;  // [rows][r], or [r][rows] (transposed)
+  const float* part;    // [n][blocks][r][128]
+  __nv_bfloat16* out;   // [rows][r], or [r][rows] (transposed)
+  __nv_bfloat16* pair;  // [rows][2 r], two bf16 a value (not transposed; either may be null)
   int64_t rows;
   int n, r;
 };
@@ -553,10 +614,10 @@ __global__ void __launch_bounds__(kRedThreads) reduce_kernel(ReduceJob a, Reduce
     __syncthreads();
     const int row = threadIdx.x >> 1, c = (threadIdx.x & 1) * 8;
     if (block * 128 + row < j.rows) {
-      uint32_t o[4];
+      Halves o[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = pack_bf16(tile[c + 2 * i][row], tile[c + 2 * i + 1][row]);
-      *reinterpret_cast<uint4*>(j.out + (block * 128 + row) * j.r + c0 + c) = make_uint4(o[0], o[1], o[2], o[3]);
+      for (int i = 0; i < 4; ++i) o[i] = split_bf16(tile[c + 2 * i][row], tile[c + 2 * i + 1][row]);
+      store_halves(j.out, j.pair, block * 128 + row, j.r, c0 + c, o[0], o[1], o[2], o[3]);
     }
   }
 }
@@ -569,9 +630,11 @@ __global__ void __launch_bounds__(kRedThreads) reduce_kernel(ReduceJob a, Reduce
 // adds up, each measured on the passes themselves: a tile takes 0.7 us to widen, or
 // the time of its bytes at 6.2 TB/s over the blocks at work (0.4 us at least) and
 // 0.2 us, more where U has one buffer; the streamed operand comes at 80 GB/s a block,
-// beside the tiles where it has two buffers; a cluster's sums cost 3 us and 40 GB/s a
+// beside the tiles where it has two buffers (a piece more costs 0.1 us then, else 0.5);
+// a cluster's sums cost 3 us and 40 GB/s a
 // block (80 GB/s without a cluster); sums that go through memory are written and read
-// at 8 TB/s, and a reduce_kernel of its own costs 5 us with its launch.
+// at 8 TB/s (kBoth's are read at 3.5 where L2 no longer holds them), and a reduce_kernel
+// of its own costs 5 us with its launch.
 PassPlan plan_pass(int64_t R, int64_t C, int r, int mode, bool eight) {
   const int64_t rb = (R + 127) / 128, cb = (C + 127) / 128;
   const int64_t inner_blocks = mode == kRow ? rb : cb, outer_blocks = mode == kRow ? cb : rb;
@@ -579,7 +642,7 @@ PassPlan plan_pass(int64_t R, int64_t C, int r, int mode, bool eight) {
   // 1 KB of the dynamic part goes into its alignment
   const uint32_t raw = eight ? (kAhead + 1) * kRawBytes : 0u;
   const uint32_t p_block = mode == kBoth ? boxes * kBox : 0u;
-  const uint32_t op_one = mode == kRow && eight ? 256u * static_cast<uint32_t>(r) : boxes * kBox;
+  const uint32_t op_one = mode != kRow ? 2 * boxes * kBox : eight ? 256u * static_cast<uint32_t>(r) : boxes * kBox;
   const uint32_t min_stages = eight ? 2 : 3, most_stages = eight ? 3 : kMaxStages;
   // clusters of 1 to 6 such blocks that a B200 holds at once, less one for the sizes
   // that depend on which SMs a chip has
@@ -592,49 +655,59 @@ PassPlan plan_pass(int64_t R, int64_t C, int r, int mode, bool eight) {
     if (inner * rc + c.u_bufs * rc > 512 && c.u_bufs == 2) c.u_bufs = 1;
     if (inner * rc + c.u_bufs * rc > 512) break;
     const uint32_t red = static_cast<uint32_t>(inner * r) * 512u;
-    c.op_bufs = 2;
-    auto fixed = [&]() { return inner * p_block + c.op_bufs * op_one + raw + 1024u; };
-    if (fixed() + min_stages * kTileBytes > kSmemMost) c.op_bufs = 1;
-    if (fixed() + min_stages * kTileBytes > kSmemMost || red + 1024u > kSmemMost) break;
-    const uint32_t fit = (kSmemMost - fixed()) / kTileBytes;
-    c.stages = static_cast<int>(fit < most_stages ? fit : most_stages);
-    c.smem = fixed() + c.stages * kTileBytes;
-    if (c.smem < red + 1024u) c.smem = red + 1024u;
+    if (red + 1024u > kSmemMost) break;
     c.tmem_cols = 32;
     while (c.tmem_cols < inner * rc + c.u_bufs * rc) c.tmem_cols *= 2;
     const int64_t n_inner = (inner_blocks + inner - 1) / inner;
     c.n_inner = static_cast<int>(n_inner);
-    const double u_cost = mode == kBoth ? 8.0 * r * 128 * static_cast<double>(n_inner * rb) / 8.0e12 : 0.0;
+    // written at 8 TB/s, read back at 3.5 where they no longer all lie in L2
+    const double u_bytes = mode == kBoth ? 4.0 * r * 128 * static_cast<double>(n_inner * rb) : 0.0;
+    const double u_cost = u_bytes / 8.0e12 + u_bytes / (u_bytes < 60e6 ? 8.0e12 : 3.5e12);
     // kBoth's sums are too many for a cluster's exchange to pay (17 us at 4608 x 12288)
     const int most_ranks = mode == kBoth ? 1 : kMaxRanks;
-    for (int ranks = 1; ranks <= most_ranks && ranks <= outer_blocks; ++ranks) {
-      const int64_t fill = kRoom[ranks] / n_inner;  // groups that still fit at once
-      for (int pass = 0; pass < (fill > 1 ? 2 : 1); ++pass) {
-        int64_t groups = pass == 0 ? 1 : fill;
-        const int64_t outer = (outer_blocks + ranks * groups - 1) / (ranks * groups);
-        groups = (outer_blocks + ranks * outer - 1) / (ranks * outer);
-        if (pass == 1 && groups == 1) continue;
-        const int64_t clusters = n_inner * groups;
-        const double waves = static_cast<double>((clusters + kRoom[ranks] - 1) / kRoom[ranks]);
-        const double at_work = static_cast<double>(clusters < kRoom[ranks] ? clusters * ranks : kRoom[ranks] * ranks);
-        const double bytes = (eight ? 16384.0 : 32768.0) * at_work / 6.2e12, least = eight ? 0.7e-6 : 0.4e-6;
-        double tile = (bytes > least ? bytes : least) + (eight ? 0.0 : 0.2e-6);
-        if (mode == kBoth && (c.u_bufs == 1 || c.op_bufs == 1)) tile *= 1.3;
-        const double tiles = inner * tile, op = op_one / 80e9;
-        const double step = c.op_bufs == 1 ? tiles + op + 0.5e-6 : tiles > op ? tiles : op;
-        double cost = waves * (outer * step + 1e-6) + u_cost;
-        if (ranks > 1) cost += 3e-6 + inner * r * 512 / 40e9;
-        if (ranks == 1 && groups == 1) cost += inner * r * 512 / 80e9;
-        if (groups > 1)
-          cost += (mode == kBoth ? 0.0 : 5e-6) + 8.0 * r * 128 * static_cast<double>(groups * inner_blocks) / 8.0e12;
-        if (best.inner == 0 || cost < best.cost) {
-          best = c;
-          best.cost = cost;
-          best.ranks = ranks;
-          best.groups = static_cast<int>(groups);
-          best.outer = static_cast<int>(outer);
+    for (int form = 0; form < 6; ++form) {  // one or two buffers; 1, 2 or 4 pieces
+      c.op_bufs = 2 - form % 2;
+      c.subs = 1 << form / 2;
+      if (mode == kRow && c.subs > 1) break;
+      const uint32_t fixed = inner * p_block + c.op_bufs * (op_one / c.subs) + raw + 1024u;
+      if (fixed + min_stages * kTileBytes > kSmemMost) continue;
+      const uint32_t fit = (kSmemMost - fixed) / kTileBytes;
+      c.stages = static_cast<int>(fit < most_stages ? fit : most_stages);
+      if (c.subs > 1 && c.stages <= inner) continue;  // the tiles of an outer block stay, and one comes
+      c.smem = fixed + c.stages * kTileBytes;
+      if (c.smem < red + 1024u) c.smem = red + 1024u;
+      for (int ranks = 1; ranks <= most_ranks && ranks <= outer_blocks; ++ranks) {
+        const int64_t fill = kRoom[ranks] / n_inner;  // groups that still fit at once
+        for (int pass = 0; pass < (fill > 1 ? 2 : 1); ++pass) {
+          int64_t groups = pass == 0 ? 1 : fill;
+          const int64_t outer = (outer_blocks + ranks * groups - 1) / (ranks * groups);
+          groups = (outer_blocks + ranks * outer - 1) / (ranks * outer);
+          if (pass == 1 && groups == 1) continue;
+          const int64_t clusters = n_inner * groups;
+          const double waves = static_cast<double>((clusters + kRoom[ranks] - 1) / kRoom[ranks]);
+          const double at_work = static_cast<double>(clusters < kRoom[ranks] ? clusters * ranks : kRoom[ranks] * ranks);
+          const double bytes = (eight ? 16384.0 : 32768.0) * at_work / 6.2e12, least = eight ? 0.7e-6 : 0.4e-6;
+          double tile = (bytes > least ? bytes : least) + (eight ? 0.0 : 0.2e-6);
+          if (mode == kBoth && (c.u_bufs == 1 || c.op_bufs == 1)) tile *= 1.3;
+          const double tiles = inner * tile, op = op_one / 80e9;
+          const double step = c.op_bufs == 1 ? tiles + op + 0.5e-6 * c.subs
+                                             : (tiles > op ? tiles : op) + 0.1e-6 * (c.subs - 1);
+          double sums = 1e-6;
+          if (ranks > 1) sums += 3e-6 + inner * r * 512 / 40e9;
+          if (ranks == 1 && groups == 1) sums += inner * r * 512 / 80e9;
+          double cost = waves * (outer * step + sums) + u_cost;
+          if (groups > 1)
+            cost += (mode == kBoth ? 0.0 : 5e-6) + 8.0 * r * 128 * static_cast<double>(groups * inner_blocks) / 8.0e12;
+          if (best.inner == 0 || cost < best.cost) {
+            best = c;
+            best.cost = cost;
+            best.ranks = ranks;
+            best.groups = static_cast<int>(groups);
+            best.outer = static_cast<int>(outer);
+          }
         }
       }
+      if (c.op_bufs == 2) break;  // more pieces are no better
     }
   }
   return best;
@@ -655,10 +728,10 @@ LoraPlan plan_lora(int64_t M, int64_t N, int64_t K, int r) {
   l.dy = plan_pass(M, N, r, kBoth, false);
   const PassPlan row = plan_pass(M, N, r, kRow, false);
   l.dy_col = plan_pass(M, N, r, kCol, false);
-  // (measured at 4608 x 12288: rank 128 102 us with kBoth, 109 without; rank 256 323, 142)
+  // (measured at 4608 x 12288: rank 64 72 us with kBoth; rank 128 131 with, 126 without)
   l.both = l.dy.cost <= row.cost + l.dy_col.cost + 5e-6;
   if (!l.both) l.dy = row;
-  const size_t mr = static_cast<size_t>(M) * r;
+  const size_t mr = static_cast<size_t>(M) * r;  // T and dT are two bf16 a value
   auto sums = [r](int64_t rows, int n) { return static_cast<size_t>((rows + 127) / 128) * 512 * r * n; };
   size_t part = 0;
   auto more = [&part](size_t n) { part = n > part ? n : part; };
@@ -667,8 +740,8 @@ LoraPlan plan_lora(int64_t M, int64_t N, int64_t K, int r) {
   if (!l.both && l.dy_col.groups > 1) more(sums(N, l.dy_col.groups));
   if (l.up.groups > 1) more(sums(K, l.up.groups));
   l.t = 0;
-  l.dt = align256(l.t + mr * 2);
-  l.u = align256(l.dt + mr * 2);
+  l.dt = align256(l.t + mr * 4);
+  l.u = align256(l.dt + mr * 4);
   l.part = align256(l.u + (l.both ? sums(M, l.dy.n_inner) : 0));
   l.total = align256(l.part + part);
   return l;
@@ -716,7 +789,7 @@ cudaError_t run(const LoraBackwardLaunch& l, cudaStream_t s) {
   const LoraPlan plan = plan_lora(l.M, l.N, l.K, l.r);
   const uint64_t M = l.M, N = l.N, K = l.K, r = l.r;
   auto* t = reinterpret_cast<__nv_bfloat16*>(l.ws + plan.t);
-  auto* dt = l.dt != nullptr ? static_cast<__nv_bfloat16*>(l.dt) : reinterpret_cast<__nv_bfloat16*>(l.ws + plan.dt);
+  auto* dt = reinterpret_cast<__nv_bfloat16*>(l.ws + plan.dt);
   auto* part = reinterpret_cast<float*>(l.ws + plan.part);
   const ReduceJob none = {};
   PassLaunch p = {};
@@ -731,53 +804,60 @@ cudaError_t run(const LoraBackwardLaunch& l, cudaStream_t s) {
   constexpr auto kSw = CU_TENSOR_MAP_SWIZZLE_128B;
 
   // one pass and, where its clusters leave several sums, their reduction
-  auto pass = [&](auto launch, const PassPlan& pass_plan, int64_t C, __nv_bfloat16* out, int64_t rows,
-                  bool transposed) {
+  auto pass = [&](auto launch, const PassPlan& pass_plan, int64_t C, __nv_bfloat16* out, __nv_bfloat16* pair,
+                  int64_t rows, bool transposed) {
     p.C = C;
     p.plan = pass_plan;
     p.out = out;
+    p.pair = pair;
     p.transposed = transposed ? 1 : 0;
     p.early = pass_plan.groups == 1 && !transposed ? 1 : 0;  // dA's pass is the last
     const cudaError_t e = launch(p, s);
     if (e != cudaSuccess || pass_plan.groups == 1) return e;
-    const ReduceJob job = {part, out, rows, pass_plan.groups, l.r};
+    const ReduceJob job = {part, out, pair, rows, pass_plan.groups, l.r};
     return transposed ? launch_reduce<true>(job, none, s) : launch_reduce<false>(job, none, s);
   };
   auto* db = static_cast<__nv_bfloat16*>(l.db);
+  auto* dt_out = static_cast<__nv_bfloat16*>(l.dt);
 
   // T = x A^T
   if (!encode_bf16_2d(&p.tm_op, l.a, K, r, K * 2, 64, static_cast<uint32_t>(r), kSw)) return cudaErrorInvalidValue;
-  cudaError_t e = pass(launch_pass<FMT, kRow>, plan.down, l.K, t, l.M, false);
+  cudaError_t e = pass(launch_pass<FMT, kRow>, plan.down, l.K, nullptr, t, l.M, false);
   if (e != cudaSuccess) return e;
 
   // dT = dY B and dB = dY^T T
-  CUtensorMap tm_b, tm_t;
+  CUtensorMap tm_b;
+  auto halves_of = [&](const __nv_bfloat16* pair, const PassPlan& c) {
+    return encode_bf16_2d(&p.tm_op, pair, 2 * r, M, 4 * r, 64, 128u / static_cast<uint32_t>(c.subs), kSw);
+  };
   if (!encode_bf16_2d(&p.tm_s, l.dy, N, M, N * 2, 64, 128, kSw) ||
-      !encode_bf16_2d(&tm_b, l.b, r, N, r * 2, 64, 128, kSw) || !encode_bf16_2d(&tm_t, t, r, M, r * 2, 64, 128, kSw))
+      !encode_bf16_2d(&tm_b, l.b, r, N, r * 2, 64, 128, kSw))
     return cudaErrorInvalidValue;
   if (plan.both) {
     p.tm_p = tm_b;
-    p.tm_op = tm_t;
+    if (!halves_of(t, plan.dy)) return cudaErrorInvalidValue;
     p.C = l.N;
     p.plan = plan.dy;
     p.out = db;
+    p.pair = nullptr;
     p.transposed = 0;
     p.early = 0;
     e = launch_pass<kSrcBf16, kBoth>(p, s);
     if (e == cudaSuccess)
-      e = launch_reduce<false>(ReduceJob{p.u_part, dt, l.M, plan.dy.n_inner, l.r},
-                               plan.dy.groups > 1 ? ReduceJob{part, db, l.N, plan.dy.groups, l.r} : none, s);
+      e = launch_reduce<false>(ReduceJob{p.u_part, dt_out, dt, l.M, plan.dy.n_inner, l.r},
+                               plan.dy.groups > 1 ? ReduceJob{part, db, nullptr, l.N, plan.dy.groups, l.r} : none, s);
   } else {
     p.tm_op = tm_b;
-    e = pass(launch_pass<kSrcBf16, kRow>, plan.dy, l.N, dt, l.M, false);
-    p.tm_op = tm_t;
-    if (e == cudaSuccess) e = pass(launch_pass<kSrcBf16, kCol>, plan.dy_col, l.N, db, l.N, false);
+    e = pass(launch_pass<kSrcBf16, kRow>, plan.dy, l.N, dt_out, dt, l.M, false);
+    if (e != cudaSuccess) return e;
+    if (!halves_of(t, plan.dy_col)) return cudaErrorInvalidValue;
+    e = pass(launch_pass<kSrcBf16, kCol>, plan.dy_col, l.N, db, nullptr, l.N, false);
   }
   if (e != cudaSuccess) return e;
 
   // dA^T = x^T dT
-  if (!encode_bf16_2d(&p.tm_op, dt, r, M, r * 2, 64, 128, kSw)) return cudaErrorInvalidValue;
-  return pass(launch_pass<FMT, kCol>, plan.up, l.K, static_cast<__nv_bfloat16*>(l.da), l.K, true);
+  if (!halves_of(dt, plan.up)) return cudaErrorInvalidValue;
+  return pass(launch_pass<FMT, kCol>, plan.up, l.K, static_cast<__nv_bfloat16*>(l.da), nullptr, l.K, true);
 }
 
 }  // namespace

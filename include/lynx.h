@@ -408,8 +408,8 @@ LYNX_API size_t lynx_lora_backward_workspace_bytes(int64_t M, int64_t N, int64_t
 /* dT = dY B [M,r], dB = dY^T T [N,r], dA = dT^T x [r,K], with T = x A^T computed
  * from the checkpoint.  All outputs bf16, overwritten; dT may be NULL (not
  * wanted).  Sums in fp32 in an order that only the shape fixes (equal calls give
- * equal bits); T and dT are rounded to bf16 before they enter the second
- * products, as T is in lynx_linear.
+ * equal bits); T and dT enter the second products as the sum of two bf16, off
+ * by at most 2^-17 of the value.
  *   dY [M,N], q and e as stored (format says how), A [r,K], B [N,r].
  *   workspace: device scratch of workspace_bytes >=
  *   lynx_lora_backward_workspace_bytes(M,N,K,r). */
