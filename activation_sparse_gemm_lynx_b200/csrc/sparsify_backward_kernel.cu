@@ -205,7 +205,7 @@ struct BackLaunch {
 
 struct BackBars {
   uint64_t full[kMaxStages], empty[kMaxStages];
-  uint64_t dt_full, d_full[kGroups], d_empty[kGroups], done[kGroups], out_empty[kGroups];
+  uint64_t dt_full, mma_done, d_full[kGroups], d_empty[kGroups], done[kGroups], out_empty[kGroups];
   uint32_t tmem_base;
   volatile uint32_t abort_flag;
 };
@@ -242,6 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1) sparsify_backward_kernel(const __
       mbar_init(&bars.empty[s], kGroupWarps);
     }
     mbar_init(&bars.dt_full, 1);
+    mbar_init(&bars.mma_done, 1);
     for (int i = 0; i < kGroups; ++i) {
       mbar_init(&bars.d_full[i], 1);
       mbar_init(&bars.d_empty[i], kGroupWarps);
@@ -283,12 +284,12 @@ __global__ void __launch_bounds__(kThreads, 1) sparsify_backward_kernel(const __
         ++issued;
         if (++slot == stages) slot = 0, phase ^= 1u;
       }
-      if (bars.abort_flag) {
-        // copies in flight must land before the block exits
-        if (LORA) mbar_wait(&bars.dt_full, 0, kWaitLimitNs / 8);
-        for (int i = issued - 1; i >= 0 && i >= issued - stages; --i)
-          mbar_wait(&bars.full[i % stages], (i / stages) & 1, kWaitLimitNs / 8);
-      }
+      // Copies in flight must land before the block exits, whichever warp gives up and
+      // whenever it does (behind the last tile they have landed already).
+      bool drained = !LORA || mbar_wait(&bars.dt_full, 0, kWaitLimitNs / 8);
+      for (int i = issued - 1; i >= 0 && i >= issued - stages; --i)
+        drained &= mbar_wait(&bars.full[i % stages], (i / stages) & 1, kWaitLimitNs / 8);
+      if (!drained) record_error(p.status, kDevTimeoutDrain);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ dT A
@@ -318,6 +319,11 @@ __global__ void __launch_bounds__(kThreads, 1) sparsify_backward_kernel(const __
         __syncwarp();
         if (++slot == stages) slot = 0, phase ^= 1u;
       }
+      // and MMAs in flight must be done before their TMEM is freed
+      if (elect_one()) tc_commit(&bars.mma_done);
+      __syncwarp();
+      if (!mbar_wait(&bars.mma_done, 0, kWaitLimitNs / 8) && lane == 0) record_error(p.status, kDevTimeoutDrain);
+      __syncwarp();
     }
   } else if (warp < kRoleWarps) {
     // ------------------------------------------------------------ stores of dX
