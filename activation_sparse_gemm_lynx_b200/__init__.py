@@ -58,5 +58,7 @@ from .lynx import (  # noqa: F401
     lynx_w4_quantize,
     lynx_version,
     lynx_workspace_bytes,
+    lynx_workspace_meta,
+    lynx_workspace_meta_offset,
     library,
 )

@@ -460,6 +460,11 @@ size_t lynx_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t r) {
   return workspace_layout(M, K, r).total;
 }
 
+size_t lynx_workspace_meta_offset(int64_t M, int64_t K) {
+  if (M <= 0 || K <= 0) return 0;
+  return workspace_layout(M, K, 0).meta;
+}
+
 size_t lynx_sparsify_workspace_bytes(int64_t M, int64_t K) {
   if (M <= 0 || K <= 0) return 0;
   return sparsify_workspace(M).total;

@@ -231,19 +231,25 @@ size_t lynx_sparsify_backward_workspace_bytes(int64_t M, int64_t K) {
   return align256(static_cast<size_t>(M) * sizeof(float2));
 }
 
-int lynx_sparsify_backward(const void* G, const void* q, const void* e, const void* dT, const void* A, int64_t M,
-                           int64_t K, int64_t r, int format, void* dX, void* workspace, size_t workspace_bytes,
-                           void* stream) {
+}  // extern "C"
+
+namespace {
+
+// meta null: the selection of the checkpoint's values
+int sparsify_backward(const void* G, const void* q, const void* e, const void* meta, const void* dT, const void* A,
+                      int64_t M, int64_t K, int64_t r, int format, void* dX, void* workspace, size_t workspace_bytes,
+                      void* stream) {
   if (any_null(G, q, e, dX) || !format_ok(format)) return LYNX_ERR_INVALID_ARG;
   if (const int st = check_branch(dT, A, r)) return st;
   if (!rows_ok(M) || !k_ok(K)) return LYNX_ERR_UNSUPPORTED_SHAPE;
-  if (any_misaligned(G, q, e, dT, A, dX, workspace)) return LYNX_ERR_MISALIGNED;
+  if (any_misaligned(G, q, e, meta, dT, A, dX, workspace)) return LYNX_ERR_MISALIGNED;
   if (workspace == nullptr) return LYNX_ERR_INVALID_ARG;
   const size_t need = lynx_sparsify_backward_workspace_bytes(M, K);
   if (workspace_bytes < need) return LYNX_ERR_WORKSPACE_TOO_SMALL;
   if (any_overlap({{dX, bytes_of(M, K, 2)}, {workspace, need}}, {{G, bytes_of(M, K, 2)},
                                                                  {q, bytes_of(M, K, 1)},
                                                                  {e, bytes_of(M, K / 32, 1)},
+                                                                 {meta, lynx_meta_bytes(M, K)},
                                                                  {dT, bytes_of(M, r, 2)},
                                                                  {A, bytes_of(r, K, 2)}}))
     return LYNX_ERR_INVALID_ARG;
@@ -257,6 +263,7 @@ int lynx_sparsify_backward(const void* G, const void* q, const void* e, const vo
   p.e = e;
   p.dt = dT;
   p.a = A;
+  p.meta = meta;
   p.dx = dX;
   p.coef = static_cast<float2*>(workspace);
   p.M = M;
@@ -266,6 +273,23 @@ int lynx_sparsify_backward(const void* G, const void* q, const void* e, const vo
   p.stall_test = stall_test_enabled();
   p.status = status;
   return status_of(launch_sparsify_backward(p, sms, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+int lynx_sparsify_backward(const void* G, const void* q, const void* e, const void* dT, const void* A, int64_t M,
+                           int64_t K, int64_t r, int format, void* dX, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  return sparsify_backward(G, q, e, nullptr, dT, A, M, K, r, format, dX, workspace, workspace_bytes, stream);
+}
+
+int lynx_sparsify_backward_meta(const void* G, const void* q, const void* e, const void* meta, const void* dT,
+                                const void* A, int64_t M, int64_t K, int64_t r, int format, void* dX, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  if (meta == nullptr) return LYNX_ERR_INVALID_ARG;
+  return sparsify_backward(G, q, e, meta, dT, A, M, K, r, format, dX, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -201,6 +201,7 @@ struct SparsifyBackwardLaunch {
   const void* e;   // [M,K/32] bytes
   const void* dt;  // [M,r] bf16, or null
   const void* a;   // [r,K] bf16 (with dt)
+  const void* meta;  // the forward pass's 2:4 metadata, or null: select from the checkpoint
   void* dx;        // [M,K] bf16
   float2* coef;    // [M] scratch: s and D / Lk per row
   int64_t M, K;

@@ -6,6 +6,11 @@
 // ds/dx_k = sign(x_k) / Lk - m_k sign(x_k) L / Lk^2 = sign(x_k) (1 - s m_k) / Lk.
 // The LoRA branch adds dT A, a product of rank r.
 //
+// The selection m is the forward pass's where its metadata is given (META): the 8-bit
+// values tie where x did not, and a selection made again from them differs in 3 to 11 %
+// of the groups (heavy-tailed and GELU inputs).  The metadata adds 1/8 byte a value to
+// each reading (4608 x 12288, rank 64: 94 us for 92).  Without it m is the 2:4 selection of the checkpoint's values.
+//
 // Every output needs its row's three sums, so there are two passes over G and
 // the checkpoint: row_sums_kernel streams them once, sparsify_backward_kernel
 // takes 128 x 64 tiles in the opposite order (the rows read last are still in
@@ -65,6 +70,21 @@ __device__ __forceinline__ uint32_t keep_bits(uint32_t a) {
   return two_of_three(next, over, prmt<0x2103>(next));
 }
 
+// The same bits from the metadata, for word w of 16 values: a nibble lo | hi << 2 a word
+__device__ __forceinline__ uint32_t kept_bits(uint32_t nibbles, int w) {
+  const uint32_t n = nibbles >> (4 * w);
+  return (0x80u << ((n & 3u) << 3)) | (0x80u << ((n & 12u) << 1));
+}
+
+// Where the 16 bits of a row's first 16 values lie in its row block's metadata; those of
+// 16-value unit i are meta_unit(i) behind it (the operand layout of tcgen05.mma.sp)
+__device__ __forceinline__ uint32_t meta_row(uint32_t row) {
+  return ((row & 7u) + 16u * (row >> 4)) * 16u + ((row >> 3) & 1u) * 2u;
+}
+__device__ __forceinline__ int64_t meta_unit(int i) {
+  return static_cast<int64_t>(i >> 3) * kMetaBlockBytes + (i & 1) * 128 + ((i >> 1) & 3) * 4;
+}
+
 // ---------------------------------------------------------------------------
 // row sums
 
@@ -73,14 +93,14 @@ constexpr int kRowWarps = kRowThreads / 32;
 constexpr int kAhead = 2;  // steps in flight (3, with a quarter fewer blocks an SM, took 49 us for 38)
 
 // 16 values: sums of |x|, of the kept |x| and of the kept g x, before the factor
-template <int FMT>
-__device__ __forceinline__ void sums16(const uint4& qv, const uint4& ga, const uint4& gb, float& bl, float& bk,
-                                       float& bd) {
+template <int FMT, bool META>
+__device__ __forceinline__ void sums16(const uint4& qv, const uint4& ga, const uint4& gb, uint32_t nibbles, float& bl,
+                                       float& bk, float& bd) {
   const uint32_t qw[4] = {qv.x, qv.y, qv.z, qv.w};
   const uint32_t gw[8] = {ga.x, ga.y, ga.z, ga.w, gb.x, gb.y, gb.z, gb.w};
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
-    const uint32_t keep = keep_bits(magnitudes<FMT>(qw[w]));
+    const uint32_t keep = META ? kept_bits(nibbles, w) : keep_bits(magnitudes<FMT>(qw[w]));
     float v[4];
     ckpt8_decode4<FMT>(qw[w], v);
     const float g[4] = {bf16_lo(gw[2 * w]), bf16_hi(gw[2 * w]), bf16_lo(gw[2 * w + 1]), bf16_hi(gw[2 * w + 1])};
@@ -97,7 +117,7 @@ __device__ __forceinline__ void sums16(const uint4& qv, const uint4& ga, const u
 
 // coef[m] = (s, D / Lk).  A block has `rows` rows, kRowWarps / rows warps each;
 // 16 columns a lane and step.
-template <int FMT>
+template <int FMT, bool META>
 __global__ void __launch_bounds__(kRowThreads, 4) row_sums_kernel(SparsifyBackwardLaunch p, int rows) {
   __shared__ float part[kRowWarps][3];
   pdl_wait();
@@ -110,15 +130,20 @@ __global__ void __launch_bounds__(kRowThreads, 4) row_sums_kernel(SparsifyBackwa
     const auto* q = static_cast<const uint4*>(p.q) + m * p.K / 16;
     const auto* e = static_cast<const uint8_t*>(p.e) + m * p.K / 32;
     const auto* g = static_cast<const uint4*>(p.g) + m * p.K / 8;
+    const uint8_t* meta = nullptr;
+    if (META)
+      meta = static_cast<const uint8_t*>(p.meta) + (m / kRowBlock) * ((p.K + 127) / 128) * kMetaBlockBytes +
+             meta_row(static_cast<uint32_t>(m % kRowBlock));
     const int n = static_cast<int>(p.K / 16), step = 32 * ways;
     uint4 qv[kAhead], ga[kAhead], gb[kAhead];
-    uint32_t ev[kAhead];
+    uint32_t ev[kAhead], nv[kAhead] = {};
     auto load = [&](int k, int i) {
       if (i < n) {
         qv[k] = __ldg(q + i);
         ga[k] = __ldg(g + 2 * i);
         gb[k] = __ldg(g + 2 * i + 1);
         ev[k] = __ldg(e + i / 2);
+        if (META) nv[k] = __ldg(reinterpret_cast<const uint16_t*>(meta + meta_unit(i)));
       }
     };
     int i = 32 * way + lane;
@@ -129,10 +154,11 @@ __global__ void __launch_bounds__(kRowThreads, 4) row_sums_kernel(SparsifyBackwa
       for (int k = 0; k < kAhead; ++k) {
         if (i < n) {
           const uint4 q0 = qv[k], a0 = ga[k], b0 = gb[k];
+          const uint32_t n0 = nv[k];
           const float f = ckpt8_factor<FMT>(ev[k]);
           load(k, i + kAhead * step);
           float bl = 0.f, bk = 0.f, bd = 0.f;
-          sums16<FMT>(q0, a0, b0, bl, bk, bd);
+          sums16<FMT, META>(q0, a0, b0, n0, bl, bk, bd);
           l = fmaf(bl, f, l);
           lk = fmaf(bk, f, lk);
           d = fmaf(bd, f, d);
@@ -193,6 +219,7 @@ struct BackLaunch {
   CUtensorMap tm_a;   // A [r,K], box 64 x r
   CUtensorMap tm_dx;  // dX [M,K], box 64 x 128
   const float2* coef;
+  const uint8_t* meta;  // the selection (META)
   int64_t M, K;
   int r;
   int ranges;         // blocks of a row block
@@ -220,7 +247,7 @@ __device__ __forceinline__ bool back_wait(BackBars& b, uint64_t* bar, uint32_t p
   return ok;
 }
 
-template <int FMT, bool LORA>
+template <int FMT, bool LORA, bool META>
 __global__ void __launch_bounds__(kThreads, 1) sparsify_backward_kernel(const __grid_constant__ BackLaunch p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ BackBars bars;
@@ -355,9 +382,25 @@ __global__ void __launch_bounds__(kThreads, 1) sparsify_backward_kernel(const __
     // dX = kept: s g + sign(x) c (1 - s); dropped: sign(x) c, c = D / Lk
     const float s = c.x;
     const float dropped = 2.f * c.y, kept = 2.f * (c.y * (1.f - s));
+    // the selection of this thread's two units of a tile, a tile ahead (the metadata has
+    // whole row blocks, so rows past M can be read)
+    const uint8_t* meta = nullptr;
+    uint32_t nibbles[2] = {}, following[2] = {};
+    auto select = [&](int i) {
+      if (META && i < tiles) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          following[h] = __ldg(reinterpret_cast<const uint16_t*>(
+              meta + meta_unit((tile0 + i) * 4 + 2 * static_cast<int>(half) + h)));
+      }
+    };
+    if (META) meta = p.meta + (row0 / kRowBlock) * ((p.K + 127) / 128) * kMetaBlockBytes + meta_row(row);
+    select(buf);
     int slot = buf % stages;
     uint32_t phase = static_cast<uint32_t>(buf / stages) & 1u, parity = 0;
     for (int i = buf; i < tiles; i += kGroups) {
+      nibbles[0] = following[0], nibbles[1] = following[1];
+      select(i + kGroups);
       bool ok = back_wait(bars, &bars.full[slot], phase, p.status, kDevTimeoutFull) &&
                 back_wait(bars, &bars.out_empty[buf], parity ^ 1u, p.status, kDevTimeoutEmpty);
       if (LORA) ok = ok && back_wait(bars, &bars.d_full[buf], parity, p.status, kDevTimeoutAccum);
@@ -386,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1) sparsify_backward_kernel(const __
         uint32_t out[8];
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          const uint32_t a = magnitudes<FMT>(qw[w]), bits = keep_bits(a);
+          const uint32_t a = magnitudes<FMT>(qw[w]), bits = META ? kept_bits(nibbles[h], w) : keep_bits(a);
           // the upper half of 0.5 with the sign, or of 0
           const uint32_t half_sign = ((qw[w] & 0x80808080u) | 0x3F3F3F3Fu) & prmt<0xBA98>(a + 0x7F7F7F7Fu);
           const float g[4] = {bf16_lo(gw[2 * w]), bf16_hi(gw[2 * w]), bf16_lo(gw[2 * w + 1]), bf16_hi(gw[2 * w + 1])};
@@ -420,28 +463,28 @@ __global__ void __launch_bounds__(kThreads, 1) sparsify_backward_kernel(const __
   }
 }
 
-template <int FMT, bool LORA>
+template <int FMT, bool LORA, bool META>
 cudaError_t launch(const BackLaunch& b, unsigned blocks, uint32_t smem, cudaStream_t s) {
   static std::once_flag once[64];
   static cudaError_t configured[64];
   const cudaError_t e = once_per_device(once, configured, []() {
-    return cudaFuncSetAttribute(sparsify_backward_kernel<FMT, LORA>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(sparsify_backward_kernel<FMT, LORA, META>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 static_cast<int>(kSmemMost));
   });
   if (e != cudaSuccess) return e;
-  return launch_after_previous(sparsify_backward_kernel<FMT, LORA>, dim3(blocks), dim3(kThreads), smem, s, b);
+  return launch_after_previous(sparsify_backward_kernel<FMT, LORA, META>, dim3(blocks), dim3(kThreads), smem, s, b);
 }
 
-template <int FMT>
+template <int FMT, bool META>
 cudaError_t run(const SparsifyBackwardLaunch& p, const BackLaunch& b, unsigned blocks, uint32_t smem, int sms,
                 cudaStream_t s) {
   // a warp a row, more where the rows alone would leave SMs idle
   int rows = kRowWarps;
   while (rows > 1 && (p.M + rows - 1) / rows < 2 * sms) rows /= 2;
   const cudaError_t e = launch_after_previous(
-      row_sums_kernel<FMT>, dim3(static_cast<unsigned>((p.M + rows - 1) / rows)), dim3(kRowThreads), 0, s, p, rows);
+      row_sums_kernel<FMT, META>, dim3(static_cast<unsigned>((p.M + rows - 1) / rows)), dim3(kRowThreads), 0, s, p, rows);
   if (e != cudaSuccess) return e;
-  return p.dt != nullptr ? launch<FMT, true>(b, blocks, smem, s) : launch<FMT, false>(b, blocks, smem, s);
+  return p.dt != nullptr ? launch<FMT, true, META>(b, blocks, smem, s) : launch<FMT, false, META>(b, blocks, smem, s);
 }
 
 }  // namespace
@@ -449,6 +492,7 @@ cudaError_t run(const SparsifyBackwardLaunch& p, const BackLaunch& b, unsigned b
 cudaError_t launch_sparsify_backward(const SparsifyBackwardLaunch& p, int sms, cudaStream_t s) {
   BackLaunch b = {};
   b.coef = p.coef;
+  b.meta = static_cast<const uint8_t*>(p.meta);
   b.M = p.M;
   b.K = p.K;
   b.r = p.r;
@@ -483,8 +527,11 @@ cudaError_t launch_sparsify_backward(const SparsifyBackwardLaunch& p, int sms, c
                !encode_bf16_2d(&b.tm_a, p.a, K, r, K * 2, kCols, static_cast<uint32_t>(r), kSw)))
     return cudaErrorInvalidValue;
   const unsigned blocks = static_cast<unsigned>(row_blocks * b.ranges);
-  return p.format == kCkpt8Int8 ? run<kCkpt8Int8>(p, b, blocks, smem, sms, s)
-                                : run<kCkpt8E4M3>(p, b, blocks, smem, sms, s);
+  if (p.meta != nullptr)
+    return p.format == kCkpt8Int8 ? run<kCkpt8Int8, true>(p, b, blocks, smem, sms, s)
+                                  : run<kCkpt8E4M3, true>(p, b, blocks, smem, sms, s);
+  return p.format == kCkpt8Int8 ? run<kCkpt8Int8, false>(p, b, blocks, smem, sms, s)
+                                : run<kCkpt8E4M3, false>(p, b, blocks, smem, sms, s);
 }
 
 }  // namespace lynx

@@ -318,9 +318,9 @@ PyObject* lora_backward(PyObject* const* args, Py_ssize_t n) {
   return st != LYNX_OK ? PyLong_FromLong(st) : wrap_all({dA, dB, dT});
 }
 
-// G, q, e, dT, A, dX, workspace, stream
+// G, q, e, dT, A, dX, workspace, meta, stream
 PyObject* sparsify_backward(PyObject* const* args, Py_ssize_t n) {
-  const Call c(args, n, 8, "G");
+  const Call c(args, n, 9, "G");
   const Ckpt k(c, 1);
   at::Tensor dX, ws;
   const void* g = c.in(0, "G", at::kBFloat16, {k.M, k.K});
@@ -336,7 +336,17 @@ PyObject* sparsify_backward(PyObject* const* args, Py_ssize_t n) {
   }
   void* dx = c.out(5, "dX", at::kBFloat16, {k.M, k.K}, dX);
   const auto work = c.workspace(6, lynx_sparsify_backward_workspace_bytes(k.M, k.K), ws);
-  const int st = lynx_sparsify_backward(g, q, e, dt, a, k.M, k.K, r, k.format, dx, work.first, work.second, c.stream());
+  int st;
+  if (c.given(7)) {
+    const at::Tensor& t = c.tensor(7, "meta");
+    const void* meta = c.in(7, "meta", at::kByte, {t.numel()});
+    if (static_cast<size_t>(t.numel()) < lynx_meta_bytes(k.M, k.K))
+      refuse(PyExc_ValueError, "meta must have lynx_meta_bytes(M, K) bytes");
+    st = lynx_sparsify_backward_meta(g, q, e, meta, dt, a, k.M, k.K, r, k.format, dx, work.first, work.second,
+                                     c.stream());
+  } else {
+    st = lynx_sparsify_backward(g, q, e, dt, a, k.M, k.K, r, k.format, dx, work.first, work.second, c.stream());
+  }
   return st != LYNX_OK ? PyLong_FromLong(st) : wrap(dX);
 }
 

@@ -58,6 +58,7 @@ def library():
             "lynx_vals_bytes": ([i64, i64], sz),
             "lynx_meta_bytes": ([i64, i64], sz),
             "lynx_workspace_bytes": ([i64, i64, i64, i64], sz),
+            "lynx_workspace_meta_offset": ([i64, i64], sz),
             "lynx_sparsify_workspace_bytes": ([i64, i64], sz),
             "lynx_sparsify": ([p, i64, i64, p, p, p, p, sz, p], i32),
             "lynx_sparsify_noalloc": ([p, i64, i64, p, p, p, p], i32),
@@ -85,6 +86,7 @@ def library():
             "lynx_lora_backward": ([p, p, p, p, p, i64, i64, i64, i64, i32, p, p, p, p, sz, p], i32),
             "lynx_sparsify_backward_workspace_bytes": ([i64, i64], sz),
             "lynx_sparsify_backward": ([p, p, p, p, p, i64, i64, i64, i32, p, p, sz, p], i32),
+            "lynx_sparsify_backward_meta": ([p, p, p, p, p, p, i64, i64, i64, i32, p, p, sz, p], i32),
             "lynx_check_error": ([p, p], i32),
             "lynx_meta_hw_to_canonical": ([p, p, i64, i64], i32),
             "lynx_meta_canonical_to_hw": ([p, p, i64, i64], i32),
@@ -135,6 +137,23 @@ def lynx_meta_bytes(M, K):
 
 def lynx_workspace_bytes(M, N, K, r=64):
     return library().lynx_workspace_bytes(M, N, K, r)
+
+
+def lynx_workspace_meta_offset(M, K):
+    return library().lynx_workspace_meta_offset(M, K)
+
+
+def lynx_workspace_meta(workspace, M, K):
+    """The metadata of S(X) in a workspace that lynx_linear (or lynx_linear_act,
+    lynx_linear_begin) was given, sparse path: a view, good until the workspace is
+    used again (clone it to keep it for the backward pass)."""
+    import torch
+
+    _need(workspace, "workspace", torch.uint8)
+    at, size = lynx_workspace_meta_offset(M, K), lynx_meta_bytes(M, K)
+    if size == 0 or workspace.dim() != 1 or workspace.numel() < at + size:
+        raise ValueError("workspace must be the layer's, for this M and K")
+    return workspace[at:at + size]
 
 
 def _check(status, what):
@@ -525,10 +544,15 @@ def lynx_sparsify_backward_workspace_bytes(M, K):
     return library().lynx_sparsify_backward_workspace_bytes(M, K)
 
 
-def lynx_sparsify_backward(G, q, e, dT=None, A=None, dX=None, workspace=None, stream=None):
+def lynx_sparsify_backward(G, q, e, dT=None, A=None, dX=None, workspace=None, stream=None, meta=None):
     """dX [M,K] from G, the gradient of S(X), at the checkpoint (q, e) of X, plus
-    the LoRA branch's dT A (see include/lynx.h).  Returns dX."""
-    return _result(_binding().sparsify_backward(G, q, e, dT, A, dX, workspace, stream), "lynx_sparsify_backward")
+    the LoRA branch's dT A (see include/lynx.h).  Returns dX.
+
+    `meta`: the forward pass's selection (lynx_workspace_meta after lynx_linear, or
+    lynx_sparsify's metadata).  Without it the selection is made again from the 8-bit
+    values, which is not the layer's wherever they tie and X did not."""
+    return _result(_binding().sparsify_backward(G, q, e, dT, A, dX, workspace, meta, stream),
+                   "lynx_sparsify_backward" if meta is None else "lynx_sparsify_backward_meta")
 
 
 def lynx_check_error(stream=None):

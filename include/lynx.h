@@ -107,6 +107,12 @@ LYNX_API size_t lynx_meta_bytes(int64_t M, int64_t K);
  * per 32-row slice, alignment).  r = 0 (no LoRA) sizes it as for r = 64. */
 LYNX_API size_t lynx_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t r);
 
+/* Where in that workspace the sparse path of lynx_linear, lynx_linear_act and
+ * lynx_linear_begin leaves the metadata of S(X) (lynx_meta_bytes(M,K) bytes): a
+ * byte offset, the same for every N and r.  Copied from there before the workspace
+ * is used again, it is the selection lynx_sparsify_backward_meta takes. */
+LYNX_API size_t lynx_workspace_meta_offset(int64_t M, int64_t K);
+
 /* ---- the layer --------------------------------------------------------- */
 
 /* Bytes of the scratch workspace lynx_sparsify needs (per-range partial row
@@ -397,7 +403,8 @@ LYNX_API int lynx_ckpt8_restore(const void* q, const void* e, int64_t M, int64_t
  * the activation, if one was applied), W frozen:
  *   the adapter's gradients      lynx_lora_backward
  *   G = dY W                     lynx_linear_dense(dY, W^T laid out once as [K,N])
- *   the gradient of X            lynx_sparsify_backward (sparse path);
+ *   the gradient of X            lynx_sparsify_backward_meta with the metadata of
+ *                                the forward pass (sparse path);
  *                                dense path: lynx_linear_dense(dY, W^T [K,N],
  *                                NULL, B^T [r,N], A^T [K,r])
  * (lynx_linear_dense sums over N there, so N % 64 == 0.) */
@@ -427,14 +434,33 @@ LYNX_API size_t lynx_sparsify_backward_workspace_bytes(int64_t M, int64_t K);
  *
  *   dX = s m G + sign(x) (D / Lk) (1 - s m) + dT A      (sign(0) = 0)
  *
- * the exact derivative of S(X) = s m x where the selection does not change (the
- * bf16 rounding of S(X) passed through).  A row with Lk = 0 has s = 1 and no
- * second term.  dT [M,r] and A [r,K] (both or neither): the LoRA branch's share.
+ * the derivative of S at x where the selection does not change (the bf16 rounding
+ * of S(X) passed through).  A row with Lk = 0 has s = 1 and no second term.
+ *   x is not the X of the forward pass, and neither is this m: small values of a
+ * block share a code, and ties between codes go to the lower position where X
+ * decided otherwise.  On heavy-tailed and on GELU activations 3 to 11 % of the
+ * groups are selected otherwise, and dX is 0.17 to 0.34 of its norm away from
+ * the gradient of the layer that ran.  lynx_sparsify_backward_meta is the call
+ * for that gradient.
+ *   dT [M,r] and A [r,K] (both or neither): the LoRA branch's share.
  *   workspace: device scratch of workspace_bytes >=
  *   lynx_sparsify_backward_workspace_bytes(M,K). */
 LYNX_API int lynx_sparsify_backward(const void* G, const void* q, const void* e, const void* dT,
                                     const void* A, int64_t M, int64_t K, int64_t r, int format, void* dX,
                                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* The same with m the selection that the forward pass made: `meta` is its
+ * metadata (lynx_meta_bytes(M,K) bytes in the layout given there: lynx_sparsify's
+ * output, or a copy of what lynx_linear left at lynx_workspace_meta_offset), and
+ * must not be NULL.  x, s and D are taken from the checkpoint: on the activations
+ * named above dX is within 0.02 (int8) and 0.005 (e4m3) of its norm of the gradient
+ * at the forward pass's X at K = 4096 (values stored as 0 have lost their sign, which
+ * costs more in shorter rows, as 1 / sqrt(K)).  A row whose kept values are all stored as 0 has
+ * s = 1 and no second term.  Everything else as above. */
+LYNX_API int lynx_sparsify_backward_meta(const void* G, const void* q, const void* e, const void* meta,
+                                         const void* dT, const void* A, int64_t M, int64_t K, int64_t r,
+                                         int format, void* dX, void* workspace, size_t workspace_bytes,
+                                         void* stream);
 
 /* ---- errors and metadata conversion ----------------------------------- */
 
