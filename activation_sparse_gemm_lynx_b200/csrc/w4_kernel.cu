@@ -29,6 +29,18 @@ using bf162 = __nv_bfloat162;
 __device__ __forceinline__ bf162 as_pair(uint32_t w) { return *reinterpret_cast<const bf162*>(&w); }
 __device__ __forceinline__ uint32_t as_word(const bf162& p) { return *reinterpret_cast<const uint32_t*>(&p); }
 
+// Extremes that a NaN stays in: the group's scale is then NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // Saturated to 0..15, two at a time, in the word's order
 __device__ __forceinline__ uint32_t pack_nibbles(const int (&q)[8]) {
   uint32_t w;
@@ -70,13 +82,14 @@ __global__ void __launch_bounds__(kThreads) w4_quantize_kernel(const __nv_bfloat
   for (int i = 0; i < 4; ++i) {
     const bf162 v[4] = {as_pair(rows[i].x), as_pair(rows[i].y), as_pair(rows[i].z), as_pair(rows[i].w)};
     if constexpr (ZEROS) {
-      const uint32_t most = as_word(__hmax2(__hmax2(v[0], v[1]), __hmax2(v[2], v[3])));
-      const uint32_t least = as_word(__hmin2(__hmin2(v[0], v[1]), __hmin2(v[2], v[3])));
-      hi[i] = fmaxf(fmaxf(bf16_lo(most), bf16_hi(most)), 0.f);
-      lo[i] = fminf(fminf(bf16_lo(least), bf16_hi(least)), 0.f);
+      const uint32_t most = as_word(__hmax2_nan(__hmax2_nan(v[0], v[1]), __hmax2_nan(v[2], v[3])));
+      const uint32_t least = as_word(__hmin2_nan(__hmin2_nan(v[0], v[1]), __hmin2_nan(v[2], v[3])));
+      hi[i] = max_nan(max_nan(bf16_lo(most), bf16_hi(most)), 0.f);
+      lo[i] = min_nan(min_nan(bf16_lo(least), bf16_hi(least)), 0.f);
     } else {
-      const uint32_t most = as_word(__hmax2(__hmax2(__habs2(v[0]), __habs2(v[1])), __hmax2(__habs2(v[2]), __habs2(v[3]))));
-      hi[i] = fmaxf(fmaxf(bf16_lo(most), bf16_hi(most)), 0.f);
+      const uint32_t most = as_word(__hmax2_nan(__hmax2_nan(__habs2(v[0]), __habs2(v[1])),
+                                                __hmax2_nan(__habs2(v[2]), __habs2(v[3]))));
+      hi[i] = max_nan(bf16_lo(most), bf16_hi(most));
       lo[i] = 0.f;
     }
   }
@@ -91,13 +104,14 @@ __global__ void __launch_bounds__(kThreads) w4_quantize_kernel(const __nv_bfloat
     for (int d = 4; d < kLanes; d *= 2) r = pick(r, __shfl_xor_sync(0xffffffffu, r, d));
     return r;
   };
-  const float top = exchange(hi, [](float a, float c) { return fmaxf(a, c); });
+  const float top = exchange(hi, [](float a, float c) { return max_nan(a, c); });
   float ratio;
   if constexpr (ZEROS) {
-    const float low = exchange(lo, [](float a, float c) { return fminf(a, c); });
+    const float low = exchange(lo, [](float a, float c) { return min_nan(a, c); });
     const float range = top - low;
     lo[0] = low;
-    // two bf16 more than 16 binades apart: their difference is no fp32
+    // two bf16 more than 16 binades apart: their difference is no fp32 (and where one is
+    // not finite, the scale is not either)
     if (range - top == -low && top - range == low)
       ratio = range / 15.f;
     else
@@ -109,7 +123,9 @@ __global__ void __launch_bounds__(kThreads) w4_quantize_kernel(const __nv_bfloat
   const float my_s = __bfloat162float(sb);
   int my_z = 8;
   if constexpr (ZEROS) my_z = my_s == 0.f ? 0 : max(0, min(15, __float2int_rn(-lo[0] / my_s)));
-  const float my_inv = my_s >= 0x1p-100f ? 1.f / my_s : 0.f;  // 1 / s may not be finite below
+  // 1 / s may not be finite below; 0 too where s is not: the conversion of NaN to 0 then
+  // makes every q the zero point, and the group stands for NaN throughout
+  const float my_inv = my_s >= 0x1p-100f ? 1.f / my_s : 0.f;
   if (lane % kLanes < 4) {
     s_sm[lane / kLanes][4 * warp + (lane & 3)] = sb;
     if constexpr (ZEROS) z_sm[lane / kLanes][4 * warp + (lane & 3)] = static_cast<uint8_t>(my_z);

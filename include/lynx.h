@@ -336,7 +336,10 @@ LYNX_API size_t lynx_w4_bytes(int64_t N, int64_t K);
  *   else, with hi = max(w, 0), lo = min(w, 0) over the group:
  *                   s = bf16((hi - lo) / 15), z = clamp(rint(-lo / s), 0, 15),
  *                   q = clamp(rint(w / s) + z, 0, 15).
- * A group whose s is 0 stands for zeros (q = z).  rint ties to even. */
+ * A group whose s is 0 stands for zeros (q = z).  rint ties to even.  A group with a
+ * NaN has s = NaN, one with an infinity (and no NaN) s = infinity, both q = z (z = 0
+ * where zero points are made): it stands for NaN throughout, in lynx_w4_dequantize and
+ * in the outputs of lynx_linear_w4 that it enters. */
 LYNX_API int lynx_w4_quantize(const void* W, int64_t N, int64_t K, int group, void* Wq, void* scales,
                               void* zeros, void* stream);
 
