@@ -115,17 +115,37 @@ __device__ __forceinline__ void sums16(const uint4& qv, const uint4& ga, const u
   }
 }
 
+// 2^-n, 0 below the normal range
+__device__ __forceinline__ float exp2_down(int n) {
+  return __uint_as_float(n < 127 ? static_cast<uint32_t>(127 - n) << 23 : 0u);
+}
+
+// A row's three sums in units of 2^top, top the largest block exponent so far.  Only their
+// ratios are wanted, and in absolute terms fp32 holds neither a row near 2^124 (L is
+// infinite) nor one near 2^-130 (D is 0).
+struct RowSums {
+  float l, lk, d;
+  int top;
+  __device__ __forceinline__ void raise(int to) {  // to >= top
+    const float f = exp2_down(to - top);
+    l *= f;
+    lk *= f;
+    d *= f;
+    top = to;
+  }
+};
+
 // coef[m] = (s, D / Lk).  A block has `rows` rows, kRowWarps / rows warps each;
 // 16 columns a lane and step.
 template <int FMT, bool META>
 __global__ void __launch_bounds__(kRowThreads, 4) row_sums_kernel(SparsifyBackwardLaunch p, int rows) {
-  __shared__ float part[kRowWarps][3];
+  __shared__ RowSums part[kRowWarps];
   pdl_wait();
   pdl_launch_dependents();  // the outputs' loads may start beside this, once all earlier work is done
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ways = kRowWarps / rows, way = warp % ways;
   const int64_t m = static_cast<int64_t>(blockIdx.x) * rows + warp / ways;
-  float l = 0.f, lk = 0.f, d = 0.f;
+  RowSums s = {0.f, 0.f, 0.f, 0};
   if (m < p.M) {
     const auto* q = static_cast<const uint4*>(p.q) + m * p.K / 16;
     const auto* e = static_cast<const uint8_t*>(p.e) + m * p.K / 32;
@@ -155,38 +175,39 @@ __global__ void __launch_bounds__(kRowThreads, 4) row_sums_kernel(SparsifyBackwa
         if (i < n) {
           const uint4 q0 = qv[k], a0 = ga[k], b0 = gb[k];
           const uint32_t n0 = nv[k];
-          const float f = ckpt8_factor<FMT>(ev[k]);
+          const int ex = static_cast<int>(ev[k]);  // 255: NaN throughout
+          if (ex > s.top && ex < 255) s.raise(ex);
+          const float f = ex < 255 ? exp2_down(s.top - ex) : __uint_as_float(0x7FC00000u);
           load(k, i + kAhead * step);
           float bl = 0.f, bk = 0.f, bd = 0.f;
           sums16<FMT, META>(q0, a0, b0, n0, bl, bk, bd);
-          l = fmaf(bl, f, l);
-          lk = fmaf(bk, f, lk);
-          d = fmaf(bd, f, d);
+          s.l = fmaf(bl, f, s.l);
+          s.lk = fmaf(bk, f, s.lk);
+          s.d = fmaf(bd, f, s.d);
           i += step;
         }
       }
     }
   }
+  s.raise(__reduce_max_sync(0xffffffffu, s.top));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    l += __shfl_xor_sync(0xffffffffu, l, o);
-    lk += __shfl_xor_sync(0xffffffffu, lk, o);
-    d += __shfl_xor_sync(0xffffffffu, d, o);
+    s.l += __shfl_xor_sync(0xffffffffu, s.l, o);
+    s.lk += __shfl_xor_sync(0xffffffffu, s.lk, o);
+    s.d += __shfl_xor_sync(0xffffffffu, s.d, o);
   }
-  if (lane == 0) {
-    part[warp][0] = l;
-    part[warp][1] = lk;
-    part[warp][2] = d;
-  }
+  if (lane == 0) part[warp] = s;
   __syncthreads();
   if (way == 0 && lane == 0 && m < p.M) {
-    l = lk = d = 0.f;
-    for (int w = warp; w < warp + ways; ++w) {
-      l += part[w][0];
-      lk += part[w][1];
-      d += part[w][2];
+    for (int w = warp + 1; w < warp + ways; ++w) {
+      RowSums other = part[w];
+      if (other.top > s.top) s.raise(other.top);
+      other.raise(s.top);
+      s.l += other.l;
+      s.lk += other.lk;
+      s.d += other.d;
     }
-    p.coef[m] = lk == 0.f ? make_float2(1.f, 0.f) : make_float2(l / lk, d / lk);
+    p.coef[m] = s.lk == 0.f ? make_float2(1.f, 0.f) : make_float2(s.l / s.lk, s.d / s.lk);
   }
 }
 

@@ -439,6 +439,8 @@ LYNX_API size_t lynx_sparsify_backward_workspace_bytes(int64_t M, int64_t K);
  *
  * the derivative of S at x where the selection does not change (the bf16 rounding
  * of S(X) passed through).  A row with Lk = 0 has s = 1 and no second term.
+ * Rows of any magnitude that a checkpoint holds are in range; D is summed in fp32
+ * against x in units of the row's largest block, which takes |G| up to 2^88.
  *   x is not the X of the forward pass, and neither is this m: small values of a
  * block share a code, and ties between codes go to the lower position where X
  * decided otherwise.  On heavy-tailed and on GELU activations 3 to 11 % of the
