@@ -67,6 +67,11 @@ __device__ __forceinline__ void mma_m16n8k16(float (&c)[4], uint32_t a0, uint32_
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Both values' first 8 bits, as a pair of bf16
+__device__ __forceinline__ uint32_t upper_halves(float2 v) {
+  return __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x7632);
+}
+
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
@@ -307,7 +312,8 @@ __global__ void __launch_bounds__(kFewThreads<T, NT>, 1) linear_w4_kernel(Linear
   cp_async_wait<0>();
   if (p.b != nullptr) {
     // The adapter's T B^T, 16 of r a step, the steps dealt out to the rings.  T
-    // stays fp32: it enters as the sum of three bf16 (8 bits each).
+    // stays fp32: it enters as the sum of three bf16 (8 bits each), cut off and not
+    // rounded, since the upper one of a T next to fp32's largest would round to infinity.
     // T comes from the kernel before this one, which everything above ran beside.
     pdl_wait();
     const auto* b = static_cast<const uint32_t*>(p.b);
@@ -337,9 +343,9 @@ __global__ void __launch_bounds__(kFewThreads<T, NT>, 1) linear_w4_kernel(Linear
       for (int h = 0; h < 3; ++h) {
 #pragma unroll
         for (int c = 0; c < NT; ++c) {
-          const uint32_t b0 = pack_bf16(tv[c][0].x, tv[c][0].y), b1 = pack_bf16(tv[c][1].x, tv[c][1].y);
-          tv[c][0] = make_float2(tv[c][0].x - bf16_lo(b0), tv[c][0].y - bf16_hi(b0));
-          tv[c][1] = make_float2(tv[c][1].x - bf16_lo(b1), tv[c][1].y - bf16_hi(b1));
+          const uint32_t b0 = upper_halves(tv[c][0]), b1 = upper_halves(tv[c][1]);
+          tv[c][0] = make_float2(bf16_rest(tv[c][0].x, bf16_lo(b0)), bf16_rest(tv[c][0].y, bf16_hi(b0)));
+          tv[c][1] = make_float2(bf16_rest(tv[c][1].x, bf16_lo(b1)), bf16_rest(tv[c][1].y, bf16_hi(b1)));
 #pragma unroll
           for (int u = 0; u < TW; ++u) mma_m16n8k16(acc[u][c], a[u][0], a[u][1], a[u][2], a[u][3], b0, b1);
         }

@@ -127,8 +127,8 @@ __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// What v's rounding `h` leaves of it (exact); nothing where h is not finite, so that an
-// infinity stays one in the sum of the parts
+// What v's first part `h` (rounded or cut off) leaves of it, exact; nothing where h is not
+// finite, so that an infinity stays one in the sum of the parts
 __device__ __forceinline__ float bf16_rest(float v, float h) {
   return fabsf(h) < __uint_as_float(0x7F800000u) ? v - h : 0.f;
 }
