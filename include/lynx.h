@@ -362,7 +362,10 @@ LYNX_API size_t lynx_linear_w4_workspace_bytes(int64_t M, int64_t N, int64_t K, 
  * the weight and call lynx_linear).  The dense layer: S(X) = X.
  *   X [M,K], bias [N] or NULL, A [r,K] and B [N,r] (both or neither), Y [M,N]
  *   out, act as for lynx_linear_act.  Every sum and T are kept in fp32; Y is
- *   rounded once.  The result does not depend on the other rows of X.
+ *   rounded once.  Equal calls give equal bits, and a row's do not depend on the
+ *   values in the other rows.  They do depend on M, N, K, r and the device: the
+ *   order of the sums goes by them, so the same token among 16 and among 17 rows
+ *   may differ in its last bit.
  *   workspace: device scratch of workspace_bytes >=
  *   lynx_linear_w4_workspace_bytes(M,N,K,r); may be NULL without A and B. */
 LYNX_API int lynx_linear_w4(const void* X, const void* Wq, const void* scales, const void* zeros,
