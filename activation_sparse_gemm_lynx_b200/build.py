@@ -4,7 +4,9 @@
 
 The host compiler also builds ``_build/_lynx_torch.so`` from
 ``csrc/torch_binding.cpp``: the tensor marshalling of the calls that are short
-on the device, linked to that library and to torch's own.
+on the device, linked to that library and to torch's own.  Where torch or the
+Python headers are not there it is left out: users of ``include/lynx.h`` need nvcc
+alone.
 
 One nvcc invocation compiles every ``csrc/*.cu`` file with
 ``-gencode arch=compute_100a,code=sm_100a -lineinfo`` and links a shared
@@ -13,9 +15,11 @@ through ``cudaGetDriverEntryPoint``), so the library loads on a machine
 without a GPU driver and only needs one when a kernel is launched.
 """
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -65,10 +69,17 @@ def binding_up_to_date() -> bool:
     return all(os.path.getmtime(f) <= t for f in (BINDING_SOURCE, os.path.join(INCLUDE, "lynx.h")))
 
 
+def binding_lacks() -> str:
+    """What building the tensor marshalling would need and is not here ('' if nothing)."""
+    if importlib.util.find_spec("torch") is None:
+        return "torch is not installed"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "the Python headers are not installed"
+    return ""
+
+
 def build_binding() -> str:
     """Compile the tensor marshalling against torch; return its path."""
-    import sysconfig
-
     import torch
 
     home = os.path.dirname(torch.__file__)
@@ -90,7 +101,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
     """Compile what any source is newer than; return the library's path."""
     if force or not up_to_date():
         build_library(verbose)
-    if force or not binding_up_to_date():
+    lacks = binding_lacks()
+    if lacks:
+        print(f"{os.path.basename(BINDING)} not built: {lacks}; {LIB} needs neither", file=sys.stderr)
+    elif force or not binding_up_to_date():
         build_binding()
     return LIB
 
