@@ -2,9 +2,11 @@
 
     python -m activation_sparse_gemm_lynx_b200.build [--force] [--verbose]
 
-The host compiler also builds ``_build/_lynx_torch.so`` from
+The host compiler also builds ``_build/_lynx_torch.<versions>.so`` from
 ``csrc/torch_binding.cpp``: the tensor marshalling of the calls that are short
-on the device, linked to that library and to torch's own.  Where torch or the
+on the device, linked to that library and to torch's own.  Its name holds the
+Python ABI and the torch it was compiled against, so that another one's is never
+loaded.  Where torch or the
 Python headers are not there it is left out: users of ``include/lynx.h`` need nvcc
 alone.
 
@@ -17,6 +19,7 @@ without a GPU driver and only needs one when a kernel is launched.
 import glob
 import importlib.util
 import os
+import re
 import subprocess
 import sys
 import sysconfig
@@ -27,7 +30,6 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "liblynx.so")
-BINDING = os.path.join(OUT_DIR, "_lynx_torch.so")
 BINDING_SOURCE = os.path.join(CSRC, "torch_binding.cpp")
 
 NVCC_FLAGS = [
@@ -62,11 +64,22 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
+def binding_path() -> str:
+    """Where the tensor marshalling for the running Python and torch is (or would be)."""
+    import torch
+
+    tag = "%s-torch%s-cxx11abi%d" % (sysconfig.get_config_var("SOABI"), torch.__version__,
+                                     int(torch._C._GLIBCXX_USE_CXX11_ABI))
+    return os.path.join(OUT_DIR, "_lynx_torch.%s.so" % re.sub(r"[^A-Za-z0-9.+-]", "_", tag))
+
+
 def binding_up_to_date() -> bool:
-    if not os.path.exists(BINDING):
+    path = binding_path()
+    if not os.path.exists(path):
         return False
-    t = os.path.getmtime(BINDING)
-    return all(os.path.getmtime(f) <= t for f in (BINDING_SOURCE, os.path.join(INCLUDE, "lynx.h")))
+    t = os.path.getmtime(path)
+    return all(os.path.getmtime(f) <= t
+               for f in (BINDING_SOURCE, os.path.join(INCLUDE, "lynx.h"), os.path.abspath(__file__)))
 
 
 def binding_lacks() -> str:
@@ -83,7 +96,8 @@ def build_binding() -> str:
     import torch
 
     home = os.path.dirname(torch.__file__)
-    tmp = BINDING + ".tmp%d" % os.getpid()
+    path = binding_path()
+    tmp = path + ".tmp%d" % os.getpid()
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
            "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI), "-I", INCLUDE,
@@ -93,8 +107,8 @@ def build_binding() -> str:
             "-o", tmp, BINDING_SOURCE, "-L", OUT_DIR, "-llynx", "-Wl,-rpath,$ORIGIN",
             "-L", os.path.join(home, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
     subprocess.run(cmd, check=True)
-    os.replace(tmp, BINDING)
-    return BINDING
+    os.replace(tmp, path)
+    return path
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -103,7 +117,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         build_library(verbose)
     lacks = binding_lacks()
     if lacks:
-        print(f"{os.path.basename(BINDING)} not built: {lacks}; {LIB} needs neither", file=sys.stderr)
+        print(f"tensor binding not built: {lacks}; {LIB} needs neither", file=sys.stderr)
     elif force or not binding_up_to_date():
         build_binding()
     return LIB

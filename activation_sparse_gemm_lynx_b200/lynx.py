@@ -450,7 +450,7 @@ def lynx_sparse_gemm(vals, meta, W, bias=None, T=None, B=None, Y=None, stream=No
 # ---- the weight in 4 bits, the 8-bit checkpoint, the backward pass ----------
 #
 # These calls can be shorter on the device than a tensor check in Python, so their
-# marshalling is compiled (_build/_lynx_torch.so): it checks the tensors, which
+# marshalling is compiled (_build/_lynx_torch.*.so): it checks the tensors, which
 # must be contiguous and on the current device, makes the outputs and workspaces
 # that are not given, from the memory pool of the stream, and calls the C ABI.
 
@@ -461,15 +461,14 @@ def _binding():
     global _compiled
     if _compiled is None:
         library()
-        if not os.path.exists(_build.BINDING):
-            raise ImportError(
-                f"Lynx tensor binding not built ({_build.BINDING} missing); run "
-                "`python -m activation_sparse_gemm_lynx_b200.build`")
         import importlib.util
 
-        import torch  # noqa: F401  (the binding links to its libraries)
-
-        spec = importlib.util.spec_from_file_location("_lynx_torch", _build.BINDING)
+        path = _build.binding_path()  # imports torch, whose libraries the binding links to
+        if not os.path.exists(path):
+            raise ImportError(
+                f"Lynx tensor binding not built for this Python and torch ({path} missing); run "
+                "`python -m activation_sparse_gemm_lynx_b200.build`")
+        spec = importlib.util.spec_from_file_location("_lynx_torch", path)
         _compiled = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(_compiled)
     return _compiled
