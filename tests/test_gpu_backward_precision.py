@@ -72,6 +72,83 @@ def test_the_last_block_counts(where, M, N, K, r):
             rounded_once(got[name], value)
 
 
+# Operands in 2 or 4 pieces and in single buffers, one or several inner blocks, with and
+# without clusters and groups of them: the least work that the plan gives each form.
+FORMS = [
+    (129, 4104, 64, 96), (300, 12288, 64, 96), (129, 8, 64, 80), (1, 8, 64, 80), (1025, 12288, 64, 144),
+    (129, 8, 64, 208), (1, 8, 64, 208), (129, 8, 64, 192), (1, 8, 64, 192), (129, 8, 64, 144), (1, 8, 64, 144),
+    (1025, 9216, 64, 208), (4608, 2056, 64, 208), (2049, 4104, 64, 240), (4608, 4104, 64, 240),
+    (513, 12288, 64, 256), (2049, 9216, 64, 144), (1025, 9216, 64, 192), (1025, 12288, 64, 192),
+    (4608, 8, 2112, 208), (2049, 8, 12288, 208), (513, 8, 576, 208), (1, 8, 576, 208), (513, 8, 64, 144),
+    (513, 8, 64, 192), (4608, 8, 4160, 80), (4608, 8, 12288, 80), (513, 8, 64, 80), (1025, 8, 64, 96),
+    (2049, 8, 4160, 144), (2049, 8, 1088, 208), (300, 8, 64, 208)]
+
+
+@pytest.mark.parametrize("i", range(len(FORMS)))
+def test_every_form_of_the_passes(i):
+    M, N, K, r = FORMS[i]
+    X, dY = normal(1, M, K), normal(2, M, N, std=1e-3)
+    A, B = normal(3, r, K, std=K ** -0.5), normal(4, N, r, std=N ** -0.5)
+    got, ref = gradients(X, dY, A, B, FORMATS[i % 2])
+    for name in got:
+        value, tol = ref[name]
+        assert bool(((got[name].double() - value).abs() <= tol).all())
+        if value.numel() >= 500:
+            rounded_once(got[name], value)
+    again, _ = gradients(X, dY, A, B, FORMATS[i % 2])
+    assert all(torch.equal(got[name], again[name]) for name in got)
+
+
+@pytest.mark.parametrize("M,N,K,r", [(300, 1000, 576, 16), (129, 4104, 64, 96), (513, 12288, 64, 256),
+                                     (2049, 8, 12288, 208), (1, 8, 576, 208)])
+def test_dT_may_be_null_in_every_form(M, N, K, r):
+    """The C call without dT: one pass over dY or two, with and without partial sums."""
+    q, e = lynx.lynx_ckpt8_store(normal(1, M, K))
+    dY, A, B = normal(2, M, N), normal(3, r, K), normal(4, N, r)
+    want = lynx.lynx_lora_backward(dY, q, e, A, B)
+    dA, dB = torch.empty_like(want[0]), torch.empty_like(want[1])
+    ws = torch.empty(lynx.lynx_lora_backward_workspace_bytes(M, N, K, r), dtype=torch.uint8, device=DEV)
+    p = lynx._ptr
+    st = lynx.library().lynx_lora_backward(p(dY), p(q), p(e), p(A), p(B), M, N, K, r, lynx.LYNX_CKPT8_INT8, p(dA), p(dB),
+                                           None, p(ws), ws.numel(), lynx._stream(None))
+    assert st == lynx.LYNX_OK
+    assert torch.equal(dA, want[0]) and torch.equal(dB, want[1])
+
+
+def test_two_host_threads_on_their_own_streams():
+    import threading
+
+    M, N, K, r = 600, 1032, 1088, 144
+    X, dY, G = normal(1, M, K), normal(2, M, N), normal(5, M, K)
+    A, B = normal(3, r, K), normal(4, N, r)
+    q, e = lynx.lynx_ckpt8_store(X)
+    meta = lynx.lynx_sparsify(X)[1]
+
+    def step(stream=None):
+        dA, dB, dT = lynx.lynx_lora_backward(dY, q, e, A, B, stream=stream)
+        return dA, dB, dT, lynx.lynx_sparsify_backward(G, q, e, dT, A, stream=stream, meta=meta)
+
+    want = step()
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(i):
+        torch.cuda.set_device(0)
+        s = torch.cuda.Stream()
+        for _ in range(20):
+            got[i].append(step(s))
+        s.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert all(len(g) == 20 for g in got)
+    assert all(torch.equal(a, b) for g in got for o in g for a, b in zip(o, want))
+
+
 def test_an_infinite_gradient_stays_one():
     """Where a partial product overflows, the sum of its two halves is still infinite."""
     M, N, K, r = 2, 64, 64, 16
