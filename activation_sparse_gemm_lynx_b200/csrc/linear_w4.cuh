@@ -15,9 +15,10 @@
 // about 200 cycles a box and fed the rings at half of this rate.)
 //
 // One token, 12288 x 4096, group 128 with zero points: 10.2 us (26 MB, 2.6 TB/s), with
-// an adapter of r = 64 12.6 us; 32 tokens, 9216 x 4096: 13.7 and 15.9 us.  What bounds
-// it is the unpacking: 13,000 instructions a scheduler at about half of the issue
-// slots, where the bytes take 4.4 us; then the start and the sums at the end, 1.6 us.
+// an adapter of r = 64 11.0 us; 32 tokens, 9216 x 4096: 13.7 and 15.7 us.  The bytes take
+// 4.4 us.  The time goes into the unpacking, 13,000 instructions a scheduler whose chain 4
+// warps do not cover (half of the issue slots stay empty); then the start and the sums
+// at the end, 1.6 us.
 //
 // mma wants k pairs (2t, 2t+1) and (2t+8, 2t+9) of thread t; any assignment of k
 // to those places will do if both operands share it.  Thread t takes k = 8t..8t+7

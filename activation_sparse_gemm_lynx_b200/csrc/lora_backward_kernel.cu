@@ -34,7 +34,7 @@
 //
 // At 4608 x 4096 -> 12288, rank 64, int8 (137 MB in all) 72 us: T 18 us (19 MB, bound by
 // the warps that widen it and the cluster's sums), the pass over dY 30 us behind it
-// (113 MB in, 28 MB of sums out; 24 MMAs a tile read 144 KB of shared memory, 0.6 us),
+// (113 MB in, 28 MB of sums out; its 24 MMAs a tile read 144 KB of shared memory),
 // reduce_kernel 7 us (those 28 MB from L2), dA 17 us.  One bf16 for T and dT takes 65 us;
 // at ranks 128 and 256 101 and 145 us for 126 and 202.
 #include "lynx_ckpt8.cuh"

@@ -7,9 +7,10 @@
 // The LoRA branch adds dT A, a product of rank r.
 //
 // The selection m is the forward pass's where its metadata is given (META): the 8-bit
-// values tie where x did not, and a selection made again from them differs in 3 to 11 %
+// values tie where x did not, and a selection made again from them differs in 3 to 12 %
 // of the groups (heavy-tailed and GELU inputs).  The metadata adds 1/8 byte a value to
-// each reading (4608 x 12288, rank 64: 94 us for 92).  Without it m is the 2:4 selection of the checkpoint's values.
+// each reading (4608 x 12288, rank 64: 90 us for 87).  Without it m is the 2:4 selection
+// of the checkpoint's values.
 //
 // Every output needs its row's three sums, so there are two passes over G and
 // the checkpoint: row_sums_kernel streams them once, sparsify_backward_kernel
@@ -20,11 +21,12 @@
 // passes over a quarter of the rows at a time, so that L2 holds them between, took
 // 111 us: every launch starts and drains anew.)
 //
-// At 4608 x 12288, rank 64, 85 us: row sums 38 us and outputs 55 us, 8 us of them
-// side by side.  They read G and the bytes twice and write dX, 458 MB, a quarter of
-// the second reading out of L2: 4.8 and 4.3 TB/s from memory with the integer pipe
-// half busy.  Neither bounds them alone, and neither fewer instructions (sums),
-// missing stores (outputs) nor more loads in flight (both) change the time much.
+// At 4608 x 12288, rank 64, 87 us: row sums 38 us and outputs 55 us, 6 us of them
+// side by side (90 us with the metadata, the sums 42).  They read G and the bytes twice
+// and write dX, 458 MB, a quarter of the second reading out of L2: 4.8 and 4.3 TB/s from
+// memory with the integer pipe half busy.  What stalls them is not found: neither fewer
+// instructions (sums), missing stores (outputs) nor more loads in flight (both) change
+// the time much.
 #include "lynx_ckpt8.cuh"
 #include "lynx_internal.h"
 #include "lynx_ptx.cuh"

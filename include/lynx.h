@@ -446,8 +446,8 @@ LYNX_API size_t lynx_sparsify_backward_workspace_bytes(int64_t M, int64_t K);
  * against x in units of the row's largest block, which takes |G| up to 2^88.
  *   x is not the X of the forward pass, and neither is this m: small values of a
  * block share a code, and ties between codes go to the lower position where X
- * decided otherwise.  On heavy-tailed and on GELU activations 3 to 11 % of the
- * groups are selected otherwise, and dX is 0.17 to 0.34 of its norm away from
+ * decided otherwise.  On heavy-tailed and on GELU activations 3 to 12 % of the
+ * groups are selected otherwise, and dX is 0.17 to 0.35 of its norm away from
  * the gradient of the layer that ran.  lynx_sparsify_backward_meta is the call
  * for that gradient.
  *   dT [M,r] and A [r,K] (both or neither): the LoRA branch's share.
