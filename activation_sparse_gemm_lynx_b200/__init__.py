@@ -18,11 +18,17 @@ from .lynx import (  # noqa: F401
     LYNX_CKPT8_E4M3,
     LYNX_CKPT8_INT8,
     LynxError,
+    lynx_act_backward,
+    lynx_act_backward_workspace_bytes,
     lynx_check_error,
     lynx_ckpt8_exponent_bytes,
     lynx_ckpt8_restore,
     lynx_ckpt8_store,
     lynx_debug_set_stall,
+    lynx_layer_norm,
+    lynx_layer_norm_backward,
+    lynx_layer_norm_backward_workspace_bytes,
+    lynx_layer_norm_max_cols,
     lynx_linear,
     lynx_linear_act,
     lynx_linear_begin,
@@ -32,8 +38,10 @@ from .lynx import (  # noqa: F401
     lynx_linear_host,
     lynx_linear_host_act,
     lynx_linear_host_workspace_bytes,
+    lynx_linear_residual,
     lynx_linear_w4,
     lynx_linear_w4_max_rows,
+    lynx_linear_w4_residual,
     lynx_linear_w4_workspace_bytes,
     lynx_lora_backward,
     lynx_lora_backward_workspace_bytes,

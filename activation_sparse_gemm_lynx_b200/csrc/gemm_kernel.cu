@@ -80,7 +80,10 @@ __device__ __forceinline__ void tile_coords(int tile, int ntm, int ntn, int& mb,
   nb = in_group / gm;
 }
 
-template <int BN, bool SPARSE>
+// EXT: a residual is added to the activation's value, or the value before the
+// activation is stored too.  A kernel of its own, so that the plain layer's
+// epilogue keeps its registers.
+template <int BN, bool SPARSE, bool EXT>
 __global__ void __launch_bounds__(kGemmThreads, 1)
 lynx_gemm_kernel(const __grid_constant__ GemmLaunch p) {
   using C = Cfg<BN, SPARSE>;
@@ -304,16 +307,45 @@ lynx_gemm_kernel(const __grid_constant__ GemmLaunch p) {
         uint32_t r[32];
         tmem_ld_32x32b_x32(sm.tmem_base + ((32u * q) << 16) + static_cast<uint32_t>(acc * BN + col), r);
         tmem_ld_wait();
+        // 8 columns (16 bytes) a time in the extended epilogue: N is a multiple of 8
+        uint32_t add[16] = {}, pre[16];
+        if constexpr (EXT) {
+          if (p.residual != nullptr && row_ok) {
+            const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(p.residual) + grow * p.N + n_base + col;
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              if (n_base + col + 8 * v < p.N)
+                *reinterpret_cast<uint4*>(add + 4 * v) = *reinterpret_cast<const uint4*>(from + 8 * v);
+          }
+        }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           float a = __fmaf_rn(s, __uint_as_float(r[2 * i]), sm.bias_s[col + 2 * i]);
           float b = __fmaf_rn(s, __uint_as_float(r[2 * i + 1]), sm.bias_s[col + 2 * i + 1]);
+          if constexpr (EXT) {
+            __nv_bfloat162 z = __floats2bfloat162_rn(a, b);
+            pre[i] = *reinterpret_cast<uint32_t*>(&z);
+          }
           if (p.act == kActGeluTanh) {
             a = gelu_tanh(a);
             b = gelu_tanh(b);
           }
+          if constexpr (EXT) {
+            a += __uint_as_float(add[i] << 16);
+            b += __uint_as_float(add[i] & 0xFFFF0000u);
+          }
           __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
           out[16 * c + i] = *reinterpret_cast<uint32_t*>(&h);
+        }
+        if constexpr (EXT) {
+          if (p.z != nullptr && row_ok) {
+            __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.z) + grow * p.N + n_base + col;
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              if (n_base + col + 8 * v < p.N)
+                *reinterpret_cast<uint4*>(to + 8 * v) =
+                    make_uint4(pre[4 * v], pre[4 * v + 1], pre[4 * v + 2], pre[4 * v + 3]);
+          }
         }
       }
       tc_fence_before();
@@ -336,26 +368,31 @@ lynx_gemm_kernel(const __grid_constant__ GemmLaunch p) {
   if (warp == 1) tmem_dealloc(sm.tmem_base, kTmemCols);
 }
 
-template <int BN, bool SPARSE>
+template <int BN, bool SPARSE, bool EXT>
 cudaError_t launch_variant(const GemmLaunch& p, cudaStream_t stream) {
   const size_t smem = sizeof(GemmSmem<BN, SPARSE>) + 1024;
   static std::once_flag once[64];
   static cudaError_t configured[64];
   cudaError_t e = once_per_device(once, configured, [smem]() {
-    return cudaFuncSetAttribute(lynx_gemm_kernel<BN, SPARSE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(lynx_gemm_kernel<BN, SPARSE, EXT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 static_cast<int>(smem));
   });
   if (e != cudaSuccess) return e;
-  return launch_after_previous(lynx_gemm_kernel<BN, SPARSE>, dim3(static_cast<unsigned>(p.grid)),
+  return launch_after_previous(lynx_gemm_kernel<BN, SPARSE, EXT>, dim3(static_cast<unsigned>(p.grid)),
                                dim3(kGemmThreads), smem, stream, p);
+}
+
+template <bool EXT>
+cudaError_t launch_gemm_ext(const GemmLaunch& p, cudaStream_t stream) {
+  if (p.bn == 256)
+    return p.sparse ? launch_variant<256, true, EXT>(p, stream) : launch_variant<256, false, EXT>(p, stream);
+  return p.sparse ? launch_variant<128, true, EXT>(p, stream) : launch_variant<128, false, EXT>(p, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_gemm(const GemmLaunch& p, cudaStream_t stream) {
-  if (p.bn == 256)
-    return p.sparse ? launch_variant<256, true>(p, stream) : launch_variant<256, false>(p, stream);
-  return p.sparse ? launch_variant<128, true>(p, stream) : launch_variant<128, false>(p, stream);
+  return p.ext ? launch_gemm_ext<true>(p, stream) : launch_gemm_ext<false>(p, stream);
 }
 
 }  // namespace lynx

@@ -1,5 +1,6 @@
 // gemm_pair_kernel.cu -- the Lynx GEMM on CTA pairs (tcgen05 cta_group::2):
 //   Y[M,N] = bf16( act( s_row * (S(X) W^T + T' B^T) + bias ) )   (act: none or GELU)
+// and, in the variants with EXT, Y = bf16( R + act(v) ) with v itself in bf16 as Z.
 // Same arithmetic as gemm_kernel.cu (see there and the RT-Lynx references),
 // computed on 256 x 256 output tiles by a pair of CTAs on the two SMs of a
 // TPC: each CTA holds 128 rows of A (compressed activations, or X on the dense
@@ -30,6 +31,8 @@
 //               from stage to stage; a hardware barrier between two warps does
 //               not.
 #include <cuda_bf16.h>
+
+#include <type_traits>
 
 #include "lynx_act.cuh"
 #include "lynx_internal.h"
@@ -344,7 +347,17 @@ __device__ __forceinline__ bool compress_tile_stages(Smem& sm, uint32_t& g, int 
   return true;
 }
 
-template <bool SPARSE, int ACT, bool FUSED>
+// The residual's values for 32 columns of a row: four 16-byte pieces, N a multiple
+// of 8.  Plain loads: the residual may be Y itself, whose tiles this CTA writes
+// only after it has read them here.
+__device__ __forceinline__ void load_residual(uint4 (&v)[4], const __nv_bfloat16* row, int64_t n, int64_t N, bool there) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[i] = there && n + 8 * i < N ? *reinterpret_cast<const uint4*>(row + n + 8 * i) : make_uint4(0, 0, 0, 0);
+}
+
+// EXT: Y = R + act(v), and v itself to Z where it is wanted.
+template <bool SPARSE, int ACT, bool FUSED, bool EXT>
 __global__ void __launch_bounds__(kThreads, 1)
 lynx_gemm_pair_kernel(const __grid_constant__ GemmLaunch p) {
   using C = PairCfg<SPARSE, FUSED>;
@@ -660,6 +673,21 @@ lynx_gemm_pair_kernel(const __grid_constant__ GemmLaunch p) {
         if (p.fin_mode == 1) s = __ldcg(p.fin_scale + grow);
         else if (p.row_scale != nullptr) s = p.row_scale[grow];
       }
+      // The residual of this lane's row: the first 32 columns now, while the tile's MMAs
+      // run, each further 32 one step ahead of its use; all of it on its way to L2
+      const int64_t n_warp = n_base + ch * kHalf;
+      const bool add = EXT && p.residual != nullptr;
+      const __nv_bfloat16* res_row = nullptr;
+      uint4 res[2][4];
+      if constexpr (EXT) {
+        if (add) {
+          res_row = static_cast<const __nv_bfloat16*>(p.residual) + grow * p.N;
+          load_residual(res[0], res_row, n_warp, p.N, row_ok);
+#pragma unroll
+          for (int i = 1; i < kHalf / 32; ++i)
+            if (row_ok && n_warp + 32 * i < p.N) prefetch_l2(res_row + n_warp + 32 * i);
+        }
+      }
       bool ok = !sm.abort_flag;
       if (ok && !mbar_wait(&sm.acc_full, static_cast<uint32_t>(acc_count) & 1u)) {
         record_error(p.status, kDevTimeoutAccum);
@@ -687,31 +715,58 @@ lynx_gemm_pair_kernel(const __grid_constant__ GemmLaunch p) {
 #pragma unroll
       for (int c = 0; c < kHalf / 32; ++c) {
         const int col = static_cast<int>(ch) * kHalf + 32 * c;
+        if constexpr (EXT) {
+          if (add && c + 1 < kHalf / 32) load_residual(res[(c + 1) & 1], res_row, n_warp + 32 * (c + 1), p.N, row_ok);
+        }
 #pragma unroll
-        for (int h = 0; h < 2; ++h, ++piece) {
+        for (int h = 0; h < 2; ++h) {
+          // 16 columns of the warp's 32 rows: through one of its two buffers to memory
+          auto store = [&](const uint32_t (&pk)[8], const CUtensorMap* map) {
+            uint8_t* buf = my_stage + 1024 * (piece++ & 1);
+            if (lane == 0) bulk_wait_read_le1();  // the store that last used `buf` has read it
+            __syncwarp();
+            // row `lane`, 16-byte chunks k = 0,1 at 32B-swizzled positions
+            const uint32_t sw = (lane >> 2) & 1u;
+            *reinterpret_cast<uint4*>(buf + lane * 32 + ((0u ^ sw) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            *reinterpret_cast<uint4*>(buf + lane * 32 + ((1u ^ sw) << 4)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(map, buf, static_cast<int32_t>(n_base + col + 16 * h), store_row);
+              bulk_commit();
+            }
+          };
           uint32_t pk[8];
+          if constexpr (EXT) {
+            if (p.z != nullptr) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int e = 16 * h + 2 * i;
+                __nv_bfloat162 zv = __floats2bfloat162_rn(__fmaf_rn(s, __uint_as_float(r[c][e]), sm.bias_s[col + e]),
+                                                          __fmaf_rn(s, __uint_as_float(r[c][e + 1]), sm.bias_s[col + e + 1]));
+                pk[i] = *reinterpret_cast<uint32_t*>(&zv);
+              }
+              store(pk, &p.tm_z);
+            }
+          }
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int e = 16 * h + 2 * i;
-            const float a = apply_act<ACT>(__fmaf_rn(s, __uint_as_float(r[c][e]), sm.bias_s[col + e]));
-            const float b =
+            float a = apply_act<ACT>(__fmaf_rn(s, __uint_as_float(r[c][e]), sm.bias_s[col + e]));
+            float b =
                 apply_act<ACT>(__fmaf_rn(s, __uint_as_float(r[c][e + 1]), sm.bias_s[col + e + 1]));
+            if constexpr (EXT) {
+              if (add) {
+                const uint4& v = res[c & 1][2 * h + i / 4];
+                const uint32_t w = i % 4 == 0 ? v.x : i % 4 == 1 ? v.y : i % 4 == 2 ? v.z : v.w;
+                a += __uint_as_float(w << 16);
+                b += __uint_as_float(w & 0xFFFF0000u);
+              }
+            }
             __nv_bfloat162 hv = __floats2bfloat162_rn(a, b);
             pk[i] = *reinterpret_cast<uint32_t*>(&hv);
           }
-          uint8_t* buf = my_stage + 1024 * (piece & 1);
-          if (lane == 0) bulk_wait_read_le1();  // the store that last used `buf` has read it
-          __syncwarp();
-          // row `lane`, 16-byte chunks k = 0,1 at 32B-swizzled positions
-          const uint32_t sw = (lane >> 2) & 1u;
-          *reinterpret_cast<uint4*>(buf + lane * 32 + ((0u ^ sw) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-          *reinterpret_cast<uint4*>(buf + lane * 32 + ((1u ^ sw) << 4)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tma_store_2d(&p.tm_y, buf, static_cast<int32_t>(n_base + col + 16 * h), store_row);
-            bulk_commit();
-          }
+          store(pk, &p.tm_y);
         }
       }
     }
@@ -729,17 +784,17 @@ static_assert(sizeof(PairSmem<true, false>) + 1024 <= 232448, "sparse pair GEMM 
 static_assert(sizeof(PairSmem<false, false>) + 1024 <= 232448, "dense pair GEMM shared memory");
 static_assert(sizeof(PairSmem<true, true>) + 1024 <= 232448, "fused pair GEMM shared memory");
 
-template <bool SPARSE, int ACT, bool FUSED>
+template <bool SPARSE, int ACT, bool FUSED, bool EXT>
 cudaError_t configure_pair_variant() {
   static std::once_flag once[64];
   static cudaError_t configured[64];
   return once_per_device(once, configured, []() {
-    return cudaFuncSetAttribute(lynx_gemm_pair_kernel<SPARSE, ACT, FUSED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(lynx_gemm_pair_kernel<SPARSE, ACT, FUSED, EXT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 static_cast<int>(sizeof(PairSmem<SPARSE, FUSED>) + 1024));
   });
 }
 
-template <bool SPARSE, int ACT, bool FUSED>
+template <bool SPARSE, int ACT, bool FUSED, bool EXT>
 cudaLaunchConfig_t pair_config(int grid, cudaStream_t stream, cudaLaunchAttribute (&attr)[2]) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
@@ -757,16 +812,16 @@ cudaLaunchConfig_t pair_config(int grid, cudaStream_t stream, cudaLaunchAttribut
   return cfg;
 }
 
-template <bool SPARSE, int ACT, bool FUSED>
+template <bool SPARSE, int ACT, bool FUSED, bool EXT>
 cudaError_t launch_pair_variant(const GemmLaunch& p, cudaStream_t stream) {
-  cudaError_t e = configure_pair_variant<SPARSE, ACT, FUSED>();
+  cudaError_t e = configure_pair_variant<SPARSE, ACT, FUSED, EXT>();
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
-  cudaLaunchConfig_t cfg = pair_config<SPARSE, ACT, FUSED>(p.grid, stream, attr);
-  return cudaLaunchKernelEx(&cfg, lynx_gemm_pair_kernel<SPARSE, ACT, FUSED>, p);
+  cudaLaunchConfig_t cfg = pair_config<SPARSE, ACT, FUSED, EXT>(p.grid, stream, attr);
+  return cudaLaunchKernelEx(&cfg, lynx_gemm_pair_kernel<SPARSE, ACT, FUSED, EXT>, p);
 }
 
-template <bool SPARSE, int ACT, bool FUSED>
+template <bool SPARSE, int ACT, bool FUSED, bool EXT>
 int pair_max_clusters_variant() {
   static std::once_flag once[64];
   static int clusters[64];
@@ -774,12 +829,12 @@ int pair_max_clusters_variant() {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   std::call_once(once[dev], [dev]() {
     clusters[dev] = 0;
-    if (configure_pair_variant<SPARSE, ACT, FUSED>() != cudaSuccess) return;
+    if (configure_pair_variant<SPARSE, ACT, FUSED, EXT>() != cudaSuccess) return;
     cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = pair_config<SPARSE, ACT, FUSED>(2, nullptr, attr);
+    cudaLaunchConfig_t cfg = pair_config<SPARSE, ACT, FUSED, EXT>(2, nullptr, attr);
     cfg.numAttrs = 1;  // the cluster shape is what matters here
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, lynx_gemm_pair_kernel<SPARSE, ACT, FUSED>, &cfg) == cudaSuccess)
+    if (cudaOccupancyMaxActiveClusters(&n, lynx_gemm_pair_kernel<SPARSE, ACT, FUSED, EXT>, &cfg) == cudaSuccess)
       clusters[dev] = n;
     else
       (void)cudaGetLastError();  // a failed query is not sticky; the caller falls back
@@ -787,27 +842,34 @@ int pair_max_clusters_variant() {
   return clusters[dev];
 }
 
+// One call of `use` with the variant's template arguments
+template <typename F>
+auto with_pair_variant(bool sparse, int act, bool fused, bool ext, F&& use) {
+  using std::bool_constant;
+  using std::integral_constant;
+  auto with_act = [&](auto sp, auto fu, auto ex) {
+    return act == kActGeluTanh ? use(sp, integral_constant<int, kActGeluTanh>(), fu, ex)
+                               : use(sp, integral_constant<int, kActNone>(), fu, ex);
+  };
+  constexpr bool_constant<true> yes;
+  constexpr bool_constant<false> no;
+  if (fused) return with_act(yes, yes, no);
+  if (ext) return sparse ? with_act(yes, no, yes) : with_act(no, no, yes);
+  return sparse ? with_act(yes, no, no) : with_act(no, no, no);
+}
+
 }  // namespace
 
-int gemm_pair_max_clusters(bool sparse, int act, bool fused) {
-  if (fused)
-    return act == kActGeluTanh ? pair_max_clusters_variant<true, kActGeluTanh, true>()
-                               : pair_max_clusters_variant<true, kActNone, true>();
-  if (act == kActGeluTanh)
-    return sparse ? pair_max_clusters_variant<true, kActGeluTanh, false>()
-                  : pair_max_clusters_variant<false, kActGeluTanh, false>();
-  return sparse ? pair_max_clusters_variant<true, kActNone, false>() : pair_max_clusters_variant<false, kActNone, false>();
+int gemm_pair_max_clusters(bool sparse, int act, bool fused, bool ext) {
+  return with_pair_variant(sparse, act, fused, ext, [](auto sp, auto ac, auto fu, auto ex) {
+    return pair_max_clusters_variant<sp.value, ac.value, fu.value, ex.value>();
+  });
 }
 
 cudaError_t launch_gemm_pair(const GemmLaunch& p, cudaStream_t stream) {
-  if (p.fused)
-    return p.act == kActGeluTanh ? launch_pair_variant<true, kActGeluTanh, true>(p, stream)
-                                 : launch_pair_variant<true, kActNone, true>(p, stream);
-  if (p.act == kActGeluTanh)
-    return p.sparse ? launch_pair_variant<true, kActGeluTanh, false>(p, stream)
-                    : launch_pair_variant<false, kActGeluTanh, false>(p, stream);
-  return p.sparse ? launch_pair_variant<true, kActNone, false>(p, stream)
-                  : launch_pair_variant<false, kActNone, false>(p, stream);
+  return with_pair_variant(p.sparse, p.act, p.fused, p.ext, [&](auto sp, auto ac, auto fu, auto ex) {
+    return launch_pair_variant<sp.value, ac.value, fu.value, ex.value>(p, stream);
+  });
 }
 
 }  // namespace lynx

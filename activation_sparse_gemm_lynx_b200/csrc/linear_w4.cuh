@@ -368,6 +368,7 @@ __global__ void __launch_bounds__(kFewThreads<T, NT>, 1) linear_w4_kernel(Linear
   }
   __syncthreads();
   const auto* bias = static_cast<const __nv_bfloat16*>(p.bias);
+  const auto* residual = static_cast<const __nv_bfloat16*>(p.residual);  // may be y
   auto* y = static_cast<__nv_bfloat16*>(p.y);
   for (uint32_t i = threadIdx.x; i < static_cast<uint32_t>(p.M) * rows; i += kFewThreads<T, NT>) {
     const int64_t n = n0 + i % rows;
@@ -377,6 +378,7 @@ __global__ void __launch_bounds__(kFewThreads<T, NT>, 1) linear_w4_kernel(Linear
     for (int w = 0; w < kRing; ++w) v += red[w * NT * 8 * rows + i];
     if (bias != nullptr) v += __bfloat162float(bias[n]);
     if (p.act == kActGeluTanh) v = gelu_tanh(v);
+    if (residual != nullptr) v += __bfloat162float(residual[(i / rows) * p.N + n]);
     y[(i / rows) * p.N + n] = __float2bfloat16_rn(v);
   }
 }

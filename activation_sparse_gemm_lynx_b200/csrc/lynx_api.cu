@@ -289,7 +289,7 @@ lynx_status run_gemm(DeviceState* ds, const void* a_src, bool sparse, const void
                      const float* row_scale, const void* T, const void* W, const void* bias,
                      const void* B, int64_t M, int64_t N, int64_t K, int64_t r, void* Y,
                      cudaStream_t stream, const FusedFinalize* fin = nullptr, int act = kActNone,
-                     bool fused_x = false) {
+                     bool fused_x = false, const void* R = nullptr, void* Z = nullptr) {
   GemmLaunch p;
   std::memset(&p, 0, sizeof(p));
   const bool pair = use_pair_kernel(M, N, K);
@@ -327,10 +327,15 @@ lynx_status run_gemm(DeviceState* ds, const void* a_src, bool sparse, const void
   }
   if (pair && !encode_bf16_2d(&p.tm_y, Y, N, M, N * 2, 16, 32, CU_TENSOR_MAP_SWIZZLE_32B))
     return LYNX_ERR_CUDA;
+  if (pair && Z != nullptr && !encode_bf16_2d(&p.tm_z, Z, N, M, N * 2, 16, 32, CU_TENSOR_MAP_SWIZZLE_32B))
+    return LYNX_ERR_CUDA;
   p.meta = static_cast<const uint8_t*>(meta);
   p.row_scale = row_scale;
   p.bias = bias;
   p.y = Y;
+  p.residual = R;
+  p.z = Z;
+  p.ext = (R != nullptr || Z != nullptr) ? 1 : 0;
   p.M = M;
   p.N = N;
   p.K = K;
@@ -347,7 +352,7 @@ lynx_status run_gemm(DeviceState* ds, const void* a_src, bool sparse, const void
     const int64_t tiles = ntm2 * ((N + 255) / 256);
     // one CTA pair per TPC, no more pairs than the device can hold at once
     int64_t pairs = ds->sms / 2;
-    const int fit = gemm_pair_max_clusters(sparse, act, fused_x);
+    const int fit = gemm_pair_max_clusters(sparse, act, fused_x, p.ext != 0);
     if (fit > 0 && fit < pairs) pairs = fit;
     p.grid = static_cast<int>(2 * (tiles < pairs ? tiles : pairs));
     // raster group: as many 256-row pair-rows of A as fit in ~64 MB of L2, so
@@ -530,7 +535,7 @@ namespace {
 lynx_status linear_enqueue(const void* X, const void* W, const void* bias, const void* A, const void* B,
                            int64_t M, int64_t N, int64_t K, int64_t r, int skip_sparsify, int act, void* Y,
                            void* workspace, size_t workspace_bytes, cudaStream_t s, bool do_begin,
-                           bool do_finish, bool reset_flags) {
+                           bool do_finish, bool reset_flags, const void* R = nullptr, void* Z = nullptr) {
   if (X == nullptr || W == nullptr || Y == nullptr) return LYNX_ERR_INVALID_ARG;
   if (act != LYNX_ACT_NONE && act != LYNX_ACT_GELU_TANH) return LYNX_ERR_INVALID_ARG;
   lynx_status st = check_lora(A, B, r);
@@ -538,7 +543,8 @@ lynx_status linear_enqueue(const void* X, const void* W, const void* bias, const
   st = check_shape(M, N, K);
   if (st != LYNX_OK) return st;
   if (!aligned16(X) || !aligned16(W) || !aligned16(Y) || (bias && !aligned16(bias)) ||
-      (A && !aligned16(A)) || (B && !aligned16(B)) || (workspace && !aligned16(workspace)))
+      (A && !aligned16(A)) || (B && !aligned16(B)) || (workspace && !aligned16(workspace)) || !aligned16(R) ||
+      !aligned16(Z))
     return LYNX_ERR_MISALIGNED;
   const bool lora = A != nullptr;
   const bool need_ws = lora || !skip_sparsify;
@@ -579,9 +585,19 @@ lynx_status linear_enqueue(const void* X, const void* W, const void* bias, const
     if (cudaEventRecord(static_cast<cudaEvent_t>(ev), s) != cudaSuccess) return LYNX_ERR_CUDA;
   if (!skip_sparsify)
     return run_gemm(ds, ws + wl.vals, true, ws + wl.meta, reinterpret_cast<const float*>(ws + wl.scale),
-                    t_buf, W, bias, B, M, N, K, r, Y, s, fused ? &fin : nullptr, act);
+                    t_buf, W, bias, B, M, N, K, r, Y, s, fused ? &fin : nullptr, act, false, R, Z);
   return run_gemm(ds, X, false, nullptr, nullptr, t_buf, W, bias, B, M, N, K, r, Y, s,
-                  fused ? &fin : nullptr, act);
+                  fused ? &fin : nullptr, act, false, R, Z);
+}
+
+struct Span {
+  const void* p;  // null: not there
+  size_t bytes;
+};
+
+bool overlap(const Span& a, const Span& b) {
+  const auto x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x != 0 && y != 0 && x < y + b.bytes && y < x + a.bytes;
 }
 
 }  // namespace
@@ -594,6 +610,28 @@ int lynx_linear_act(const void* X, const void* W, const void* bias, const void* 
   const int part = g_profile_part.load();
   return linear_enqueue(X, W, bias, A, B, M, N, K, r, skip_sparsify, act, Y, workspace, workspace_bytes,
                         static_cast<cudaStream_t>(stream), part != 2, part != 1, part == 2);
+}
+
+int lynx_linear_residual(const void* X, const void* W, const void* bias, const void* A, const void* B,
+                         const void* R, int64_t M, int64_t N, int64_t K, int64_t r, int skip_sparsify, int act,
+                         void* Y, void* Z, void* workspace, size_t workspace_bytes, void* stream) {
+  const lynx_status st = check_shape(M, N, K);  // the sizes below are products of these
+  if (X != nullptr && W != nullptr && Y != nullptr && st == LYNX_OK && (A == nullptr || rank_supported(r))) {
+    const size_t m = static_cast<size_t>(M), n = static_cast<size_t>(N), k = static_cast<size_t>(K);
+    const bool need_ws = A != nullptr || !skip_sparsify;
+    const Span out[3] = {{Y, m * n * 2}, {Z, m * n * 2}, {need_ws ? workspace : nullptr, workspace_layout(M, K, r).total}};
+    const size_t rr = A != nullptr ? static_cast<size_t>(r) : 0;
+    const Span in[6] = {{X, m * k * 2}, {W, n * k * 2}, {bias, n * 2}, {A, rr * k * 2}, {B, n * rr * 2}, {R, m * n * 2}};
+    for (int o = 0; o < 3; ++o) {
+      for (const Span& i : in)
+        if (overlap(out[o], i) && !(o == 0 && i.p == R && R == Y)) return LYNX_ERR_INVALID_ARG;
+      for (int q = 0; q < o; ++q)
+        if (overlap(out[o], out[q])) return LYNX_ERR_INVALID_ARG;
+    }
+  }
+  const int part = g_profile_part.load();
+  return linear_enqueue(X, W, bias, A, B, M, N, K, r, skip_sparsify, act, Y, workspace, workspace_bytes,
+                        static_cast<cudaStream_t>(stream), part != 2, part != 1, part == 2, R, Z);
 }
 
 int lynx_linear_begin(const void* X, const void* W, const void* bias, const void* A, const void* B,

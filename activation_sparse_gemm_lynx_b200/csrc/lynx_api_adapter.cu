@@ -1,6 +1,7 @@
 // lynx_api_adapter.cu -- the C ABI's entry points for the weight in 4 bits, the
 // 8-bit activation checkpoint and the backward pass: argument checks and
 // launches.  As everywhere, a failed check launches nothing.
+#include <cmath>
 #include <cstring>
 #include <initializer_list>
 
@@ -30,6 +31,8 @@ bool k_ok(int64_t K) { return K >= 64 && K % 64 == 0 && K <= kMaxExtent; }
 bool n_ok(int64_t N) { return N >= 8 && N % 8 == 0 && N <= kMaxExtent; }
 bool group_ok(int64_t K, int group) { return (group == 32 || group == 64 || group == 128) && K % group == 0; }
 bool rank_ok(int64_t r) { return lynx_lora_rank_supported(r) != 0; }
+bool norm_cols_ok(int64_t K) { return K >= 8 && K % 8 == 0 && K <= kLayerNormMaxCols; }
+bool eps_ok(float eps) { return eps >= 0.f && std::isfinite(eps); }
 bool format_ok(int format) { return format == LYNX_CKPT8_INT8 || format == LYNX_CKPT8_E4M3; }
 
 int status_of(cudaError_t e) { return e == cudaSuccess ? LYNX_OK : LYNX_ERR_CUDA; }
@@ -112,13 +115,20 @@ size_t lynx_linear_w4_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t r
 int lynx_linear_w4(const void* X, const void* Wq, const void* scales, const void* zeros, const void* bias,
                    const void* A, const void* B, int64_t M, int64_t N, int64_t K, int64_t r, int group, int act,
                    void* Y, void* workspace, size_t workspace_bytes, void* stream) {
+  return lynx_linear_w4_residual(X, Wq, scales, zeros, bias, A, B, nullptr, M, N, K, r, group, act, Y, workspace,
+                                 workspace_bytes, stream);
+}
+
+int lynx_linear_w4_residual(const void* X, const void* Wq, const void* scales, const void* zeros, const void* bias,
+                            const void* A, const void* B, const void* R, int64_t M, int64_t N, int64_t K, int64_t r,
+                            int group, int act, void* Y, void* workspace, size_t workspace_bytes, void* stream) {
   static_assert(kLinearW4MaxRows == LYNX_LINEAR_W4_MAX_ROWS, "");
   if (any_null(X, Wq, scales, Y)) return LYNX_ERR_INVALID_ARG;
   if (act != LYNX_ACT_NONE && act != LYNX_ACT_GELU_TANH) return LYNX_ERR_INVALID_ARG;
   if (const int st = check_branch(A, B, r)) return st;
   if (M < 1 || M > LYNX_LINEAR_W4_MAX_ROWS || !n_ok(N) || !k_ok(K) || !group_ok(K, group))
     return LYNX_ERR_UNSUPPORTED_SHAPE;
-  if (any_misaligned(X, Wq, scales, zeros, bias, A, B, Y, workspace)) return LYNX_ERR_MISALIGNED;
+  if (any_misaligned(X, Wq, scales, zeros, bias, A, B, R, Y, workspace)) return LYNX_ERR_MISALIGNED;
   if (A != nullptr) {
     if (workspace == nullptr) return LYNX_ERR_INVALID_ARG;
     if (workspace_bytes < lynx_linear_w4_workspace_bytes(M, N, K, r)) return LYNX_ERR_WORKSPACE_TOO_SMALL;
@@ -131,7 +141,9 @@ int lynx_linear_w4(const void* X, const void* Wq, const void* scales, const void
                    {zeros, bytes_of(K / group, N, 1)},
                    {bias, bytes_of(1, N, 2)},
                    {A, bytes_of(r, K, 2)},
-                   {B, bytes_of(N, r, 2)}}))
+                   {B, bytes_of(N, r, 2)},
+                   {R != Y ? R : nullptr, bytes_of(M, N, 2)}}) ||
+      any_overlap({ws}, {{R, bytes_of(M, N, 2)}}))
     return LYNX_ERR_INVALID_ARG;
   const int sms = device_sm_count();
   if (sms == 0) return LYNX_ERR_CUDA;
@@ -152,6 +164,7 @@ int lynx_linear_w4(const void* X, const void* Wq, const void* scales, const void
   p.r = A != nullptr ? static_cast<int>(r) : 0;
   p.group = group;
   p.act = act;
+  p.residual = R;
   return status_of(launch_linear_w4(p, sms, static_cast<cudaStream_t>(stream)));
 }
 
@@ -290,6 +303,113 @@ int lynx_sparsify_backward_meta(const void* G, const void* q, const void* e, con
                                 size_t workspace_bytes, void* stream) {
   if (meta == nullptr) return LYNX_ERR_INVALID_ARG;
   return sparsify_backward(G, q, e, meta, dT, A, M, K, r, format, dX, workspace, workspace_bytes, stream);
+}
+
+// ---- layer norm, the activation's backward pass
+
+int64_t lynx_layer_norm_max_cols(void) { return LYNX_LAYER_NORM_MAX_COLS; }
+
+int lynx_layer_norm(const void* X, const void* weight, const void* bias, int64_t M, int64_t K, float eps, void* Y,
+                    float* mean, float* rstd, void* stream) {
+  static_assert(kLayerNormMaxCols == LYNX_LAYER_NORM_MAX_COLS, "");
+  if (any_null(X, Y) || (mean == nullptr) != (rstd == nullptr) || !eps_ok(eps)) return LYNX_ERR_INVALID_ARG;
+  if (!rows_ok(M) || !norm_cols_ok(K)) return LYNX_ERR_UNSUPPORTED_SHAPE;
+  if (any_misaligned(X, weight, bias, Y, mean, rstd)) return LYNX_ERR_MISALIGNED;
+  if (any_overlap({{Y, bytes_of(M, K, 2)}, {mean, bytes_of(M, 1, 4)}, {rstd, bytes_of(M, 1, 4)}},
+                  {{X, bytes_of(M, K, 2)}, {weight, bytes_of(1, K, 2)}, {bias, bytes_of(1, K, 2)}}))
+    return LYNX_ERR_INVALID_ARG;
+  const int sms = device_sm_count();
+  if (sms == 0) return LYNX_ERR_CUDA;
+  LayerNormLaunch p = {};
+  p.x = X;
+  p.w = weight;
+  p.b = bias;
+  p.y = Y;
+  p.mean = mean;
+  p.rstd = rstd;
+  p.M = M;
+  p.K = K;
+  p.eps = eps;
+  return status_of(launch_layer_norm(p, sms, static_cast<cudaStream_t>(stream)));
+}
+
+size_t lynx_layer_norm_backward_workspace_bytes(int64_t M, int64_t K) {
+  if (!rows_ok(M) || !norm_cols_ok(K)) return 0;
+  return align256(layer_norm_backward_workspace(M, K));
+}
+
+int lynx_layer_norm_backward(const void* dY, const void* X, const float* mean, const float* rstd, const void* weight,
+                             const void* dR, int64_t M, int64_t K, void* dX, void* dweight, void* dbias, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  if (any_null(dY, X, mean, rstd, dX)) return LYNX_ERR_INVALID_ARG;
+  if (!rows_ok(M) || !norm_cols_ok(K)) return LYNX_ERR_UNSUPPORTED_SHAPE;
+  if (any_misaligned(dY, X, mean, rstd, weight, dR, dX, dweight, dbias, workspace)) return LYNX_ERR_MISALIGNED;
+  const bool sums = dweight != nullptr || dbias != nullptr;
+  const size_t need = sums ? lynx_layer_norm_backward_workspace_bytes(M, K) : 0;
+  if (sums) {
+    if (workspace == nullptr) return LYNX_ERR_INVALID_ARG;
+    if (workspace_bytes < need) return LYNX_ERR_WORKSPACE_TOO_SMALL;
+  }
+  const Span ws = {sums ? workspace : nullptr, need}, dw = {dweight, bytes_of(1, K, 2)}, db = {dbias, bytes_of(1, K, 2)};
+  if (any_overlap({{dX, bytes_of(M, K, 2)}, dw, db, ws},
+                  {{dY, bytes_of(M, K, 2)},
+                   {X, bytes_of(M, K, 2)},
+                   {mean, bytes_of(M, 1, 4)},
+                   {rstd, bytes_of(M, 1, 4)},
+                   {weight, bytes_of(1, K, 2)},
+                   {dR != dX ? dR : nullptr, bytes_of(M, K, 2)}}) ||
+      any_overlap({dw, db, ws}, {{dR, bytes_of(M, K, 2)}}))
+    return LYNX_ERR_INVALID_ARG;
+  if (device_sm_count() == 0) return LYNX_ERR_CUDA;
+  LayerNormBackwardLaunch p = {};
+  p.dy = dY;
+  p.x = X;
+  p.w = weight;
+  p.mean = mean;
+  p.rstd = rstd;
+  p.dr = dR;
+  p.dx = dX;
+  p.dw = dweight;
+  p.db = dbias;
+  p.part = static_cast<float*>(workspace);
+  p.M = M;
+  p.K = K;
+  return status_of(launch_layer_norm_backward(p, static_cast<cudaStream_t>(stream)));
+}
+
+size_t lynx_act_backward_workspace_bytes(int64_t M, int64_t N) {
+  if (!rows_ok(M) || !n_ok(N)) return 0;
+  return align256(column_pass_workspace(M, N, 1));
+}
+
+int lynx_act_backward(const void* dY, const void* Z, int64_t M, int64_t N, int act, void* dZ, void* dbias,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+  if (act != LYNX_ACT_NONE && act != LYNX_ACT_GELU_TANH) return LYNX_ERR_INVALID_ARG;
+  if (dY == nullptr) return LYNX_ERR_INVALID_ARG;
+  if (act == LYNX_ACT_NONE ? Z != nullptr || dZ != nullptr || dbias == nullptr : any_null(Z, dZ))
+    return LYNX_ERR_INVALID_ARG;
+  if (!rows_ok(M) || !n_ok(N)) return LYNX_ERR_UNSUPPORTED_SHAPE;
+  if (any_misaligned(dY, Z, dZ, dbias, workspace)) return LYNX_ERR_MISALIGNED;
+  const size_t need = dbias != nullptr ? lynx_act_backward_workspace_bytes(M, N) : 0;
+  if (dbias != nullptr) {
+    if (workspace == nullptr) return LYNX_ERR_INVALID_ARG;
+    if (workspace_bytes < need) return LYNX_ERR_WORKSPACE_TOO_SMALL;
+  }
+  const Span ws = {dbias != nullptr ? workspace : nullptr, need}, db = {dbias, bytes_of(1, N, 2)};
+  const Span dy = {dY, bytes_of(M, N, 2)}, z = {Z, bytes_of(M, N, 2)};
+  if (any_overlap({{dZ, bytes_of(M, N, 2)}, db, ws}, {z}) || any_overlap({db, ws}, {dy}) ||
+      (dZ != dY && any_overlap({{dZ, bytes_of(M, N, 2)}}, {dy})))
+    return LYNX_ERR_INVALID_ARG;
+  if (device_sm_count() == 0) return LYNX_ERR_CUDA;
+  ColumnPassLaunch p = {};
+  p.dy = dY;
+  p.z = Z;
+  p.dz = dZ;
+  p.out0 = dbias;
+  p.part = dbias != nullptr ? static_cast<float*>(workspace) : nullptr;
+  p.M = M;
+  p.N = N;
+  return status_of(launch_act_backward(p, act, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

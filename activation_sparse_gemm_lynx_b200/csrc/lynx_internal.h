@@ -93,10 +93,14 @@ struct GemmLaunch {
   CUtensorMap tm_lb;    // B [N,r] box 32 x BN, SW64 (lora)
   CUtensorMap tm_e;     // metadata as uint8 [blocks*8, 256], box 256 x 8 (pair kernel)
   CUtensorMap tm_y;     // Y [M,N] bf16, box 16 x 32, 32B swizzle (pair kernel stores)
+  CUtensorMap tm_z;     // Z, the same (pair kernel, ext with z)
   const uint8_t* meta;  // hardware metadata blocks (sparse)
   const void* bias;     // [N] bf16 or null
   const float* row_scale;  // [M] fp32 multiplier of each accumulator row, or null
   void* y;              // [M,N] bf16
+  const void* residual;  // [M,N] bf16 added to the activation's value, or null (ext)
+  void* z;              // [M,N] bf16: the value before the activation, or null (ext)
+  int ext;              // residual or z is there (not with `fused`)
   int64_t M, N, K;
   int r;                // LoRA rank (lora)
   int sparse;
@@ -129,7 +133,7 @@ cudaError_t launch_gemm(const GemmLaunch& p, cudaStream_t stream);       // 128 
 cudaError_t launch_gemm_pair(const GemmLaunch& p, cudaStream_t stream);  // 256 x 256 tiles, CTA pairs
 // CTA pairs of the pair GEMM (this variant) that the current device can hold at
 // once; 0 if the query failed.  Computed once per device and variant.
-int gemm_pair_max_clusters(bool sparse, int act, bool fused = false);
+int gemm_pair_max_clusters(bool sparse, int act, bool fused = false, bool ext = false);
 
 // Per-device one-time set-up of a kernel's dynamic shared-memory limit:
 // `configure` runs once for each device (thread-safe); its result is kept.
@@ -171,6 +175,7 @@ struct LinearW4Launch {
   void* y;             // [M,N] bf16
   int64_t N, K;
   int M, r, group, act;
+  const void* residual;  // [M,N] bf16 added to the activation's value, or null
 };
 cudaError_t launch_linear_w4(const LinearW4Launch& p, int sms, cudaStream_t s);
 cudaError_t launch_linear_w4_g32(const LinearW4Launch& p, int sms, cudaStream_t s);
@@ -210,6 +215,56 @@ struct SparsifyBackwardLaunch {
   uint32_t* status;  // the stream's status word
 };
 cudaError_t launch_sparsify_backward(const SparsifyBackwardLaunch& p, int sms, cudaStream_t s);
+
+// ---- layer norm, the activation's backward pass ------------------------------
+
+constexpr int64_t kLayerNormMaxCols = 32768;
+
+struct LayerNormLaunch {
+  const void* x;  // [M,K] bf16
+  const void* w;  // [K] bf16, or null: 1
+  const void* b;  // [K] bf16, or null: 0
+  void* y;        // [M,K] bf16
+  float* mean;    // [M], or null
+  float* rstd;    // [M] (with mean)
+  int64_t M, K;
+  float eps;
+};
+cudaError_t launch_layer_norm(const LayerNormLaunch& p, int sms, cudaStream_t s);
+
+struct LayerNormBackwardLaunch {
+  const void* dy;     // [M,K] bf16
+  const void* x;      // [M,K] bf16
+  const void* w;      // [K] bf16, or null: 1
+  const float* mean;  // [M]
+  const float* rstd;  // [M]
+  const void* dr;     // [M,K] bf16 added to dx, or null
+  void* dx;           // [M,K] bf16
+  void* dw;           // [K] bf16, or null
+  void* db;           // [K] bf16, or null
+  float* part;        // workspace (with dw or db)
+  int64_t M, K;
+};
+size_t layer_norm_backward_workspace(int64_t M, int64_t K);
+cudaError_t launch_layer_norm_backward(const LayerNormBackwardLaunch& p, cudaStream_t s);
+
+// A pass over dy that sums its columns
+struct ColumnPassLaunch {
+  const void* dy;     // [M,N] bf16
+  const void* z;      // [M,N] bf16: the pre-activation, or layer norm's x
+  const float* mean;  // [M] (layer norm)
+  const float* rstd;  // [M]
+  void* dz;           // [M,N] bf16 (activation)
+  void* out0;         // [N] bf16: the bias's gradient, or layer norm's weight's, or null
+  void* out1;         // [N] bf16: layer norm's bias's, or null
+  float* part;        // workspace; null: no sums
+  int64_t M, N;
+};
+size_t column_pass_workspace(int64_t M, int64_t N, int sums);
+cudaError_t launch_act_backward(const ColumnPassLaunch& p, int act, cudaStream_t s);
+cudaError_t launch_layer_norm_columns(const ColumnPassLaunch& p, cudaStream_t s);
+// part [count][2K] -> out0, out1 [K] bf16 (either may be null)
+cudaError_t launch_column_sums(const float* part, int count, int64_t K, void* out0, void* out1, cudaStream_t s);
 
 // ---- helpers ----------------------------------------------------------------
 

@@ -109,6 +109,15 @@ class Call {
     return static_cast<int>(v);
   }
 
+  float real(int i) const {
+    const double v = PyFloat_AsDouble(args_[i]);
+    if (v == -1.0 && PyErr_Occurred()) {
+      PyErr_Clear();
+      refuse(PyExc_TypeError, "a number is required");
+    }
+    return static_cast<float>(v);
+  }
+
   bool truth(int i) const {
     const int v = PyObject_IsTrue(args_[i]);
     if (v < 0) {
@@ -242,9 +251,11 @@ PyObject* w4_dequantize(PyObject* const* args, Py_ssize_t n) {
   return st != LYNX_OK ? PyLong_FromLong(st) : wrap(W);
 }
 
-// X, Wq, scales, zeros, bias, A, B, act, Y, workspace, stream
-PyObject* linear_w4(PyObject* const* args, Py_ssize_t n) {
-  const Call c(args, n, 11, "X");
+// The arguments of linear_w4 (without R) and linear_w4_residual (with it)
+template <bool RESIDUAL>
+PyObject* linear_few(PyObject* const* args, Py_ssize_t n) {
+  constexpr int at = RESIDUAL ? 8 : 7;  // of act; then Y, workspace, stream
+  const Call c(args, n, at + 4, "X");
   const W4 g(c, 1, 2);
   const auto [M, k] = c.matrix(0, "X");
   if (k != g.K) refuse(PyExc_ValueError, "X must be [M,K] with K = 2 * Wq.shape[1]");
@@ -262,12 +273,109 @@ PyObject* linear_w4(PyObject* const* args, Py_ssize_t n) {
     r = c.matrix(5, "A").first;
     a = c.in(5, "A", at::kBFloat16, {r, g.K});
     b = c.in(6, "B", at::kBFloat16, {g.N, r});
-    work = c.workspace(9, lynx_linear_w4_workspace_bytes(M, g.N, g.K, r), ws);
+    work = c.workspace(at + 2, lynx_linear_w4_workspace_bytes(M, g.N, g.K, r), ws);
   }
-  void* y = c.out(8, "Y", at::kBFloat16, {M, g.N}, Y);
-  const int st = lynx_linear_w4(x, q, s, z, bias, a, b, M, g.N, g.K, r, g.group(), c.integer(7), y,
-                                work.first, work.second, c.stream());
+  const void* res = RESIDUAL ? c.optional_in(7, "R", at::kBFloat16, {M, g.N}) : nullptr;
+  void* y = c.out(at + 1, "Y", at::kBFloat16, {M, g.N}, Y);
+  const int st = lynx_linear_w4_residual(x, q, s, z, bias, a, b, res, M, g.N, g.K, r, g.group(), c.integer(at), y,
+                                         work.first, work.second, c.stream());
   return st != LYNX_OK ? PyLong_FromLong(st) : wrap(Y);
+}
+
+// X, Wq, scales, zeros, bias, A, B, act, Y, workspace, stream
+PyObject* linear_w4(PyObject* const* args, Py_ssize_t n) { return linear_few<false>(args, n); }
+
+// X, Wq, scales, zeros, bias, A, B, R, act, Y, workspace, stream
+PyObject* linear_w4_residual(PyObject* const* args, Py_ssize_t n) { return linear_few<true>(args, n); }
+
+// X, W, bias, A, B, R, skip_sparsify, act, Y, Z, want_Z, workspace, stream
+PyObject* linear_residual(PyObject* const* args, Py_ssize_t n) {
+  const Call c(args, n, 13, "X");
+  const auto [M, K] = c.matrix(0, "X");
+  const int64_t N = c.matrix(1, "W").first;
+  at::Tensor Y, Z, ws;
+  const void* x = c.in(0, "X", at::kBFloat16, {M, K});
+  const void* w = c.in(1, "W", at::kBFloat16, {N, K});
+  const void* bias = c.optional_in(2, "bias", at::kBFloat16, {N});
+  const void *a = nullptr, *b = nullptr;
+  int64_t r = 0;
+  if (c.given(3) != c.given(4)) refuse(PyExc_ValueError, "A and B must both be given or both be None");
+  if (c.given(3)) {
+    r = c.matrix(3, "A").first;
+    a = c.in(3, "A", at::kBFloat16, {r, K});
+    b = c.in(4, "B", at::kBFloat16, {N, r});
+  }
+  const void* res = c.optional_in(5, "R", at::kBFloat16, {M, N});
+  const int skip = c.truth(6) ? 1 : 0, act = c.integer(7);
+  const auto work = c.workspace(11, skip && a == nullptr ? 0 : lynx_workspace_bytes(M, N, K, r), ws);
+  void* y = c.out(8, "Y", at::kBFloat16, {M, N}, Y);
+  void* z = c.given(9) || c.truth(10) ? c.out(9, "Z", at::kBFloat16, {M, N}, Z) : nullptr;
+  const int st = lynx_linear_residual(x, w, bias, a, b, res, M, N, K, r, skip, act, y, z, work.first, work.second,
+                                      c.stream());
+  return st != LYNX_OK ? PyLong_FromLong(st) : wrap_all({Y, Z});
+}
+
+// dY, Z, act, want_bias, dZ, dbias, workspace, stream
+PyObject* act_backward(PyObject* const* args, Py_ssize_t n) {
+  const Call c(args, n, 8, "dY");
+  const auto [M, N] = c.matrix(0, "dY");
+  const int act = c.integer(2);
+  at::Tensor dZ, dbias, ws;
+  const void* dy = c.in(0, "dY", at::kBFloat16, {M, N});
+  const void* z = c.optional_in(1, "Z", at::kBFloat16, {M, N});
+  const bool none = act == LYNX_ACT_NONE;
+  if (none ? c.given(1) || c.given(4) : !c.given(1))
+    refuse(PyExc_ValueError, none ? "without an activation there is no Z, and dZ is dY" : "Z is required");
+  void* dz = none ? nullptr : c.out(4, "dZ", at::kBFloat16, {M, N}, dZ);
+  void* db = nullptr;
+  std::pair<void*, size_t> work{nullptr, 0};
+  if (c.given(5) || c.truth(3)) {
+    db = c.out(5, "dbias", at::kBFloat16, {N}, dbias);
+    work = c.workspace(6, lynx_act_backward_workspace_bytes(M, N), ws);
+  }
+  const int st = lynx_act_backward(dy, z, M, N, act, dz, db, work.first, work.second, c.stream());
+  if (st != LYNX_OK) return PyLong_FromLong(st);
+  return wrap_all({none ? c.tensor(0, "dY") : dZ, dbias});
+}
+
+// X, weight, bias, eps, want_stats, Y, mean, rstd, stream
+PyObject* layer_norm(PyObject* const* args, Py_ssize_t n) {
+  const Call c(args, n, 9, "X");
+  const auto [M, K] = c.matrix(0, "X");
+  at::Tensor Y, mean, rstd;
+  const void* x = c.in(0, "X", at::kBFloat16, {M, K});
+  const void* w = c.optional_in(1, "weight", at::kBFloat16, {K});
+  const void* b = c.optional_in(2, "bias", at::kBFloat16, {K});
+  const float eps = c.real(3);
+  void* y = c.out(5, "Y", at::kBFloat16, {M, K}, Y);
+  void *m = nullptr, *s = nullptr;
+  if (c.given(6) || c.given(7) || c.truth(4)) {
+    m = c.out(6, "mean", at::kFloat, {M}, mean);
+    s = c.out(7, "rstd", at::kFloat, {M}, rstd);
+  }
+  const int st = lynx_layer_norm(x, w, b, M, K, eps, y, static_cast<float*>(m), static_cast<float*>(s), c.stream());
+  return st != LYNX_OK ? PyLong_FromLong(st) : wrap_all({Y, mean, rstd});
+}
+
+// dY, X, mean, rstd, weight, dR, want_weight, want_bias, dX, dweight, dbias, workspace, stream
+PyObject* layer_norm_backward(PyObject* const* args, Py_ssize_t n) {
+  const Call c(args, n, 13, "dY");
+  const auto [M, K] = c.matrix(0, "dY");
+  at::Tensor dX, dw, db, ws;
+  const void* dy = c.in(0, "dY", at::kBFloat16, {M, K});
+  const void* x = c.in(1, "X", at::kBFloat16, {M, K});
+  const void* mean = c.in(2, "mean", at::kFloat, {M});
+  const void* rstd = c.in(3, "rstd", at::kFloat, {M});
+  const void* w = c.optional_in(4, "weight", at::kBFloat16, {K});
+  const void* dr = c.optional_in(5, "dR", at::kBFloat16, {M, K});
+  void* dx = c.out(8, "dX", at::kBFloat16, {M, K}, dX);
+  void* dwp = c.given(9) || c.truth(6) ? c.out(9, "dweight", at::kBFloat16, {K}, dw) : nullptr;
+  void* dbp = c.given(10) || c.truth(7) ? c.out(10, "dbias", at::kBFloat16, {K}, db) : nullptr;
+  std::pair<void*, size_t> work{nullptr, 0};
+  if (dwp != nullptr || dbp != nullptr) work = c.workspace(11, lynx_layer_norm_backward_workspace_bytes(M, K), ws);
+  const int st = lynx_layer_norm_backward(dy, x, static_cast<const float*>(mean), static_cast<const float*>(rstd), w, dr,
+                                          M, K, dx, dwp, dbp, work.first, work.second, c.stream());
+  return st != LYNX_OK ? PyLong_FromLong(st) : wrap_all({dX, dw, db});
 }
 
 // X, format, q, e, stream
@@ -362,6 +470,11 @@ PyMethodDef g_methods[] = {method<w4_quantize>("w4_quantize"),
                            method<ckpt8_restore>("ckpt8_restore"),
                            method<lora_backward>("lora_backward"),
                            method<sparsify_backward>("sparsify_backward"),
+                           method<linear_w4_residual>("linear_w4_residual"),
+                           method<linear_residual>("linear_residual"),
+                           method<act_backward>("act_backward"),
+                           method<layer_norm>("layer_norm"),
+                           method<layer_norm_backward>("layer_norm_backward"),
                            {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_lynx_torch", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

@@ -50,6 +50,7 @@ def library():
                 "`python -m activation_sparse_gemm_lynx_b200.build`")
         lib = ctypes.CDLL(LIB_PATH)
         p, i64, sz, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
+        f32 = ctypes.c_float
         sigs = {
             "lynx_status_string": ([i32], ctypes.c_char_p),
             "lynx_version": ([], i32),
@@ -65,6 +66,7 @@ def library():
             "lynx_sparsify_noalloc_max_rows": ([], i64),
             "lynx_linear": ([p, p, p, p, p, i64, i64, i64, i64, i32, p, p, sz, p], i32),
             "lynx_linear_act": ([p, p, p, p, p, i64, i64, i64, i64, i32, i32, p, p, sz, p], i32),
+            "lynx_linear_residual": ([p, p, p, p, p, p, i64, i64, i64, i64, i32, i32, p, p, p, sz, p], i32),
             "lynx_linear_begin": ([p, p, p, p, p, i64, i64, i64, i64, i32, i32, p, p, sz, p], i32),
             "lynx_linear_finish": ([p, p, p, p, p, i64, i64, i64, i64, i32, i32, p, p, sz, p], i32),
             "lynx_linear_dense": ([p, p, p, p, p, i64, i64, i64, i64, p, p, sz, p], i32),
@@ -79,6 +81,7 @@ def library():
             "lynx_linear_w4_max_rows": ([], i64),
             "lynx_linear_w4_workspace_bytes": ([i64, i64, i64, i64], sz),
             "lynx_linear_w4": ([p, p, p, p, p, p, p, i64, i64, i64, i64, i32, i32, p, p, sz, p], i32),
+            "lynx_linear_w4_residual": ([p, p, p, p, p, p, p, p, i64, i64, i64, i64, i32, i32, p, p, sz, p], i32),
             "lynx_ckpt8_exponent_bytes": ([i64, i64], sz),
             "lynx_ckpt8_store": ([p, i64, i64, i32, p, p, p], i32),
             "lynx_ckpt8_restore": ([p, p, i64, i64, i32, p, p], i32),
@@ -87,6 +90,12 @@ def library():
             "lynx_sparsify_backward_workspace_bytes": ([i64, i64], sz),
             "lynx_sparsify_backward": ([p, p, p, p, p, i64, i64, i64, i32, p, p, sz, p], i32),
             "lynx_sparsify_backward_meta": ([p, p, p, p, p, p, i64, i64, i64, i32, p, p, sz, p], i32),
+            "lynx_act_backward_workspace_bytes": ([i64, i64], sz),
+            "lynx_act_backward": ([p, p, i64, i64, i32, p, p, p, sz, p], i32),
+            "lynx_layer_norm_max_cols": ([], i64),
+            "lynx_layer_norm": ([p, p, p, i64, i64, f32, p, p, p, p], i32),
+            "lynx_layer_norm_backward_workspace_bytes": ([i64, i64], sz),
+            "lynx_layer_norm_backward": ([p, p, p, p, p, p, i64, i64, p, p, p, p, sz, p], i32),
             "lynx_check_error": ([p, p], i32),
             "lynx_meta_hw_to_canonical": ([p, p, i64, i64], i32),
             "lynx_meta_canonical_to_hw": ([p, p, i64, i64], i32),
@@ -447,7 +456,7 @@ def lynx_sparse_gemm(vals, meta, W, bias=None, T=None, B=None, Y=None, stream=No
     return Y
 
 
-# ---- the weight in 4 bits, the 8-bit checkpoint, the backward pass ----------
+# ---- the weight in 4 bits, the 8-bit checkpoint, the backward pass, layer norm --
 #
 # These calls can be shorter on the device than a tensor check in Python, so their
 # marshalling is compiled (_build/_lynx_torch.*.so): it checks the tensors, which
@@ -510,6 +519,63 @@ def lynx_linear_w4(X, Wq, scales, zeros=None, bias=None, A=None, B=None, act=LYN
     (lynx_w4_quantize's outputs).  Returns Y."""
     return _result(_binding().linear_w4(X, Wq, scales, zeros, bias, A, B, act, Y, workspace, stream),
                    "lynx_linear_w4")
+
+
+def lynx_linear_w4_residual(X, Wq, scales, zeros=None, bias=None, A=None, B=None, R=None, act=LYNX_ACT_NONE,
+                            Y=None, workspace=None, stream=None):
+    """Y = R + act(X W^T + bias + (X A^T) B^T): lynx_linear_w4 with the residual
+    stream R [M,N] added before the one rounding.  Y may be R.  Returns Y."""
+    return _result(_binding().linear_w4_residual(X, Wq, scales, zeros, bias, A, B, R, act, Y, workspace, stream),
+                   "lynx_linear_w4_residual")
+
+
+def lynx_linear_residual(X, W, bias=None, A=None, B=None, R=None, skip_sparsify=False, act=LYNX_ACT_NONE, Y=None,
+                         Z=None, want_Z=False, workspace=None, stream=None):
+    """Y = R + act(P), P = S(X) W^T + bias + (X A^T) B^T, the residual stream R [M,N]
+    added in the GEMM's epilogue (S(X) = X if skip_sparsify).  Y may be R.  Returns
+    (Y, Z): Z is P in bf16, what lynx_act_backward takes, or None where neither
+    `want_Z` nor a Z to write is given."""
+    return _result(_binding().linear_residual(X, W, bias, A, B, R, skip_sparsify, act, Y, Z, want_Z, workspace,
+                                              stream), "lynx_linear_residual")
+
+
+def lynx_act_backward_workspace_bytes(M, N):
+    return library().lynx_act_backward_workspace_bytes(M, N)
+
+
+def lynx_act_backward(dY, Z=None, act=LYNX_ACT_GELU_TANH, want_bias=True, dZ=None, dbias=None, workspace=None,
+                      stream=None):
+    """The gradient of P from that of Y = R + act(P): returns (dZ [M,N], dbias [N]),
+    dZ = dY act'(Z) and dbias its sum over the rows (None without `want_bias`).
+    With LYNX_ACT_NONE there is no Z and dZ is dY, the tensor given.  A dZ to write
+    may be dY (in place)."""
+    return _result(_binding().act_backward(dY, Z, act, want_bias, dZ, dbias, workspace, stream), "lynx_act_backward")
+
+
+def lynx_layer_norm_max_cols():
+    return library().lynx_layer_norm_max_cols()
+
+
+def lynx_layer_norm(X, weight=None, bias=None, eps=1e-6, want_stats=False, Y=None, mean=None, rstd=None,
+                    stream=None):
+    """Layer norm of the rows of X [M,K]: (x - mean) rstd weight + bias.  Returns Y,
+    or with `want_stats` (Y, mean [M] f32, rstd [M] f32), what the backward pass takes."""
+    Y, mean, rstd = _result(_binding().layer_norm(X, weight, bias, eps, want_stats, Y, mean, rstd, stream),
+                            "lynx_layer_norm")
+    return (Y, mean, rstd) if want_stats else Y
+
+
+def lynx_layer_norm_backward_workspace_bytes(M, K):
+    return library().lynx_layer_norm_backward_workspace_bytes(M, K)
+
+
+def lynx_layer_norm_backward(dY, X, mean, rstd, weight=None, dR=None, want_weight=True, want_bias=True, dX=None,
+                             dweight=None, dbias=None, workspace=None, stream=None):
+    """The gradients of lynx_layer_norm: returns (dX [M,K], dweight [K], dbias [K]);
+    the last two are None where they are not wanted.  dR [M,K], the gradient that
+    reaches X beside the norm, is added to dX; a dX to write may be dR (in place)."""
+    return _result(_binding().layer_norm_backward(dY, X, mean, rstd, weight, dR, want_weight, want_bias, dX, dweight,
+                                                  dbias, workspace, stream), "lynx_layer_norm_backward")
 
 
 def lynx_ckpt8_exponent_bytes(M, K):

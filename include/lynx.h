@@ -239,6 +239,22 @@ LYNX_API int lynx_linear_act(const void* X, const void* W, const void* bias, con
                              int skip_sparsify, int act, void* Y, void* workspace,
                              size_t workspace_bytes, void* stream);
 
+/* Y = R + act(P), P = S(X) W^T + bias + (X A^T) B^T: lynx_linear_act with the residual
+ * stream added in the same epilogue, and with P itself kept for the backward pass.
+ *   R   [M,N] bf16, or NULL: nothing is added.  R may be Y itself (the stream is
+ *       updated in place).
+ *   Z   [M,N] bf16 out: P rounded once, or NULL: not kept.  lynx_act_backward takes it.
+ * Y is rounded once, after the sum with R in fp32 (the value that act sees is P
+ * before it is rounded to Z).  Saves the passes that would add R (two reads and a
+ * write of M*N*2 bytes) and recompute P.  Without R and Z the call is
+ * lynx_linear_act.  Every other argument, the workspace and the errors are those of
+ * lynx_linear_act; and a buffer that the call writes (the workspace among them)
+ * must overlap no other of its buffers but for R == Y, else LYNX_ERR_INVALID_ARG. */
+LYNX_API int lynx_linear_residual(const void* X, const void* W, const void* bias, const void* A,
+                                  const void* B, const void* R, int64_t M, int64_t N, int64_t K,
+                                  int64_t r, int skip_sparsify, int act, void* Y, void* Z,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---- the fully fused variant ------------------------------------------- */
 
 /* Y = act(S(X) W^T + bias + (X A^T) B^T) like lynx_linear_act, with the 2:4
@@ -373,6 +389,13 @@ LYNX_API int lynx_linear_w4(const void* X, const void* Wq, const void* scales, c
                             int64_t K, int64_t r, int group, int act, void* Y, void* workspace,
                             size_t workspace_bytes, void* stream);
 
+/* The same with the residual stream: Y = R + act(X W^T + bias + (X A^T) B^T), R [M,N]
+ * bf16 or NULL; R may be Y itself.  Rounded once, after the sum with R. */
+LYNX_API int lynx_linear_w4_residual(const void* X, const void* Wq, const void* scales, const void* zeros,
+                                     const void* bias, const void* A, const void* B, const void* R,
+                                     int64_t M, int64_t N, int64_t K, int64_t r, int group, int act,
+                                     void* Y, void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---- activation checkpoints in 8 bits ---------------------------------- */
 
 /* X kept for the backward pass in 8 bits: per row, every 32 consecutive values
@@ -405,8 +428,8 @@ LYNX_API int lynx_ckpt8_restore(const void* q, const void* e, int64_t M, int64_t
 
 /* ---- the layer's backward pass from a checkpoint ------------------------ */
 
-/* With x the checkpoint's values and dY [M,N] bf16 the gradient of Y (before
- * the activation, if one was applied), W frozen:
+/* With x the checkpoint's values and dY [M,N] bf16 the gradient of Y (of Z, before
+ * the activation, if one was applied: lynx_act_backward makes it), W frozen:
  *   the adapter's gradients      lynx_lora_backward
  *   G = dY W                     lynx_linear_dense(dY, W^T laid out once as [K,N])
  *   the gradient of X            lynx_sparsify_backward_meta with the metadata of
@@ -469,6 +492,71 @@ LYNX_API int lynx_sparsify_backward_meta(const void* G, const void* q, const voi
                                          const void* dT, const void* A, int64_t M, int64_t K, int64_t r,
                                          int format, void* dX, void* workspace, size_t workspace_bytes,
                                          void* stream);
+
+/* ---- the activation's backward pass --------------------------------------- */
+
+/* Bytes of the workspace lynx_act_backward needs where dbias is wanted. */
+LYNX_API size_t lynx_act_backward_workspace_bytes(int64_t M, int64_t N);
+
+/* dZ = dY act'(Z) [M,N], dbias = sum over the rows of dZ [N]; all bf16, rounded once
+ * (dbias from the unrounded dZ, summed in fp32 in an order that only the shape fixes:
+ * equal calls give equal bits).  With Y = R + act(P) of lynx_linear_residual, Z its
+ * Z: dZ is the gradient of P, what lynx_lora_backward and lynx_linear_dense (G = dZ W)
+ * take as dY; dbias is the bias's; R's is dY itself.
+ *   act == LYNX_ACT_GELU_TANH: Z and dZ are given; dZ may be dY itself; dbias may be
+ *     NULL (not wanted).  The derivative is that of LYNX_ACT_GELU_TANH's formula, with
+ *     the same hardware approximations (a few fp32 ulps).
+ *   act == LYNX_ACT_NONE: dZ is dY, so Z and dZ must be NULL and dbias is what is
+ *     computed; else LYNX_ERR_INVALID_ARG.
+ *   Any M >= 1, N % 8 == 0.  workspace: device scratch of workspace_bytes >=
+ *   lynx_act_backward_workspace_bytes(M,N), needed with dbias only. */
+LYNX_API int lynx_act_backward(const void* dY, const void* Z, int64_t M, int64_t N, int act, void* dZ,
+                               void* dbias, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- layer norm ------------------------------------------------------------ */
+
+/* What makes the layer's X from the residual stream, and its backward pass.  With mu
+ * and v the mean and the variance (over K, not K - 1) of a row of X [M,K],
+ *
+ *     rstd = (v + eps)^(-1/2),   Y = (x - mu) rstd weight + bias
+ *
+ * weight and bias [K] bf16, each or NULL (1 and 0).  Statistics in fp32, the mean
+ * taken off before anything is squared; Y is rounded once.  A row's squares must stay
+ * inside fp32 (|x - mu| below 2^63 / sqrt(K)).  A row with an infinity or a NaN gives
+ * NaN in that row alone.  M >= 1; 8 <= K <= LYNX_LAYER_NORM_MAX_COLS with K % 8 == 0.
+ * Buffers that a call of this section writes overlap no other of its buffers, but
+ * where it says so (else LYNX_ERR_INVALID_ARG). */
+#define LYNX_LAYER_NORM_MAX_COLS 32768
+
+/* LYNX_LAYER_NORM_MAX_COLS, for callers without the header. */
+LYNX_API int64_t lynx_layer_norm_max_cols(void);
+
+/*   Y [M,K] out; mean and rstd [M] fp32 out, both or neither (NULL): what the backward
+ *   pass takes.  eps finite and >= 0 (else LYNX_ERR_INVALID_ARG); with eps = 0 a
+ *   constant row gives NaN. */
+LYNX_API int lynx_layer_norm(const void* X, const void* weight, const void* bias, int64_t M, int64_t K,
+                             float eps, void* Y, float* mean, float* rstd, void* stream);
+
+/* Bytes of the workspace lynx_layer_norm_backward needs where dweight or dbias is
+ * wanted. */
+LYNX_API size_t lynx_layer_norm_backward_workspace_bytes(int64_t M, int64_t K);
+
+/* With xh = (x - mean) rstd and g = dY weight, the means over K:
+ *
+ *     dX = rstd (g - mean(g) - xh mean(g xh)) + dR
+ *     dweight = sum over the rows of dY xh,   dbias = sum over the rows of dY
+ *
+ *   dY, X [M,K], mean and rstd as lynx_layer_norm left them, weight as given there.
+ *   dR [M,K] or NULL: the gradient that reaches X beside the norm (the residual
+ *   branch's); dR may be dX itself.  dweight and dbias [K] out, each or NULL (not
+ *   wanted).  All bf16, rounded once; sums in fp32 in an order that only the shape
+ *   fixes (equal calls give equal bits).
+ *   workspace: device scratch of workspace_bytes >=
+ *   lynx_layer_norm_backward_workspace_bytes(M,K), needed with dweight or dbias only. */
+LYNX_API int lynx_layer_norm_backward(const void* dY, const void* X, const float* mean, const float* rstd,
+                                      const void* weight, const void* dR, int64_t M, int64_t K, void* dX,
+                                      void* dweight, void* dbias, void* workspace, size_t workspace_bytes,
+                                      void* stream);
 
 /* ---- errors and metadata conversion ----------------------------------- */
 
