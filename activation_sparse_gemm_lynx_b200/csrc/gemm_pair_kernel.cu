@@ -347,13 +347,42 @@ __device__ __forceinline__ bool compress_tile_stages(Smem& sm, uint32_t& g, int 
   return true;
 }
 
-// The residual's values for 32 columns of a row: four 16-byte pieces, N a multiple
-// of 8.  Plain loads: the residual may be Y itself, whose tiles this CTA writes
-// only after it has read them here.
-__device__ __forceinline__ void load_residual(uint4 (&v)[4], const __nv_bfloat16* row, int64_t n, int64_t N, bool there) {
+// 16 columns of this lane's row of the residual, and the same of Z.  The stages leave
+// next to no L1, so what is asked for twice comes from L2 twice, and the operands keep L2
+// at its rate: 32 bytes (a sector) go in one access where the rows lie on 32 bytes, else
+// in two of 16.  N is a multiple of 8.  The residual may be Y itself, whose tiles this CTA
+// writes only after it has read them here.
+__device__ __forceinline__ void load_residual(uint32_t (&v)[8], const __nv_bfloat16* at, int left, bool wide) {
+  if (wide) {
+    if (left > 0)
+      asm volatile("ld.global.L1::no_allocate.L2::256B.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                   : "l"(at)
+                   : "memory");
+  } else {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    v[i] = there && n + 8 * i < N ? *reinterpret_cast<const uint4*>(row + n + 8 * i) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < 2; ++i) {
+      if (left > 8 * i)
+        asm volatile("ld.global.L1::no_allocate.L2::256B.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v[4 * i]), "=r"(v[4 * i + 1]), "=r"(v[4 * i + 2]), "=r"(v[4 * i + 3])
+                     : "l"(at + 8 * i)
+                     : "memory");
+    }
+  }
+}
+
+__device__ __forceinline__ void store_z(__nv_bfloat16* at, const uint32_t (&v)[8], int left, bool wide) {
+  if (wide) {
+    if (left > 0)
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                   "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (left > 8 * i)
+        *reinterpret_cast<uint4*>(at + 8 * i) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  }
 }
 
 // EXT: Y = R + act(v), and v itself to Z where it is wanted.
@@ -673,20 +702,13 @@ lynx_gemm_pair_kernel(const __grid_constant__ GemmLaunch p) {
         if (p.fin_mode == 1) s = __ldcg(p.fin_scale + grow);
         else if (p.row_scale != nullptr) s = p.row_scale[grow];
       }
-      // The residual of this lane's row: the first 32 columns now, while the tile's MMAs
-      // run, each further 32 one step ahead of its use; all of it on its way to L2
-      const int64_t n_warp = n_base + ch * kHalf;
-      const bool add = EXT && p.residual != nullptr;
-      const __nv_bfloat16* res_row = nullptr;
-      uint4 res[2][4];
+      // The residual of this lane's row: the first 16 columns now, while the tile's MMAs
+      // run, each further 16 one step ahead of their use
+      const int left = EXT && row_ok ? static_cast<int>(p.N - n_base) - static_cast<int>(ch) * kHalf : 0;  // columns from the warp's first on
+      const int64_t at = EXT ? grow * p.N + n_base + ch * kHalf : 0;
+      uint32_t next[8];
       if constexpr (EXT) {
-        if (add) {
-          res_row = static_cast<const __nv_bfloat16*>(p.residual) + grow * p.N;
-          load_residual(res[0], res_row, n_warp, p.N, row_ok);
-#pragma unroll
-          for (int i = 1; i < kHalf / 32; ++i)
-            if (row_ok && n_warp + 32 * i < p.N) prefetch_l2(res_row + n_warp + 32 * i);
-        }
+        if (p.residual != nullptr) load_residual(next, static_cast<const __nv_bfloat16*>(p.residual) + at, left, p.wide);
       }
       bool ok = !sm.abort_flag;
       if (ok && !mbar_wait(&sm.acc_full, static_cast<uint32_t>(acc_count) & 1u)) {
@@ -715,13 +737,10 @@ lynx_gemm_pair_kernel(const __grid_constant__ GemmLaunch p) {
 #pragma unroll
       for (int c = 0; c < kHalf / 32; ++c) {
         const int col = static_cast<int>(ch) * kHalf + 32 * c;
-        if constexpr (EXT) {
-          if (add && c + 1 < kHalf / 32) load_residual(res[(c + 1) & 1], res_row, n_warp + 32 * (c + 1), p.N, row_ok);
-        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           // 16 columns of the warp's 32 rows: through one of its two buffers to memory
-          auto store = [&](const uint32_t (&pk)[8], const CUtensorMap* map) {
+          auto store = [&](const uint32_t (&pk)[8]) {
             uint8_t* buf = my_stage + 1024 * (piece++ & 1);
             if (lane == 0) bulk_wait_read_le1();  // the store that last used `buf` has read it
             __syncwarp();
@@ -732,12 +751,21 @@ lynx_gemm_pair_kernel(const __grid_constant__ GemmLaunch p) {
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-              tma_store_2d(map, buf, static_cast<int32_t>(n_base + col + 16 * h), store_row);
+              tma_store_2d(&p.tm_y, buf, static_cast<int32_t>(n_base + col + 16 * h), store_row);
               bulk_commit();
             }
           };
-          uint32_t pk[8];
+          uint32_t pk[8], res[8];
+          constexpr int kPieces = kHalf / 16;
+          const int done = 2 * c + h;  // pieces before this one
           if constexpr (EXT) {
+            if (p.residual != nullptr) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) res[i] = next[i];
+              if (done + 1 < kPieces)
+                load_residual(next, static_cast<const __nv_bfloat16*>(p.residual) + at + 16 * (done + 1),
+                              left - 16 * (done + 1), p.wide);
+            }
             if (p.z != nullptr) {
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
@@ -746,7 +774,7 @@ lynx_gemm_pair_kernel(const __grid_constant__ GemmLaunch p) {
                                                           __fmaf_rn(s, __uint_as_float(r[c][e + 1]), sm.bias_s[col + e + 1]));
                 pk[i] = *reinterpret_cast<uint32_t*>(&zv);
               }
-              store(pk, &p.tm_z);
+              store_z(static_cast<__nv_bfloat16*>(p.z) + at + 16 * done, pk, left - 16 * done, p.wide);
             }
           }
 #pragma unroll
@@ -756,17 +784,15 @@ lynx_gemm_pair_kernel(const __grid_constant__ GemmLaunch p) {
             float b =
                 apply_act<ACT>(__fmaf_rn(s, __uint_as_float(r[c][e + 1]), sm.bias_s[col + e + 1]));
             if constexpr (EXT) {
-              if (add) {
-                const uint4& v = res[c & 1][2 * h + i / 4];
-                const uint32_t w = i % 4 == 0 ? v.x : i % 4 == 1 ? v.y : i % 4 == 2 ? v.z : v.w;
-                a += __uint_as_float(w << 16);
-                b += __uint_as_float(w & 0xFFFF0000u);
+              if (p.residual != nullptr) {
+                a += __uint_as_float(res[i] << 16);
+                b += __uint_as_float(res[i] & 0xFFFF0000u);
               }
             }
             __nv_bfloat162 hv = __floats2bfloat162_rn(a, b);
             pk[i] = *reinterpret_cast<uint32_t*>(&hv);
           }
-          store(pk, &p.tm_y);
+          store(pk);
         }
       }
     }

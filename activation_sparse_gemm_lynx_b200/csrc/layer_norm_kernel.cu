@@ -19,7 +19,7 @@
 // rows read dY and X once more, by columns (column_pass_kernel.cu).
 #include <cuda_bf16.h>
 
-#include "lynx_ckpt8.cuh"
+#include "lynx_f32x2.cuh"
 #include "lynx_internal.h"
 #include "lynx_ptx.cuh"
 
@@ -27,45 +27,61 @@ namespace lynx {
 
 namespace {
 
-constexpr int kMaxThreads = 512;
+constexpr int kMaxThreads = 1024;  // forward
+constexpr int kMaxThreadsBackward = 512;
+constexpr int kMaxWarps = kMaxThreads / 32;
+constexpr int kMaxWarpsBackward = kMaxThreadsBackward / 32;
+constexpr int kMaxGroups = 8;  // rows of a block
 constexpr int kMaxStages = 4;
 constexpr uint32_t kRingMost = 200 * 1024;
 constexpr int64_t kFusedCols = 8192;
-constexpr int kBackwardBlocks = 296;  // two on every SM of a B200
+constexpr int kBackwardBlocks = 148;  // one on every SM of a B200
 
 constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// The sums of `a` and `b` over the tx threads of a row, in a fixed order.  `red` is
-// this call's own [2][kMaxThreads / 32] floats: two calls in a row take different ones,
-// and the barrier of the second says that all have read the first's.
-__device__ __forceinline__ float2 row_sums(float a, float b, float (*red)[kMaxThreads / 32], int group, int tx) {
+// The sums over the threads of a row, in an order that only their number fixes.
+// `mine` is this warp's entry of the row's own in shared memory, `all` the first of
+// them (those past its warps stay zero).  Two calls in a row take different ones, and the
+// barrier of the second says that all have read the first's.
+__device__ __forceinline__ float row_sum(float a, float* mine, const float* all, int warps, int barrier) {
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    a += __shfl_xor_sync(0xffffffffu, a, d);
-    b += __shfl_xor_sync(0xffffffffu, b, d);
+  for (int d = 16; d > 0; d >>= 1) a += __shfl_xor_sync(0xffffffffu, a, d);
+  if (warps == 1) return a;
+  *mine = a;  // every lane the same
+  named_bar_sync(barrier, 32 * warps);
+  a = 0.f;
+#pragma unroll 1  // unrolled behind conditions, every step would be issued
+  for (int w = 0; w < warps; w += 4) {
+    const float4 v = *reinterpret_cast<const float4*>(all + w);
+    a += (v.x + v.y) + (v.z + v.w);
   }
-  if (tx == 32) return make_float2(a, b);
-  const int warp = threadIdx.x >> 5, warps = tx >> 5, first = group * warps;
-  if ((threadIdx.x & 31u) == 0) {
-    red[0][warp] = a;
-    red[1][warp] = b;
-  }
-  named_bar_sync(1 + group, tx);
-  float2 s = make_float2(0.f, 0.f);
-  for (int w = first; w < first + warps; ++w) {
-    s.x += red[0][w];
-    s.y += red[1][w];
-  }
-  return s;
+  return a;
 }
 
-__device__ __forceinline__ void unpack8(const uint4& p, float (&v)[8]) {
-  v[0] = bf16_lo(p.x), v[1] = bf16_hi(p.x), v[2] = bf16_lo(p.y), v[3] = bf16_hi(p.y);
-  v[4] = bf16_lo(p.z), v[5] = bf16_hi(p.z), v[6] = bf16_lo(p.w), v[7] = bf16_hi(p.w);
+// Two sums at once: the first step leaves a lane with one of them
+__device__ __forceinline__ float2 row_sums(float a, float b, float2* mine, const float2* all, int warps, int barrier) {
+  const bool low = (threadIdx.x & 16u) == 0;
+  float v = (low ? a : b) + __shfl_xor_sync(0xffffffffu, low ? b : a, 16);
+#pragma unroll
+  for (int d = 8; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  if (warps == 1) return make_float2(__shfl_sync(0xffffffffu, v, 0), __shfl_sync(0xffffffffu, v, 16));
+  reinterpret_cast<float*>(mine)[low ? 0 : 1] = v;
+  named_bar_sync(barrier, 32 * warps);
+  f32x2 s = both(0.f);
+#pragma unroll 1
+  for (int w = 0; w < warps; w += 4) {
+    const float4 q = *reinterpret_cast<const float4*>(all + w), r = *reinterpret_cast<const float4*>(all + w + 2);
+    s = add2(s, add2(add2(pair_f32(q.x, q.y), pair_f32(q.z, q.w)), add2(pair_f32(r.x, r.y), pair_f32(r.z, r.w))));
+  }
+  return halves(s);
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
-  return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+__device__ __forceinline__ void widen8(const uint4& p, f32x2 (&v)[4]) {
+  v[0] = widen(p.x), v[1] = widen(p.y), v[2] = widen(p.z), v[3] = widen(p.w);
+}
+
+__device__ __forceinline__ uint4 narrow8(const f32x2 (&v)[4]) {
+  return make_uint4(narrow(v[0]), narrow(v[1]), narrow(v[2]), narrow(v[3]));
 }
 
 __device__ __forceinline__ uint4 ones() { return make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u); }
@@ -81,76 +97,74 @@ __device__ __forceinline__ void wait_ring(int stages) {
     cp_async_wait<0>();
 }
 
-template <int V>
-__global__ void __launch_bounds__(kMaxThreads) layer_norm_kernel(LayerNormLaunch p, int tx, int stages) {
-  extern __shared__ __align__(16) uint4 ring[];  // [stage][V][threads]
-  __shared__ float red[2][2][kMaxThreads / 32];
+// A warp owns 32 V neighbouring pieces of a row, a lane every 32nd of them, so that
+// its addresses are one register and constants.  FULL: there is no piece past the row's
+// end (K == 8 V tx); else each is behind a branch, about 60 of them a row and warp.
+template <int V, bool FULL>
+__global__ void __launch_bounds__(kMaxThreads) layer_norm_kernel(LayerNormLaunch p, int tx) {
+  extern __shared__ __align__(16) uint4 ring[];  // [V threads]
+  __shared__ __align__(16) float red[2][kMaxGroups][kMaxWarps];
   const int threads = static_cast<int>(blockDim.x), tid = static_cast<int>(threadIdx.x);
-  const int group = tid / tx, t = tid % tx, ty = threads / tx;
-  const int pieces = static_cast<int>(p.K / 8);
-  const int64_t step = static_cast<int64_t>(gridDim.x) * ty;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * ty + group;
-  const auto* x = static_cast<const uint4*>(p.x) + t;
-  auto* y = static_cast<uint4*>(p.y) + t;
+  const int group = tid / tx, t = tid - group * tx, ty = threads / tx, warps = tx / 32;
+  const int pieces = static_cast<int>(p.K / 8), first = (t >> 5) * (32 * V) + (t & 31);
+  auto on = [&](int v) { return FULL || first + 32 * v < pieces; };
+  const int M = static_cast<int>(p.M), step = static_cast<int>(gridDim.x) * ty;
+  int row = static_cast<int>(blockIdx.x) * ty + group;
+  for (int i = tid; i < 2 * kMaxGroups * kMaxWarps; i += threads) (&red[0][0][0])[i] = 0.f;
+  __syncthreads();
+  const uint4* const slot = ring + (tid >> 5) * (32 * V) + (tid & 31);
+  const uint4* w = static_cast<const uint4*>(p.w) + first;
+  const uint4* b = static_cast<const uint4*>(p.b) + first;
+  const float inv_k = 1.f / static_cast<float>(p.K);
   pdl_wait();
-  auto fill = [&](int64_t row, int stage) {
-    if (row < p.M) {
+  auto fetch = [&](int next) {
+    if (next < M) {
+      const uint4* x = static_cast<const uint4*>(p.x) + static_cast<int64_t>(next) * pieces + first;
 #pragma unroll
       for (int v = 0; v < V; ++v)
-        if (t + v * tx < pieces)
-          cp_async_16(smem_u32(ring + (stage * V + v) * threads + tid), x + row * pieces + v * tx, 16u);
+        if (on(v)) cp_async_16(smem_u32(slot) + 512 * v, x + 32 * v, 16u);
     }
     cp_async_commit();
   };
-  for (int s = 0; s < stages; ++s) fill(row0 + s * step, s);
-  // weight and bias stay in registers where they fit, else they come from L1 for each row
-  constexpr bool kKeep = V <= 2;
-  auto weight = [&](int v) { return p.w ? __ldg(static_cast<const uint4*>(p.w) + t + v * tx) : ones(); };
-  auto bias = [&](int v) { return p.b ? __ldg(static_cast<const uint4*>(p.b) + t + v * tx) : make_uint4(0, 0, 0, 0); };
-  uint4 w[kKeep ? V : 1], b[kKeep ? V : 1];
-  if (kKeep) {
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (t + v * tx < pieces) w[v] = weight(v), b[v] = bias(v);
-  }
-  const float inv_k = 1.f / static_cast<float>(p.K);
-  int stage = 0;
-  for (int64_t row = row0; row < p.M; row += step) {
-    wait_ring(stages);
-    uint4 in[V];
-    float s = 0.f;
+  fetch(row);
+  for (; row < M; row += step) {
+    cp_async_wait<0>();
+    f32x2 d[V][4];
+    f32x2 s2 = both(0.f);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      in[v] = make_uint4(0, 0, 0, 0);
-      if (t + v * tx < pieces) in[v] = ring[(stage * V + v) * threads + tid];
-      float f[8];
-      unpack8(in[v], f);
-      s += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
-    }
-    const float mean = row_sums(s, 0.f, red[0], group, tx).x * inv_k;
-    fill(row + stages * step, stage);  // its values are in registers
-    if (++stage == stages) stage = 0;
-    float q = 0.f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      if (t + v * tx < pieces) {
-        float f[8];
-        unpack8(in[v], f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q = fmaf(f[i] - mean, f[i] - mean, q);
+      if (on(v)) {
+        widen8(slot[32 * v], d[v]);
+        s2 = add2(s2, add2(add2(d[v][0], d[v][1]), add2(d[v][2], d[v][3])));
       }
     }
-    const float rstd = rsqrtf(fmaf(row_sums(q, 0.f, red[1], group, tx).x, inv_k, p.eps));
+    const float mean = row_sum(sum_of(s2), &red[0][group][t >> 5], red[0][group], warps, 1 + group) * inv_k;
+    fetch(row + step);  // this row's values are in registers
+    const f32x2 less = both(-mean);
+    f32x2 q2 = both(0.f);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      if (t + v * tx < pieces) {
-        float f[8], ww[8], bb[8];
-        unpack8(in[v], f);
-        unpack8(kKeep ? w[kKeep ? v : 0] : weight(v), ww);
-        unpack8(kKeep ? b[kKeep ? v : 0] : bias(v), bb);
+      if (on(v)) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = fmaf((f[i] - mean) * rstd, ww[i], bb[i]);
-        y[row * pieces + v * tx] = pack8(f);
+        for (int i = 0; i < 4; ++i) {
+          d[v][i] = add2(d[v][i], less);
+          q2 = fma2(d[v][i], d[v][i], q2);
+        }
+      }
+    }
+    const float rstd = rsqrtf(fmaf(row_sum(sum_of(q2), &red[1][group][t >> 5], red[1][group], warps, 1 + group), inv_k, p.eps));
+    const f32x2 scale = both(rstd);
+    uint4* y = static_cast<uint4*>(p.y) + static_cast<int64_t>(row) * pieces + first;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if (on(v)) {
+        // weight and bias from L1 for each row: in registers they would halve the rows an SM holds
+        f32x2 ww[4], bb[4];
+        widen8(p.w ? __ldg(w + 32 * v) : ones(), ww);
+        widen8(p.b ? __ldg(b + 32 * v) : make_uint4(0, 0, 0, 0), bb);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[v][i] = fma2(mul2(d[v][i], scale), ww[i], bb[i]);
+        y[32 * v] = narrow8(d[v]);
       }
     }
     if (t == 0 && p.mean != nullptr) {
@@ -161,109 +175,113 @@ __global__ void __launch_bounds__(kMaxThreads) layer_norm_kernel(LayerNormLaunch
 }
 
 // SUMS: the columns' sums of the block's rows go to part[block][2][K] (dw, then db).
-template <int V, bool SUMS>
-__global__ void __launch_bounds__(kMaxThreads) layer_norm_backward_kernel(LayerNormBackwardLaunch p, int tx, int stages) {
-  constexpr bool kKeep = V <= 2;  // a row's values in registers between the sums and the results
-  extern __shared__ __align__(16) uint4 ring[];  // [stage][dy, x, dr][V][threads]
-  __shared__ float red[2][2][kMaxThreads / 32];
+template <int V, bool SUMS, bool FULL>
+__global__ void __launch_bounds__(kMaxThreadsBackward, 1)
+layer_norm_backward_kernel(LayerNormBackwardLaunch p, int tx, int stages) {
+  constexpr bool kKeep = V <= 2;  // the row's values in registers between the sums and the results
+  extern __shared__ __align__(16) uint4 ring[];  // [stage][dy, x, dr][V threads]
+  __shared__ __align__(16) float2 red[2][kMaxGroups][kMaxWarpsBackward];
   const int threads = static_cast<int>(blockDim.x), tid = static_cast<int>(threadIdx.x);
-  const int group = tid / tx, t = tid % tx, ty = threads / tx;
-  const int pieces = static_cast<int>(p.K / 8);
-  const int64_t step = static_cast<int64_t>(gridDim.x) * ty;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * ty + group;
+  const int group = tid / tx, t = tid - group * tx, ty = threads / tx, warps = tx / 32;
+  const int pieces = static_cast<int>(p.K / 8), first = (t >> 5) * (32 * V) + (t & 31);
+  auto on = [&](int v) { return FULL || first + 32 * v < pieces; };
+  const int M = static_cast<int>(p.M), step = static_cast<int>(gridDim.x) * ty;
+  int row = static_cast<int>(blockIdx.x) * ty + group;
+  for (int i = tid; i < 2 * kMaxGroups * kMaxWarpsBackward; i += threads) (&red[0][0][0])[i] = make_float2(0.f, 0.f);
+  __syncthreads();
   const bool add = p.dr != nullptr;
-  const int streams = add ? 3 : 2;
-  const auto* dy = static_cast<const uint4*>(p.dy) + t;
-  const auto* x = static_cast<const uint4*>(p.x) + t;
-  const auto* dr = static_cast<const uint4*>(p.dr) + t;
-  auto* dx = static_cast<uint4*>(p.dx) + t;
+  const int stream = V * threads, stage_size = (add ? 3 : 2) * stream;  // in pieces
+  int ahead = row;  // what is copied next
+  const uint4* const slot = ring + (tid >> 5) * (32 * V) + (tid & 31);
   pdl_wait();
-  auto fill = [&](int64_t row, int stage) {
-    if (row < p.M) {
-      uint4* at = ring + stage * streams * V * threads + tid;
+  auto fill = [&](int stage) {
+    if (ahead < M) {
+      const uint32_t at = smem_u32(slot + stage * stage_size);
+      const int64_t next = static_cast<int64_t>(ahead) * pieces + first;
+      const uint4* dy = static_cast<const uint4*>(p.dy) + next;
+      const uint4* x = static_cast<const uint4*>(p.x) + next;
+      const uint4* dr = static_cast<const uint4*>(p.dr) + next;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        if (t + v * tx < pieces) {
-          const int64_t from = row * pieces + v * tx;
-          cp_async_16(smem_u32(at + v * threads), dy + from, 16u);
-          cp_async_16(smem_u32(at + (V + v) * threads), x + from, 16u);
-          if (add) cp_async_16(smem_u32(at + (2 * V + v) * threads), dr + from, 16u);
+        if (on(v)) {
+          cp_async_16(at + 512 * v, dy + 32 * v, 16u);
+          cp_async_16(at + stream * 16 + 512 * v, x + 32 * v, 16u);
+          if (add) cp_async_16(at + stream * 32 + 512 * v, dr + 32 * v, 16u);
         }
       }
     }
+    ahead += step;
     cp_async_commit();
   };
-  for (int s = 0; s < stages; ++s) fill(row0 + s * step, s);
-  uint4 w[V];
+  for (int s = 0; s < stages; ++s) fill(s);
+  f32x2 w[V][4];
 #pragma unroll
-  for (int v = 0; v < V; ++v)
-    w[v] = p.w && t + v * tx < pieces ? __ldg(static_cast<const uint4*>(p.w) + t + v * tx) : ones();
-  float sw[SUMS ? V : 1][8] = {}, sb[SUMS ? V : 1][8] = {};
+  for (int v = 0; v < V; ++v) widen8(p.w && on(v) ? __ldg(static_cast<const uint4*>(p.w) + first + 32 * v) : ones(), w[v]);
+  f32x2 sw[SUMS ? V : 1][4] = {}, sb[SUMS ? V : 1][4] = {};  // +0
   const float inv_k = 1.f / static_cast<float>(p.K);
   float mean = 0.f, rstd = 0.f;
-  if (row0 < p.M) mean = p.mean[row0], rstd = p.rstd[row0];
+  if (row < M) mean = p.mean[row], rstd = p.rstd[row];
   int stage = 0, turn = 0;
-  for (int64_t row = row0; row < p.M; row += step) {
-    const int64_t next = row + step;
-    float mean_next = 0.f, rstd_next = 0.f;
-    if (next < p.M) mean_next = p.mean[next], rstd_next = p.rstd[next];
+  for (; row < M; row += step) {
     wait_ring(stages);
-    const uint4* at = ring + stage * streams * V * threads + tid;
-    uint4 keep[kKeep ? V : 1][3];
-    float s1 = 0.f, s2 = 0.f;
+    const uint4* at = slot + stage * stage_size;
+    const f32x2 less = both(-mean), scale = both(rstd);
+    f32x2 g[kKeep ? V : 1][4], xh[kKeep ? V : 1][4];
+    uint4 r[kKeep ? V : 1];
+    f32x2 s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      if (t + v * tx < pieces) {
-        uint4(&k)[3] = keep[kKeep ? v : 0];
-        k[0] = at[v * threads];
-        k[1] = at[(V + v) * threads];
-        if (kKeep) k[2] = add ? at[(2 * V + v) * threads] : make_uint4(0, 0, 0, 0);
-        float f[8], h[8], ww[8];
-        unpack8(k[0], f);
-        unpack8(k[1], h);
-        unpack8(w[v], ww);
+      if (on(v)) {
+        f32x2 f[4];
+        auto& gv = g[kKeep ? v : 0];
+        auto& xv = xh[kKeep ? v : 0];
+        widen8(at[32 * v], f);
+        widen8(at[stream + 32 * v], xv);
+        if (kKeep) r[kKeep ? v : 0] = add ? at[2 * stream + 32 * v] : make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float xh = (h[i] - mean) * rstd, g = f[i] * ww[i];
-          s1 += g;
-          s2 = fmaf(g, xh, s2);
+        for (int i = 0; i < 4; ++i) {
+          xv[i] = mul2(add2(xv[i], less), scale);
+          gv[i] = mul2(f[i], w[v][i]);
+          s1 = add2(s1, gv[i]);
+          s2 = fma2(gv[i], xv[i], s2);
           if constexpr (SUMS) {
-            sw[v][i] = fmaf(f[i], xh, sw[v][i]);
-            sb[v][i] += f[i];
+            sw[v][i] = fma2(f[i], xv[i], sw[v][i]);
+            sb[v][i] = add2(f[i], sb[v][i]);
           }
         }
       }
     }
-    const float2 s = row_sums(s1, s2, red[turn], group, tx);
+    if (row + step < M) mean = p.mean[row + step], rstd = p.rstd[row + step];
+    const float2 s = row_sums(sum_of(s1), sum_of(s2), &red[turn][group][t >> 5], red[turn][group], warps, 1 + group);
     turn ^= 1;
-    if (kKeep) fill(row + stages * step, stage);  // its values are in registers
-    const float c1 = s.x * inv_k, c2 = s.y * inv_k;
+    if (kKeep) fill(stage);  // its values are in registers
+    const f32x2 c1 = both(-s.x * inv_k), c2 = both(-s.y * inv_k);
+    uint4* to = static_cast<uint4*>(p.dx) + static_cast<int64_t>(row) * pieces + first;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      if (t + v * tx < pieces) {
-        uint4(&k)[3] = keep[kKeep ? v : 0];
+      if (on(v)) {
+        auto& gv = g[kKeep ? v : 0];
+        auto& xv = xh[kKeep ? v : 0];
+        auto& rv = r[kKeep ? v : 0];
         if (!kKeep) {
-          k[0] = at[v * threads];
-          k[1] = at[(V + v) * threads];
-          k[2] = add ? at[(2 * V + v) * threads] : make_uint4(0, 0, 0, 0);
-        }
-        float f[8], h[8], ww[8], r[8];
-        unpack8(k[0], f);
-        unpack8(k[1], h);
-        unpack8(w[v], ww);
-        unpack8(k[2], r);
+          widen8(at[32 * v], gv);
+          widen8(at[stream + 32 * v], xv);
+          rv = add ? at[2 * stream + 32 * v] : make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float xh = (h[i] - mean) * rstd;
-          f[i] = fmaf(rstd, fmaf(-xh, c2, fmaf(f[i], ww[i], -c1)), r[i]);
+          for (int i = 0; i < 4; ++i) {
+            xv[i] = mul2(add2(xv[i], less), scale);
+            gv[i] = mul2(gv[i], w[v][i]);
+          }
         }
-        dx[row * pieces + v * tx] = pack8(f);
+        f32x2 out[4];
+        widen8(rv, out);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) out[i] = fma2(scale, fma2(xv[i], c2, add2(gv[i], c1)), out[i]);
+        to[32 * v] = narrow8(out);
       }
     }
-    if (!kKeep) fill(row + stages * step, stage);  // the results above have used its values
+    if (!kKeep) fill(stage);  // the results above have used its values
     if (++stage == stages) stage = 0;
-    mean = mean_next;
-    rstd = rstd_next;
   }
   if constexpr (SUMS) {
     float* out = p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.K;
@@ -273,53 +291,62 @@ __global__ void __launch_bounds__(kMaxThreads) layer_norm_backward_kernel(LayerN
       __syncthreads();
       out = reinterpret_cast<float*>(ring) + group * 2 * K;
     }
+    auto put = [](float* to, const f32x2(&s)[4]) {
+      const float2 a = halves(s[0]), b = halves(s[1]), c = halves(s[2]), d = halves(s[3]);
+      *reinterpret_cast<float4*>(to) = make_float4(a.x, a.y, b.x, b.y);
+      *reinterpret_cast<float4*>(to + 4) = make_float4(c.x, c.y, d.x, d.y);
+    };
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      if (t + v * tx < pieces) {
-        float* at = out + 8 * (t + v * tx);
-        *reinterpret_cast<float4*>(at) = make_float4(sw[v][0], sw[v][1], sw[v][2], sw[v][3]);
-        *reinterpret_cast<float4*>(at + 4) = make_float4(sw[v][4], sw[v][5], sw[v][6], sw[v][7]);
-        *reinterpret_cast<float4*>(at + K) = make_float4(sb[v][0], sb[v][1], sb[v][2], sb[v][3]);
-        *reinterpret_cast<float4*>(at + K + 4) = make_float4(sb[v][4], sb[v][5], sb[v][6], sb[v][7]);
+      if (on(v)) {
+        put(out + 8 * (first + 32 * v), sw[v]);
+        put(out + K + 8 * (first + 32 * v), sb[v]);
       }
     }
     if (ty > 1) {
       __syncthreads();
       const auto* sums = reinterpret_cast<const float4*>(ring);
-      auto* to = reinterpret_cast<float4*>(p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.K);
+      auto* sum = reinterpret_cast<float4*>(p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.K);
       for (int i = tid; i < K / 2; i += threads) {
         float4 a = sums[i];
-        for (int g = 1; g < ty; ++g) {
-          const float4 c = sums[g * (K / 2) + i];
+        for (int q = 1; q < ty; ++q) {
+          const float4 c = sums[q * (K / 2) + i];
           a.x += c.x, a.y += c.y, a.z += c.z, a.w += c.w;
         }
-        to[i] = a;
+        sum[i] = a;
       }
     }
   }
 }
 
-// Threads of a row, rows of a block.  Two pieces a thread (16 values) make the
-// shuffles of the sums cheap beside the values; narrow rows share a block of 256.
+// Pieces of a thread, threads of a row, rows of a block
 struct RowShape {
   int v, tx, ty;
 };
 
-RowShape row_shape(int64_t K) {
-  const int64_t pieces = K / 8;
+RowShape row_shape(int64_t K, int v, int block) {
   RowShape s;
-  s.v = pieces <= 128 ? 1 : 2;
-  while (ceil_div(pieces, s.v) > kMaxThreads) s.v *= 2;
-  s.tx = static_cast<int>(ceil_div(ceil_div(pieces, s.v), 32) * 32);
-  s.ty = s.tx >= 256 ? 1 : 256 / s.tx;
+  s.v = v;
+  s.tx = static_cast<int>(ceil_div(K / 8, 32 * v) * 32);
+  s.ty = s.tx >= block ? 1 : block / s.tx;
+  if (s.ty > kMaxGroups) s.ty = kMaxGroups;
   return s;
 }
 
-// Stages and shared memory of a ring of `streams` rows
-int ring_stages(const RowShape& s, int streams) {
-  const int64_t row = static_cast<int64_t>(streams) * s.v * s.tx * s.ty * 16;
-  const int64_t fit = kRingMost / row;
-  return static_cast<int>(fit < kMaxStages ? fit : kMaxStages);
+// Four pieces a thread (32 values) make the two sums, about 30 instructions a warp each,
+// cheap beside the values: 4608 x 4096 takes 13.8 us with four, 16.2 with two, 26.1 with one.
+RowShape forward_shape(int64_t K) {
+  const int64_t pieces = K / 8;
+  return row_shape(K, pieces <= 32 ? 1 : pieces <= 64 ? 2 : 4, 256);
+}
+
+// Two pieces a thread leave room for the sums of their columns; 512 threads of 128
+// registers are what an SM holds, so each gets one block, whose rows' sums meet in it
+// (4608 x 4096: 30.1 us; 31.3 with two blocks of 256, 35 with one piece and two rows at a time).
+RowShape backward_shape(int64_t K) {
+  int v = 2;
+  while (K / 8 > v * kMaxThreadsBackward) v *= 2;
+  return row_shape(K, v, 512);
 }
 
 template <typename Kernel>
@@ -329,33 +356,44 @@ cudaError_t allow_ring(Kernel* kernel, std::once_flag (&once)[64], cudaError_t (
   });
 }
 
-template <int V>
+template <int V, bool FULL>
 cudaError_t launch_forward(const LayerNormLaunch& p, const RowShape& s, int sms, cudaStream_t stream) {
   static std::once_flag once[64];
   static cudaError_t configured[64];
-  cudaError_t e = allow_ring(layer_norm_kernel<V>, once, configured);
+  cudaError_t e = allow_ring(layer_norm_kernel<V, FULL>, once, configured);
   if (e != cudaSuccess) return e;
-  const int threads = s.tx * s.ty, stages = ring_stages(s, 1);
-  const size_t smem = static_cast<size_t>(stages) * V * threads * 16;
-  const int64_t want = ceil_div(p.M, s.ty), most = static_cast<int64_t>(sms) * (1024 / threads);
-  return launch_after_previous(layer_norm_kernel<V>, dim3(static_cast<unsigned>(want < most ? want : most)), dim3(threads),
-                               smem, stream, p, s.tx, stages);
+  const int threads = s.tx * s.ty;
+  const int64_t want = ceil_div(p.M, s.ty), most = static_cast<int64_t>(sms) * (kMaxThreads / threads);
+  return launch_after_previous(layer_norm_kernel<V, FULL>, dim3(static_cast<unsigned>(want < most ? want : most)),
+                               dim3(threads), static_cast<size_t>(V) * threads * 16, stream, p, s.tx);
 }
 
-template <int V, bool SUMS>
+template <int V, bool SUMS, bool FULL>
 cudaError_t launch_backward(const LayerNormBackwardLaunch& p, const RowShape& s, int blocks, cudaStream_t stream) {
   static std::once_flag once[64];
   static cudaError_t configured[64];
-  cudaError_t e = allow_ring(layer_norm_backward_kernel<V, SUMS>, once, configured);
+  cudaError_t e = allow_ring(layer_norm_backward_kernel<V, SUMS, FULL>, once, configured);
   if (e != cudaSuccess) return e;
-  const int threads = s.tx * s.ty, streams = p.dr != nullptr ? 3 : 2, stages = ring_stages(s, streams);
-  size_t smem = static_cast<size_t>(stages) * streams * V * threads * 16;
+  const int threads = s.tx * s.ty, stage = (p.dr != nullptr ? 3 : 2) * V * threads * 16;
+  const int fit = static_cast<int>(kRingMost) / stage, stages = fit < kMaxStages ? fit : kMaxStages;
+  size_t smem = static_cast<size_t>(stages) * stage;
   if (SUMS && s.ty > 1) {
     const size_t sums = static_cast<size_t>(s.ty) * 2 * static_cast<size_t>(p.K) * 4;
     if (sums > smem) smem = sums;
   }
-  return launch_after_previous(layer_norm_backward_kernel<V, SUMS>, dim3(static_cast<unsigned>(blocks)), dim3(threads), smem,
-                               stream, p, s.tx, stages);
+  return launch_after_previous(layer_norm_backward_kernel<V, SUMS, FULL>, dim3(static_cast<unsigned>(blocks)), dim3(threads),
+                               smem, stream, p, s.tx, stages);
+}
+
+template <int V>
+cudaError_t launch_forward_as(const LayerNormLaunch& p, const RowShape& s, int sms, cudaStream_t stream) {
+  return p.K == 8 * V * s.tx ? launch_forward<V, true>(p, s, sms, stream) : launch_forward<V, false>(p, s, sms, stream);
+}
+
+template <int V, bool SUMS>
+cudaError_t launch_backward_as(const LayerNormBackwardLaunch& p, const RowShape& s, int blocks, cudaStream_t stream) {
+  return p.K == 8 * V * s.tx ? launch_backward<V, SUMS, true>(p, s, blocks, stream)
+                             : launch_backward<V, SUMS, false>(p, s, blocks, stream);
 }
 
 int backward_blocks(int64_t M, const RowShape& s) {
@@ -366,36 +404,31 @@ int backward_blocks(int64_t M, const RowShape& s) {
 }  // namespace
 
 cudaError_t launch_layer_norm(const LayerNormLaunch& p, int sms, cudaStream_t stream) {
-  const RowShape s = row_shape(p.K);
+  const RowShape s = forward_shape(p.K);
   switch (s.v) {
-    case 1: return launch_forward<1>(p, s, sms, stream);
-    case 2: return launch_forward<2>(p, s, sms, stream);
-    case 4: return launch_forward<4>(p, s, sms, stream);
-    default: return launch_forward<8>(p, s, sms, stream);
+    case 1: return launch_forward_as<1>(p, s, sms, stream);
+    case 2: return launch_forward_as<2>(p, s, sms, stream);
+    default: return launch_forward_as<4>(p, s, sms, stream);
   }
 }
 
 size_t layer_norm_backward_workspace(int64_t M, int64_t K) {
   if (K > kFusedCols) return column_pass_workspace(M, K, 2);
-  return static_cast<size_t>(backward_blocks(M, row_shape(K))) * 2 * static_cast<size_t>(K) * 4;
+  return static_cast<size_t>(backward_blocks(M, backward_shape(K))) * 2 * static_cast<size_t>(K) * 4;
 }
 
 cudaError_t launch_layer_norm_backward(const LayerNormBackwardLaunch& p, cudaStream_t stream) {
-  const RowShape s = row_shape(p.K);
+  const RowShape s = backward_shape(p.K);
   const int blocks = backward_blocks(p.M, s);
-  if ((p.dw != nullptr || p.db != nullptr) && p.K <= kFusedCols) {
-    cudaError_t e = s.v == 1 ? launch_backward<1, true>(p, s, blocks, stream) : launch_backward<2, true>(p, s, blocks, stream);
-    if (e != cudaSuccess) return e;
-    return launch_column_sums(p.part, blocks, p.K, p.dw, p.db, stream);
+  const bool sums = p.dw != nullptr || p.db != nullptr;
+  if (sums && p.K <= kFusedCols) {
+    const cudaError_t e = launch_backward_as<2, true>(p, s, blocks, stream);
+    return e != cudaSuccess ? e : launch_column_sums(p.part, blocks, p.K, p.dw, p.db, stream);
   }
-  cudaError_t e;
-  switch (s.v) {
-    case 1: e = launch_backward<1, false>(p, s, blocks, stream); break;
-    case 2: e = launch_backward<2, false>(p, s, blocks, stream); break;
-    case 4: e = launch_backward<4, false>(p, s, blocks, stream); break;
-    default: e = launch_backward<8, false>(p, s, blocks, stream); break;
-  }
-  if (e != cudaSuccess || (p.dw == nullptr && p.db == nullptr)) return e;
+  const cudaError_t e = s.v == 2   ? launch_backward_as<2, false>(p, s, blocks, stream)
+                        : s.v == 4 ? launch_backward_as<4, false>(p, s, blocks, stream)
+                                   : launch_backward_as<8, false>(p, s, blocks, stream);
+  if (e != cudaSuccess || !sums) return e;
   ColumnPassLaunch c = {};
   c.dy = p.dy;
   c.z = p.x;

@@ -327,8 +327,6 @@ lynx_status run_gemm(DeviceState* ds, const void* a_src, bool sparse, const void
   }
   if (pair && !encode_bf16_2d(&p.tm_y, Y, N, M, N * 2, 16, 32, CU_TENSOR_MAP_SWIZZLE_32B))
     return LYNX_ERR_CUDA;
-  if (pair && Z != nullptr && !encode_bf16_2d(&p.tm_z, Z, N, M, N * 2, 16, 32, CU_TENSOR_MAP_SWIZZLE_32B))
-    return LYNX_ERR_CUDA;
   p.meta = static_cast<const uint8_t*>(meta);
   p.row_scale = row_scale;
   p.bias = bias;
@@ -336,6 +334,7 @@ lynx_status run_gemm(DeviceState* ds, const void* a_src, bool sparse, const void
   p.residual = R;
   p.z = Z;
   p.ext = (R != nullptr || Z != nullptr) ? 1 : 0;
+  p.wide = N % 16 == 0 && ((reinterpret_cast<uintptr_t>(R) | reinterpret_cast<uintptr_t>(Z)) & 31u) == 0 ? 1 : 0;
   p.M = M;
   p.N = N;
   p.K = K;

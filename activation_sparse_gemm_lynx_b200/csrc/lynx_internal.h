@@ -93,7 +93,6 @@ struct GemmLaunch {
   CUtensorMap tm_lb;    // B [N,r] box 32 x BN, SW64 (lora)
   CUtensorMap tm_e;     // metadata as uint8 [blocks*8, 256], box 256 x 8 (pair kernel)
   CUtensorMap tm_y;     // Y [M,N] bf16, box 16 x 32, 32B swizzle (pair kernel stores)
-  CUtensorMap tm_z;     // Z, the same (pair kernel, ext with z)
   const uint8_t* meta;  // hardware metadata blocks (sparse)
   const void* bias;     // [N] bf16 or null
   const float* row_scale;  // [M] fp32 multiplier of each accumulator row, or null
@@ -101,6 +100,7 @@ struct GemmLaunch {
   const void* residual;  // [M,N] bf16 added to the activation's value, or null (ext)
   void* z;              // [M,N] bf16: the value before the activation, or null (ext)
   int ext;              // residual or z is there (not with `fused`)
+  int wide;             // their rows lie on 32 bytes
   int64_t M, N, K;
   int r;                // LoRA rank (lora)
   int sparse;
