@@ -105,7 +105,7 @@ def build_binding() -> str:
     cmd += ["-isystem", os.path.join(home, "include"),
             "-isystem", os.path.join(home, "include", "torch", "csrc", "api", "include"),
             "-o", tmp, BINDING_SOURCE, "-L", OUT_DIR, "-llynx", "-Wl,-rpath,$ORIGIN",
-            "-L", os.path.join(home, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+            "-L", os.path.join(home, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python"]
     subprocess.run(cmd, check=True)
     os.replace(tmp, path)
     return path

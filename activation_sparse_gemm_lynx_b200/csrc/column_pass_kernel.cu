@@ -15,7 +15,7 @@
 // (z + 0.044715 z^3), the derivative of z sig(a).
 #include <cuda_bf16.h>
 
-#include "lynx_ckpt8.cuh"
+#include "lynx_f32x2.cuh"
 #include "lynx_internal.h"
 #include "lynx_ptx.cuh"
 
@@ -28,6 +28,7 @@ enum ColumnMode : int { kColSum, kColGelu, kColNorm };
 constexpr int kThreads = 256;
 constexpr int kUnroll = 4;  // rows of a thread in flight
 constexpr int kSumThreads = 256;
+constexpr int kSlots = 148 * 3;  // blocks a B200 holds
 
 constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -37,31 +38,42 @@ struct ColumnPlan {
   int64_t rows;    // of a chunk
 };
 
-// Strips of 256 columns, or as narrow as the matrix; rows in ranges of equal length, as many as
-// fill the card with a few blocks an SM, a range no shorter than 4 turns of its threads.
+// Strips of 256 columns, or as narrow as the matrix; rows in ranges of equal length, so many
+// that strips x ranges come out just below a whole number of times what the card holds (up to
+// four; 4608 x 12288 in one round of 432 of 444 blocks), a range no shorter than one turn of
+// its threads.
 ColumnPlan column_plan(int64_t M, int64_t N) {
   ColumnPlan c;
   c.tx = 32;
   while (c.tx > 8 && 8 * (c.tx / 2) >= N) c.tx /= 2;
   c.strips = static_cast<int>(ceil_div(N, 8 * c.tx));
-  const int64_t turn = kThreads / c.tx * kUnroll;
-  int64_t chunks = ceil_div(148 * 8, c.strips);
-  const int64_t most = ceil_div(M, turn);
+  int64_t chunks = 1;
+  double best = 0;
+  for (int rounds = 1; rounds <= 4; ++rounds) {
+    const int64_t slots = static_cast<int64_t>(rounds) * kSlots, n = slots / c.strips;
+    const double full = static_cast<double>(n * c.strips) / static_cast<double>(slots) - 0.02 * rounds;
+    if (n > 0 && full > best) best = full, chunks = n;
+  }
+  const int64_t turn = kThreads / c.tx * kUnroll, most = ceil_div(M, turn);
   if (chunks > most) chunks = most;
   c.rows = ceil_div(ceil_div(M, chunks), kThreads / c.tx) * (kThreads / c.tx);
   c.chunks = static_cast<int>(ceil_div(M, c.rows));
   return c;
 }
 
-// d gelu / dz.  Beyond |z| = 16 it is 0 or 1 in fp32: cut off there, z^2 stays finite.
-__device__ __forceinline__ float gelu_tanh_slope(float z) {
-  const float q = z * z;
-  const float x = z * __fmaf_rn(q, 0.044715f, 1.0f) * -2.3022081981f;  // -a log2 e
-  float e, sig;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(sig) : "f"(1.0f + e));
-  const float slope = __fmaf_rn(q, 0.2140644488f, 1.5957691216f);  // a'
-  return __fmaf_rn(z * slope, __fmaf_rn(-sig, sig, sig), sig);
+// d gelu / dz of a pair.  Beyond |z| = 16 it is 0 or 1 in fp32: cut off there, z^2 stays finite.
+__device__ __forceinline__ f32x2 gelu_tanh_slope(f32x2 z) {
+  const f32x2 one = both(1.f), q = mul2(z, z);
+  const float2 x = halves(mul2(z, fma2(q, both(-2.3022081981f * 0.044715f), both(-2.3022081981f))));  // -a log2 e
+  float2 e, sig;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(x.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(x.y));
+  const float2 d = halves(add2(pair_f32(e.x, e.y), one));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(sig.x) : "f"(d.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(sig.y) : "f"(d.y));
+  const f32x2 s = pair_f32(sig.x, sig.y);
+  const f32x2 u = mul2(z, fma2(q, both(0.2140644488f), both(1.5957691216f)));  // z a'
+  return fma2(u, mul2(s, fma2(s, both(-1.f), one)), s);
 }
 
 __device__ __forceinline__ uint32_t clamp16(uint32_t pair) {
@@ -71,7 +83,7 @@ __device__ __forceinline__ uint32_t clamp16(uint32_t pair) {
 }
 
 template <int MODE>
-__global__ void __launch_bounds__(kThreads) column_pass_kernel(ColumnPassLaunch p, int tx, int64_t rows) {
+__global__ void __launch_bounds__(kThreads, 3) column_pass_kernel(ColumnPassLaunch p, int tx, int64_t rows) {
   constexpr int kSums = MODE == kColNorm ? 2 : 1;
   __shared__ float red[kSums][kThreads][9];  // 9: rows of 8 would share banks
   const int t = static_cast<int>(threadIdx.x) % tx, ry = static_cast<int>(threadIdx.x) / tx, ways = kThreads / tx;
@@ -83,7 +95,7 @@ __global__ void __launch_bounds__(kThreads) column_pass_kernel(ColumnPassLaunch 
   const auto* dy = static_cast<const uint4*>(p.dy) + piece;
   const auto* z = static_cast<const uint4*>(p.z) + piece;
   auto* dz = static_cast<uint4*>(p.dz) + piece;
-  float s0[8] = {}, s1[8] = {};
+  f32x2 s0[4] = {}, s1[4] = {};  // +0
   pdl_wait();
   if (on) {
     for (int64_t row = row0 + ry; row < end; row += kUnroll * ways) {
@@ -103,40 +115,36 @@ __global__ void __launch_bounds__(kThreads) column_pass_kernel(ColumnPassLaunch 
         const int64_t r = row + u * ways;
         if (r < end) {
           const uint32_t aw[4] = {a[u].x, a[u].y, a[u].z, a[u].w};
-          float f[8];
+          const uint32_t bw[4] = {b[u].x, b[u].y, b[u].z, b[u].w};
+          uint32_t out[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) f[2 * i] = bf16_lo(aw[i]), f[2 * i + 1] = bf16_hi(aw[i]);
-          if constexpr (MODE == kColGelu) {
-            const uint32_t bw[4] = {clamp16(b[u].x), clamp16(b[u].y), clamp16(b[u].z), clamp16(b[u].w)};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              f[2 * i] *= gelu_tanh_slope(bf16_lo(bw[i]));
-              f[2 * i + 1] *= gelu_tanh_slope(bf16_hi(bw[i]));
+          for (int i = 0; i < 4; ++i) {
+            f32x2 f = widen(aw[i]);
+            if constexpr (MODE == kColGelu) {
+              f = mul2(f, gelu_tanh_slope(widen(clamp16(bw[i]))));
+              out[i] = narrow(f);
             }
-            dz[r * pieces] = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
-                                        pack_bf16(f[6], f[7]));
-          }
-          if constexpr (MODE == kColNorm) {
-            const uint32_t bw[4] = {b[u].x, b[u].y, b[u].z, b[u].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              s1[2 * i] += f[2 * i];
-              s1[2 * i + 1] += f[2 * i + 1];
-              f[2 * i] *= (bf16_lo(bw[i]) - mean[u]) * rstd[u];
-              f[2 * i + 1] *= (bf16_hi(bw[i]) - mean[u]) * rstd[u];
+            if constexpr (MODE == kColNorm) {
+              s1[i] = add2(s1[i], f);
+              f = mul2(f, mul2(add2(widen(bw[i]), both(-mean[u])), both(rstd[u])));
             }
+            s0[i] = add2(s0[i], f);
           }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) s0[i] += f[i];
+          if constexpr (MODE == kColGelu) dz[r * pieces] = make_uint4(out[0], out[1], out[2], out[3]);
         }
       }
     }
   }
   if (p.part == nullptr) return;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    red[0][threadIdx.x][i] = s0[i];
-    if constexpr (kSums == 2) red[1][threadIdx.x][i] = s1[i];
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = halves(s0[i]), w = halves(s1[i]);
+    red[0][threadIdx.x][2 * i] = v.x;
+    red[0][threadIdx.x][2 * i + 1] = v.y;
+    if constexpr (kSums == 2) {
+      red[1][threadIdx.x][2 * i] = w.x;
+      red[1][threadIdx.x][2 * i + 1] = w.y;
+    }
   }
   __syncthreads();
   float* out = p.part + static_cast<int64_t>(blockIdx.y) * kSums * p.N;

@@ -6,8 +6,9 @@
 // Each function takes its arguments by position.  It returns its tensors, or a
 // lynx_status that is not LYNX_OK as an int; a tensor that does not fit raises.
 // The same checks through Python attributes took 8 us a call of the 12.
-#include <ATen/Functions.h>
 #include <ATen/core/Tensor.h>
+#include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -85,20 +86,21 @@ class Call {
       made = tensor(i, name);
       return check(made, name, type, shape);
     }
-    made = at::empty(shape, at::TensorOptions().dtype(type).device(at::kCUDA, static_cast<c10::DeviceIndex>(here_)));
+    made = empty(shape, type);
     return made.data_ptr();
   }
 
-  // (address, bytes) of the caller's workspace, or of one kept in `made`
-  std::pair<void*, size_t> workspace(int i, size_t need, at::Tensor& made) const {
+  // (address, bytes) of the caller's workspace, or of one kept in `made`: memory of the
+  // stream's pool without a tensor around it
+  std::pair<void*, size_t> workspace(int i, size_t need, c10::DataPtr& made) const {
     if (given(i)) {
-      made = tensor(i, "workspace");
-      void* p = check(made, "workspace", at::kByte, {made.numel()});
-      return {p, static_cast<size_t>(made.numel())};
+      const at::Tensor& t = tensor(i, "workspace");
+      void* p = check(t, "workspace", at::kByte, {t.numel()});
+      return {p, static_cast<size_t>(t.numel())};
     }
     if (need == 0) return {nullptr, 0};
-    void* p = out(i, "workspace", at::kByte, {static_cast<int64_t>(need)}, made);
-    return {p, need};
+    made = c10::cuda::CUDACachingAllocator::get()->allocate(need);
+    return {made.get(), need};
   }
 
   int integer(int i) const {
@@ -139,6 +141,11 @@ class Call {
       refuse(PyExc_TypeError, "stream must be a torch.cuda.Stream");
     }
     return r;
+  }
+
+  // at::empty without the dispatcher, which takes as long as the allocation
+  at::Tensor empty(at::IntArrayRef shape, at::ScalarType type) const {
+    return at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(here_)), std::nullopt);
   }
 
   void* check(const at::Tensor& t, const char* name, at::ScalarType type, at::IntArrayRef shape) const {
@@ -259,7 +266,8 @@ PyObject* linear_few(PyObject* const* args, Py_ssize_t n) {
   const W4 g(c, 1, 2);
   const auto [M, k] = c.matrix(0, "X");
   if (k != g.K) refuse(PyExc_ValueError, "X must be [M,K] with K = 2 * Wq.shape[1]");
-  at::Tensor Y, ws;
+  at::Tensor Y;
+  c10::DataPtr ws;
   const void* x = c.in(0, "X", at::kBFloat16, {M, g.K});
   const void* q = c.in(1, "Wq", at::kByte, {g.N, g.K / 2});
   const void* s = c.in(2, "scales", at::kBFloat16, {g.groups, g.N});
@@ -293,7 +301,8 @@ PyObject* linear_residual(PyObject* const* args, Py_ssize_t n) {
   const Call c(args, n, 13, "X");
   const auto [M, K] = c.matrix(0, "X");
   const int64_t N = c.matrix(1, "W").first;
-  at::Tensor Y, Z, ws;
+  at::Tensor Y, Z;
+  c10::DataPtr ws;
   const void* x = c.in(0, "X", at::kBFloat16, {M, K});
   const void* w = c.in(1, "W", at::kBFloat16, {N, K});
   const void* bias = c.optional_in(2, "bias", at::kBFloat16, {N});
@@ -320,7 +329,8 @@ PyObject* act_backward(PyObject* const* args, Py_ssize_t n) {
   const Call c(args, n, 8, "dY");
   const auto [M, N] = c.matrix(0, "dY");
   const int act = c.integer(2);
-  at::Tensor dZ, dbias, ws;
+  at::Tensor dZ, dbias;
+  c10::DataPtr ws;
   const void* dy = c.in(0, "dY", at::kBFloat16, {M, N});
   const void* z = c.optional_in(1, "Z", at::kBFloat16, {M, N});
   const bool none = act == LYNX_ACT_NONE;
@@ -361,7 +371,8 @@ PyObject* layer_norm(PyObject* const* args, Py_ssize_t n) {
 PyObject* layer_norm_backward(PyObject* const* args, Py_ssize_t n) {
   const Call c(args, n, 13, "dY");
   const auto [M, K] = c.matrix(0, "dY");
-  at::Tensor dX, dw, db, ws;
+  at::Tensor dX, dw, db;
+  c10::DataPtr ws;
   const void* dy = c.in(0, "dY", at::kBFloat16, {M, K});
   const void* x = c.in(1, "X", at::kBFloat16, {M, K});
   const void* mean = c.in(2, "mean", at::kFloat, {M});
@@ -411,7 +422,8 @@ PyObject* lora_backward(PyObject* const* args, Py_ssize_t n) {
   const auto [m, N] = c.matrix(0, "dY");
   if (m != k.M) refuse(PyExc_ValueError, "dY must be [M,N] with the checkpoint's M");
   const int64_t r = c.matrix(3, "A").first;
-  at::Tensor dA, dB, dT, ws;
+  at::Tensor dA, dB, dT;
+  c10::DataPtr ws;
   const void* dy = c.in(0, "dY", at::kBFloat16, {k.M, N});
   const void* q = c.in(1, "q", k.type, {k.M, k.K});
   const void* e = c.in(2, "e", at::kByte, {k.M, k.K / 32});
@@ -430,7 +442,8 @@ PyObject* lora_backward(PyObject* const* args, Py_ssize_t n) {
 PyObject* sparsify_backward(PyObject* const* args, Py_ssize_t n) {
   const Call c(args, n, 9, "G");
   const Ckpt k(c, 1);
-  at::Tensor dX, ws;
+  at::Tensor dX;
+  c10::DataPtr ws;
   const void* g = c.in(0, "G", at::kBFloat16, {k.M, k.K});
   const void* q = c.in(1, "q", k.type, {k.M, k.K});
   const void* e = c.in(2, "e", at::kByte, {k.M, k.K / 32});
