@@ -22,12 +22,13 @@
 //               tcgen05.commit to release stages / publish the accumulator.
 //   warps 2-9   epilogue: tcgen05.ld 32x32b -> s * acc + bias -> bf16 -> global
 //               (two warps per TMEM lane quarter, half of the columns each).
-// Accumulators: 1 TMEM buffer for BN = 256, 2 (double buffered) for BN = 128.
+// Accumulators: 1 TMEM buffer for BN = 256, 2 (double buffered) below.
 #include <cuda_bf16.h>
 
 #include "lynx_act.cuh"
 #include "lynx_internal.h"
 #include "lynx_ptx.cuh"
+#include "lynx_rows.cuh"
 
 namespace lynx {
 
@@ -40,10 +41,15 @@ constexpr int kEslots = 4;
 
 template <int BN, bool SPARSE>
 struct Cfg {
+  // K-steps of 64 a stage.  A wait and a commit take the MMA warp about as long as the
+  // MMAs of four steps; at 256 columns two steps would leave two stages.
+  static constexpr int kSub = BN == 256 ? 1 : 2;
   static constexpr uint32_t kABytes = SPARSE ? 128u * 64u : 128u * 128u;  // one k-step of A
   static constexpr uint32_t kBBytes = static_cast<uint32_t>(BN) * 128u;   // BN rows x 64 dense K
   static constexpr uint32_t kEBytes = SPARSE ? 2048u : 0u;
-  static constexpr uint32_t kStageBytes = ((kABytes + kBBytes + kEBytes + 1023u) / 1024u) * 1024u;
+  static constexpr uint32_t kBOff = kSub * kABytes;                       // the steps' A, then their B, then metadata
+  static constexpr uint32_t kEOff = kSub * (kABytes + kBBytes);
+  static constexpr uint32_t kStageBytes = ((kEOff + kEBytes + 1023u) / 1024u) * 1024u;
   static constexpr int kStages = static_cast<int>((212u * 1024u) / kStageBytes);
   static constexpr int kAcc = BN > 128 ? 1 : 2;
   static constexpr uint32_t kEcol0 = static_cast<uint32_t>(kAcc * BN);
@@ -66,6 +72,9 @@ struct __align__(1024) GemmSmem {
   uint32_t tmem_base;
   volatile uint32_t abort_flag;
 };
+
+__device__ __forceinline__ void tmem_ld_chunk(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld_32x32b_x32(taddr, r); }
+__device__ __forceinline__ void tmem_ld_chunk(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld_32x32b_x16(taddr, r); }
 
 constexpr uint32_t kBarEpilogue = 2;  // named barrier of the 8 epilogue warps
 constexpr uint32_t kEpiThreads = 256;
@@ -96,7 +105,8 @@ lynx_gemm_kernel(const __grid_constant__ GemmLaunch p) {
   const int ntm = static_cast<int>((p.M + 127) / 128);
   const int ntn = static_cast<int>((p.N + BN - 1) / BN);
   const int ntiles = ntm * ntn;
-  const int nk = static_cast<int>(p.K / 64);  // 64 dense K per stage
+  const int nk = static_cast<int>(p.K / 64);  // steps of 64 dense K
+  const int nks = (nk + C::kSub - 1) / C::kSub;  // and their stages
   const int kblocks = static_cast<int>((p.K + 127) / 128);
   const bool lora = p.lora != 0;
   const int lsteps = lora ? (p.r + 31) / 32 : 0;  // LoRA-up stages of K = 32 (zero-filled past r)
@@ -125,144 +135,158 @@ lynx_gemm_kernel(const __grid_constant__ GemmLaunch p) {
   // its outputs are read only from here on
   pdl_wait();
 
+  // a bounded wait of a whole warp: every lane waits, and all take the same decision
+  auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t code) {
+    const bool late = sm.abort_flag || !mbar_wait(bar, parity);
+    if (!__any_sync(0xffffffffu, late)) return true;
+    if (lane == 0 && !sm.abort_flag) {
+      record_error(p.status, code);
+      sm.abort_flag = 1u;
+    }
+    return false;
+  };
+
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
+    // (the whole warp, one elected lane issuing: see the MMA issuer)
+    if (elect_one()) {
       tma_prefetch_desc(&p.tm_a);
       tma_prefetch_desc(&p.tm_b);
       if (lora) {
         tma_prefetch_desc(&p.tm_t);
         tma_prefetch_desc(&p.tm_lb);
       }
-      uint32_t g = 0;
-      bool ok = !p.stall_test;
-      for (int tile = blockIdx.x; ok && tile < ntiles; tile += gridDim.x) {
-        int mb, nb;
-        tile_coords(tile, ntm, ntn, mb, nb);
-        const int32_t row0 = mb * 128;
-        const int32_t col0 = nb * BN;
-        const int steps = nk + lsteps;
-        for (int kit = 0; kit < steps; ++kit, ++g) {
-          const uint32_t slot = g % C::kStages;
-          const uint32_t ph = (g / C::kStages) & 1u;
-          if (sm.abort_flag || !mbar_wait(&sm.empty[slot], ph ^ 1u)) {
-            if (!sm.abort_flag) {
-              record_error(p.status, kDevTimeoutEmpty);
-              sm.abort_flag = 1u;
+    }
+    __syncwarp();
+    uint32_t g = 0;
+    bool ok = !p.stall_test;
+    for (int tile = blockIdx.x; ok && tile < ntiles; tile += gridDim.x) {
+      int mb, nb;
+      tile_coords(tile, ntm, ntn, mb, nb);
+      const int32_t row0 = mb * 128;
+      const int32_t col0 = nb * BN;
+      const int steps = nks + lsteps;
+      for (int kit = 0; kit < steps; ++kit, ++g) {
+        const uint32_t slot = g % C::kStages;
+        const uint32_t ph = (g / C::kStages) & 1u;
+        ok = wait(&sm.empty[slot], ph ^ 1u, kDevTimeoutEmpty);
+        if (!ok) break;
+        uint8_t* st = sm.stage[slot];
+        if (kit < nks) {
+          const int k0 = kit * C::kSub;
+          const uint32_t subs = k0 + C::kSub <= nk ? C::kSub : 1u;
+          const bool load_e = SPARSE && k0 % 2 == 0;
+          if (elect_one()) {
+            mbar_arrive_expect_tx(&sm.full[slot], subs * (C::kABytes + C::kBBytes) + (load_e ? 2048u : 0u));
+#pragma unroll
+            for (uint32_t u = 0; u < C::kSub; ++u) {
+              if (u < subs) {
+                tma_load_2d(st + u * C::kABytes, &p.tm_a, &sm.full[slot], (k0 + u) * (SPARSE ? 32 : 64), row0);
+                tma_load_2d(st + C::kBOff + u * C::kBBytes, &p.tm_b, &sm.full[slot], (k0 + u) * 64, col0);
+              }
             }
-            ok = false;
-            break;
-          }
-          uint8_t* st = sm.stage[slot];
-          if (kit < nk) {
-            const bool load_e = SPARSE && (kit % 2 == 0);
-            mbar_arrive_expect_tx(&sm.full[slot], C::kABytes + C::kBBytes + (load_e ? 2048u : 0u));
-            if (SPARSE)
-              tma_load_2d(st, &p.tm_a, &sm.full[slot], kit * 32, row0);
-            else
-              tma_load_2d(st, &p.tm_a, &sm.full[slot], kit * 64, row0);
-            tma_load_2d(st + C::kABytes, &p.tm_b, &sm.full[slot], kit * 64, col0);
             if (load_e) {
               const uint8_t* src =
-                  p.meta + (static_cast<size_t>(mb) * kblocks + kit / 2) * kMetaBlockBytes;
-              bulk_load(st + C::kABytes + C::kBBytes, src, 2048u, &sm.full[slot]);
+                  p.meta + (static_cast<size_t>(mb) * kblocks + k0 / 2) * kMetaBlockBytes;
+              bulk_load(st + C::kEOff, src, 2048u, &sm.full[slot]);
             }
-          } else {
-            const int l = kit - nk;
+          }
+        } else {
+          const int l = kit - nks;
+          if (elect_one()) {
             mbar_arrive_expect_tx(&sm.full[slot], C::kLoraABytes + C::kLoraBBytes);
             tma_load_2d(st, &p.tm_t, &sm.full[slot], l * 32, row0);
-            tma_load_2d(st + C::kABytes, &p.tm_lb, &sm.full[slot], l * 32, col0);
+            tma_load_2d(st + C::kBOff, &p.tm_lb, &sm.full[slot], l * 32, col0);
           }
         }
-      }
-      // drain: the last fill of every stage must have landed before exit
-      const uint32_t issued = g;
-      for (uint32_t b = issued; b > 0 && b + C::kStages > issued; --b) {
-        const uint32_t x = b - 1;
-        if (!mbar_wait(&sm.full[x % C::kStages], (x / C::kStages) & 1u, kWaitLimitNs / 4))
-          record_error(p.status, kDevTimeoutDrain);
+        __syncwarp();
       }
     }
+    // drain: the last fill of every stage must have landed before exit
+    const uint32_t issued = g;
+    for (uint32_t b = issued; b > 0 && b + C::kStages > issued; --b) {
+      const uint32_t x = b - 1;
+      if (!mbar_wait(&sm.full[x % C::kStages], (x / C::kStages) & 1u, kWaitLimitNs / 4) && lane == 0)
+        record_error(p.status, kDevTimeoutDrain);
+    }
+    __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      const uint32_t idesc_main = make_idesc_bf16(128, BN, SPARSE);
-      const uint32_t idesc_dense = make_idesc_bf16(128, BN, false);
-      uint32_t g = 0, eslot = 0;
-      int acc_count = 0;
-      bool ok = true;
-      for (int tile = blockIdx.x; ok && tile < ntiles; tile += gridDim.x, ++acc_count) {
-        const int acc = acc_count % C::kAcc;
-        const uint32_t acc_ph = static_cast<uint32_t>(acc_count / C::kAcc) & 1u;
-        if (sm.abort_flag || !mbar_wait(&sm.acc_empty[acc], acc_ph ^ 1u)) {
-          if (!sm.abort_flag) {
-            record_error(p.status, kDevTimeoutAccum);
-            sm.abort_flag = 1u;
-          }
-          break;
-        }
+    // The whole warp runs the loop, so that the operands stay warp-uniform, and one
+    // elected lane issues each tcgen05 instruction.  Issued from a branch that only one
+    // lane takes, an MMA costs more than its bytes: 20 tokens of 4096 -> 4096 took 34 us.
+    const uint32_t idesc_main = make_idesc_bf16(128, BN, SPARSE);
+    const uint32_t idesc_dense = make_idesc_bf16(128, BN, false);
+    uint32_t g = 0, eslot = 0;
+    int acc_count = 0;
+    bool ok = true;
+    for (int tile = blockIdx.x; ok && tile < ntiles; tile += gridDim.x, ++acc_count) {
+      const int acc = acc_count % C::kAcc;
+      const uint32_t acc_ph = static_cast<uint32_t>(acc_count / C::kAcc) & 1u;
+      if (!wait(&sm.acc_empty[acc], acc_ph ^ 1u, kDevTimeoutAccum)) break;
+      tc_fence_after();
+      const uint32_t d_tmem = sm.tmem_base + static_cast<uint32_t>(acc * BN);
+      const int steps = nks + lsteps;
+      for (int kit = 0; kit < steps; ++kit, ++g) {
+        const uint32_t slot = g % C::kStages;
+        const uint32_t ph = (g / C::kStages) & 1u;
+        ok = wait(&sm.full[slot], ph, kDevTimeoutFull);
+        if (!ok) break;
         tc_fence_after();
-        const uint32_t d_tmem = sm.tmem_base + static_cast<uint32_t>(acc * BN);
-        const int steps = nk + lsteps;
-        uint32_t accumulate = 0;
-        for (int kit = 0; kit < steps; ++kit, ++g) {
-          const uint32_t slot = g % C::kStages;
-          const uint32_t ph = (g / C::kStages) & 1u;
-          if (sm.abort_flag || !mbar_wait(&sm.full[slot], ph)) {
-            if (!sm.abort_flag) {
-              record_error(p.status, kDevTimeoutFull);
-              sm.abort_flag = 1u;
+        const uint32_t sa = smem_u32(sm.stage[slot]);
+        const uint32_t sb = sa + C::kBOff;
+        const int k0 = kit * C::kSub;
+        if (SPARSE && kit < nks && k0 % 2 == 0) eslot = (eslot + 1) % kEslots;
+        // one election a stage: each costs as much as an MMA of this size
+        if (elect_one()) {
+          if (kit < nks) {
+            if (SPARSE && k0 % 2 == 0) {
+              const uint64_t edesc = make_sdesc(sa + C::kEOff, 2048, 128, kSwNone);
+              tc_cp_128x128b(sm.tmem_base + C::kEcol0 + 4 * eslot, edesc);
             }
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t sa = smem_u32(sm.stage[slot]);
-          const uint32_t sb = sa + C::kABytes;
-          if (kit < nk) {
-            if (SPARSE) {
-              if (kit % 2 == 0) {
-                eslot = (eslot + 1) % kEslots;
-                const uint64_t edesc = make_sdesc(sb + C::kBBytes, 2048, 128, kSwNone);
-                tc_cp_128x128b(sm.tmem_base + C::kEcol0 + 4 * eslot, edesc);
-              }
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const uint32_t ecol = C::kEcol0 + 4 * eslot + 2 * (kit % 2) + j;
-                const uint64_t da = make_sdesc(sa + 32 * j, 16, 512, kSw64);
-                const uint64_t db = make_sdesc(sb + 64 * j, 16, 1024, kSw128);
-                const uint32_t idesc = idesc_main | (ecol & 1u);
-                mma_sp_bf16(d_tmem, da, db, sm.tmem_base + (ecol & ~1u), idesc, accumulate);
-                accumulate = 1;
-              }
-            } else {
+            for (int u = 0; u < C::kSub; ++u) {
+              if (k0 + u >= nk) break;
+              const uint32_t ua = sa + u * C::kABytes, ub = sb + u * C::kBBytes;
+              if (SPARSE) {
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk) {
-                const uint64_t da = make_sdesc(sa + 32 * kk, 16, 1024, kSw128);
-                const uint64_t db = make_sdesc(sb + 32 * kk, 16, 1024, kSw128);
-                mma_bf16(d_tmem, da, db, idesc_main, accumulate);
-                accumulate = 1;
+                for (int j = 0; j < 2; ++j) {
+                  const uint32_t ecol = C::kEcol0 + 4 * eslot + 2 * ((k0 + u) % 2) + j;
+                  const uint64_t da = make_sdesc(ua + 32 * j, 16, 512, kSw64);
+                  const uint64_t db = make_sdesc(ub + 64 * j, 16, 1024, kSw128);
+                  const uint32_t idesc = idesc_main | (ecol & 1u);
+                  mma_sp_bf16(d_tmem, da, db, sm.tmem_base + (ecol & ~1u), idesc, kit > 0 || u > 0 || j > 0);
+                }
+              } else {
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                  const uint64_t da = make_sdesc(ua + 32 * kk, 16, 1024, kSw128);
+                  const uint64_t db = make_sdesc(ub + 32 * kk, 16, 1024, kSw128);
+                  mma_bf16(d_tmem, da, db, idesc_main, kit > 0 || u > 0 || kk > 0);
+                }
               }
             }
           } else {
-            const int l = kit - nk;
+            const int l = kit - nks;
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {
               if (32 * l + 16 * kk >= p.r) break;  // past r: the zero-filled half of the box
               const uint64_t da = make_sdesc(sa + 32 * kk, 16, 512, kSw64);
               const uint64_t db = make_sdesc(sb + 32 * kk, 16, 512, kSw64);
-              mma_bf16(d_tmem, da, db, idesc_dense, accumulate);
-              accumulate = 1;
+              mma_bf16(d_tmem, da, db, idesc_dense, 1);
             }
           }
           tc_commit(&sm.empty[slot]);
         }
-        if (!ok) break;
-        tc_commit(&sm.acc_full[acc]);
+        __syncwarp();
       }
-      tc_commit(&sm.drain);
-      if (!mbar_wait(&sm.drain, 0)) record_error(p.status, kDevTimeoutDrain);
+      if (!ok) break;
+      if (elect_one()) tc_commit(&sm.acc_full[acc]);
+      __syncwarp();
     }
+    if (elect_one()) tc_commit(&sm.drain);
+    __syncwarp();
+    if (!mbar_wait(&sm.drain, 0) && lane == 0) record_error(p.status, kDevTimeoutDrain);
     __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue
@@ -270,6 +294,7 @@ lynx_gemm_kernel(const __grid_constant__ GemmLaunch p) {
     // draining half of the columns into registers; the TMEM buffer is released
     // before the global stores, so the next tile's MMAs overlap them.
     constexpr int kHalf = BN / 2;
+    constexpr int kChunk = kHalf < 32 ? kHalf : 32;  // columns read from TMEM at a time
     const uint32_t q = warp & 3u;              // TMEM lane quarter this warp may access
     const uint32_t ch = (warp - 2u) >> 2;      // which half of the columns
     const uint32_t row = 32u * q + lane;
@@ -302,49 +327,45 @@ lynx_gemm_kernel(const __grid_constant__ GemmLaunch p) {
       tc_fence_after();
       uint32_t out[kHalf / 2];
 #pragma unroll
-      for (int c = 0; c < kHalf / 32; ++c) {
-        const int col = static_cast<int>(ch) * kHalf + 32 * c;
-        uint32_t r[32];
-        tmem_ld_32x32b_x32(sm.tmem_base + ((32u * q) << 16) + static_cast<uint32_t>(acc * BN + col), r);
+      for (int c = 0; c < kHalf / kChunk; ++c) {
+        const int col = static_cast<int>(ch) * kHalf + kChunk * c;
+        uint32_t r[kChunk];
+        tmem_ld_chunk(sm.tmem_base + ((32u * q) << 16) + static_cast<uint32_t>(acc * BN + col), r);
         tmem_ld_wait();
-        // 8 columns (16 bytes) a time in the extended epilogue: N is a multiple of 8
-        uint32_t add[16] = {}, pre[16];
+        uint32_t add[kChunk / 16][8] = {}, pre[kChunk / 16][8];
+        const int left = row_ok ? static_cast<int>(p.N - n_base) - col : 0;
+        const int64_t at = grow * p.N + n_base + col;
         if constexpr (EXT) {
-          if (p.residual != nullptr && row_ok) {
-            const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(p.residual) + grow * p.N + n_base + col;
+          if (p.residual != nullptr) {
 #pragma unroll
-            for (int v = 0; v < 4; ++v)
-              if (n_base + col + 8 * v < p.N)
-                *reinterpret_cast<uint4*>(add + 4 * v) = *reinterpret_cast<const uint4*>(from + 8 * v);
+            for (int v = 0; v < kChunk / 16; ++v)
+              load_row16(add[v], static_cast<const __nv_bfloat16*>(p.residual) + at + 16 * v, left - 16 * v, p.wide);
           }
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < kChunk / 2; ++i) {
           float a = __fmaf_rn(s, __uint_as_float(r[2 * i]), sm.bias_s[col + 2 * i]);
           float b = __fmaf_rn(s, __uint_as_float(r[2 * i + 1]), sm.bias_s[col + 2 * i + 1]);
           if constexpr (EXT) {
             __nv_bfloat162 z = __floats2bfloat162_rn(a, b);
-            pre[i] = *reinterpret_cast<uint32_t*>(&z);
+            pre[i / 8][i % 8] = *reinterpret_cast<uint32_t*>(&z);
           }
           if (p.act == kActGeluTanh) {
             a = gelu_tanh(a);
             b = gelu_tanh(b);
           }
           if constexpr (EXT) {
-            a += __uint_as_float(add[i] << 16);
-            b += __uint_as_float(add[i] & 0xFFFF0000u);
+            a += __uint_as_float(add[i / 8][i % 8] << 16);
+            b += __uint_as_float(add[i / 8][i % 8] & 0xFFFF0000u);
           }
           __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-          out[16 * c + i] = *reinterpret_cast<uint32_t*>(&h);
+          out[kChunk / 2 * c + i] = *reinterpret_cast<uint32_t*>(&h);
         }
         if constexpr (EXT) {
-          if (p.z != nullptr && row_ok) {
-            __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.z) + grow * p.N + n_base + col;
+          if (p.z != nullptr) {
 #pragma unroll
-            for (int v = 0; v < 4; ++v)
-              if (n_base + col + 8 * v < p.N)
-                *reinterpret_cast<uint4*>(to + 8 * v) =
-                    make_uint4(pre[4 * v], pre[4 * v + 1], pre[4 * v + 2], pre[4 * v + 3]);
+            for (int v = 0; v < kChunk / 16; ++v)
+              store_row16(static_cast<__nv_bfloat16*>(p.z) + at + 16 * v, pre[v], left - 16 * v, p.wide);
           }
         }
       }
@@ -382,17 +403,21 @@ cudaError_t launch_variant(const GemmLaunch& p, cudaStream_t stream) {
                                dim3(kGemmThreads), smem, stream, p);
 }
 
-template <bool EXT>
-cudaError_t launch_gemm_ext(const GemmLaunch& p, cudaStream_t stream) {
-  if (p.bn == 256)
-    return p.sparse ? launch_variant<256, true, EXT>(p, stream) : launch_variant<256, false, EXT>(p, stream);
-  return p.sparse ? launch_variant<128, true, EXT>(p, stream) : launch_variant<128, false, EXT>(p, stream);
+template <int BN>
+cudaError_t launch_bn(const GemmLaunch& p, cudaStream_t stream) {
+  if (p.ext) return p.sparse ? launch_variant<BN, true, true>(p, stream) : launch_variant<BN, false, true>(p, stream);
+  return p.sparse ? launch_variant<BN, true, false>(p, stream) : launch_variant<BN, false, false>(p, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_gemm(const GemmLaunch& p, cudaStream_t stream) {
-  return p.ext ? launch_gemm_ext<true>(p, stream) : launch_gemm_ext<false>(p, stream);
+  switch (p.bn) {
+    case 32: return launch_bn<32>(p, stream);
+    case 64: return launch_bn<64>(p, stream);
+    case 128: return launch_bn<128>(p, stream);
+    default: return launch_bn<256>(p, stream);
+  }
 }
 
 }  // namespace lynx

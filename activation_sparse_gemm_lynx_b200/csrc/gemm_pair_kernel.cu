@@ -37,6 +37,7 @@
 #include "lynx_act.cuh"
 #include "lynx_internal.h"
 #include "lynx_ptx.cuh"
+#include "lynx_rows.cuh"
 #include "lynx_select.cuh"
 
 namespace lynx {
@@ -347,44 +348,6 @@ __device__ __forceinline__ bool compress_tile_stages(Smem& sm, uint32_t& g, int 
   return true;
 }
 
-// 16 columns of this lane's row of the residual, and the same of Z.  The stages leave
-// next to no L1, so what is asked for twice comes from L2 twice, and the operands keep L2
-// at its rate: 32 bytes (a sector) go in one access where the rows lie on 32 bytes, else
-// in two of 16.  N is a multiple of 8.  The residual may be Y itself, whose tiles this CTA
-// writes only after it has read them here.
-__device__ __forceinline__ void load_residual(uint32_t (&v)[8], const __nv_bfloat16* at, int left, bool wide) {
-  if (wide) {
-    if (left > 0)
-      asm volatile("ld.global.L1::no_allocate.L2::256B.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                   : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-                   : "l"(at)
-                   : "memory");
-  } else {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (left > 8 * i)
-        asm volatile("ld.global.L1::no_allocate.L2::256B.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(v[4 * i]), "=r"(v[4 * i + 1]), "=r"(v[4 * i + 2]), "=r"(v[4 * i + 3])
-                     : "l"(at + 8 * i)
-                     : "memory");
-    }
-  }
-}
-
-__device__ __forceinline__ void store_z(__nv_bfloat16* at, const uint32_t (&v)[8], int left, bool wide) {
-  if (wide) {
-    if (left > 0)
-      asm volatile("st.global.L1::no_allocate.L2::evict_first.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-                   "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                   : "memory");
-  } else {
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (left > 8 * i)
-        *reinterpret_cast<uint4*>(at + 8 * i) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-  }
-}
-
 // EXT: Y = R + act(v), and v itself to Z where it is wanted.
 template <bool SPARSE, int ACT, bool FUSED, bool EXT>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -562,7 +525,6 @@ lynx_gemm_pair_kernel(const __grid_constant__ GemmLaunch p) {
         }
         tc_fence_after();
         const uint32_t d_tmem = sm.tmem_base;
-        uint32_t accumulate = 0;
         for (int kit = 0; kit < steps; ++kit, ++g) {
           const uint32_t slot = g % C::kStages;
           // the helper warp says when stage g has landed; both warps leave
@@ -574,48 +536,51 @@ lynx_gemm_pair_kernel(const __grid_constant__ GemmLaunch p) {
           tc_fence_after();
           const uint32_t sa = smem_u32(sm.stage[slot]);
           const uint32_t sb = sa + C::kBOff;
-          if (kit < nk) {
-            if (SPARSE) {
-              eslot = (eslot + 1) % kEslots;
-              const uint64_t edesc = make_sdesc(sa + C::kEOff, 2048, 128, kSwNone);
-              if (elect_one()) tc_cp_128x128b_pair(sm.tmem_base + C::kEcol0 + 4 * eslot, edesc);
-              __syncwarp();
+          // one elected lane issues; the operands are computed by all and stay warp-uniform
+          auto elected = [](auto&& issue) {
+            if (elect_one()) issue();
+            __syncwarp();
+          };
+          if (SPARSE && kit < nk) {
+            // (one election for all of the stage's MMAs, as below, is 0.5% slower here)
+            eslot = (eslot + 1) % kEslots;
+            const uint64_t edesc = make_sdesc(sa + C::kEOff, 2048, 128, kSwNone);
+            elected([&] { tc_cp_128x128b_pair(sm.tmem_base + C::kEcol0 + 4 * eslot, edesc); });
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const uint32_t ecol = C::kEcol0 + 4 * eslot + j;
-                const uint64_t da = make_sdesc(sa + 32 * j, 16, 1024, kSw128);
-                const uint64_t db = make_sdesc(sb + (j >> 1) * 16384 + 64 * (j & 1), 16, 1024, kSw128);
-                if (elect_one())
-                  mma_sp_bf16_pair(d_tmem, da, db, sm.tmem_base + (ecol & ~1u), idesc_main | (ecol & 1u),
-                                   accumulate);
-                __syncwarp();
-                accumulate = 1;
-              }
-            } else {
-#pragma unroll
-              for (int kk = 0; kk < 8; ++kk) {
-                const uint32_t off = (kk >> 2) * 16384 + 32 * (kk & 3);
-                const uint64_t da = make_sdesc(sa + off, 16, 1024, kSw128);
-                const uint64_t db = make_sdesc(sb + off, 16, 1024, kSw128);
-                if (elect_one()) mma_bf16_pair(d_tmem, da, db, idesc_main, accumulate);
-                __syncwarp();
-                accumulate = 1;
-              }
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t ecol = C::kEcol0 + 4 * eslot + j;
+              const uint64_t da = make_sdesc(sa + 32 * j, 16, 1024, kSw128);
+              const uint64_t db = make_sdesc(sb + (j >> 1) * 16384 + 64 * (j & 1), 16, 1024, kSw128);
+              elected([&] {
+                mma_sp_bf16_pair(d_tmem, da, db, sm.tmem_base + (ecol & ~1u), idesc_main | (ecol & 1u),
+                                 kit > 0 || j > 0);
+              });
             }
+            elected([&] { tc_commit_pair_mc(&sm.empty[slot], kPairMask); });
           } else {
-            const int l = kit - nk;
+            // an election an MMA costs the dense path 4% (4096 x 4096 -> 4096: 108 us for 112)
+            elected([&] {
+              if (kit < nk) {
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-              if (32 * l + 16 * kk >= p.r) break;  // past r: the zero-filled half of the box
-              const uint64_t da = make_sdesc(sa + 32 * kk, 16, 512, kSw64);
-              const uint64_t db = make_sdesc(sb + 32 * kk, 16, 512, kSw64);
-              if (elect_one()) mma_bf16_pair(d_tmem, da, db, idesc_dense, accumulate);
-              __syncwarp();
-              accumulate = 1;
-            }
+                for (int kk = 0; kk < 8; ++kk) {
+                  const uint32_t off = (kk >> 2) * 16384 + 32 * (kk & 3);
+                  const uint64_t da = make_sdesc(sa + off, 16, 1024, kSw128);
+                  const uint64_t db = make_sdesc(sb + off, 16, 1024, kSw128);
+                  mma_bf16_pair(d_tmem, da, db, idesc_main, kit > 0 || kk > 0);
+                }
+              } else {
+                const int l = kit - nk;
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk) {
+                  if (32 * l + 16 * kk >= p.r) break;  // past r: the zero-filled half of the box
+                  const uint64_t da = make_sdesc(sa + 32 * kk, 16, 512, kSw64);
+                  const uint64_t db = make_sdesc(sb + 32 * kk, 16, 512, kSw64);
+                  mma_bf16_pair(d_tmem, da, db, idesc_dense, 1);
+                }
+              }
+              tc_commit_pair_mc(&sm.empty[slot], kPairMask);
+            });
           }
-          if (elect_one()) tc_commit_pair_mc(&sm.empty[slot], kPairMask);
-          __syncwarp();
         }
         if (stop) break;
         if (elect_one()) tc_commit_pair_mc(&sm.acc_full, kPairMask);
@@ -703,13 +668,15 @@ lynx_gemm_pair_kernel(const __grid_constant__ GemmLaunch p) {
         else if (p.row_scale != nullptr) s = p.row_scale[grow];
       }
       // The residual of this lane's row: the first 16 columns now, while the tile's MMAs
-      // run, each further 16 one step ahead of their use
+      // run, each further 16 two steps ahead of their use
       const int left = EXT && row_ok ? static_cast<int>(p.N - n_base) - static_cast<int>(ch) * kHalf : 0;  // columns from the warp's first on
       const int64_t at = EXT ? grow * p.N + n_base + ch * kHalf : 0;
-      uint32_t next[8];
-      if constexpr (EXT) {
-        if (p.residual != nullptr) load_residual(next, static_cast<const __nv_bfloat16*>(p.residual) + at, left, p.wide);
-      }
+      uint32_t res[2][8];
+      auto fetch = [&](int i) {
+        if (p.residual != nullptr)
+          load_row16(res[i & 1], static_cast<const __nv_bfloat16*>(p.residual) + at + 16 * i, left - 16 * i, p.wide);
+      };
+      if constexpr (EXT) fetch(0);
       bool ok = !sm.abort_flag;
       if (ok && !mbar_wait(&sm.acc_full, static_cast<uint32_t>(acc_count) & 1u)) {
         record_error(p.status, kDevTimeoutAccum);
@@ -733,6 +700,7 @@ lynx_gemm_pair_kernel(const __grid_constant__ GemmLaunch p) {
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(lead_acc_empty);
+      if constexpr (EXT) fetch(1);
       int piece = 0;
 #pragma unroll
       for (int c = 0; c < kHalf / 32; ++c) {
@@ -755,17 +723,9 @@ lynx_gemm_pair_kernel(const __grid_constant__ GemmLaunch p) {
               bulk_commit();
             }
           };
-          uint32_t pk[8], res[8];
-          constexpr int kPieces = kHalf / 16;
-          const int done = 2 * c + h;  // pieces before this one
+          uint32_t pk[8];
+          const int done = 2 * c + h;  // pieces of 16 columns before this one
           if constexpr (EXT) {
-            if (p.residual != nullptr) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) res[i] = next[i];
-              if (done + 1 < kPieces)
-                load_residual(next, static_cast<const __nv_bfloat16*>(p.residual) + at + 16 * (done + 1),
-                              left - 16 * (done + 1), p.wide);
-            }
             if (p.z != nullptr) {
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
@@ -774,7 +734,7 @@ lynx_gemm_pair_kernel(const __grid_constant__ GemmLaunch p) {
                                                           __fmaf_rn(s, __uint_as_float(r[c][e + 1]), sm.bias_s[col + e + 1]));
                 pk[i] = *reinterpret_cast<uint32_t*>(&zv);
               }
-              store_z(static_cast<__nv_bfloat16*>(p.z) + at + 16 * done, pk, left - 16 * done, p.wide);
+              store_row16(static_cast<__nv_bfloat16*>(p.z) + at + 16 * done, pk, left - 16 * done, p.wide);
             }
           }
 #pragma unroll
@@ -785,12 +745,15 @@ lynx_gemm_pair_kernel(const __grid_constant__ GemmLaunch p) {
                 apply_act<ACT>(__fmaf_rn(s, __uint_as_float(r[c][e + 1]), sm.bias_s[col + e + 1]));
             if constexpr (EXT) {
               if (p.residual != nullptr) {
-                a += __uint_as_float(res[i] << 16);
-                b += __uint_as_float(res[i] & 0xFFFF0000u);
+                a += __uint_as_float(res[done & 1][i] << 16);
+                b += __uint_as_float(res[done & 1][i] & 0xFFFF0000u);
               }
             }
             __nv_bfloat162 hv = __floats2bfloat162_rn(a, b);
             pk[i] = *reinterpret_cast<uint32_t*>(&hv);
+          }
+          if constexpr (EXT) {
+            if (done + 2 < kHalf / 16) fetch(done + 2);
           }
           store(pk);
         }

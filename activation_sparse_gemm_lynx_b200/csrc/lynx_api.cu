@@ -224,7 +224,21 @@ lynx_status check_lora(const void* A, const void* B, int64_t r) {
 
 lynx_status map_cuda(cudaError_t e) { return e == cudaSuccess ? LYNX_OK : LYNX_ERR_CUDA; }
 
-int gemm_bn(int64_t N) { return N >= 1024 ? 256 : 128; }
+// Columns of a 1-CTA GEMM tile: as few (from 256 down to 32) as come out at one tile an SM at
+// most.  A few rows are bound by reading W, in which every SM has to take part: 20 tokens of
+// 4096 -> 4096, dense, 16 tiles of 256 columns 24.8 us, 128 of 32 15.5.  Sparse, the blocks of a
+// row block all read its metadata at once, and past 64 of them that costs more (128 of 32: 34 us,
+// 64 of 64: 25).
+int gemm_bn(int64_t M, int64_t N, bool sparse, int sms) {
+  const int64_t ntm = (M + 127) / 128;
+  int bn = N >= 1024 ? 256 : 128;
+  while (bn > 32) {
+    const int64_t ntn = (N + bn / 2 - 1) / (bn / 2);
+    if (ntm * ntn > sms || (sparse && bn == 64 && ntn > 64)) break;
+    bn /= 2;
+  }
+  return bn;
+}
 
 // The pair GEMM combines the sparsify pass's partials itself (no finalize_kernel).
 struct FusedFinalize {
@@ -277,10 +291,16 @@ lynx_status run_sparsify(DeviceState* ds, const void* X, const void* A, int64_t 
   return map_cuda(launch_sparsify(p, stream));
 }
 
-// CTA pairs (256 x 256 tiles) unless the problem is too small to feed them; the
-// pair kernel steps K by 128 on both paths
-bool use_pair_kernel(int64_t M, int64_t N, int64_t K) {
-  return M > 128 && N >= 256 && K % 128 == 0;
+// What the CTA-pair kernel takes: it steps K by 128 on both paths.
+bool pair_kernel_takes(int64_t M, int64_t N, int64_t K) { return M > 128 && N >= 256 && K % 128 == 0; }
+
+// CTA pairs (256 x 256 tiles) unless one round of the 1-CTA kernel's smaller tiles has a tile for
+// every SM at most: 200 x 1024 -> 2000 takes 6.2 us there and 10.8 in pairs, 1000 x 4096 -> 2000
+// 21 and 27.  Sparse, a long K on few tiles is the pairs' (1000 x 4096 -> 2000: 28 us for 30).
+// Either gives the same bits.
+bool use_pair_kernel(int64_t M, int64_t N, int64_t K, bool sparse, int sms) {
+  if (!pair_kernel_takes(M, N, K)) return false;
+  return (M + 127) / 128 * ((N + 127) / 128) > sms || (sparse && K > 2048);
 }
 
 // fused_x: a_src is the dense X and the pair kernel compresses it itself (the
@@ -292,9 +312,9 @@ lynx_status run_gemm(DeviceState* ds, const void* a_src, bool sparse, const void
                      bool fused_x = false, const void* R = nullptr, void* Z = nullptr) {
   GemmLaunch p;
   std::memset(&p, 0, sizeof(p));
-  const bool pair = use_pair_kernel(M, N, K);
+  const bool pair = fused_x ? pair_kernel_takes(M, N, K) : use_pair_kernel(M, N, K, sparse, ds->sms);
   if (fused_x && !pair) return LYNX_ERR_UNSUPPORTED_SHAPE;
-  const int bn = pair ? 256 : gemm_bn(N);
+  const int bn = pair ? 256 : gemm_bn(M, N, sparse, ds->sms);
   const uint32_t b_rows = pair ? 128u : static_cast<uint32_t>(bn);  // W rows one CTA loads
   if (fused_x) {
     // the dense X in 128 x 64 boxes, as on the dense path
@@ -555,7 +575,7 @@ lynx_status linear_enqueue(const void* X, const void* W, const void* bias, const
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   void* t_buf = lora ? ws + wl.t : nullptr;
   // with the CTA-pair GEMM, the GEMM itself combines the pass's K-range partials
-  const bool fused = use_pair_kernel(M, N, K) && (!skip_sparsify || lora);
+  const bool fused = use_pair_kernel(M, N, K, !skip_sparsify, ds->sms) && (!skip_sparsify || lora);
   FusedFinalize fin;
   if (fused) {
     fin.mode = skip_sparsify ? 2 : 1;
@@ -657,7 +677,7 @@ int lynx_linear_fused(const void* X, const void* W, const void* bias, const void
   st = check_shape(M, N, K);
   if (st != LYNX_OK) return st;
   // shapes the CTA-pair kernel does not take run the two-pass layer
-  if (!use_pair_kernel(M, N, K))
+  if (!pair_kernel_takes(M, N, K))
     return lynx_linear_act(X, W, bias, A, B, M, N, K, r, 0, act, Y, workspace, workspace_bytes, stream);
   if (!aligned16(X) || !aligned16(W) || !aligned16(Y) || (bias && !aligned16(bias)) ||
       (A && !aligned16(A)) || (B && !aligned16(B)) || (workspace && !aligned16(workspace)))
