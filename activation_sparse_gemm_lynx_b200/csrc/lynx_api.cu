@@ -637,15 +637,17 @@ int lynx_linear_residual(const void* X, const void* W, const void* bias, const v
   const lynx_status st = check_shape(M, N, K);  // the sizes below are products of these
   if (X != nullptr && W != nullptr && Y != nullptr && st == LYNX_OK && (A == nullptr || rank_supported(r))) {
     const size_t m = static_cast<size_t>(M), n = static_cast<size_t>(N), k = static_cast<size_t>(K);
-    const bool need_ws = A != nullptr || !skip_sparsify;
-    const Span out[3] = {{Y, m * n * 2}, {Z, m * n * 2}, {need_ws ? workspace : nullptr, workspace_layout(M, K, r).total}};
     const size_t rr = A != nullptr ? static_cast<size_t>(r) : 0;
-    const Span in[6] = {{X, m * k * 2}, {W, n * k * 2}, {bias, n * 2}, {A, rr * k * 2}, {B, n * rr * 2}, {R, m * n * 2}};
-    for (int o = 0; o < 3; ++o) {
+    const bool need_ws = A != nullptr || !skip_sparsify;
+    const Span out[] = {{Y, m * n * 2}, {Z, m * n * 2}, {need_ws ? workspace : nullptr, workspace_layout(M, K, r).total}};
+    const Span in[] = {{X, m * k * 2}, {W, n * k * 2}, {bias, n * 2}, {A, rr * k * 2}, {B, n * rr * 2}};
+    const Span res = {R, m * n * 2};
+    for (const Span& o : out) {
       for (const Span& i : in)
-        if (overlap(out[o], i) && !(o == 0 && i.p == R && R == Y)) return LYNX_ERR_INVALID_ARG;
-      for (int q = 0; q < o; ++q)
-        if (overlap(out[o], out[q])) return LYNX_ERR_INVALID_ARG;
+        if (overlap(o, i)) return LYNX_ERR_INVALID_ARG;
+      for (const Span& q : out)
+        if (&q != &o && overlap(o, q)) return LYNX_ERR_INVALID_ARG;
+      if (overlap(o, res) && !(&o == &out[0] && R == Y)) return LYNX_ERR_INVALID_ARG;
     }
   }
   const int part = g_profile_part.load();

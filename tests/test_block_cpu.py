@@ -72,7 +72,7 @@ def test_layer_norm_backward_refusals(lib):
         assert need >= 2 * K * 4
         assert norm_backward(lib, K=K, ws_bytes=need - 1) == lynx.LYNX_ERR_WORKSPACE_TOO_SMALL
     for kw in (dict(dX=at(1)), dict(dX=at(2)), dict(dX=at(5)), dict(dX=at(6, 16)), dict(dw=at(9)), dict(dw=at(6)), dict(db=at(6)),
-               dict(ws=at(6)), dict(ws=at(7)), dict(db=at(5)), dict(dw=at(3))):
+               dict(ws=at(6)), dict(ws=at(7)), dict(db=at(5)), dict(dw=at(3)), dict(dY=at(6), dX=at(6)), dict(X=at(6), dX=at(6))):
         assert norm_backward(lib, **kw) == lynx.LYNX_ERR_INVALID_ARG
 
 
@@ -100,7 +100,8 @@ def test_linear_residual_refusals(lib):
     need = lynx.lynx_workspace_bytes(300, 1000, 576, 16)
     assert residual(lib, ws_bytes=need - 1) == lynx.LYNX_ERR_WORKSPACE_TOO_SMALL
     for kw in (dict(Y=at(1)), dict(Y=at(2)), dict(Y=at(6, 16)), dict(Z=at(6)), dict(Z=at(7)), dict(Y=at(8)), dict(ws=at(6)),
-               dict(ws=at(7)), dict(Z=at(5)), dict(Y=at(6), Z=at(6)), dict(ws=at(8, 256))):
+               dict(ws=at(7)), dict(Z=at(5)), dict(Y=at(6), Z=at(6)), dict(ws=at(8, 256)),
+               dict(X=at(6), Y=at(6)), dict(W=at(6), Y=at(6)), dict(bias=at(6), Y=at(6))):
         assert residual(lib, **kw) == lynx.LYNX_ERR_INVALID_ARG, kw
 
 
@@ -119,7 +120,7 @@ def few(lib, X=at(1), Wq=at(2), scales=at(3), zeros=at(4), bias=at(5), A=at(6), 
 def test_linear_w4_residual_refusals(lib):
     assert few(lib, M=33) == lynx.LYNX_ERR_UNSUPPORTED_SHAPE
     assert few(lib, R=at(8, 8)) == lynx.LYNX_ERR_MISALIGNED
-    for kw in (dict(Y=at(8, 16)), dict(ws=at(8)), dict(ws=at(8), Y=at(8)), dict(Y=at(1)), dict(act=2)):
+    for kw in (dict(Y=at(8, 16)), dict(ws=at(8)), dict(ws=at(8), Y=at(8)), dict(Y=at(1)), dict(act=2), dict(X=at(8), Y=at(8))):
         assert few(lib, **kw) == lynx.LYNX_ERR_INVALID_ARG, kw
 
 
@@ -139,7 +140,8 @@ def test_act_backward_refusals(lib):
     need = lynx.lynx_act_backward_workspace_bytes(300, 1000)
     assert need >= 4000
     assert act_backward(lib, ws_bytes=need - 1) == lynx.LYNX_ERR_WORKSPACE_TOO_SMALL
-    for kw in (dict(dZ=at(2)), dict(dZ=at(1, 16)), dict(db=at(1)), dict(ws=at(1)), dict(ws=at(3)), dict(db=at(3)), dict(db=at(5))):
+    for kw in (dict(dZ=at(2)), dict(dZ=at(1, 16)), dict(db=at(1)), dict(ws=at(1)), dict(ws=at(3)), dict(db=at(3)), dict(db=at(5)),
+               dict(Z=at(1), dZ=at(1))):
         assert act_backward(lib, **kw) == lynx.LYNX_ERR_INVALID_ARG, kw
 
 
