@@ -8,8 +8,11 @@
 //
 // One pass, bound by memory.  A block has a strip of columns and a range of rows;
 // a thread has 8 columns (16 bytes) and every ry-th row, a few rows' loads in
-// flight.  The block's sums meet in shared memory and leave as fp32, one row of
-// `part` for each range; column_sums_kernel adds those in their order.  No atomics.
+// flight.  The block's sums meet in shared memory.  Up to kClusterRows rows the ranges of a
+// strip are a cluster, whose blocks add each other's sums from there: one launch, 2.5 us of
+// the host's time less and no more of the device's up to 100 rows (300 x 1000: 4.8 us for 4.2).
+// Above, the sums leave as fp32, one row of `part` for each range, and
+// column_sums_kernel adds those.  Either in the order of the ranges; no atomics.
 //
 // gelu'(z) = sig + z sig (1 - sig) a' with sig = 1 / (1 + e^-a), a = 2 sqrt(2/pi)
 // (z + 0.044715 z^3), the derivative of z sig(a).
@@ -28,6 +31,8 @@ enum ColumnMode : int { kColSum, kColGelu, kColNorm };
 constexpr int kThreads = 256;
 constexpr int kUnroll = 4;  // rows of a thread in flight
 constexpr int kSumThreads = 256;
+constexpr int kMaxCluster = 8;
+constexpr int64_t kClusterRows = 320;
 constexpr int kSlots = 148 * 3;  // blocks a B200 holds
 
 constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -36,25 +41,28 @@ struct ColumnPlan {
   int tx;          // threads across a strip (8 columns each), a power of two
   int strips, chunks;
   int64_t rows;    // of a chunk
+  bool cluster;    // the chunks of a strip are one cluster
 };
 
 // Strips of 256 columns, or as narrow as the matrix; rows in ranges of equal length, so many
 // that strips x ranges come out just below a whole number of times what the card holds (up to
 // four; 4608 x 12288 in one round of 432 of 444 blocks), a range no shorter than one turn of
 // its threads.
-ColumnPlan column_plan(int64_t M, int64_t N) {
+ColumnPlan column_plan(int64_t M, int64_t N, bool sums) {
   ColumnPlan c;
   c.tx = 32;
   while (c.tx > 8 && 8 * (c.tx / 2) >= N) c.tx /= 2;
   c.strips = static_cast<int>(ceil_div(N, 8 * c.tx));
+  const int64_t turn = kThreads / c.tx * kUnroll, most = ceil_div(M, turn);
   int64_t chunks = 1;
   double best = 0;
-  for (int rounds = 1; rounds <= 4; ++rounds) {
+  c.cluster = sums && M <= kClusterRows;
+  if (c.cluster) chunks = kMaxCluster;
+  for (int rounds = 1; rounds <= 4 && !c.cluster; ++rounds) {
     const int64_t slots = static_cast<int64_t>(rounds) * kSlots, n = slots / c.strips;
     const double full = static_cast<double>(n * c.strips) / static_cast<double>(slots) - 0.02 * rounds;
     if (n > 0 && full > best) best = full, chunks = n;
   }
-  const int64_t turn = kThreads / c.tx * kUnroll, most = ceil_div(M, turn);
   if (chunks > most) chunks = most;
   c.rows = ceil_div(ceil_div(M, chunks), kThreads / c.tx) * (kThreads / c.tx);
   c.chunks = static_cast<int>(ceil_div(M, c.rows));
@@ -86,6 +94,7 @@ template <int MODE>
 __global__ void __launch_bounds__(kThreads, 3) column_pass_kernel(ColumnPassLaunch p, int tx, int64_t rows) {
   constexpr int kSums = MODE == kColNorm ? 2 : 1;
   __shared__ float red[kSums][kThreads][9];  // 9: rows of 8 would share banks
+  __shared__ float own[kSums * 256];
   const int t = static_cast<int>(threadIdx.x) % tx, ry = static_cast<int>(threadIdx.x) / tx, ways = kThreads / tx;
   const int64_t piece = static_cast<int64_t>(blockIdx.x) * tx + t;  // of 8 columns
   const int64_t pieces = p.N / 8;
@@ -135,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 3) column_pass_kernel(ColumnPassLaun
       }
     }
   }
-  if (p.part == nullptr) return;
+  if (p.out0 == nullptr && p.out1 == nullptr) return;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 v = halves(s0[i]), w = halves(s1[i]);
@@ -147,15 +156,35 @@ __global__ void __launch_bounds__(kThreads, 3) column_pass_kernel(ColumnPassLaun
     }
   }
   __syncthreads();
+  const int cols = 8 * tx;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * cols;
   float* out = p.part + static_cast<int64_t>(blockIdx.y) * kSums * p.N;
-  for (int i = static_cast<int>(threadIdx.x); i < kSums * 8 * tx; i += kThreads) {
-    const int which = i / (8 * tx), c = i % (8 * tx);
-    const int64_t n = static_cast<int64_t>(blockIdx.x) * 8 * tx + c;
-    if (n >= p.N) continue;
+  for (int i = static_cast<int>(threadIdx.x); i < kSums * cols; i += kThreads) {
+    const int which = i / cols, c = i % cols;
     float s = 0.f;
     for (int w = 0; w < ways; ++w) s += red[which][w * tx + c / 8][c % 8];
-    out[which * p.N + n] = s;
+    if (p.part == nullptr)
+      own[i] = s;
+    else if (n0 + c < p.N)
+      out[which * p.N + n0 + c] = s;
   }
+  if (p.part != nullptr) return;
+  __syncwarp();
+  cluster_sync_all();
+  const int ranks = static_cast<int>(cluster_nctarank());
+  for (int i = static_cast<int>(cluster_ctarank()) * kThreads + static_cast<int>(threadIdx.x); i < kSums * cols;
+       i += ranks * kThreads) {
+    float v[kMaxCluster], s = 0.f;  // all ranks' on their way at once
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r)
+      v[r] = r < ranks ? ld_cluster_f32(mapa_shared(smem_u32(own + i), static_cast<uint32_t>(r))) : 0.f;
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) s += v[r];
+    auto* to = static_cast<__nv_bfloat16*>(i < cols ? p.out0 : p.out1);
+    if (to != nullptr && n0 + i % cols < p.N) to[n0 + i % cols] = __float2bfloat16_rn(s);
+  }
+  __syncwarp();
+  cluster_sync_all();  // the others have read this block's sums
 }
 
 // part [count][C] -> bf16, the first `split` columns to out0, the rest to out1 (either may be null).
@@ -193,11 +222,10 @@ __global__ void __launch_bounds__(kSumThreads) column_sums_kernel(const float* p
 }
 
 template <int MODE>
-cudaError_t launch_pass(const ColumnPassLaunch& p, cudaStream_t s) {
-  const ColumnPlan c = column_plan(p.M, p.N);
-  return launch_after_previous(column_pass_kernel<MODE>,
-                               dim3(static_cast<unsigned>(c.strips), static_cast<unsigned>(c.chunks)), dim3(kThreads), 0, s, p,
-                               c.tx, c.rows);
+cudaError_t launch_pass(const ColumnPassLaunch& p, const ColumnPlan& c, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>(c.strips), static_cast<unsigned>(c.chunks));
+  if (!c.cluster) return launch_after_previous(column_pass_kernel<MODE>, grid, dim3(kThreads), 0, s, p, c.tx, c.rows);
+  return launch_clusters_after_previous(column_pass_kernel<MODE>, grid, dim3(kThreads), dim3(1, grid.y), 0, s, p, c.tx, c.rows);
 }
 
 cudaError_t launch_sums(const float* part, int count, int64_t C, int64_t split, void* out0, void* out1, cudaStream_t s) {
@@ -208,7 +236,8 @@ cudaError_t launch_sums(const float* part, int count, int64_t C, int64_t split, 
 }  // namespace
 
 size_t column_pass_workspace(int64_t M, int64_t N, int sums) {
-  return static_cast<size_t>(column_plan(M, N).chunks) * static_cast<size_t>(sums) * static_cast<size_t>(N) * 4;
+  const ColumnPlan c = column_plan(M, N, true);
+  return c.cluster ? 0 : static_cast<size_t>(c.chunks) * static_cast<size_t>(sums) * static_cast<size_t>(N) * 4;
 }
 
 cudaError_t launch_column_sums(const float* part, int count, int64_t K, void* out0, void* out1, cudaStream_t s) {
@@ -216,15 +245,17 @@ cudaError_t launch_column_sums(const float* part, int count, int64_t K, void* ou
 }
 
 cudaError_t launch_act_backward(const ColumnPassLaunch& p, int act, cudaStream_t s) {
-  cudaError_t e = act == kActGeluTanh ? launch_pass<kColGelu>(p, s) : launch_pass<kColSum>(p, s);
-  if (e != cudaSuccess || p.part == nullptr) return e;
-  return launch_sums(p.part, column_plan(p.M, p.N).chunks, p.N, p.N, p.out0, nullptr, s);
+  const ColumnPlan c = column_plan(p.M, p.N, p.out0 != nullptr);
+  const cudaError_t e = act == kActGeluTanh ? launch_pass<kColGelu>(p, c, s) : launch_pass<kColSum>(p, c, s);
+  if (e != cudaSuccess || p.out0 == nullptr || c.cluster) return e;
+  return launch_sums(p.part, c.chunks, p.N, p.N, p.out0, nullptr, s);
 }
 
 cudaError_t launch_layer_norm_columns(const ColumnPassLaunch& p, cudaStream_t s) {
-  cudaError_t e = launch_pass<kColNorm>(p, s);
-  if (e != cudaSuccess) return e;
-  return launch_sums(p.part, column_plan(p.M, p.N).chunks, 2 * p.N, p.N, p.out0, p.out1, s);
+  const ColumnPlan c = column_plan(p.M, p.N, true);
+  const cudaError_t e = launch_pass<kColNorm>(p, c, s);
+  if (e != cudaSuccess || c.cluster) return e;
+  return launch_sums(p.part, c.chunks, 2 * p.N, p.N, p.out0, p.out1, s);
 }
 
 }  // namespace lynx

@@ -15,7 +15,7 @@
 //
 // dw and db: each thread adds up its columns over the block's rows, the blocks'
 // sums go to the workspace and launch_column_sums adds them in the order of the
-// blocks.  2 x 8 fp32 sums a piece fit in registers up to kFusedCols columns; wider
+// blocks.  Few rows are one block, whose sums are the result.  2 x 8 fp32 sums a piece fit in registers up to kFusedCols columns; wider
 // rows read dY and X once more, by columns (column_pass_kernel.cu).
 #include <cuda_bf16.h>
 
@@ -35,6 +35,7 @@ constexpr int kMaxGroups = 8;  // rows of a block
 constexpr int kMaxStages = 4;
 constexpr uint32_t kRingMost = 200 * 1024;
 constexpr int64_t kFusedCols = 8192;
+constexpr int kRowsAlone = 2;
 constexpr int kBackwardBlocks = 148;  // one on every SM of a B200
 
 constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -284,13 +285,17 @@ layer_norm_backward_kernel(LayerNormBackwardLaunch p, int tx, int stages) {
     if (++stage == stages) stage = 0;
   }
   if constexpr (SUMS) {
-    float* out = p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.K;
+    // The sums of the rows side by side in a block meet in the ring: [group][2][K]
     const int K = static_cast<int>(p.K);
-    if (ty > 1) {  // the groups' sums meet in the ring: [group][2][K]
+    const bool alone = p.part == nullptr;  // one block: its sums are dw and db
+    auto* const sums = reinterpret_cast<float4*>(ring);
+    auto* const block_sums = reinterpret_cast<float4*>(p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.K);
+    const bool meet = ty > 1 || alone;
+    if (meet) {
       cp_async_wait<0>();
       __syncthreads();
-      out = reinterpret_cast<float*>(ring) + group * 2 * K;
     }
+    float* out = reinterpret_cast<float*>(meet ? sums + group * (K / 2) : block_sums);
     auto put = [](float* to, const f32x2(&s)[4]) {
       const float2 a = halves(s[0]), b = halves(s[1]), c = halves(s[2]), d = halves(s[3]);
       *reinterpret_cast<float4*>(to) = make_float4(a.x, a.y, b.x, b.y);
@@ -303,18 +308,21 @@ layer_norm_backward_kernel(LayerNormBackwardLaunch p, int tx, int stages) {
         put(out + K + 8 * (first + 32 * v), sb[v]);
       }
     }
-    if (ty > 1) {
-      __syncthreads();
-      const auto* sums = reinterpret_cast<const float4*>(ring);
-      auto* sum = reinterpret_cast<float4*>(p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.K);
-      for (int i = tid; i < K / 2; i += threads) {
-        float4 a = sums[i];
-        for (int q = 1; q < ty; ++q) {
-          const float4 c = sums[q * (K / 2) + i];
-          a.x += c.x, a.y += c.y, a.z += c.z, a.w += c.w;
-        }
-        sum[i] = a;
+    if (!meet) return;
+    __syncthreads();
+    for (int i = tid; i < K / 2; i += threads) {
+      float4 a = sums[i];
+      for (int q = 1; q < ty; ++q) {
+        const float4 c = sums[q * (K / 2) + i];
+        a.x += c.x, a.y += c.y, a.z += c.z, a.w += c.w;
       }
+      if (!alone) {
+        block_sums[i] = a;
+        continue;
+      }
+      auto* to = static_cast<__nv_bfloat16*>(4 * i < K ? p.dw : p.db);
+      if (to != nullptr)
+        *reinterpret_cast<uint2*>(to + (4 * i < K ? 4 * i : 4 * i - K)) = make_uint2(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w));
     }
   }
 }
@@ -377,7 +385,7 @@ cudaError_t launch_backward(const LayerNormBackwardLaunch& p, const RowShape& s,
   const int threads = s.tx * s.ty, stage = (p.dr != nullptr ? 3 : 2) * V * threads * 16;
   const int fit = static_cast<int>(kRingMost) / stage, stages = fit < kMaxStages ? fit : kMaxStages;
   size_t smem = static_cast<size_t>(stages) * stage;
-  if (SUMS && s.ty > 1) {
+  if (SUMS) {
     const size_t sums = static_cast<size_t>(s.ty) * 2 * static_cast<size_t>(p.K) * 4;
     if (sums > smem) smem = sums;
   }
@@ -395,6 +403,11 @@ cudaError_t launch_backward_as(const LayerNormBackwardLaunch& p, const RowShape&
   return p.K == 8 * V * s.tx ? launch_backward<V, SUMS, true>(p, s, blocks, stream)
                              : launch_backward<V, SUMS, false>(p, s, blocks, stream);
 }
+
+// A second kernel for the blocks' sums takes as long as two rows after one another (2 us;
+// and another launch on the host): so many stay in one block.  (A cluster of 8 blocks for eight
+// times as many was slower: 7.0 us for 5.6 with 16 x 4096.)
+bool one_block(int64_t M, const RowShape& s) { return M <= static_cast<int64_t>(s.ty) * kRowsAlone; }
 
 int backward_blocks(int64_t M, const RowShape& s) {
   const int64_t want = ceil_div(M, s.ty);
@@ -414,7 +427,8 @@ cudaError_t launch_layer_norm(const LayerNormLaunch& p, int sms, cudaStream_t st
 
 size_t layer_norm_backward_workspace(int64_t M, int64_t K) {
   if (K > kFusedCols) return column_pass_workspace(M, K, 2);
-  return static_cast<size_t>(backward_blocks(M, backward_shape(K))) * 2 * static_cast<size_t>(K) * 4;
+  const RowShape s = backward_shape(K);
+  return one_block(M, s) ? 0 : static_cast<size_t>(backward_blocks(M, s)) * 2 * static_cast<size_t>(K) * 4;
 }
 
 cudaError_t launch_layer_norm_backward(const LayerNormBackwardLaunch& p, cudaStream_t stream) {
@@ -422,8 +436,9 @@ cudaError_t launch_layer_norm_backward(const LayerNormBackwardLaunch& p, cudaStr
   const int blocks = backward_blocks(p.M, s);
   const bool sums = p.dw != nullptr || p.db != nullptr;
   if (sums && p.K <= kFusedCols) {
-    const cudaError_t e = launch_backward_as<2, true>(p, s, blocks, stream);
-    return e != cudaSuccess ? e : launch_column_sums(p.part, blocks, p.K, p.dw, p.db, stream);
+    const bool alone = one_block(p.M, s);
+    const cudaError_t e = launch_backward_as<2, true>(p, s, alone ? 1 : blocks, stream);
+    return e != cudaSuccess || alone ? e : launch_column_sums(p.part, blocks, p.K, p.dw, p.db, stream);
   }
   const cudaError_t e = s.v == 2   ? launch_backward_as<2, false>(p, s, blocks, stream)
                         : s.v == 4 ? launch_backward_as<4, false>(p, s, blocks, stream)

@@ -73,12 +73,6 @@ __device__ __forceinline__ uint32_t upper_halves(float2 v) {
   return __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x7632);
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
-
 // T[m][j] = sum_k x[m,k] a[j,k]: 16 adapter rows a cluster, K over its blocks and
 // their 16 warps, 8 NT tokens.  4 us for one token (r = 64, K = 4096), 8 us for 32, most of it
 // latency: the main kernel starts beside it and needs T only at its end.

@@ -346,11 +346,9 @@ int lynx_layer_norm_backward(const void* dY, const void* X, const float* mean, c
   if (any_misaligned(dY, X, mean, rstd, weight, dR, dX, dweight, dbias, workspace)) return LYNX_ERR_MISALIGNED;
   const bool sums = dweight != nullptr || dbias != nullptr;
   const size_t need = sums ? lynx_layer_norm_backward_workspace_bytes(M, K) : 0;
-  if (sums) {
-    if (workspace == nullptr) return LYNX_ERR_INVALID_ARG;
-    if (workspace_bytes < need) return LYNX_ERR_WORKSPACE_TOO_SMALL;
-  }
-  const Span ws = {sums ? workspace : nullptr, need}, dw = {dweight, bytes_of(1, K, 2)}, db = {dbias, bytes_of(1, K, 2)};
+  if (need != 0 && workspace == nullptr) return LYNX_ERR_INVALID_ARG;
+  if (workspace_bytes < need) return LYNX_ERR_WORKSPACE_TOO_SMALL;
+  const Span ws = {need != 0 ? workspace : nullptr, need}, dw = {dweight, bytes_of(1, K, 2)}, db = {dbias, bytes_of(1, K, 2)};
   if (any_overlap({{dX, bytes_of(M, K, 2)}, dw, db, ws},
                   {{dY, bytes_of(M, K, 2)},
                    {X, bytes_of(M, K, 2)},
@@ -371,7 +369,7 @@ int lynx_layer_norm_backward(const void* dY, const void* X, const float* mean, c
   p.dx = dX;
   p.dw = dweight;
   p.db = dbias;
-  p.part = static_cast<float*>(workspace);
+  p.part = need != 0 ? static_cast<float*>(workspace) : nullptr;
   p.M = M;
   p.K = K;
   return status_of(launch_layer_norm_backward(p, static_cast<cudaStream_t>(stream)));
@@ -391,11 +389,9 @@ int lynx_act_backward(const void* dY, const void* Z, int64_t M, int64_t N, int a
   if (!rows_ok(M) || !n_ok(N)) return LYNX_ERR_UNSUPPORTED_SHAPE;
   if (any_misaligned(dY, Z, dZ, dbias, workspace)) return LYNX_ERR_MISALIGNED;
   const size_t need = dbias != nullptr ? lynx_act_backward_workspace_bytes(M, N) : 0;
-  if (dbias != nullptr) {
-    if (workspace == nullptr) return LYNX_ERR_INVALID_ARG;
-    if (workspace_bytes < need) return LYNX_ERR_WORKSPACE_TOO_SMALL;
-  }
-  const Span ws = {dbias != nullptr ? workspace : nullptr, need}, db = {dbias, bytes_of(1, N, 2)};
+  if (need != 0 && workspace == nullptr) return LYNX_ERR_INVALID_ARG;
+  if (workspace_bytes < need) return LYNX_ERR_WORKSPACE_TOO_SMALL;
+  const Span ws = {need != 0 ? workspace : nullptr, need}, db = {dbias, bytes_of(1, N, 2)};
   const Span dy = {dY, bytes_of(M, N, 2)}, z = {Z, bytes_of(M, N, 2)};
   if (any_overlap({{dZ, bytes_of(M, N, 2)}, db, ws}, {z}) || any_overlap({db, ws}, {dy}) ||
       (dZ != dY && any_overlap({{dZ, bytes_of(M, N, 2)}}, {dy})))
@@ -406,7 +402,7 @@ int lynx_act_backward(const void* dY, const void* Z, int64_t M, int64_t N, int a
   p.z = Z;
   p.dz = dZ;
   p.out0 = dbias;
-  p.part = dbias != nullptr ? static_cast<float*>(workspace) : nullptr;
+  p.part = need != 0 ? static_cast<float*>(workspace) : nullptr;
   p.M = M;
   p.N = N;
   return status_of(launch_act_backward(p, act, static_cast<cudaStream_t>(stream)));

@@ -80,6 +80,27 @@ cudaError_t launch_after_previous(void (*kernel)(Params...), dim3 grid, dim3 blo
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
+// The same in clusters of `cluster` blocks (the grid a multiple of it in each dimension)
+template <typename... Params, typename... Args>
+cudaError_t launch_clusters_after_previous(void (*kernel)(Params...), dim3 grid, dim3 block, dim3 cluster, size_t smem,
+                                           cudaStream_t stream, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster.x;
+  attr[1].val.clusterDim.y = cluster.y;
+  attr[1].val.clusterDim.z = cluster.z;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
 cudaError_t launch_sparsify(const SparsifyLaunch& p, cudaStream_t stream);
 int choose_sparsify_split(int64_t M, int64_t K, int num_sms);
 size_t sparsify_smem_bytes(int mode, int r);
@@ -242,7 +263,7 @@ struct LayerNormBackwardLaunch {
   void* dx;           // [M,K] bf16
   void* dw;           // [K] bf16, or null
   void* db;           // [K] bf16, or null
-  float* part;        // workspace (with dw or db)
+  float* part;        // workspace (with dw or db, where it has any bytes)
   int64_t M, K;
 };
 size_t layer_norm_backward_workspace(int64_t M, int64_t K);
@@ -257,7 +278,7 @@ struct ColumnPassLaunch {
   void* dz;           // [M,N] bf16 (activation)
   void* out0;         // [N] bf16: the bias's gradient, or layer norm's weight's, or null
   void* out1;         // [N] bf16: layer norm's bias's, or null
-  float* part;        // workspace; null: no sums
+  float* part;        // workspace (with out0 or out1, where it has any bytes)
   int64_t M, N;
 };
 size_t column_pass_workspace(int64_t M, int64_t N, int sums);

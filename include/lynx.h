@@ -495,7 +495,7 @@ LYNX_API int lynx_sparsify_backward_meta(const void* G, const void* q, const voi
 
 /* ---- the activation's backward pass --------------------------------------- */
 
-/* Bytes of the workspace lynx_act_backward needs where dbias is wanted. */
+/* Bytes of the workspace lynx_act_backward needs where dbias is wanted; 0 for few rows. */
 LYNX_API size_t lynx_act_backward_workspace_bytes(int64_t M, int64_t N);
 
 /* dZ = dY act'(Z) [M,N], dbias = sum over the rows of dZ [N]; all bf16, rounded once
@@ -509,7 +509,8 @@ LYNX_API size_t lynx_act_backward_workspace_bytes(int64_t M, int64_t N);
  *   act == LYNX_ACT_NONE: dZ is dY, so Z and dZ must be NULL and dbias is what is
  *     computed; else LYNX_ERR_INVALID_ARG.
  *   Any M >= 1, N % 8 == 0.  workspace: device scratch of workspace_bytes >=
- *   lynx_act_backward_workspace_bytes(M,N), needed with dbias only. */
+ *   lynx_act_backward_workspace_bytes(M,N), needed with dbias only (NULL where it has no
+ *   bytes). */
 LYNX_API int lynx_act_backward(const void* dY, const void* Z, int64_t M, int64_t N, int act, void* dZ,
                                void* dbias, void* workspace, size_t workspace_bytes, void* stream);
 
@@ -522,8 +523,9 @@ LYNX_API int lynx_act_backward(const void* dY, const void* Z, int64_t M, int64_t
  *
  * weight and bias [K] bf16, each or NULL (1 and 0).  Statistics in fp32, the mean
  * taken off before anything is squared; Y is rounded once.  A row's squares must stay
- * inside fp32 (|x - mu| below 2^63 / sqrt(K)).  A row with an infinity or a NaN gives
- * NaN in that row alone.  M >= 1; 8 <= K <= LYNX_LAYER_NORM_MAX_COLS with K % 8 == 0.
+ * inside fp32 (|x - mu| below 2^63 / sqrt(K)); those below its range count as 0.  A row
+ * with an infinity or a NaN gives NaN in that row of Y and dX (and in dweight, which sums
+ * over the rows).  M >= 1; 8 <= K <= LYNX_LAYER_NORM_MAX_COLS with K % 8 == 0.
  * Buffers that a call of this section writes overlap no other of its buffers, but
  * where it says so (else LYNX_ERR_INVALID_ARG). */
 #define LYNX_LAYER_NORM_MAX_COLS 32768
@@ -538,7 +540,7 @@ LYNX_API int lynx_layer_norm(const void* X, const void* weight, const void* bias
                              float eps, void* Y, float* mean, float* rstd, void* stream);
 
 /* Bytes of the workspace lynx_layer_norm_backward needs where dweight or dbias is
- * wanted. */
+ * wanted; 0 for few rows. */
 LYNX_API size_t lynx_layer_norm_backward_workspace_bytes(int64_t M, int64_t K);
 
 /* With xh = (x - mean) rstd and g = dY weight, the means over K:
@@ -552,7 +554,8 @@ LYNX_API size_t lynx_layer_norm_backward_workspace_bytes(int64_t M, int64_t K);
  *   wanted).  All bf16, rounded once; sums in fp32 in an order that only the shape
  *   fixes (equal calls give equal bits).
  *   workspace: device scratch of workspace_bytes >=
- *   lynx_layer_norm_backward_workspace_bytes(M,K), needed with dweight or dbias only. */
+ *   lynx_layer_norm_backward_workspace_bytes(M,K), needed with dweight or dbias only (NULL
+ *   where it has no bytes). */
 LYNX_API int lynx_layer_norm_backward(const void* dY, const void* X, const float* mean, const float* rstd,
                                       const void* weight, const void* dR, int64_t M, int64_t K, void* dX,
                                       void* dweight, void* dbias, void* workspace, size_t workspace_bytes,

@@ -54,7 +54,7 @@ def test_layer_norm_accepts(lib):
         assert norm(lib, **kw) in OK
 
 
-def norm_backward(lib, dY=at(1), X=at(2), mean=at(3), rstd=at(4), w=at(5), dR=at(6), M=300, K=576, dX=at(7), dw=at(8), db=at(9),
+def norm_backward(lib, dY=at(1), X=at(2), mean=at(3), rstd=at(4), w=at(5), dR=at(6), M=3000, K=576, dX=at(7), dw=at(8), db=at(9),
                   ws=at(10), ws_bytes=1 << 30):
     return lib.lynx_layer_norm_backward(dY, X, mean, rstd, w, dR, M, K, dX, dw, db, ws, ws_bytes, None)
 
@@ -68,9 +68,10 @@ def test_layer_norm_backward_refusals(lib):
     for i, name in enumerate(("dY", "X", "mean", "rstd", "w", "dR", "dX", "dw", "db", "ws")):
         assert norm_backward(lib, **{name: at(i + 1, 8)}) == lynx.LYNX_ERR_MISALIGNED, name
     for K in (8, 576, 4096, 8192, 8200, 32768):
-        need = lynx.lynx_layer_norm_backward_workspace_bytes(300, K)
+        need = lynx.lynx_layer_norm_backward_workspace_bytes(3000, K)
         assert need >= 2 * K * 4
-        assert norm_backward(lib, K=K, ws_bytes=need - 1) == lynx.LYNX_ERR_WORKSPACE_TOO_SMALL
+        assert norm_backward(lib, M=3000, K=K, ws_bytes=need - 1) == lynx.LYNX_ERR_WORKSPACE_TOO_SMALL
+        assert lynx.lynx_layer_norm_backward_workspace_bytes(1, K) == 0
     for kw in (dict(dX=at(1)), dict(dX=at(2)), dict(dX=at(5)), dict(dX=at(6, 16)), dict(dw=at(9)), dict(dw=at(6)), dict(db=at(6)),
                dict(ws=at(6)), dict(ws=at(7)), dict(db=at(5)), dict(dw=at(3)), dict(dY=at(6), dX=at(6)), dict(X=at(6), dX=at(6))):
         assert norm_backward(lib, **kw) == lynx.LYNX_ERR_INVALID_ARG
@@ -79,7 +80,7 @@ def test_layer_norm_backward_refusals(lib):
 @needs_no_device
 def test_layer_norm_backward_accepts(lib):
     for kw in ({}, dict(w=None), dict(dR=None), dict(dX=at(6)), dict(dw=None), dict(db=None), dict(K=32768),
-               dict(dw=None, db=None, ws=None, ws_bytes=0)):
+               dict(dw=None, db=None, ws=None, ws_bytes=0), dict(M=1, ws=None, ws_bytes=0)):
         assert norm_backward(lib, **kw) in OK
 
 
@@ -124,7 +125,7 @@ def test_linear_w4_residual_refusals(lib):
         assert few(lib, **kw) == lynx.LYNX_ERR_INVALID_ARG, kw
 
 
-def act_backward(lib, dY=at(1), Z=at(2), M=300, N=1000, act=1, dZ=at(3), db=at(4), ws=at(5), ws_bytes=1 << 30):
+def act_backward(lib, dY=at(1), Z=at(2), M=3000, N=1000, act=1, dZ=at(3), db=at(4), ws=at(5), ws_bytes=1 << 30):
     return lib.lynx_act_backward(dY, Z, M, N, act, dZ, db, ws, ws_bytes, None)
 
 
@@ -137,8 +138,9 @@ def test_act_backward_refusals(lib):
         assert lynx.lynx_act_backward_workspace_bytes(M, N) == 0
     for i, name in enumerate(("dY", "Z", "dZ", "db", "ws")):
         assert act_backward(lib, **{name: at(i + 1, 4)}) == lynx.LYNX_ERR_MISALIGNED, name
-    need = lynx.lynx_act_backward_workspace_bytes(300, 1000)
+    need = lynx.lynx_act_backward_workspace_bytes(3000, 1000)
     assert need >= 4000
+    assert lynx.lynx_act_backward_workspace_bytes(300, 1000) == 0
     assert act_backward(lib, ws_bytes=need - 1) == lynx.LYNX_ERR_WORKSPACE_TOO_SMALL
     for kw in (dict(dZ=at(2)), dict(dZ=at(1, 16)), dict(db=at(1)), dict(ws=at(1)), dict(ws=at(3)), dict(db=at(3)), dict(db=at(5)),
                dict(Z=at(1), dZ=at(1))):
@@ -147,7 +149,8 @@ def test_act_backward_refusals(lib):
 
 @needs_no_device
 def test_act_backward_accepts(lib):
-    for kw in ({}, dict(dZ=at(1)), dict(db=None, ws=None, ws_bytes=0), dict(act=0, Z=None, dZ=None)):
+    for kw in ({}, dict(dZ=at(1)), dict(db=None, ws=None, ws_bytes=0), dict(act=0, Z=None, dZ=None),
+               dict(M=300, ws=None, ws_bytes=0)):
         assert act_backward(lib, **kw) in OK, kw
 
 
