@@ -1,6 +1,9 @@
 // gemm_pair_kernel.cu -- the Lynx GEMM on CTA pairs (tcgen05 cta_group::2):
 //   Y[M,N] = bf16( act( s_row * (S(X) W^T + T' B^T) + bias ) )   (act: none or GELU)
-// and, in the variants with EXT, Y = bf16( R + act(v) ) with v itself in bf16 as Z.
+// and, in the variants with EXT, Y = bf16( R + act(v) ) with v itself in bf16 as Z.  The
+// sparse main loop draws 53 bytes a clock and SM from L2, next to what an SM can take, so
+// each tensor that the epilogue adds costs nearly its own time: 4608 x 4096 -> 12288, 210 us,
+// with R 230, with Z 229, with GELU and Z 236 (113 MB each, 17 us of the memory's).
 // Same arithmetic as gemm_kernel.cu (see there and the RT-Lynx references),
 // computed on 256 x 256 output tiles by a pair of CTAs on the two SMs of a
 // TPC: each CTA holds 128 rows of A (compressed activations, or X on the dense
@@ -745,8 +748,9 @@ lynx_gemm_pair_kernel(const __grid_constant__ GemmLaunch p) {
                 apply_act<ACT>(__fmaf_rn(s, __uint_as_float(r[c][e + 1]), sm.bias_s[col + e + 1]));
             if constexpr (EXT) {
               if (p.residual != nullptr) {
-                a += __uint_as_float(res[done & 1][i] << 16);
-                b += __uint_as_float(res[done & 1][i] & 0xFFFF0000u);
+                // (not contracted with the activation's product: the 1-CTA kernel's bits)
+                a = __fadd_rn(a, __uint_as_float(res[done & 1][i] << 16));
+                b = __fadd_rn(b, __uint_as_float(res[done & 1][i] & 0xFFFF0000u));
               }
             }
             __nv_bfloat162 hv = __floats2bfloat162_rn(a, b);

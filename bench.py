@@ -56,9 +56,12 @@ DRAM_TRAFFIC = {
                  "bytes": {"mlp_up": 28733696, "attn_out": 25589248, "mlp_down": 145459968}},
 }
 
-def uses_pair_gemm(M, N, K):
-    """The library's choice: the CTA-pair GEMM unless the shape cannot feed it."""
-    return M > 128 and N >= 256 and K % 128 == 0
+def uses_pair_gemm(M, N, K, sparse=True, sms=148):
+    """The library's choice: the CTA-pair GEMM unless the shape cannot feed it, or its
+    128 x 128 tiles come out at one an SM (a long K on the sparse path aside)."""
+    if not (M > 128 and N >= 256 and K % 128 == 0):
+        return False
+    return -(-M // 128) * -(-N // 128) > sms or (sparse and K > 2048)
 
 
 def launches_per_linear(M, N, K, skip=False, lora=True):
@@ -67,14 +70,14 @@ def launches_per_linear(M, N, K, skip=False, lora=True):
     the pass's partials itself, and the GEMM."""
     if skip and not lora:
         return 1
-    return 2 if uses_pair_gemm(M, N, K) else 3
+    return 2 if uses_pair_gemm(M, N, K, sparse=not skip) else 3
 
 
 def gemm_kernel_name(M, N, K):
     """Name of the GEMM kernel the library picks for a sparse call of this shape."""
     if uses_pair_gemm(M, N, K):
         return "lynx_gemm_pair_kernel<1> (CTA pair, 256x256 tiles)"
-    return f"lynx_gemm_kernel<{256 if N >= 1024 else 128},1>"
+    return "lynx_gemm_kernel<BN,1> (one CTA, 128 x BN tiles)"
 
 
 def parse_args(argv=None):

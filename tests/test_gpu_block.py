@@ -9,6 +9,10 @@ dX is 0.01 of its norm off at widths of 1024 (0.005 at 4096, as 1 / sqrt(K)) eac
 2^-8 and 0.02, 0.071.  An adapter's A gradient sums over checkpoint values that are off by
 2^-4 at most (rms below 2^-4 / sqrt(3) = 0.036) beside the same chain: 0.11.
 """
+import subprocess
+import sys
+from pathlib import Path
+
 import pytest
 import torch
 
@@ -171,3 +175,42 @@ def test_refusals():
         MlpBlock((None, None), layer(2056, 1024, 16, 1, False), layer(1024, 2056, 16, 2, False))
     with pytest.raises(ValueError):
         MlpBlock((None, None), up, down).forward(normal((4, 512), 1, 1.0))
+
+
+FIRST = """
+import torch
+from activation_sparse_gemm_lynx_b200 import lynx
+torch.manual_seed(1)
+def r(*s):
+    return torch.randn(*s, device="cuda").bfloat16()
+cases = []
+for M, K, N in ((40, 256, 136), (700, 1024, 4096), (9, 12288, 64)):
+    cases.append((r(M, K), r(N, K), r(N), r(16, K), r(N, 16), r(M, N), r(K), r(M, K), r(M, N)))
+def step():
+    out = []
+    for X, W, bias, A, B, R, w, dX, dY in cases:
+        Y, mean, rstd = lynx.lynx_layer_norm(X, w, want_stats=True)
+        P, Z = lynx.lynx_linear_residual(Y, W, bias, A, B, R=R, act=lynx.LYNX_ACT_GELU_TANH, want_Z=True)
+        D, _ = lynx.lynx_linear_residual(Y, W, bias, R=R, skip_sparsify=True)
+        dZ, db = lynx.lynx_act_backward(dY, Z)
+        _, db2 = lynx.lynx_act_backward(dY, act=lynx.LYNX_ACT_NONE)
+        out += [Y, mean, rstd, P, Z, D, dZ, db, db2, *lynx.lynx_layer_norm_backward(dX, X, mean, rstd, w, dR=X)]
+    return out
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = step()
+for t in got:
+    t.view(torch.uint8).fill_(0x5A)
+graph.replay()
+torch.cuda.synchronize()
+want = step()
+assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(got, want))
+assert lynx.lynx_check_error()[0] == lynx.LYNX_OK
+print("equal")
+"""
+
+
+def test_first_calls_of_a_process_in_a_capture():
+    run = subprocess.run([sys.executable, "-c", FIRST], cwd=Path(__file__).resolve().parent.parent, timeout=300,
+                         capture_output=True, text=True)
+    assert run.returncode == 0 and "equal" in run.stdout, run.stdout + run.stderr

@@ -179,3 +179,70 @@ def test_residual_offsets_past_32_bits():
     Y, _ = lynx.lynx_linear_residual(X, W, bias, R=R, skip_sparsify=True)
     for rows in (slice(0, 200), slice(M - 200, M)):
         oracle.check(Y[rows], oracle.linear_residual(X[rows], W, bias, None, None, R[rows], True, False)["Y"], "Y")
+
+
+@pytest.mark.parametrize("M,N,K", [(300, 512, 576), (600, 4096, 512)])  # the 1-CTA kernel and the CTA pairs
+def test_a_stalled_call_gives_up_and_the_next_one_works(M, N, K):
+    X, W, bias, A, B = layer(M, N, K, 16, seed=6)
+    R = normal((M, N), 9)
+    want, wz = lynx.lynx_linear_residual(X, W, bias, A, B, R=R, want_Z=True)
+    assert lynx.lynx_check_error() == (lynx.LYNX_OK, 0)
+    lynx.lynx_debug_set_stall(True)
+    try:
+        lynx.lynx_linear_residual(X, W, bias, A, B, R=R, want_Z=True)
+        status, code = lynx.lynx_check_error()
+    finally:
+        lynx.lynx_debug_set_stall(False)
+    assert status == lynx.LYNX_ERR_DEVICE_TIMEOUT and code != 0
+    Y, Z = lynx.lynx_linear_residual(X, W, bias, A, B, R=R, want_Z=True)
+    assert lynx.lynx_check_error() == (lynx.LYNX_OK, 0)
+    assert torch.equal(Y, want) and torch.equal(Z, wz)
+
+
+def test_either_gemm_kernel_gives_the_same_bits():
+    """Rows of a problem that the CTA pairs take, alone, where the 1-CTA kernel takes them with tiles of 32 to 128
+    columns.  Dense and without an adapter nothing but the GEMM is in between: equal bits."""
+    M, N, K = 2304, 2048, 512
+    X, W, bias, _, _ = layer(M, N, K, 0, seed=7)
+    R = normal((M, N), 9)
+    for act in (NONE, GELU):
+        Y, Z = lynx.lynx_linear_residual(X, W, bias, R=R, skip_sparsify=True, act=act, want_Z=True)
+        for r0, r1 in ((0, 1), (0, 128), (256, 512), (1000, 1900)):
+            y, z = lynx.lynx_linear_residual(X[r0:r1], W, bias, R=R[r0:r1], skip_sparsify=True, act=act, want_Z=True)
+            assert torch.equal(y, Y[r0:r1]) and torch.equal(z, Z[r0:r1])
+
+
+def test_two_host_threads_on_two_streams():
+    """Both at once, each on its own stream with its own buffers: what each gives alone."""
+    import threading
+
+    X, W, bias, A, B = layer(700, 1024, 512, 16, seed=8)
+    R, dY = normal((700, 1024), 9), normal((700, 1024), 10)
+    w = normal((1024,), 11)
+
+    def step():
+        Y, Z = lynx.lynx_linear_residual(X, W, bias, A, B, R=R, act=GELU, want_Z=True)
+        N, mean, rstd = lynx.lynx_layer_norm(Y, w, want_stats=True)
+        dZ, db = lynx.lynx_act_backward(dY, Z)
+        return (Y, Z, N, dZ, db, *lynx.lynx_layer_norm_backward(dZ, Y, mean, rstd, w, dR=dY))
+
+    want = step()
+    torch.cuda.synchronize()
+    bad = []
+
+    def work():
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(20):
+                got = step()
+            torch.cuda.current_stream().synchronize()
+            if not all(torch.equal(a, b) for a, b in zip(got, want)):
+                bad.append("different")
+            if lynx.lynx_check_error()[0] != lynx.LYNX_OK:
+                bad.append("error")
+
+    threads = [threading.Thread(target=work) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
