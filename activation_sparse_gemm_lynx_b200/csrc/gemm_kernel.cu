@@ -26,8 +26,8 @@
 //               (two warps per TMEM lane quarter, half of the columns each).
 // Accumulators: 1 TMEM buffer for BN = 256, 2 (double buffered) below.
 //
-// 20 rows of 4096 -> 4096, dense: 15.5 us, 33.5 MB of W (5.1 us); 64 rows of 2048 -> 1000
-// 8.7 us.  Bound by the MMA warp: a stage's wait, election and commit take it about 300
+// 20 rows of 4096 -> 4096, dense: 15.6 us, 33.5 MB of W (5.1 us); 64 rows of 2048 -> 1000
+// 8.6 us.  Bound by the MMA warp: a stage's wait, election and commit take it about 300
 // cycles beside 8 MMAs of 40.
 #include <cuda_bf16.h>
 
@@ -50,7 +50,8 @@ struct Cfg {
   // K-steps of 64 a stage.  A wait and a commit take the MMA warp about as long as the
   // MMAs of four steps; at 256 columns two steps would leave two stages.
   static constexpr int kSub = BN == 256 ? 1 : 2;
-  static constexpr uint32_t kABytes = SPARSE ? 128u * 64u : 128u * 128u;  // one k-step of A
+  static constexpr uint32_t kARowBytes = SPARSE ? 64u : 128u;             // a row of one k-step of A
+  static constexpr uint32_t kABytes = 128u * kARowBytes;
   static constexpr uint32_t kBBytes = static_cast<uint32_t>(BN) * 128u;   // BN rows x 64 dense K
   static constexpr uint32_t kEBytes = SPARSE ? 2048u : 0u;
   static constexpr uint32_t kBOff = kSub * kABytes;                       // the steps' A, then their B, then metadata
@@ -59,7 +60,6 @@ struct Cfg {
   static constexpr int kStages = static_cast<int>((212u * 1024u) / kStageBytes);
   static constexpr int kAcc = BN > 128 ? 1 : 2;
   static constexpr uint32_t kEcol0 = static_cast<uint32_t>(kAcc * BN);
-  static constexpr uint32_t kLoraABytes = 128u * 64u;                     // T: 128 rows x 32
   static constexpr uint32_t kLoraBBytes = static_cast<uint32_t>(BN) * 64u;  // B: BN rows x 32
   static_assert(kStages >= 3, "pipeline too shallow");
   static_assert(kEcol0 + 4 * kEslots <= kTmemCols, "TMEM budget");
@@ -116,6 +116,7 @@ lynx_gemm_kernel(const __grid_constant__ GemmLaunch p) {
   const int kblocks = static_cast<int>((p.K + 127) / 128);
   const bool lora = p.lora != 0;
   const int lsteps = lora ? (p.r + 31) / 32 : 0;  // LoRA-up stages of K = 32 (zero-filled past r)
+  const uint32_t a_rows = static_cast<uint32_t>(p.a_rows);  // rows of a box of A or T: the rest of its 128 is not written
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
@@ -183,7 +184,7 @@ lynx_gemm_kernel(const __grid_constant__ GemmLaunch p) {
           const uint32_t subs = k0 + C::kSub <= nk ? C::kSub : 1u;
           const bool load_e = SPARSE && k0 % 2 == 0;
           if (elect_one()) {
-            mbar_arrive_expect_tx(&sm.full[slot], subs * (C::kABytes + C::kBBytes) + (load_e ? 2048u : 0u));
+            mbar_arrive_expect_tx(&sm.full[slot], subs * (a_rows * C::kARowBytes + C::kBBytes) + (load_e ? 2048u : 0u));
 #pragma unroll
             for (uint32_t u = 0; u < C::kSub; ++u) {
               if (u < subs) {
@@ -200,7 +201,7 @@ lynx_gemm_kernel(const __grid_constant__ GemmLaunch p) {
         } else {
           const int l = kit - nks;
           if (elect_one()) {
-            mbar_arrive_expect_tx(&sm.full[slot], C::kLoraABytes + C::kLoraBBytes);
+            mbar_arrive_expect_tx(&sm.full[slot], a_rows * 64u + C::kLoraBBytes);
             tma_load_2d(st, &p.tm_t, &sm.full[slot], l * 32, row0);
             tma_load_2d(st + C::kBOff, &p.tm_lb, &sm.full[slot], l * 32, col0);
           }

@@ -226,17 +226,12 @@ lynx_status map_cuda(cudaError_t e) { return e == cudaSuccess ? LYNX_OK : LYNX_E
 
 // Columns of a 1-CTA GEMM tile: as few (from 256 down to 32) as come out at one tile an SM at
 // most.  A few rows are bound by reading W, in which every SM has to take part: 20 tokens of
-// 4096 -> 4096, dense, 16 tiles of 256 columns 24.8 us, 128 of 32 15.5.  Sparse, the blocks of a
-// row block all read its metadata at once, and past 64 of them that costs more (128 of 32: 34 us,
-// 64 of 64: 25).
-int gemm_bn(int64_t M, int64_t N, bool sparse, int sms) {
+// 4096 -> 4096, dense, 16 tiles of 256 columns 24.8 us, 128 of 32 15.6; sparse, 64 of 64 23.2,
+// 128 of 32 22.4.
+int gemm_bn(int64_t M, int64_t N, int sms) {
   const int64_t ntm = (M + 127) / 128;
   int bn = N >= 1024 ? 256 : 128;
-  while (bn > 32) {
-    const int64_t ntn = (N + bn / 2 - 1) / (bn / 2);
-    if (ntm * ntn > sms || (sparse && bn == 64 && ntn > 64)) break;
-    bn /= 2;
-  }
+  while (bn > 32 && ntm * ((N + bn / 2 - 1) / (bn / 2)) <= sms) bn /= 2;
   return bn;
 }
 
@@ -314,15 +309,20 @@ lynx_status run_gemm(DeviceState* ds, const void* a_src, bool sparse, const void
   std::memset(&p, 0, sizeof(p));
   const bool pair = fused_x ? pair_kernel_takes(M, N, K) : use_pair_kernel(M, N, K, sparse, ds->sms);
   if (fused_x && !pair) return LYNX_ERR_UNSUPPORTED_SHAPE;
-  const int bn = pair ? 256 : gemm_bn(M, N, sparse, ds->sms);
+  const int bn = pair ? 256 : gemm_bn(M, N, ds->sms);
   const uint32_t b_rows = pair ? 128u : static_cast<uint32_t>(bn);  // W rows one CTA loads
+  // Boxes of A and T are no higher than the rows that there are, in whole 8-row swizzle atoms (the
+  // products of the tile's other rows are not stored).  Rows past M are zeros that no memory holds,
+  // but a box fetches for them all the same, and every block at once: one token of 4096 -> 4096,
+  // dense, 15.4 us for 26.6, of 16384 -> 4096 50 for 93.
+  const uint32_t a_rows = M < 128 ? static_cast<uint32_t>((M + 7) / 8 * 8) : 128u;
   if (fused_x) {
     // the dense X in 128 x 64 boxes, as on the dense path
     if (!encode_bf16_2d(&p.tm_a, a_src, K, M, K * 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B))
       return LYNX_ERR_CUDA;
   } else if (sparse) {
     // pair kernel: 128-byte rows of 64 kept values; single-CTA kernel: 64-byte rows
-    if (!encode_bf16_2d(&p.tm_a, a_src, K / 2, M, K, pair ? 64 : 32, 128,
+    if (!encode_bf16_2d(&p.tm_a, a_src, K / 2, M, K, pair ? 64 : 32, a_rows,
                         pair ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
       return LYNX_ERR_CUDA;
     // metadata blocks of 2 KB seen as 8 rows of 256 bytes
@@ -331,7 +331,7 @@ lynx_status run_gemm(DeviceState* ds, const void* a_src, bool sparse, const void
                               256, 8))
       return LYNX_ERR_CUDA;
   } else {
-    if (!encode_bf16_2d(&p.tm_a, a_src, K, M, K * 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B))
+    if (!encode_bf16_2d(&p.tm_a, a_src, K, M, K * 2, 64, a_rows, CU_TENSOR_MAP_SWIZZLE_128B))
       return LYNX_ERR_CUDA;
   }
   if (!encode_bf16_2d(&p.tm_b, W, K, N, K * 2, 64, b_rows, CU_TENSOR_MAP_SWIZZLE_128B))
@@ -340,7 +340,7 @@ lynx_status run_gemm(DeviceState* ds, const void* a_src, bool sparse, const void
   if (lora) {
     // boxes of 32 columns; for r % 32 == 16 the last box reads past r, which
     // the TMA fills with zeros (and the kernels skip that half's MMA)
-    if (!encode_bf16_2d(&p.tm_t, T, r, M, r * 2, 32, 128, CU_TENSOR_MAP_SWIZZLE_64B))
+    if (!encode_bf16_2d(&p.tm_t, T, r, M, r * 2, 32, a_rows, CU_TENSOR_MAP_SWIZZLE_64B))
       return LYNX_ERR_CUDA;
     if (!encode_bf16_2d(&p.tm_lb, B, r, N, r * 2, 32, b_rows, CU_TENSOR_MAP_SWIZZLE_64B))
       return LYNX_ERR_CUDA;
@@ -362,6 +362,7 @@ lynx_status run_gemm(DeviceState* ds, const void* a_src, bool sparse, const void
   p.sparse = sparse ? 1 : 0;
   p.lora = lora ? 1 : 0;
   p.bn = bn;
+  p.a_rows = static_cast<int>(a_rows);
   p.stall_test = g_stall.load();
   p.act = act;
   p.fused = fused_x ? 1 : 0;

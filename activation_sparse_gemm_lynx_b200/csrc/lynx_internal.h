@@ -108,9 +108,9 @@ size_t sparsify_smem_bytes(int mode, int r);
 // ---- tcgen05 GEMM with LoRA-up + bias epilogue ------------------------------
 
 struct GemmLaunch {
-  CUtensorMap tm_a;     // sparse: vals [M,K/2] box 32x128 SW64; dense: X [M,K] box 64x128 SW128
+  CUtensorMap tm_a;     // sparse: vals [M,K/2] box 32 x a_rows SW64; dense: X [M,K] box 64 x a_rows SW128
   CUtensorMap tm_b;     // W [N,K] box 64 x BN, SW128
-  CUtensorMap tm_t;     // T [M,r] box 32 x 128, SW64 (lora)
+  CUtensorMap tm_t;     // T [M,r] box 32 x a_rows, SW64 (lora)
   CUtensorMap tm_lb;    // B [N,r] box 32 x BN, SW64 (lora)
   CUtensorMap tm_e;     // metadata as uint8 [blocks*8, 256], box 256 x 8 (pair kernel)
   CUtensorMap tm_y;     // Y [M,N] bf16, box 16 x 32, 32B swizzle (pair kernel stores)
@@ -126,7 +126,8 @@ struct GemmLaunch {
   int r;                // LoRA rank (lora)
   int sparse;
   int lora;
-  int bn;               // 128 or 256
+  int bn;               // 32 to 256
+  int a_rows;           // rows of the boxes of A and T: 128, or M rounded up to 8 below (1-CTA kernel)
   int grid;             // persistent CTAs
   int group_m;          // tile rows (of 128 or of 256 for CTA pairs) per raster group
   int stall_test;

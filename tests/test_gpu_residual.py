@@ -212,6 +212,32 @@ def test_either_gemm_kernel_gives_the_same_bits():
             assert torch.equal(y, Y[r0:r1]) and torch.equal(z, Z[r0:r1])
 
 
+def test_few_rows_are_alone_in_their_tile():
+    """The rows of a tile that are not there hold what the launch before left in shared memory: NaN here.
+    The rows that are there give the bits they give among 128."""
+    M, N, K, r = 128, 1000, 640, 48
+    X, W, bias, _, B = layer(M, N, K, r, seed=9)
+    R, T = normal((M, N), 10), normal((M, r), 11)
+    vals, meta, _ = lynx.lynx_sparsify(X)
+    nan = torch.full_like(X, float("nan"))
+    nan_t = torch.full_like(T, float("nan"))
+
+    def poison():
+        lynx.lynx_linear(nan, W, skip_sparsify=True)
+        lynx.lynx_sparse_gemm(torch.full_like(vals, float("nan")), meta, W, T=nan_t, B=B)
+
+    dense, Z = lynx.lynx_linear_residual(X, W, bias, R=R, skip_sparsify=True, act=GELU, want_Z=True)
+    sparse = lynx.lynx_sparse_gemm(vals, meta, W, bias, T=T, B=B)
+    assert torch.isfinite(sparse.float()).all()
+    for m in (1, 7, 8, 9, 64, 100, 127):
+        poison()
+        y, z = lynx.lynx_linear_residual(X[:m], W, bias, R=R[:m], skip_sparsify=True, act=GELU, want_Z=True)
+        assert torch.equal(y, dense[:m]) and torch.equal(z, Z[:m]), m
+        poison()
+        assert torch.equal(lynx.lynx_sparse_gemm(vals[:m], meta, W, bias, T=T[:m], B=B), sparse[:m]), m
+    assert lynx.lynx_check_error() == (lynx.LYNX_OK, 0)
+
+
 def test_two_host_threads_on_two_streams():
     """Both at once, each on its own stream with its own buffers: what each gives alone."""
     import threading
