@@ -672,7 +672,8 @@ lynx_gemm_pair_kernel(const __grid_constant__ GemmLaunch p) {
       }
       // The residual of this lane's row: the first 16 columns now, while the tile's MMAs
       // run, each further 16 two steps ahead of their use
-      const int left = EXT && row_ok ? static_cast<int>(p.N - n_base) - static_cast<int>(ch) * kHalf : 0;  // columns from the warp's first on
+      // columns from the warp's first on
+      const int left = EXT && row_ok ? static_cast<int>(p.N - n_base) - static_cast<int>(ch) * kHalf : 0;
       const int64_t at = EXT ? grow * p.N + n_base + ch * kHalf : 0;
       uint32_t res[2][8];
       auto fetch = [&](int i) {

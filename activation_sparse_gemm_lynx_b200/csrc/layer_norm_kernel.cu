@@ -9,14 +9,18 @@
 // Both are bound by memory: each tensor moves once.  A row belongs to a group of
 // tx threads, which own its 16-byte pieces t, t + tx, ... and keep them in
 // registers from the first sum to the result (the mean is taken off before
-// anything is squared).  Rows come through a ring of cp.async copies a few rows
-// deep; a thread copies what it will read itself, so the ring needs no barrier,
-// and what is left between the threads of a row is the two sums.
+// anything is squared).  Rows come through shared memory by cp.async, forward one
+// ahead of the row at work, backward in a ring of up to kMaxStages; a thread copies
+// what it will read itself, so that no barrier is needed, and what is left between
+// the threads of a row is the two sums.
 //
 // dw and db: each thread adds up its columns over the block's rows, the blocks'
 // sums go to the workspace and launch_column_sums adds them in the order of the
-// blocks.  Few rows are one block, whose sums are the result.  2 x 8 fp32 sums a piece fit in registers up to kFusedCols columns; wider
-// rows read dY and X once more, by columns (column_pass_kernel.cu).
+// blocks.  Few rows are one block, whose sums are the result.  2 x 8 fp32 sums a
+// piece fit in registers up to kFusedCols columns; wider rows read dY and X once
+// more, by columns (column_pass_kernel.cu).
+//
+// 4608 x 4096: forward 13.8 us for 75.5 MB, backward with dr, dw and db 30.1 for 151.
 #include <cuda_bf16.h>
 
 #include "lynx_f32x2.cuh"

@@ -36,8 +36,8 @@ __device__ __forceinline__ void load_row16(uint32_t (&v)[8], const __nv_bfloat16
 __device__ __forceinline__ void store_row16(__nv_bfloat16* at, const uint32_t (&v)[8], int left, bool wide) {
   if (wide) {
     if (left > 0)
-      asm volatile("st.global.L1::no_allocate.L2::evict_first.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-                   "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+      asm volatile("st.global.L1::no_allocate.L2::evict_first.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at),
+                   "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                    : "memory");
   } else {
 #pragma unroll
