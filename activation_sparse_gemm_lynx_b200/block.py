@@ -10,8 +10,8 @@ their epilogues, and for a training step the 8-bit checkpoints of X and H, the
 selections the forward pass made and Z, from which ``backward`` takes every
 gradient.  ``forward_few`` serves up to 32 tokens on the weights in 4 bits.
 
-Everything runs on the current stream.  The one workspace is the block's own: two
-steps of one block must not overlap.
+Everything runs on the current stream, captured or not.  Nothing is kept from one
+step for the next but the layouts of W.
 """
 from . import lynx
 
@@ -36,23 +36,16 @@ class MlpBlock:
             layer.setdefault("skip", False)
             layer["Wt"] = None  # W^T, laid out once before the first backward pass
             layer["w4"] = None
-        self._workspace = None
-
-    def _room(self, M):
-        import torch
-
-        need = 0
-        for layer in (self.up, self.down):
-            N, K = layer["W"].shape
-            r = layer["A"].shape[0] if layer["A"] is not None else lynx.lynx_lora_rank()
-            need = max(need, lynx.lynx_workspace_bytes(M, N, K, r))
-        if self._workspace is None or self._workspace.numel() < need:
-            self._workspace = torch.empty(need, dtype=torch.uint8, device=self.up["W"].device)
-        return self._workspace
 
     def _layer(self, layer, X, keep, **kw):
         """One layer's Y and Z, and what its backward pass needs."""
-        ws = self._room(X.shape[0])
+        import torch
+
+        ws = None
+        if keep and not layer["skip"]:  # the selection is taken from it
+            r = layer["A"].shape[0] if layer["A"] is not None else 0
+            ws = torch.empty(lynx.lynx_workspace_bytes(X.shape[0], *layer["W"].shape, r), dtype=torch.uint8,
+                             device=X.device)
         Y, Z = lynx.lynx_linear_residual(X, layer["W"], layer["bias"], layer["A"], layer["B"],
                                          skip_sparsify=layer["skip"], workspace=ws, **kw)
         if not keep:
@@ -72,19 +65,30 @@ class MlpBlock:
         return out, (h, mean, rstd, up, down)
 
     @staticmethod
-    def _layer_backward(layer, dP, q, e, meta, want):
+    def _transposed(layer):
+        import torch
+
+        if layer["Wt"] is not None:
+            return layer["Wt"]
+        Wt = layer["W"].t().contiguous()
+        if not torch.cuda.is_current_stream_capturing():  # a capture's is the graph's, filled when it is replayed
+            torch.cuda.current_stream().synchronize()  # once: later steps may be on other streams
+            layer["Wt"] = Wt
+        return Wt
+
+    @classmethod
+    def _layer_backward(cls, layer, dP, q, e, meta, want):
         """dX of one layer from the gradient of P, and the adapter's gradients into ``want``."""
-        if layer["Wt"] is None:
-            layer["Wt"] = layer["W"].t().contiguous()
+        Wt = cls._transposed(layer)
         A, B = layer["A"], layer["B"]
         dT = None
         if A is not None:
             want["A"], want["B"], dT = lynx.lynx_lora_backward(dP, q, e, A, B)
         if layer["skip"]:
             if A is None:
-                return lynx.lynx_linear_dense(dP, layer["Wt"])
-            return lynx.lynx_linear_dense(dP, layer["Wt"], None, B.t().contiguous(), A.t().contiguous())
-        G = lynx.lynx_linear_dense(dP, layer["Wt"])
+                return lynx.lynx_linear_dense(dP, Wt)
+            return lynx.lynx_linear_dense(dP, Wt, None, B.t().contiguous(), A.t().contiguous())
+        G = lynx.lynx_linear_dense(dP, Wt)
         return lynx.lynx_sparsify_backward(G, q, e, dT, A, meta=meta)
 
     def backward(self, saved, dout):

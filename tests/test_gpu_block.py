@@ -138,6 +138,35 @@ def test_a_captured_training_step():
         assert torch.equal(x, y)
 
 
+def test_a_block_whose_first_step_is_captured():
+    """The first backward pass lays out W^T: in a capture that is the graph's alone, and eager steps before and
+    after a replay, of more rows too, neither read it nor move what the graph writes to."""
+    b, plain = block(K=512, F=1024), block(K=512, F=1024)
+    h, dout = normal((200, 512), 3, 1.0), normal((200, 512), 4, 1e-2)
+    H, dOut = normal((900, 512), 5, 1.0), normal((900, 512), 6, 1e-2)
+
+    def step(b, h, dout):
+        out, saved = b.forward(h, train=True)
+        dh, grads = b.backward(saved, dout)
+        return [out, dh, grads["up"]["A"], grads["down"]["B"]]
+
+    want, more = step(plain, h, dout), step(plain, H, dOut)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(b, h, dout)
+    for x, y in zip(step(b, H, dOut), more):  # before any replay
+        assert torch.equal(x, y)
+    hold = [torch.zeros(1 << 20, device="cuda") for _ in range(16)]  # whatever is free
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(not t.any() for t in hold)
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)
+    for x, y in zip(step(b, H, dOut), more):
+        assert torch.equal(x, y)
+
+
 def test_another_stream_gives_the_same():
     b = block(K=512, F=1024)
     h, dout = normal((200, 512), 3, 1.0), normal((200, 512), 4, 1e-2)
