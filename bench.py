@@ -42,18 +42,18 @@ FALLBACK_PEAKS = {"hbm_gbs": 6650.0, "bf16_tflops": 1590.0, "bf16_tflops_sustain
 # sources still hash the same, else null ("stale").
 # The sources each kernel's launch depends on (the host code sets its grid and raster).
 KERNEL_SOURCES = {
-    "gemm": ("gemm_pair_kernel.cu", "lynx_ptx.cuh", "lynx_internal.h", "lynx_act.cuh", "lynx_select.cuh",
-             "lynx_api.cu"),
+    "gemm": ("gemm_pair_kernel.cu", "lynx_rows.cuh", "lynx_ptx.cuh", "lynx_internal.h", "lynx_act.cuh",
+             "lynx_select.cuh", "lynx_api.cu"),
     "sparsify": ("sparsify_kernel.cu", "lynx_select.cuh", "lynx_ptx.cuh", "lynx_internal.h", "lynx_api.cu"),
 }
 # dram__bytes_read.sum + dram__bytes_write.sum per launch from one ncu capture per
 # workload (profile_layer, L2 flushed before the call), stamped with the hash of
 # the kernel's sources at capture; reported only while the sources still hash so.
 DRAM_TRAFFIC = {
-    "gemm": {"src": "b2df0e86ed85", "captured": "2026-12-06",
-             "bytes": {"mlp_up": 181327360, "attn_out": 42262272, "mlp_down": 308163328}},
-    "sparsify": {"src": "eeb6bcc09ae5", "captured": "2026-12-06",
-                 "bytes": {"mlp_up": 28733696, "attn_out": 25589248, "mlp_down": 145459968}},
+    "gemm": {"src": "5330e20f9581", "captured": "2026-12-09",
+             "bytes": {"mlp_up": 181745152, "attn_out": 42383104, "mlp_down": 308182784}},
+    "sparsify": {"src": "4f0fb003cefe", "captured": "2026-12-09",
+                 "bytes": {"mlp_up": 28734208, "attn_out": 25588224, "mlp_down": 145707520}},
 }
 
 def uses_pair_gemm(M, N, K, sparse=True, sms=148):
