@@ -69,7 +69,7 @@ ColumnPlan column_plan(int64_t M, int64_t N, bool sums) {
   return c;
 }
 
-// d gelu / dz of a pair.  Beyond |z| = 16 it is 0 or 1 in fp32: cut off there, z^2 stays finite.
+// d gelu / dz of a pair.  Beyond |z| = 16 it is 0 or 1 in fp32: cut off there, z^2 stays finite (clamp16).
 __device__ __forceinline__ f32x2 gelu_tanh_slope(f32x2 z) {
   const f32x2 one = both(1.f), q = mul2(z, z);
   const float2 x = halves(mul2(z, fma2(q, both(-2.3022081981f * 0.044715f), both(-2.3022081981f))));  // -a log2 e
@@ -84,10 +84,12 @@ __device__ __forceinline__ f32x2 gelu_tanh_slope(f32x2 z) {
   return fma2(u, mul2(s, fma2(s, both(-1.f), one)), s);
 }
 
+// An infinity has no slope (GELU of -inf is NaN): 0 v is NaN there and adds nothing to a finite v's.
 __device__ __forceinline__ uint32_t clamp16(uint32_t pair) {
-  __nv_bfloat162 v = *reinterpret_cast<__nv_bfloat162*>(&pair);
-  v = __hmin2_nan(__hmax2_nan(v, __floats2bfloat162_rn(-16.f, -16.f)), __floats2bfloat162_rn(16.f, 16.f));
-  return *reinterpret_cast<uint32_t*>(&v);
+  const __nv_bfloat162 v = *reinterpret_cast<__nv_bfloat162*>(&pair);
+  __nv_bfloat162 c = __hmin2_nan(__hmax2_nan(v, __floats2bfloat162_rn(-16.f, -16.f)), __floats2bfloat162_rn(16.f, 16.f));
+  c = __hfma2(v, __floats2bfloat162_rn(0.f, 0.f), c);
+  return *reinterpret_cast<uint32_t*>(&c);
 }
 
 template <int MODE>

@@ -505,7 +505,8 @@ LYNX_API size_t lynx_act_backward_workspace_bytes(int64_t M, int64_t N);
  * take as dY; dbias is the bias's; R's is dY itself.
  *   act == LYNX_ACT_GELU_TANH: Z and dZ are given; dZ may be dY itself; dbias may be
  *     NULL (not wanted).  The derivative is that of LYNX_ACT_GELU_TANH's formula, with
- *     the same hardware approximations (a few fp32 ulps).
+ *     the same hardware approximations (a few fp32 ulps).  Where Z is an infinity or a NaN
+ *     the derivative is NaN, and dZ and the column's dbias with it.
  *   act == LYNX_ACT_NONE: dZ is dY, so Z and dZ must be NULL and dbias is what is
  *     computed; else LYNX_ERR_INVALID_ARG.
  *   Any M >= 1, N % 8 == 0.  workspace: device scratch of workspace_bytes >=

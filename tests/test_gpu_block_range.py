@@ -1,0 +1,33 @@
+"""Layer norm, the residual epilogue and the activation's gradient at the ends of their ranges."""
+import pytest
+import torch
+
+from activation_sparse_gemm_lynx_b200 import lynx
+
+pytestmark = pytest.mark.gpu
+
+BF = torch.bfloat16
+
+
+def normal(shape, seed, std=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(shape, generator=g, device="cuda") * std).to(BF)
+
+
+@pytest.mark.parametrize("M,N", [(300, 1000), (4608, 256)])  # a cluster's sums, and sums through the workspace
+def test_an_infinite_z_has_no_slope(M, N):
+    """GELU's derivative is NaN at either infinity by its formula (and GELU of -inf is NaN), so a row that
+    diverged does not send finite gradients back.  Everything else keeps its bits."""
+    dY, Z = normal((M, N), 1), normal((M, N), 2)
+    Z[0, 0], Z[5, 1], Z[M - 1, N - 2], Z[7, 64] = 3e38, -3e38, -16.0, 16.0  # finite: 0 or 1
+    want, wb = lynx.lynx_act_backward(dY, Z)
+    assert torch.isfinite(want).all() and float(want[0, 0]) == float(dY[0, 0]) and float(want[5, 1]) == 0.0
+    places = [(0, 8, "inf"), (0, 9, "-inf"), (M // 2, 63, "-inf"), (M - 1, N - 1, "inf"), (3, 200, "nan")]
+    bad = torch.zeros((M, N), dtype=torch.bool, device="cuda")
+    for m, n, v in places:
+        Z[m, n] = float(v)
+        bad[m, n] = True
+    dZ, db = lynx.lynx_act_backward(dY, Z)
+    assert torch.isnan(dZ[bad]).all() and torch.equal(dZ[~bad], want[~bad])
+    cols = bad.any(0)
+    assert torch.isnan(db[cols]).all() and torch.equal(db[~cols], wb[~cols])
