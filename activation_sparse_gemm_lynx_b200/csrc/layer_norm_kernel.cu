@@ -20,7 +20,7 @@
 // piece fit in registers up to kFusedCols columns; wider rows read dY and X once
 // more, by columns (column_pass_kernel.cu).
 //
-// 4608 x 4096: forward 13.8 us for 75.5 MB, backward with dr, dw and db 30.1 for 151.
+// 4608 x 4096: forward 13.9 us for 75.5 MB, backward with dr, dw and db 30.1 for 151.
 #include <cuda_bf16.h>
 
 #include "lynx_f32x2.cuh"
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kMaxThreads) layer_norm_kernel(LayerNormLaunch
   const uint4* const slot = ring + (tid >> 5) * (32 * V) + (tid & 31);
   const uint4* w = static_cast<const uint4*>(p.w) + first;
   const uint4* b = static_cast<const uint4*>(p.b) + first;
-  const float inv_k = 1.f / static_cast<float>(p.K);
+  const float cols = static_cast<float>(p.K), inv_k = 1.f / cols;
   pdl_wait();
   auto fetch = [&](int next) {
     if (next < M) {
@@ -143,7 +143,9 @@ __global__ void __launch_bounds__(kMaxThreads) layer_norm_kernel(LayerNormLaunch
         s2 = add2(s2, add2(add2(d[v][0], d[v][1]), add2(d[v][2], d[v][3])));
       }
     }
-    const float mean = row_sum(sum_of(s2), &red[0][group][t >> 5], red[0][group], warps, 1 + group) * inv_k;
+    // divided, not times 1 / K: a constant row's sum is exact, and so is its mean then.  Off by one
+    // rounding, a row of 30080 would lie 0.9 standard deviations (of sqrt(eps)) from it.
+    const float mean = __fdiv_rn(row_sum(sum_of(s2), &red[0][group][t >> 5], red[0][group], warps, 1 + group), cols);
     fetch(row + step);  // this row's values are in registers
     const f32x2 less = both(-mean);
     f32x2 q2 = both(0.f);

@@ -523,8 +523,9 @@ LYNX_API int lynx_act_backward(const void* dY, const void* Z, int64_t M, int64_t
  *     rstd = (v + eps)^(-1/2),   Y = (x - mu) rstd weight + bias
  *
  * weight and bias [K] bf16, each or NULL (1 and 0).  Statistics in fp32, the mean
- * taken off before anything is squared; Y is rounded once.  A row's squares must stay
- * inside fp32 (|x - mu| below 2^63 / sqrt(K)); those below its range count as 0.  A row
+ * taken off before anything is squared; Y is rounded once.  Equal values have no variance: such
+ * a row of Y is the bias.  A row's sum and its squares must stay inside fp32 (|x| below
+ * 2^127 / K, |x - mu| below 2^63 / sqrt(K)); squares below its range count as 0.  A row
  * with an infinity or a NaN gives NaN in that row of Y and dX (and in dweight, which sums
  * over the rows).  M >= 1; 8 <= K <= LYNX_LAYER_NORM_MAX_COLS with K % 8 == 0.
  * Buffers that a call of this section writes overlap no other of its buffers, but

@@ -31,3 +31,17 @@ def test_an_infinite_z_has_no_slope(M, N):
     assert torch.isnan(dZ[bad]).all() and torch.equal(dZ[~bad], want[~bad])
     cols = bad.any(0)
     assert torch.isnan(db[cols]).all() and torch.equal(db[~cols], wb[~cols])
+
+
+@pytest.mark.parametrize("K", [56, 104, 328, 448, 1000, 1920, 4032, 4224, 8560, 32760])  # one row a warp to one a block
+def test_a_constant_row_has_no_variance(K):
+    """K c has at most 15 + 8 bits, so the row's sum is exact and its mean is c itself: Y is the bias, bit for bit,
+    however far from zero the row lies (K's reciprocal is not exact, and c K (1 / K) is not c for these)."""
+    values = torch.tensor([3.0, 251.0, -100.0, 30080.0, 2.0 ** 100, -1.0078125, 0.0], device="cuda")
+    X = values[:, None].expand(-1, K).to(BF).contiguous()
+    bias = normal((K,), 1)
+    Y, mean, rstd = lynx.lynx_layer_norm(X, normal((K,), 2), bias, eps=1e-6, want_stats=True)
+    assert torch.equal(mean, X[:, 0].float())
+    assert torch.equal(Y, bias.expand_as(Y))
+    assert torch.allclose(rstd, torch.full_like(rstd, 1e3), rtol=1e-5)
+    assert torch.isnan(lynx.lynx_layer_norm(X, eps=0.0)).all()
