@@ -362,8 +362,10 @@ lynx_gemm_kernel(const __grid_constant__ GemmLaunch p) {
             b = gelu_tanh(b);
           }
           if constexpr (EXT) {
-            a = __fadd_rn(a, __uint_as_float(add[i / 8][i % 8] << 16));
-            b = __fadd_rn(b, __uint_as_float(add[i / 8][i % 8] & 0xFFFF0000u));
+            if (p.residual != nullptr) {  // +0 added would turn -0 into +0
+              a = __fadd_rn(a, __uint_as_float(add[i / 8][i % 8] << 16));
+              b = __fadd_rn(b, __uint_as_float(add[i / 8][i % 8] & 0xFFFF0000u));
+            }
           }
           __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
           out[kChunk / 2 * c + i] = *reinterpret_cast<uint32_t*>(&h);

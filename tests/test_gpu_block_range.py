@@ -45,3 +45,25 @@ def test_a_constant_row_has_no_variance(K):
     assert torch.equal(Y, bias.expand_as(Y))
     assert torch.allclose(rstd, torch.full_like(rstd, 1e3), rtol=1e-5)
     assert torch.isnan(lynx.lynx_layer_norm(X, eps=0.0)).all()
+
+
+def bits(t):
+    return t.view(torch.int16)
+
+
+@pytest.mark.parametrize("skip", [False, True])
+@pytest.mark.parametrize("M,N,K", [(1, 64, 64), (300, 1000, 576), (1300, 2056, 256)])  # 1-CTA tiles, CTA pairs
+def test_a_negative_zero_keeps_its_sign(M, N, K, skip):
+    """GELU of values below about -10 is -0.  Without a residual nothing is added to it: with Z the bits of Y are
+    those without."""
+    X, W, bias = normal((M, K), 1), normal((N, K), 2, K ** -0.5), normal((N,), 3)
+    bias[::5] = -40.0
+    want = lynx.lynx_linear_act(X, W, bias, act=lynx.LYNX_ACT_GELU_TANH, skip_sparsify=skip)
+    assert (bits(want) == -32768).any()
+    Y, Z = lynx.lynx_linear_residual(X, W, bias, act=lynx.LYNX_ACT_GELU_TANH, skip_sparsify=skip, want_Z=True)
+    assert torch.equal(bits(Y), bits(want))
+    # a residual of -0 leaves it, one of +0 does not
+    for zero, sign in ((-0.0, -32768), (0.0, 0)):
+        R = torch.full((M, N), zero, dtype=BF, device="cuda")
+        Y, _ = lynx.lynx_linear_residual(X, W, bias, R=R, act=lynx.LYNX_ACT_GELU_TANH, skip_sparsify=skip)
+        assert torch.all(bits(Y)[bits(want) == -32768] == sign)
