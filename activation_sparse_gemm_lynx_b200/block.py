@@ -110,9 +110,16 @@ class MlpBlock:
         return dh, {"norm": (dweight, dnorm), "up": up, "down": down}
 
     def quantize(self, group=128, zero_points=True):
-        """Lay out the weights in 4 bits for ``forward_few`` (the bf16 weights stay)."""
-        for layer in (self.up, self.down):
-            layer["w4"] = lynx.lynx_w4_quantize(layer["W"], group, zero_points=zero_points)
+        """Lay out the weights in 4 bits for ``forward_few`` (the bf16 weights stay).  Waits
+        for the current stream: ``forward_few`` may follow on any.  Not inside a capture.
+        Laid out again, the layout before is given up: graphs captured on it are void."""
+        import torch
+
+        if torch.cuda.is_current_stream_capturing():  # the graph's memory, without values until it is replayed
+            raise RuntimeError("quantize() before the capture")
+        laid = [lynx.lynx_w4_quantize(layer["W"], group, zero_points=zero_points) for layer in (self.up, self.down)]
+        torch.cuda.current_stream().synchronize()
+        self.up["w4"], self.down["w4"] = laid
 
     def forward_few(self, h):
         """h' for up to 32 tokens on the weights in 4 bits (``quantize`` first), both
