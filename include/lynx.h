@@ -242,7 +242,8 @@ LYNX_API int lynx_linear_act(const void* X, const void* W, const void* bias, con
 /* Y = R + act(P), P = S(X) W^T + bias + (X A^T) B^T: lynx_linear_act with the residual
  * stream added in the same epilogue, and with P itself kept for the backward pass.
  *   R   [M,N] bf16, or NULL: nothing is added.  R may be Y itself (the stream is
- *       updated in place).
+ *       updated in place): not where R's values are needed again, as by
+ *       lynx_layer_norm_backward, which takes the norm's input.
  *   Z   [M,N] bf16 out: P rounded once, or NULL: not kept.  lynx_act_backward takes it.
  * Y is rounded once, after the sum with R in fp32 (the value that act sees is P
  * before it is rounded to Z).  Saves the passes that would add R (two reads and a
@@ -550,7 +551,8 @@ LYNX_API size_t lynx_layer_norm_backward_workspace_bytes(int64_t M, int64_t K);
  *     dX = rstd (g - mean(g) - xh mean(g xh)) + dR
  *     dweight = sum over the rows of dY xh,   dbias = sum over the rows of dY
  *
- *   dY, X [M,K], mean and rstd as lynx_layer_norm left them, weight as given there.
+ *   dY [M,K]; X [M,K] the norm's input, unchanged, mean and rstd as lynx_layer_norm left
+ *   them, weight as given there.
  *   dR [M,K] or NULL: the gradient that reaches X beside the norm (the residual
  *   branch's); dR may be dX itself.  dweight and dbias [K] out, each or NULL (not
  *   wanted).  All bf16, rounded once; sums in fp32 in an order that only the shape
