@@ -738,7 +738,7 @@ lynx_gemm_pair_kernel(const __grid_constant__ GemmLaunch p) {
                                                           __fmaf_rn(s, __uint_as_float(r[c][e + 1]), sm.bias_s[col + e + 1]));
                 pk[i] = *reinterpret_cast<uint32_t*>(&zv);
               }
-              store_row16(static_cast<__nv_bfloat16*>(p.z) + at + 16 * done, pk, left - 16 * done, p.wide);
+              store_row16<false>(static_cast<__nv_bfloat16*>(p.z) + at + 16 * done, pk, left - 16 * done, p.wide);
             }
           }
 #pragma unroll

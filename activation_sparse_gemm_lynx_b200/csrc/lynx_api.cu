@@ -354,6 +354,7 @@ lynx_status run_gemm(DeviceState* ds, const void* a_src, bool sparse, const void
   p.residual = R;
   p.z = Z;
   p.ext = (R != nullptr || Z != nullptr) ? 1 : 0;
+  p.wide_y = N % 16 == 0 && (reinterpret_cast<uintptr_t>(Y) & 31u) == 0 ? 1 : 0;
   p.wide = N % 16 == 0 && ((reinterpret_cast<uintptr_t>(R) | reinterpret_cast<uintptr_t>(Z)) & 31u) == 0 ? 1 : 0;
   p.M = M;
   p.N = N;

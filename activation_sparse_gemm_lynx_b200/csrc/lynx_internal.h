@@ -122,6 +122,7 @@ struct GemmLaunch {
   void* z;              // [M,N] bf16: the value before the activation, or null (ext)
   int ext;              // residual or z is there (not with `fused`)
   int wide;             // their rows lie on 32 bytes
+  int wide_y;           // Y's do
   int64_t M, N, K;
   int r;                // LoRA rank (lora)
   int sparse;
