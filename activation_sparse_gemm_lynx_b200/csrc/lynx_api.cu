@@ -291,24 +291,37 @@ bool pair_kernel_takes(int64_t M, int64_t N, int64_t K) { return M > 128 && N >=
 
 // CTA pairs (256 x 256 tiles) unless one round of the 1-CTA kernel's smaller tiles has a tile for
 // every SM at most: 200 x 1024 -> 2000 takes 6.2 us there and 10.8 in pairs, 1000 x 4096 -> 2000
-// 21 and 27.  Sparse, a long K on few tiles is the pairs' (1000 x 4096 -> 2000: 28 us for 30).
+// 21 and 27.  Sparse, past a K of 2048 the pairs have them all (1000 x 4096 -> 2000: 28 us for 30);
+// past 1536 those whose tiles would be 128 columns wide, where at most 32 ranks are to be joined: a
+// layer's 1-CTA product is behind a kernel that joins the pass's partials, which a pair does itself.
+// join: the ranks of T to be joined, 0 for s alone, -1 where nothing is.  Sparse, pairs and 1-CTA
+// kernel, us:
+//                       product alone    r = 0            r = 16           r = 32           r = 64
+//   1000 x 2048 -> 2304   11.5  11.0     16.6  17.1       18.8  18.9       18.9  19.0       20.7  19.9
+//   1000 x 2048 -> 1504                  16.2  16.9       18.4  18.7       18.6  18.7       20.5  19.6
+//   500 x 2048 -> 4600                   16.5  17.7       18.3  19.4       18.7  19.3       20.6  20.2
+//   1000 x 1792 -> 2304                  16.1  16.4       18.2  18.1       18.4  18.1       19.9  19.1
+//   1000 x 1536 -> 2304   10.1   9.5     15.7  15.1       17.3  16.9       17.2  16.9       18.9  17.7
+//   500 x 512 -> 4608      7.1   6.3     11.6  10.3       14.6  12.0                        16.6  12.9
+//   1000 x 2048 -> 1000                  16.2  15.7       18.4  17.2       18.9  17.3       20.4  18.2  (64 columns)
 // Either gives the same bits.
-bool use_pair_kernel(int64_t M, int64_t N, int64_t K, bool sparse, int sms) {
+bool use_pair_kernel(int64_t M, int64_t N, int64_t K, bool sparse, int64_t join, int sms) {
   if (!pair_kernel_takes(M, N, K)) return false;
-  return (M + 127) / 128 * ((N + 127) / 128) > sms || (sparse && K > 2048);
+  const int64_t ntm = (M + 127) / 128;
+  if (ntm * ((N + 127) / 128) > sms) return true;
+  if (!sparse) return false;
+  return K > 2048 || (K > 1536 && join >= 0 && join <= 32 && ntm * ((N + 63) / 64) > sms);
 }
 
-// fused_x: a_src is the dense X and the pair kernel compresses it itself (the
-// shape must take the pair kernel; no metadata is read)
-lynx_status run_gemm(DeviceState* ds, const void* a_src, bool sparse, const void* meta,
+// pair: the CTA-pair kernel, else the 1-CTA kernel.  fused_x: a_src is the dense X and the
+// pair kernel compresses it itself (no metadata is read)
+lynx_status run_gemm(DeviceState* ds, const void* a_src, bool sparse, bool pair, const void* meta,
                      const float* row_scale, const void* T, const void* W, const void* bias,
                      const void* B, int64_t M, int64_t N, int64_t K, int64_t r, void* Y,
                      cudaStream_t stream, const FusedFinalize* fin = nullptr, int act = kActNone,
                      bool fused_x = false, const void* R = nullptr, void* Z = nullptr) {
   GemmLaunch p;
   std::memset(&p, 0, sizeof(p));
-  const bool pair = fused_x ? pair_kernel_takes(M, N, K) : use_pair_kernel(M, N, K, sparse, ds->sms);
-  if (fused_x && !pair) return LYNX_ERR_UNSUPPORTED_SHAPE;
   const int bn = pair ? 256 : gemm_bn(M, N, ds->sms);
   const uint32_t b_rows = pair ? 128u : static_cast<uint32_t>(bn);  // W rows one CTA loads
   // Boxes of A and T are no higher than the rows that there are, in whole 8-row swizzle atoms (the
@@ -577,7 +590,8 @@ lynx_status linear_enqueue(const void* X, const void* W, const void* bias, const
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   void* t_buf = lora ? ws + wl.t : nullptr;
   // with the CTA-pair GEMM, the GEMM itself combines the pass's K-range partials
-  const bool fused = use_pair_kernel(M, N, K, !skip_sparsify, ds->sms) && (!skip_sparsify || lora);
+  const bool pair = use_pair_kernel(M, N, K, !skip_sparsify, lora ? r : 0, ds->sms);
+  const bool fused = pair && (!skip_sparsify || lora);
   FusedFinalize fin;
   if (fused) {
     fin.mode = skip_sparsify ? 2 : 1;
@@ -605,9 +619,10 @@ lynx_status linear_enqueue(const void* X, const void* W, const void* bias, const
   if (void* ev = g_split_event.load())
     if (cudaEventRecord(static_cast<cudaEvent_t>(ev), s) != cudaSuccess) return LYNX_ERR_CUDA;
   if (!skip_sparsify)
-    return run_gemm(ds, ws + wl.vals, true, ws + wl.meta, reinterpret_cast<const float*>(ws + wl.scale),
-                    t_buf, W, bias, B, M, N, K, r, Y, s, fused ? &fin : nullptr, act, false, R, Z);
-  return run_gemm(ds, X, false, nullptr, nullptr, t_buf, W, bias, B, M, N, K, r, Y, s,
+    return run_gemm(ds, ws + wl.vals, true, pair, ws + wl.meta,
+                    reinterpret_cast<const float*>(ws + wl.scale), t_buf, W, bias, B, M, N, K, r, Y, s,
+                    fused ? &fin : nullptr, act, false, R, Z);
+  return run_gemm(ds, X, false, pair, nullptr, nullptr, t_buf, W, bias, B, M, N, K, r, Y, s,
                   fused ? &fin : nullptr, act, false, R, Z);
 }
 
@@ -711,7 +726,7 @@ int lynx_linear_fused(const void* X, const void* W, const void* bias, const void
   if (st != LYNX_OK) return st;
   if (void* ev = g_split_event.load())
     if (cudaEventRecord(static_cast<cudaEvent_t>(ev), s) != cudaSuccess) return LYNX_ERR_CUDA;
-  return run_gemm(ds, X, true, nullptr, nullptr, t_buf, W, bias, B, M, N, K, r, Y, s, &fin, act, true);
+  return run_gemm(ds, X, true, true, nullptr, nullptr, t_buf, W, bias, B, M, N, K, r, Y, s, &fin, act, true);
 }
 
 size_t lynx_linear_host_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t r) {
@@ -799,7 +814,8 @@ int lynx_sparse_gemm(const void* vals, const void* meta, const void* T, const vo
     return LYNX_ERR_MISALIGNED;
   DeviceState* ds = device_state();
   if (ds == nullptr) return LYNX_ERR_CUDA;
-  return run_gemm(ds, vals, true, meta, nullptr, T, W, bias, B, M, N, K, r, Y,
+  const bool pair = use_pair_kernel(M, N, K, true, -1, ds->sms);
+  return run_gemm(ds, vals, true, pair, meta, nullptr, T, W, bias, B, M, N, K, r, Y,
                   static_cast<cudaStream_t>(stream));
 }
 

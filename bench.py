@@ -56,12 +56,16 @@ DRAM_TRAFFIC = {
                  "bytes": {"mlp_up": 28734208, "attn_out": 25588224, "mlp_down": 145707520}},
 }
 
-def uses_pair_gemm(M, N, K, sparse=True, sms=148):
+def uses_pair_gemm(M, N, K, sparse=True, r=64, sms=148):
     """The library's choice: the CTA-pair GEMM unless the shape cannot feed it, or its
-    128 x 128 tiles come out at one an SM (a long K on the sparse path aside)."""
+    128 x 128 tiles come out at one an SM (a long K on the sparse path aside).  r: the
+    adapter's rank, 0 without one."""
     if not (M > 128 and N >= 256 and K % 128 == 0):
         return False
-    return -(-M // 128) * -(-N // 128) > sms or (sparse and K > 2048)
+    rows = -(-M // 128)
+    if rows * -(-N // 128) > sms:
+        return True
+    return sparse and (K > 2048 or (K > 1536 and r <= 32 and rows * -(-N // 64) > sms))
 
 
 def launches_per_linear(M, N, K, skip=False, lora=True):
@@ -70,7 +74,7 @@ def launches_per_linear(M, N, K, skip=False, lora=True):
     the pass's partials itself, and the GEMM."""
     if skip and not lora:
         return 1
-    return 2 if uses_pair_gemm(M, N, K, sparse=not skip) else 3
+    return 2 if uses_pair_gemm(M, N, K, sparse=not skip, r=64 if lora else 0) else 3
 
 
 def gemm_kernel_name(M, N, K):
