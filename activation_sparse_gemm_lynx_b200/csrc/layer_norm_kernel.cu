@@ -20,7 +20,7 @@
 // piece fit in registers up to kFusedCols columns; wider rows read dY and X once
 // more, by columns (column_pass_kernel.cu).
 //
-// 4608 x 4096: forward 13.9 us for 75.5 MB, backward with dr, dw and db 30.1 for 151.
+// 4608 x 4096: forward 13.8 us for 75.5 MB, backward with dr, dw and db 30.1 for 151.
 #include <cuda_bf16.h>
 
 #include "lynx_f32x2.cuh"
@@ -79,6 +79,15 @@ __device__ __forceinline__ float2 row_sums(float a, float b, float2* mine, const
     s = add2(s, add2(add2(pair_f32(q.x, q.y), pair_f32(q.z, q.w)), add2(pair_f32(r.x, r.y), pair_f32(r.z, r.w))));
   }
   return halves(s);
+}
+
+// sum / k, given inv = 1 / k rounded: sum inv, off by two roundings at most, and one step of iterative
+// refinement, q + (sum - q k) inv, whose residual fma leaves unrounded.  A row of equal values c has
+// the sum k c exactly, and c comes out: sum inv alone, one rounding off for some k, would set a row
+// of 30080 0.9 standard deviations (of sqrt(eps)) apart.  (__fdiv_rn spills: 14.0 us for 13.6.)
+__device__ __forceinline__ float quotient(float sum, float k, float inv) {
+  const float q = sum * inv, rest = fmaf(-q, k, sum);
+  return rest == rest ? fmaf(rest, inv, q) : q;  // an infinite sum leaves no residual
 }
 
 __device__ __forceinline__ void widen8(const uint4& p, f32x2 (&v)[4]) {
@@ -143,9 +152,7 @@ __global__ void __launch_bounds__(kMaxThreads) layer_norm_kernel(LayerNormLaunch
         s2 = add2(s2, add2(add2(d[v][0], d[v][1]), add2(d[v][2], d[v][3])));
       }
     }
-    // divided, not times 1 / K: a constant row's sum is exact, and so is its mean then.  Off by one
-    // rounding, a row of 30080 would lie 0.9 standard deviations (of sqrt(eps)) from it.
-    const float mean = __fdiv_rn(row_sum(sum_of(s2), &red[0][group][t >> 5], red[0][group], warps, 1 + group), cols);
+    const float mean = quotient(row_sum(sum_of(s2), &red[0][group][t >> 5], red[0][group], warps, 1 + group), cols, inv_k);
     fetch(row + step);  // this row's values are in registers
     const f32x2 less = both(-mean);
     f32x2 q2 = both(0.f);
