@@ -4,14 +4,17 @@
     H  = gelu(S(X) Wu^T + bu + (X Au^T) Bu^T)
     h' = h + S(H) Wd^T + bd + (H Ad^T) Bd^T
 
-W frozen, the adapters, the biases and the norm trained.  Every step is one call
-of the library: the norm, the two layers with GELU and the residual stream in
-their epilogues, and for a training step the 8-bit checkpoints of X and H, the
+W frozen, the adapters, the biases and the norm trained.  The norm and the two
+layers with GELU and the residual stream in their epilogues are one call of the
+library each, and so are for a training step the 8-bit checkpoints of X and H, the
 selections the forward pass made and Z, from which ``backward`` takes every
-gradient.  ``forward_few`` serves up to 32 tokens on the weights in 4 bits.
+gradient (torch copies a selection out of its workspace, and transposes the adapter
+of a layer that selective skipping leaves dense).  ``forward_few`` serves up to 32
+tokens on the weights in 4 bits.
 
 Everything runs on the current stream, captured or not.  Nothing is kept from one
-step for the next but the layouts of W.
+step for the next but the layouts of W (W^T from the first backward pass that is not
+captured: a graph captured before it transposes W in every replay).
 """
 from . import lynx
 
@@ -54,7 +57,8 @@ class MlpBlock:
         return Y, (*lynx.lynx_ckpt8_store(X, format=self.checkpoint), meta, Z)
 
     def forward(self, h, train=False):
-        """h' [M,K]; with ``train`` (h', saved), ``saved`` for one call of ``backward``."""
+        """h' [M,K]; with ``train`` (h', saved), ``saved`` for ``backward``: it holds h itself, which
+        must stay as it is until then."""
         if not train:
             X = lynx.lynx_layer_norm(h, self.weight, self.bias, eps=self.eps)
             H, _ = self._layer(self.up, X, False, act=lynx.LYNX_ACT_GELU_TANH)

@@ -10,7 +10,8 @@
 // a thread has 8 columns (16 bytes) and every ry-th row, a few rows' loads in
 // flight.  The block's sums meet in shared memory.  Up to kClusterRows rows the ranges of a
 // strip are a cluster, whose blocks add each other's sums from there: one launch, 2.5 us of
-// the host's time less and no more of the device's up to 100 rows (300 x 1000: 4.8 us for 4.2).
+// the host's time less and no more of the device's up to 100 rows (300 x 1000: 4.8 us for 4.2, so
+// that up to 320 rows it pays for eager calls and loses 0.6 us in a captured step).
 // Above, the sums leave as fp32, one row of `part` for each range, and
 // column_sums_kernel adds those.  Either in the order of the ranges; no atomics.
 //
@@ -33,7 +34,7 @@ constexpr int kUnroll = 4;  // rows of a thread in flight
 constexpr int kSumThreads = 256;
 constexpr int kMaxCluster = 8;
 constexpr int64_t kClusterRows = 320;
-constexpr int kSlots = 148 * 3;  // blocks a B200 holds
+constexpr int kSlots = 148 * 3;  // blocks a B200 holds; with fewer SMs the ranges are only less even
 
 constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -191,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 3) column_pass_kernel(ColumnPassLaun
 
 // part [count][C] -> bf16, the first `split` columns to out0, the rest to out1 (either may be null).
 // A block has 32 columns (a line of each row) and adds kSumThreads / 8 rows at a time, so
-// that all of `part` is on its way at once: 4608 x 4096's 296 rows of 8192, 9.7 MB from L2.
+// that all of `part` is on its way at once: 4608 x 4096's 148 rows of 8192, 4.9 MB from L2.
 __global__ void __launch_bounds__(kSumThreads) column_sums_kernel(const float* part, int count, int64_t C, int64_t split,
                                                                   __nv_bfloat16* out0, __nv_bfloat16* out1) {
   constexpr int kWays = kSumThreads / 8;

@@ -26,8 +26,8 @@
 //               (two warps per TMEM lane quarter, half of the columns each).
 // Accumulators: 1 TMEM buffer for BN = 256, 2 (double buffered) below.
 //
-// 20 rows of 4096 -> 4096, dense: 15.6 us, 33.5 MB of W (5.1 us); 64 rows of 2048 -> 1000
-// 8.6 us.  Bound by the MMA warp: a stage's wait, election and commit take it about 300
+// 20 rows of 4096 -> 4096, dense: 15.0 us, 33.5 MB of W (5.1 us); 64 rows of 2048 -> 1000
+// 8.3 us.  Bound by the MMA warp: a stage's wait, election and commit take it about 300
 // cycles beside 8 MMAs of 40.
 #include <cuda_bf16.h>
 

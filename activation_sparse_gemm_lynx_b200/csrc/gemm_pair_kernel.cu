@@ -3,7 +3,8 @@
 // and, in the variants with EXT, Y = bf16( R + act(v) ) with v itself in bf16 as Z.  The
 // sparse main loop draws 53 bytes a clock and SM from L2, next to what an SM can take, so
 // each tensor that the epilogue adds costs nearly its own time: 4608 x 4096 -> 12288, 210 us,
-// with R 230, with Z 229, with GELU and Z 236 (113 MB each, 17 us of the memory's).
+// with R 230, with Z 229, with GELU and Z 236 (113 MB each, 17 us of the memory's).  These
+// variants also spill 64 to 72 bytes at 168 registers.
 // Same arithmetic as gemm_kernel.cu (see there and the RT-Lynx references),
 // computed on 256 x 256 output tiles by a pair of CTAs on the two SMs of a
 // TPC: each CTA holds 128 rows of A (compressed activations, or X on the dense

@@ -1,6 +1,7 @@
 // lynx_api_adapter.cu -- the C ABI's entry points for the weight in 4 bits, the
-// 8-bit activation checkpoint and the backward pass: argument checks and
-// launches.  As everywhere, a failed check launches nothing.
+// 8-bit activation checkpoint, the backward pass, layer norm and the activation's
+// gradient: argument checks and launches.  As everywhere, a failed check launches
+// nothing.
 #include <cmath>
 #include <cstring>
 #include <initializer_list>

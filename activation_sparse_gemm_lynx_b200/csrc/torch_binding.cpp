@@ -6,6 +6,10 @@
 // Each function takes its arguments by position.  It returns its tensors, or a
 // lynx_status that is not LYNX_OK as an int; a tensor that does not fit raises.
 // The same checks through Python attributes took 8 us a call of the 12.
+//
+// Outputs and workspaces come from the allocator without the dispatcher (4 us a call of
+// the backward passes): dispatch modes do not see them, and memory that is filled under
+// deterministic algorithms is not (every output is written whole).
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDACachingAllocator.h>
