@@ -33,14 +33,15 @@ __device__ __forceinline__ void load_row16(uint32_t (&v)[8], const __nv_bfloat16
   }
 }
 
-// SOON: the next kernel reads them; else they make way in L2 (Z, until the backward pass)
+// SOON: the next kernel reads them; else they make way in L2 (Z, until the backward pass).  Past L1
+// either way: allocating there, 500 x 512 -> 4096, dense, takes 7.2 us for 6.7.
 template <bool SOON>
 __device__ __forceinline__ void store_row16(__nv_bfloat16* at, const uint32_t (&v)[8], int left, bool wide) {
   if (wide) {
     if (left <= 0) return;
     if constexpr (SOON)
-      asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-                   "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+      asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(v[0]),
+                   "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                    : "memory");
     else
       asm volatile("st.global.L1::no_allocate.L2::evict_first.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at),
